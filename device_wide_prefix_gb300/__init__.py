@@ -60,6 +60,14 @@ EXPORTS = [
     "dwp_read_lookback_stats",
     "dwp_debug_set_delay",
     "dwp_debug_warp_scan_trace",
+    "dwp_causal_conv",
+    "dwp_causal_conv_backward",
+    "dwp_causal_conv_step",
+    "dwp_selective_scan",
+    "dwp_selective_scan_backward",
+    "dwp_selective_scan_step",
+    "dwp_block_norm",
+    "dwp_block_norm_backward",
 ]
 
 _lib = None
@@ -121,6 +129,15 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.dwp_scan_static_scratch.restype = c.c_int
     lib.dwp_scan_two_level.argtypes = [c.c_int, c.c_int, P, P, S, P, Z, P]
     lib.dwp_scan_two_level.restype = c.c_int
+    lib.dwp_causal_conv.argtypes = [c.c_char_p, P]
+    lib.dwp_causal_conv_step.argtypes = [c.c_char_p, P]
+    lib.dwp_selective_scan_step.argtypes = [c.c_char_p, P]
+    lib.dwp_block_norm.argtypes = [c.c_char_p, P]
+    for name in ("dwp_causal_conv_backward", "dwp_selective_scan", "dwp_selective_scan_backward",
+                 "dwp_block_norm_backward"):
+        getattr(lib, name).argtypes = [c.c_char_p, P, Z, P]
+    for name in EXPORTS[-8:]:
+        getattr(lib, name).restype = c.c_int
     if path == LIB_PATH:
         _lib = lib
     return lib
@@ -537,3 +554,19 @@ def read_fallbacks(scratch, stream=None) -> int:
     st, v = dwp_read_fallbacks(scratch.data_ptr(), _stream_of(scratch, stream))
     _check(st, "dwp_read_fallbacks")
     return v
+
+
+# ---------------------------------------------------------------------------
+# sequence operators (their module needs torch, which the C layer does not)
+
+_SEQUENCE = ("causal_conv", "causal_conv_backward", "causal_conv_step", "selective_scan",
+             "selective_scan_backward", "selective_scan_step", "block_norm", "block_norm_backward")
+
+
+def __getattr__(name):
+    if name in _SEQUENCE:
+        from . import sequence
+        for k in _SEQUENCE:
+            globals()[k] = getattr(sequence, k)
+        return globals()[name]
+    raise AttributeError("module %r has no attribute %r" % (__name__, name))

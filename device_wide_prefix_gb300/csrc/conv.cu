@@ -1,0 +1,338 @@
+// Short causal depthwise convolution over packed rows: forward, gradient and
+// the single-token form.
+//
+//   p[t] = bias + sum_k w[k] x[t - (W-1) + k],   y = p or p * sigmoid(p)
+//
+// per channel, where rows before a segment's first come from its state rows.
+// Every element is read and written once: the work is HBM traffic.
+#include "sequence.cuh"
+
+namespace dwp {
+
+namespace {
+
+constexpr int kConvThreads = 128;
+constexpr int kConvStrip = 32;  // rows one thread walks
+
+// Where a packed row lies: its segment and the segment's rows.
+struct Span {
+    uint32_t seg;
+    int64_t begin, end;  // rows [begin, end) of this batch entry's stream
+};
+
+// Segment span at row t (packed: by offsets; otherwise the whole batch entry).
+// A row that no segment covers gets begin > t.
+__device__ __forceinline__ Span span_at(const uint32_t *offsets, uint32_t nseg, uint32_t batch,
+                                        int64_t rows, int64_t t) {
+    if (!offsets) return {batch, 0, rows};
+    const uint32_t s = segment_of(offsets, nseg, static_cast<uint32_t>(t));
+    if (s >= nseg) return {s, rows, rows};
+    return {s, int64_t(offsets[s]), min(int64_t(offsets[s + 1]), rows)};
+}
+
+// Forward.  A thread walks kConvStrip rows of V channels with the last W - 1
+// inputs and the taps in registers, so each input is read once (plus W - 1
+// rows per strip).
+template <class T, int V, int W>
+__global__ void __launch_bounds__(kConvThreads) conv_kernel(ConvParams p) {
+    pdl_trigger();
+    pdl_wait();
+    const int64_t c0 = (int64_t(blockIdx.y) * kConvThreads + threadIdx.x) * V;
+    if (c0 >= p.channels) return;
+    const uint32_t b = blockIdx.x / p.strips;
+    const int64_t t0 = int64_t(blockIdx.x % p.strips) * kConvStrip;
+    const int64_t t1 = min(t0 + kConvStrip, p.rows);
+    const int halo = p.width - 1;
+
+    // taps w[W-1] for the row itself, w[W-1-j] for j rows before; 0 past the width
+    float w[W][V], bias[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+#pragma unroll
+        for (int j = 0; j < W; ++j)
+            w[j][i] = j <= halo ? load_param<T>(p.weight, (c0 + i) * p.width + (halo - j), p.weight_f32) : 0.0f;
+        bias[i] = p.bias ? load_param<T>(p.bias, c0 + i, p.weight_f32) : 0.0f;
+    }
+    const T *x = static_cast<const T *>(p.x) + int64_t(b) * p.x_batch + c0;
+    T *y = static_cast<T *>(p.y) + int64_t(b) * p.y_batch + c0;
+    const T *init = static_cast<const T *>(p.initial_state);
+    T *fin = static_cast<T *>(p.final_state);
+
+    float win[W][V];  // win[j]: the input j rows before the current one
+    Span sp{0, p.rows, 0};
+    for (int64_t t = t0; t < t1; ++t) {
+        if (t == t0 || t >= sp.end) {
+            sp = span_at(p.offsets, p.num_segments, b, p.rows, t);
+            if (sp.begin <= t) {
+#pragma unroll
+                for (int j = 1; j < W; ++j) {  // row t - j, or the state row that stands for it
+                    const int64_t r = t - j;
+#pragma unroll
+                    for (int i = 0; i < V; ++i) win[j - 1][i] = 0.0f;
+                    if (j <= halo) {
+                        if (r >= sp.begin) load_f32<V>(win[j - 1], x + r * p.x_row);
+                        else if (init)
+                            load_f32<V>(win[j - 1], init + (int64_t(sp.seg) * halo + (r - sp.begin + halo)) * p.channels + c0);
+                    }
+                }
+            }
+        }
+        if (sp.begin > t) continue;  // outside every segment: left unwritten
+#pragma unroll
+        for (int j = W - 1; j > 0; --j)
+#pragma unroll
+            for (int i = 0; i < V; ++i) win[j][i] = win[j - 1][i];
+        load_f32<V>(win[0], x + t * p.x_row);
+        float o[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            float a = bias[i];
+#pragma unroll
+            for (int j = 0; j < W; ++j) a = fmaf(w[j][i], win[j][i], a);
+            o[i] = p.silu ? silu(a) : a;
+        }
+        store_f32<V>(y + t * p.y_row, o);
+        if (fin && t == sp.end - 1) {
+#pragma unroll
+            for (int j = 0; j < W; ++j)
+                if (j < halo)
+                    store_f32<V>(fin + (int64_t(sp.seg) * halo + (halo - 1 - j)) * p.channels + c0, win[j]);
+        }
+    }
+}
+
+// An empty segment hands its state on: dst rows = src rows (0 without src).
+template <class T>
+__global__ void __launch_bounds__(kConvThreads)
+    empty_state_kernel(const uint32_t *offsets, int64_t count, const T *src, T *dst) {
+    pdl_trigger();
+    pdl_wait();
+    const uint32_t s = blockIdx.x;
+    if (offsets && offsets[s] < offsets[s + 1]) return;
+    for (int64_t i = threadIdx.x; i < count; i += kConvThreads)
+        dst[s * count + i] = src ? src[s * count + i] : from_f32<T>(0.0f);
+}
+
+// Gradient.  With g[t] = dy[t] * act'(p[t]), each tap scatters g backwards:
+// row t - j of the segment (or the state row that stands for it) receives
+// w[W-1-j] g[t].  A thread walks its strip and W - 1 rows past it with the
+// unfinished sums in registers, and writes a row's sum once the last tap
+// reached it.  Each row's g also adds to the taps' gradients, which are
+// summed over the block's strips in shared memory, written per block, and
+// summed over the blocks in a fixed order by a second kernel.
+template <class T, int V, int W>
+__global__ void __launch_bounds__(kConvThreads) conv_backward_kernel(ConvBackwardParams q) {
+    pdl_trigger();
+    pdl_wait();
+    const ConvParams &p = q.c;
+    const int64_t c0 = (int64_t(blockIdx.y) * kConvThreads + threadIdx.x) * V;
+    if (c0 >= p.channels) return;
+    const uint32_t b = blockIdx.x / p.strips;
+    const int64_t t0 = int64_t(blockIdx.x % p.strips) * q.strip_rows;
+    const int64_t t1 = min(t0 + q.strip_rows, p.rows);
+    const int64_t te = min(t1 + p.width - 1, p.rows);
+    const int halo = p.width - 1;
+
+    float w[W][V], bias[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+#pragma unroll
+        for (int j = 0; j < W; ++j)
+            w[j][i] = j <= halo ? load_param<T>(p.weight, (c0 + i) * p.width + (halo - j), p.weight_f32) : 0.0f;
+        bias[i] = p.bias ? load_param<T>(p.bias, c0 + i, p.weight_f32) : 0.0f;
+    }
+    const T *x = static_cast<const T *>(p.x) + int64_t(b) * p.x_batch + c0;
+    const T *dy = static_cast<const T *>(q.grad_out) + int64_t(b) * q.grad_batch + c0;
+    T *dx = static_cast<T *>(q.grad_x) + int64_t(b) * q.gx_batch + c0;
+    const T *init = static_cast<const T *>(p.initial_state);
+    T *dinit = static_cast<T *>(q.grad_initial);
+    const T *dfin = static_cast<const T *>(q.grad_final);
+
+    float win[W][V], acc[W][V], dw[W][V], db[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        db[i] = 0.0f;
+#pragma unroll
+        for (int j = 0; j < W; ++j) dw[j][i] = acc[j][i] = win[j][i] = 0.0f;
+    }
+    Span sp{0, p.rows, 0};
+    // the finished sum of row r: an own row of the strip, or a state row of a
+    // segment that begins in the strip
+    auto put = [&](int64_t r, const float(&v)[V]) {
+        if (r >= sp.begin) {
+            if (r >= t0 && r < t1) store_f32<V>(dx + r * q.gx_row, v);
+        } else if (dinit && sp.begin >= t0 && sp.begin < t1 && r >= sp.begin - halo) {
+            store_f32<V>(dinit + (int64_t(sp.seg) * halo + (r - sp.begin + halo)) * p.channels + c0, v);
+        }
+    };
+    for (int64_t t = t0; t < te; ++t) {
+        if (t == t0 || t >= sp.end) {
+            sp = span_at(p.offsets, p.num_segments, b, p.rows, t);
+            if (sp.begin <= t) {
+                if (t >= t1) {
+                    if (sp.begin == t) break;  // a segment of the next strip
+                }
+#pragma unroll
+                for (int j = 1; j < W; ++j) {
+                    const int64_t r = t - j;
+#pragma unroll
+                    for (int i = 0; i < V; ++i) win[j - 1][i] = 0.0f, acc[j - 1][i] = 0.0f;
+                    if (j <= halo) {
+                        if (r >= sp.begin) load_f32<V>(win[j - 1], x + r * p.x_row);
+                        else if (init)
+                            load_f32<V>(win[j - 1], init + (int64_t(sp.seg) * halo + (r - sp.begin + halo)) * p.channels + c0);
+                    }
+                }
+            }
+        }
+        if (sp.begin > t) continue;
+#pragma unroll
+        for (int j = W - 1; j > 0; --j)
+#pragma unroll
+            for (int i = 0; i < V; ++i) win[j][i] = win[j - 1][i], acc[j][i] = acc[j - 1][i];
+        load_f32<V>(win[0], x + t * p.x_row);
+        float g[V];
+        load_f32<V>(g, dy + t * q.grad_row);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            float a = bias[i];
+#pragma unroll
+            for (int j = 0; j < W; ++j) a = fmaf(w[j][i], win[j][i], a);
+            if (p.silu) g[i] *= silu_slope(a);
+            acc[0][i] = 0.0f;
+#pragma unroll
+            for (int j = 0; j < W; ++j) acc[j][i] = fmaf(w[j][i], g[i], acc[j][i]);
+            if (t < t1) {
+                db[i] += g[i];
+#pragma unroll
+                for (int j = 0; j < W; ++j) dw[j][i] = fmaf(g[i], win[j][i], dw[j][i]);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < W; ++j)
+            if (j == halo) put(t - j, acc[j]);
+        if (t == sp.end - 1) {  // the rows that no later row of the segment reaches
+#pragma unroll
+            for (int j = 0; j < W - 1; ++j)
+                if (j < halo) {
+                    float v[V];
+#pragma unroll
+                    for (int i = 0; i < V; ++i) v[i] = 0.0f;
+                    if (dfin) load_f32<V>(v, dfin + (int64_t(sp.seg) * halo + (halo - 1 - j)) * p.channels + c0);
+#pragma unroll
+                    for (int i = 0; i < V; ++i) v[i] += acc[j][i];
+                    put(t - j, v);
+                }
+        }
+    }
+    float *part = q.partial + (int64_t(blockIdx.x) * (p.width + 1)) * p.channels + c0;
+#pragma unroll
+    for (int j = 0; j < W; ++j)
+        if (j <= halo) store_f32<V>(part + int64_t(halo - j) * p.channels, dw[j]);
+    store_f32<V>(part + int64_t(p.width) * p.channels, db);
+}
+
+// One token for each row of a batch: the slot's W - 1 state rows and the new
+// input give the output, and the state moves on by one row.
+template <class T, int V, int W>
+__global__ void __launch_bounds__(kConvThreads) conv_step_kernel(ConvStepParams p) {
+    pdl_trigger();
+    pdl_wait();
+    const int64_t c0 = (int64_t(blockIdx.y) * kConvThreads + threadIdx.x) * V;
+    if (c0 >= p.channels) return;
+    const int64_t b = blockIdx.x;
+    const int halo = p.width - 1;
+    T *y = static_cast<T *>(p.y) + b * p.y_row + c0;
+    const int64_t slot = p.slots ? p.slots[b] : b;
+    float o[V];
+    if (slot < 0 || slot >= p.num_slots) {  // a padding row
+#pragma unroll
+        for (int i = 0; i < V; ++i) o[i] = 0.0f;
+        store_f32<V>(y, o);
+        return;
+    }
+    T *st = static_cast<T *>(p.state) + slot * p.state_slot + c0;
+    float win[W][V];
+    load_f32<V>(win[0], static_cast<const T *>(p.x) + b * p.x_row + c0);
+#pragma unroll
+    for (int j = 1; j < W; ++j) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) win[j][i] = 0.0f;
+        if (j <= halo) load_f32<V>(win[j], st + int64_t(halo - j) * p.channels);
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        float a = p.bias ? load_param<T>(p.bias, c0 + i, p.weight_f32) : 0.0f;
+#pragma unroll
+        for (int j = 0; j < W; ++j)
+            if (j <= halo)
+                a = fmaf(load_param<T>(p.weight, (c0 + i) * p.width + (halo - j), p.weight_f32), win[j][i], a);
+        o[i] = p.silu ? silu(a) : a;
+    }
+    store_f32<V>(y, o);
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j)
+        if (j < halo) store_f32<V>(st + int64_t(halo - 1 - j) * p.channels, win[j]);
+}
+
+template <class T, int V>
+cudaError_t conv_forward_w(const ConvParams &p, cudaStream_t s) {
+    const dim3 grid(uint32_t(p.batch * p.strips), uint32_t((p.channels + kConvThreads * V - 1) / (kConvThreads * V)));
+    if (p.width <= 4) return launch_pdl(conv_kernel<T, V, 4>, grid, dim3(kConvThreads), 0, s, p);
+    return launch_pdl(conv_kernel<T, V, 8>, grid, dim3(kConvThreads), 0, s, p);
+}
+
+template <class T, int V>
+cudaError_t conv_backward_w(const ConvBackwardParams &q, cudaStream_t s) {
+    const ConvParams &p = q.c;
+    const dim3 grid(uint32_t(p.batch * p.strips), uint32_t((p.channels + kConvThreads * V - 1) / (kConvThreads * V)));
+    if (p.width <= 4) return launch_pdl(conv_backward_kernel<T, V, 4>, grid, dim3(kConvThreads), 0, s, q);
+    return launch_pdl(conv_backward_kernel<T, V, 8>, grid, dim3(kConvThreads), 0, s, q);
+}
+
+template <class T, int V>
+cudaError_t conv_step_w(const ConvStepParams &p, cudaStream_t s) {
+    const dim3 grid(uint32_t(p.batch), uint32_t((p.channels + kConvThreads * V - 1) / (kConvThreads * V)));
+    if (p.width <= 4) return launch_pdl(conv_step_kernel<T, V, 4>, grid, dim3(kConvThreads), 0, s, p);
+    return launch_pdl(conv_step_kernel<T, V, 8>, grid, dim3(kConvThreads), 0, s, p);
+}
+
+template <class T>
+cudaError_t empty_states(const uint32_t *offsets, int64_t segments, int64_t count, const void *src, void *dst,
+                         cudaStream_t s) {
+    return launch_pdl(empty_state_kernel<T>, dim3(uint32_t(segments)), dim3(kConvThreads), 0, s, offsets, count,
+                      static_cast<const T *>(src), static_cast<T *>(dst));
+}
+
+}  // namespace
+
+int64_t conv_strip_rows() { return kConvStrip; }
+
+cudaError_t launch_empty_states(dwp_dtype t, const uint32_t *offsets, int64_t segments, int64_t count,
+                                const void *src, void *dst, cudaStream_t s) {
+    if (segments == 0 || count == 0) return cudaSuccess;
+    if (t == DWP_F32) return empty_states<float>(offsets, segments, count, src, dst, s);
+    if (t == DWP_BF16) return empty_states<__nv_bfloat16>(offsets, segments, count, src, dst, s);
+    return empty_states<__half>(offsets, segments, count, src, dst, s);
+}
+
+cudaError_t launch_conv(dwp_dtype t, const ConvParams &p, bool vec, cudaStream_t s) {
+    if (t == DWP_F32) return vec ? conv_forward_w<float, 4>(p, s) : conv_forward_w<float, 1>(p, s);
+    if (t == DWP_BF16) return vec ? conv_forward_w<__nv_bfloat16, 8>(p, s) : conv_forward_w<__nv_bfloat16, 1>(p, s);
+    return vec ? conv_forward_w<__half, 8>(p, s) : conv_forward_w<__half, 1>(p, s);
+}
+
+cudaError_t launch_conv_backward(dwp_dtype t, const ConvBackwardParams &p, bool vec, cudaStream_t s) {
+    if (t == DWP_F32) return vec ? conv_backward_w<float, 4>(p, s) : conv_backward_w<float, 1>(p, s);
+    if (t == DWP_BF16)
+        return vec ? conv_backward_w<__nv_bfloat16, 4>(p, s) : conv_backward_w<__nv_bfloat16, 1>(p, s);
+    return vec ? conv_backward_w<__half, 4>(p, s) : conv_backward_w<__half, 1>(p, s);
+}
+
+cudaError_t launch_conv_step(dwp_dtype t, const ConvStepParams &p, bool vec, cudaStream_t s) {
+    if (t == DWP_F32) return vec ? conv_step_w<float, 4>(p, s) : conv_step_w<float, 1>(p, s);
+    if (t == DWP_BF16) return vec ? conv_step_w<__nv_bfloat16, 8>(p, s) : conv_step_w<__nv_bfloat16, 1>(p, s);
+    return vec ? conv_step_w<__half, 8>(p, s) : conv_step_w<__half, 1>(p, s);
+}
+
+}  // namespace dwp

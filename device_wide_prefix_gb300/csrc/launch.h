@@ -101,4 +101,118 @@ uint32_t recurrence_tile_elems();
 cudaError_t launch_recurrence(const float *a, const float *b, float *h, uint64_t n, bool inclusive,
                               void *scratch, cudaStream_t stream);
 
+// ---------------------------------------------------------------------------
+// Sequence operators (conv.cu, selscan.cu, selscan_bwd.cu, norm.cu).  Strides
+// are in elements.
+
+struct ConvParams {
+    int64_t channels, batch, rows, strips;  // strips: blocks of rows per batch entry
+    int width, silu;
+    bool weight_f32;
+    const void *x, *weight, *bias, *initial_state;
+    void *y, *final_state;
+    int64_t x_batch, x_row, y_batch, y_row;
+    const uint32_t *offsets;
+    uint32_t num_segments;
+};
+struct ConvBackwardParams {
+    ConvParams c;
+    int64_t strip_rows;
+    const void *grad_out, *grad_final;
+    void *grad_x, *grad_initial;
+    int64_t grad_batch, grad_row, gx_batch, gx_row;
+    float *partial;  // [batch * strips][width + 1][channels]
+};
+struct ConvStepParams {
+    int64_t channels, batch, num_slots;
+    int width, silu;
+    bool weight_f32;
+    const void *x, *weight, *bias;
+    void *y, *state;
+    int64_t x_row, y_row, state_slot;
+    const int32_t *slots;
+};
+int64_t conv_strip_rows();
+cudaError_t launch_conv(dwp_dtype t, const ConvParams &p, bool vec, cudaStream_t s);
+cudaError_t launch_conv_backward(dwp_dtype t, const ConvBackwardParams &p, bool vec, cudaStream_t s);
+cudaError_t launch_conv_step(dwp_dtype t, const ConvStepParams &p, bool vec, cudaStream_t s);
+// Empty segments (all, if offsets is NULL) hand `count` state elements on.
+cudaError_t launch_empty_states(dwp_dtype t, const uint32_t *offsets, int64_t segments, int64_t count,
+                                const void *src, void *dst, cudaStream_t s);
+
+// Where column sums go: columns [0, end[0]) to out[0], up to end[1] to out[1],
+// up to end[2] to out[2] (a NULL out drops its columns).  The first range is
+// `planes` planes of equal length, written interleaved.
+struct ColumnOut {
+    float *out[3];
+    int64_t end[3];
+    int64_t planes;
+};
+cudaError_t launch_column_sums(const float *part, int64_t blocks, int64_t cols, const ColumnOut &o,
+                               cudaStream_t s);
+
+struct ScanParams {
+    int64_t channels, group, groups, batch, rows;  // group: channels of a group
+    int64_t chunk_rows, chunks, tiles;             // tiles: saved states per batch entry
+    int states, softplus;
+    uint32_t group_blocks;  // channel blocks of a group (set by the launcher)
+    const void *u, *dt, *z, *B, *C;
+    void *out;
+    int64_t u_batch, u_row, dt_batch, dt_row, z_batch, z_row, out_batch, out_row;
+    int64_t b_batch, b_row, b_group, c_batch, c_row, c_group;
+    const float *A, *D, *dt_bias, *initial;
+    float *final, *checkpoints;
+    const uint32_t *segmap;  // NULL, or a code word per packed row
+};
+struct ScanBackwardParams {
+    ScanParams f;
+    const void *grad_out;
+    int64_t grad_batch, grad_row;
+    const float *grad_final;
+    void *grad_u, *grad_dt, *grad_z, *grad_B, *grad_C;
+    float *grad_initial;
+    float *partial;     // [batch * chunks][channels * (states + 2)]
+    float *partial_bc;  // [channel blocks of a group][batch * rows][groups][2][states]
+};
+struct ScanStepParams {
+    int64_t channels, group, groups, batch, num_slots;
+    int states, softplus;
+    uint32_t group_blocks;
+    const void *u, *dt, *z, *B, *C;
+    void *out;
+    int64_t u_row, dt_row, z_row, out_row, b_row, b_group, c_row, c_group;
+    const float *A, *D, *dt_bias;
+    float *state;
+    int64_t state_slot;
+    const int32_t *slots;
+};
+// Channels one block of the selective scan covers at this many states.
+int64_t scan_block_channels(int64_t states);
+cudaError_t launch_segment_map(const uint32_t *offsets, uint32_t nseg, uint32_t rows, uint32_t *map,
+                               cudaStream_t s);
+cudaError_t launch_selscan(dwp_dtype t, const ScanParams &p, cudaStream_t s);
+cudaError_t launch_selscan_backward(dwp_dtype t, const ScanBackwardParams &p, cudaStream_t s);
+cudaError_t launch_selscan_step(dwp_dtype t, const ScanStepParams &p, cudaStream_t s);
+
+struct NormParams {
+    int64_t channels, group, groups, rows;  // group: elements normed together
+    float eps;
+    int gate_after;
+    bool weight_f32, residual_f32;
+    const void *x, *residual, *gate, *weight, *scale;
+    void *y, *sum;
+    int64_t x_row, residual_row, gate_row, y_row, sum_row;
+};
+struct NormBackwardParams {
+    NormParams n;
+    int64_t blocks;  // blocks a group's rows are spread over
+    const void *v, *x_in, *grad_out, *grad_sum;  // v: the norm's input; x_in: x, for the scale's gradient
+    bool v_f32;
+    void *grad_x, *grad_residual, *grad_gate;
+    int64_t v_row, xin_row, grad_row, gsum_row, gx_row, gres_row, ggate_row;
+    float *partial;  // [blocks][1 or 2][channels]
+};
+cudaError_t launch_norm(dwp_dtype t, const NormParams &p, bool vec, cudaStream_t s);
+cudaError_t launch_norm_backward(dwp_dtype t, const NormBackwardParams &p, bool vec, cudaStream_t s);
+
 }  // namespace dwp

@@ -1,0 +1,285 @@
+// Block norm: the root-mean-square norm before and after a block, fused with
+// the residual add and its scale (before) and with the gate (after), and its
+// gradient.
+//
+//   v = residual + scale * x            (or x);  sum = v
+//   t = v * silu(gate)                  (gate before the norm; else t = v)
+//   y = t * rsqrt(mean_group(t^2) + eps) * weight   (* silu(gate) after it)
+//
+// One block per row and group; a row's elements stay in registers between
+// the statistics and the output, so each input is read once.
+#include "sequence.cuh"
+
+namespace dwp {
+
+namespace {
+
+// Sum of `a` and `b` over the block; every thread gets both.
+template <int N>
+__device__ __forceinline__ void block_sums(float (&v)[N], float *sh) {
+    const int warps = (blockDim.x + 31) / 32, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+    if (warps == 1) return;
+    __syncthreads();  // the previous use of sh is over
+    if (lane == 0)
+#pragma unroll
+        for (int k = 0; k < N; ++k) sh[k * 32 + warp] = v[k];
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        float s = lane < warps ? sh[k * 32 + lane] : 0.0f;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        v[k] = s;
+    }
+}
+
+template <class T, int V>
+__device__ __forceinline__ void load_residual(float (&f)[V], const void *p, int64_t i, bool is_f32) {
+    if (is_f32) load_f32<V>(f, static_cast<const float *>(p) + i);
+    else load_f32<V>(f, static_cast<const T *>(p) + i);
+}
+template <class T, int V>
+__device__ __forceinline__ void store_residual(void *p, int64_t i, const float (&f)[V], bool is_f32) {
+    if (is_f32) store_f32<V>(static_cast<float *>(p) + i, f);
+    else store_f32<V>(static_cast<T *>(p) + i, f);
+}
+
+template <class T, int V, int K>
+__global__ void __launch_bounds__(1024) norm_kernel(NormParams p) {
+    __shared__ float sh[32];
+    pdl_trigger();
+    pdl_wait();
+    const int64_t row = blockIdx.x / p.groups;
+    const int64_t g0 = int64_t(blockIdx.x % p.groups) * p.group;
+    const T *x = static_cast<const T *>(p.x) + row * p.x_row + g0;
+    const T *z = p.gate ? static_cast<const T *>(p.gate) + row * p.gate_row + g0 : nullptr;
+    T *y = static_cast<T *>(p.y) + row * p.y_row + g0;
+    float v[K][V], gt[K][V], ss[1] = {0.0f};
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int64_t i = (int64_t(k) * blockDim.x + threadIdx.x) * V;
+#pragma unroll
+        for (int j = 0; j < V; ++j) v[k][j] = 0.0f, gt[k][j] = 1.0f;
+        if (i < p.group) {
+            load_f32<V>(v[k], x + i);
+            if (p.residual) {
+                float r[V];
+                load_residual<T, V>(r, p.residual, row * p.residual_row + g0 + i, p.residual_f32);
+#pragma unroll
+                for (int j = 0; j < V; ++j)
+                    v[k][j] = p.scale ? fmaf(load_param<T>(p.scale, g0 + i + j, p.weight_f32), v[k][j], r[j])
+                                      : v[k][j] + r[j];
+                store_residual<T, V>(p.sum, row * p.sum_row + g0 + i, v[k], p.residual_f32);
+            }
+            if (z) {
+                load_f32<V>(gt[k], z + i);
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    gt[k][j] = silu(gt[k][j]);
+                    if (!p.gate_after) v[k][j] *= gt[k][j];
+                }
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < V; ++j) ss[0] = fmaf(v[k][j], v[k][j], ss[0]);
+    }
+    block_sums(ss, sh);
+    const float r = rsqrtf(ss[0] / float(p.group) + p.eps);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int64_t i = (int64_t(k) * blockDim.x + threadIdx.x) * V;
+        if (i < p.group) {
+            float o[V];
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                o[j] = v[k][j] * r * load_param<T>(p.weight, g0 + i + j, p.weight_f32);
+                if (p.gate_after) o[j] *= gt[k][j];
+            }
+            store_f32<V>(y + i, o);
+        }
+    }
+}
+
+// Gradient.  With h = t r (r the inverse root mean square) and gw = dy * weight
+// (after: dy * silu(gate) * weight):
+//   dt = r (gw - h mean(gw h)),  dweight = sum_rows dy h (* silu(gate)).
+// Both means come from one reduction (t^2 and gw t).  A block keeps one
+// group's columns and walks rows blockIdx.x, + gridDim.x, ..., so the column
+// sums stay in registers; each block writes its share and a second kernel
+// adds the shares in a fixed order.
+template <class T, int V, int K>
+__global__ void __launch_bounds__(K *V >= 16 ? 512 : 1024) norm_backward_kernel(NormBackwardParams q) {
+    __shared__ float sh[64];
+    pdl_trigger();
+    pdl_wait();
+    const NormParams &p = q.n;
+    const int64_t g0 = int64_t(blockIdx.y) * p.group;
+    float dw[K][V], ds[K][V];
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int j = 0; j < V; ++j) dw[k][j] = ds[k][j] = 0.0f;
+    for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+        const T *dy = static_cast<const T *>(q.grad_out) + row * q.grad_row + g0;
+        const T *z = p.gate ? static_cast<const T *>(p.gate) + row * p.gate_row + g0 : nullptr;
+        float t[K][V], gw[K][V], red[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int64_t i = (int64_t(k) * blockDim.x + threadIdx.x) * V;
+#pragma unroll
+            for (int j = 0; j < V; ++j) t[k][j] = gw[k][j] = 0.0f;
+            if (i < p.group) {
+                load_residual<T, V>(t[k], q.v, row * q.v_row + g0 + i, q.v_f32);
+                load_f32<V>(gw[k], dy + i);
+                float gt[V];
+                if (z) load_f32<V>(gt, z + i);
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    const float s = z ? silu(gt[j]) : 1.0f;
+                    if (z && !p.gate_after) t[k][j] *= s;
+                    if (z && p.gate_after) gw[k][j] *= s;
+                    gw[k][j] *= load_param<T>(p.weight, g0 + i + j, p.weight_f32);
+                    red[0] = fmaf(t[k][j], t[k][j], red[0]);
+                    red[1] = fmaf(gw[k][j], t[k][j], red[1]);
+                }
+            }
+        }
+        block_sums(red, sh);
+        const float r = rsqrtf(red[0] / float(p.group) + p.eps);
+        const float m = red[1] * r / float(p.group) * r;  // mean(gw h) r: dt = r gw - t r m
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int64_t i = (int64_t(k) * blockDim.x + threadIdx.x) * V;
+            if (i < p.group) {
+                float g[V], gt[V], dz[V], xs[V], dv[V];
+                load_f32<V>(g, dy + i);
+                if (z) load_f32<V>(gt, z + i);
+                float vin[V];
+                if (z && !p.gate_after) load_residual<T, V>(vin, q.v, row * q.v_row + g0 + i, q.v_f32);
+                if (q.x_in) load_f32<V>(xs, static_cast<const T *>(q.x_in) + row * q.xin_row + g0 + i);
+                float dr[V];
+                if (q.grad_sum) load_residual<T, V>(dr, q.grad_sum, row * q.gsum_row + g0 + i, q.v_f32);
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    const float w = load_param<T>(p.weight, g0 + i + j, p.weight_f32);
+                    const float h = t[k][j] * r;
+                    float d = r * fmaf(-t[k][j], m, gw[k][j]);
+                    if (z && p.gate_after) {
+                        dz[j] = g[j] * h * w * silu_slope(gt[j]);
+                        dw[k][j] = fmaf(g[j] * silu(gt[j]), h, dw[k][j]);
+                    } else {
+                        dw[k][j] = fmaf(g[j], h, dw[k][j]);
+                    }
+                    if (z && !p.gate_after) {
+                        dz[j] = d * vin[j] * silu_slope(gt[j]);
+                        d *= silu(gt[j]);
+                    }
+                    if (q.grad_sum) d += dr[j];
+                    dv[j] = d;
+                    if (q.x_in) ds[k][j] = fmaf(d, xs[j], ds[k][j]);
+                }
+                if (z) store_f32<V>(static_cast<T *>(q.grad_gate) + row * q.ggate_row + g0 + i, dz);
+                if (q.grad_residual)
+                    store_residual<T, V>(q.grad_residual, row * q.gres_row + g0 + i, dv, q.v_f32);
+                if (q.grad_x) {
+#pragma unroll
+                    for (int j = 0; j < V; ++j)
+                        if (p.scale) dv[j] *= load_param<T>(p.scale, g0 + i + j, p.weight_f32);
+                    store_f32<V>(static_cast<T *>(q.grad_x) + row * q.gx_row + g0 + i, dv);
+                }
+            }
+        }
+    }
+    float *part = q.partial + int64_t(blockIdx.x) * (q.x_in ? 2 : 1) * p.channels + g0;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int64_t i = (int64_t(k) * blockDim.x + threadIdx.x) * V;
+        if (i < p.group) {
+            store_f32<V>(part + i, dw[k]);
+            if (q.x_in) store_f32<V>(part + p.channels + i, ds[k]);
+        }
+    }
+}
+
+// Threads for a group of `n` elements at V per access and K accesses a thread.
+uint32_t threads_for(int64_t n, int v, int k) {
+    const int64_t need = (n + int64_t(v) * k - 1) / (int64_t(v) * k);
+    return uint32_t((need + 31) / 32 * 32);
+}
+
+template <class T, int V>
+cudaError_t norm_v(const NormParams &p, cudaStream_t s) {
+    const dim3 grid(uint32_t(p.rows * p.groups));
+    if (threads_for(p.group, V, 2) <= 512)
+        return launch_pdl(norm_kernel<T, V, 2>, grid, dim3(threads_for(p.group, V, 2)), 0, s, p);
+    if (threads_for(p.group, V, 4) <= 1024)
+        return launch_pdl(norm_kernel<T, V, 4>, grid, dim3(threads_for(p.group, V, 4)), 0, s, p);
+    return launch_pdl(norm_kernel<T, V, 16>, grid, dim3(threads_for(p.group, V, 16)), 0, s, p);
+}
+
+template <class T, int V>
+cudaError_t norm_backward_v(const NormBackwardParams &q, cudaStream_t s) {
+    const NormParams &p = q.n;
+    const dim3 grid(uint32_t(q.blocks), uint32_t(p.groups));
+    const uint32_t most = V * 2 >= 16 ? 512 : 1024;
+    if (threads_for(p.group, V, 2) <= most)
+        return launch_pdl(norm_backward_kernel<T, V, 2>, grid, dim3(threads_for(p.group, V, 2)), 0, s, q);
+    return launch_pdl(norm_backward_kernel<T, V, 4 * (8 / V)>, grid, dim3(threads_for(p.group, V, 4 * (8 / V))), 0, s,
+                      q);
+}
+
+constexpr int kColThreads = 256;
+
+// out[c] = sum over blocks of part[b][c], c < cols: 32 columns by 8 strands
+// of blocks per thread block, the strands joined in order.
+__global__ void __launch_bounds__(kColThreads)
+    column_sums_kernel(const float *part, int64_t blocks, int64_t cols, ColumnOut o) {
+    __shared__ float sh[8][33];
+    pdl_trigger();
+    pdl_wait();
+    const int lane = threadIdx.x % 32, strand = threadIdx.x / 32;
+    const int64_t c = int64_t(blockIdx.x) * 32 + lane;
+    float s = 0.0f;
+    if (c < cols)
+        for (int64_t b = strand; b < blocks; b += 8) s += part[b * cols + c];
+    sh[strand][lane] = s;
+    __syncthreads();
+    if (strand == 0 && c < cols) {
+        s = sh[0][lane];
+#pragma unroll
+        for (int k = 1; k < 8; ++k) s += sh[k][lane];
+        if (c < o.end[0]) {  // column c is entry c % inner of plane c / inner
+            const int64_t inner = o.end[0] / o.planes;
+            if (o.out[0]) o.out[0][c % inner * o.planes + c / inner] = s;
+        } else if (c < o.end[1]) {
+            if (o.out[1]) o.out[1][c - o.end[0]] = s;
+        } else if (c < o.end[2]) {
+            if (o.out[2]) o.out[2][c - o.end[1]] = s;
+        }
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_column_sums(const float *part, int64_t blocks, int64_t cols, const ColumnOut &o, cudaStream_t s) {
+    return launch_pdl(column_sums_kernel, dim3(uint32_t((cols + 31) / 32)), dim3(kColThreads), 0, s, part, blocks,
+                      cols, o);
+}
+
+cudaError_t launch_norm(dwp_dtype t, const NormParams &p, bool vec, cudaStream_t s) {
+    if (t == DWP_F32) return vec ? norm_v<float, 4>(p, s) : norm_v<float, 1>(p, s);
+    if (t == DWP_BF16) return vec ? norm_v<__nv_bfloat16, 8>(p, s) : norm_v<__nv_bfloat16, 1>(p, s);
+    return vec ? norm_v<__half, 8>(p, s) : norm_v<__half, 1>(p, s);
+}
+
+cudaError_t launch_norm_backward(dwp_dtype t, const NormBackwardParams &p, bool vec, cudaStream_t s) {
+    if (t == DWP_F32) return vec ? norm_backward_v<float, 4>(p, s) : norm_backward_v<float, 1>(p, s);
+    if (t == DWP_BF16) return vec ? norm_backward_v<__nv_bfloat16, 8>(p, s) : norm_backward_v<__nv_bfloat16, 1>(p, s);
+    return vec ? norm_backward_v<__half, 8>(p, s) : norm_backward_v<__half, 1>(p, s);
+}
+
+}  // namespace dwp

@@ -1,0 +1,105 @@
+// Building blocks of the sequence operators (causal convolution, selective
+// scan, block norm): element types, loads and stores of a few neighbouring
+// channels, the smooth functions, and the walk over packed segments.
+//
+// Rows are tokens and the channels of a row are contiguous, so a thread takes
+// V neighbouring channels: V elements fill 16 bytes (or 8) where every row
+// of the tensor starts on such a boundary, and V = 1 serves every other
+// stride, base or odd channel count.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "device.cuh"
+#include "launch.h"
+
+namespace dwp {
+
+template <class T>
+__device__ __forceinline__ float to_f32(T v);
+template <>
+__device__ __forceinline__ float to_f32<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <>
+__device__ __forceinline__ float to_f32<__half>(__half v) { return __half2float(v); }
+
+template <class T>
+__device__ __forceinline__ T from_f32(float v);
+template <>
+__device__ __forceinline__ float from_f32<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+template <>
+__device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
+
+// V elements moved as one access; V * sizeof(T) is 2, 4, 8, 16 or 32 bytes.
+template <class T, int V>
+struct alignas((V * sizeof(T)) < 16 ? V * sizeof(T) : 16) Pack {
+    T e[V];
+};
+
+template <int V, class T>
+__device__ __forceinline__ void load_f32(float (&f)[V], const T *p) {
+    const Pack<T, V> r = *reinterpret_cast<const Pack<T, V> *>(p);
+#pragma unroll
+    for (int i = 0; i < V; ++i) f[i] = to_f32<T>(r.e[i]);
+}
+
+template <int V, class T>
+__device__ __forceinline__ void store_f32(T *p, const float (&f)[V]) {
+    Pack<T, V> r;
+#pragma unroll
+    for (int i = 0; i < V; ++i) r.e[i] = from_f32<T>(f[i]);
+    *reinterpret_cast<Pack<T, V> *>(p) = r;
+}
+
+// A parameter held in f32 or in the activations' type.
+template <class T>
+__device__ __forceinline__ float load_param(const void *p, uint64_t i, bool is_f32) {
+    return is_f32 ? static_cast<const float *>(p)[i] : to_f32<T>(static_cast<const T *>(p)[i]);
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// Logistic function 1 / (1 + e^-x); for large -x the exponential is +inf and
+// the quotient 0, the limit.
+__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.0f, 1.0f + __expf(-x)); }
+// x * sigmoid(x); below -88 the product is under the smallest normal f32, and
+// an infinite x would give inf * 0.
+__device__ __forceinline__ float silu(float x) { return x < -88.0f ? 0.0f : x * sigmoid(x); }
+// d/dx of x * sigmoid(x), with its limits 0 and 1.
+__device__ __forceinline__ float silu_slope(float x) {
+    if (x < -88.0f) return 0.0f;
+    if (x > 88.0f) return 1.0f;
+    const float s = sigmoid(x);
+    return s * (1.0f + x * (1.0f - s));
+}
+// log(1 + e^x); above 20 it equals x to f32 rounding.
+__device__ __forceinline__ float softplus(float x) { return x > 20.0f ? x : log1pf(expf(x)); }
+
+// Segment of packed row `t` by CSR offsets (num_segments + 1 entries): the
+// first s with offsets[s + 1] > t, or num_segments if there is none.  Empty
+// segments are passed over.  Any offsets give s <= num_segments.
+__device__ __forceinline__ uint32_t segment_of(const uint32_t *offsets, uint32_t num_segments,
+                                               uint32_t t) {
+    uint32_t lo = 0, hi = num_segments;
+    while (lo < hi) {
+        const uint32_t mid = lo + (hi - lo) / 2u;
+        if (offsets[mid + 1] > t) hi = mid;
+        else lo = mid + 1u;
+    }
+    return lo;
+}
+
+}  // namespace dwp

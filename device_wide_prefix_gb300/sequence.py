@@ -1,0 +1,436 @@
+"""Sequence operators of libdwp.so: the causal convolution, the selective
+state space scan and the block norm (include/dwp.h, "Sequence operators").
+
+Rows are tokens.  A tensor of rows is (batch, rows, channels), or (rows,
+channels) for one packed stream: cut by CSR `offsets` into segments, or one
+sequence without them.  Channels are contiguous; batch and row strides are
+free, so views of a wider projection need no copy.
+
+These helpers marshal arguments and allocate outputs and scratch, as the
+others of the package do; allocations belong to the stream the call runs on.
+Parameters (weight, bias, A, D, ...) and their gradients are described at
+each function; gradients of parameters are float32.
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+import struct
+
+import torch
+
+import device_wide_prefix_gb300 as _dwp
+
+DWP_F32, DWP_BF16, DWP_F16 = 0, 1, 2
+CHECKPOINT_ROWS = 32  # DWP_SCAN_CHECKPOINT_ROWS
+NORM_MAX_GROUP = 16384  # DWP_NORM_MAX_GROUP
+
+_DTYPES = {torch.float32: DWP_F32, torch.bfloat16: DWP_BF16, torch.float16: DWP_F16}
+_NO_ROWS = (0, 0, 0)
+
+# Every field of the argument structures is 8 bytes wide.
+_CONV = "8q 3q 3q 5q"
+_CONV_BACKWARD = _CONV + " 3q 3q 4q"
+_CONV_STEP = "7q 3q 3q 5q"
+_SCAN = "8q 18q 2q 3q 4q"
+_SCAN_BACKWARD = _SCAN + " 3q 10q"
+_SCAN_STEP = "7q 18q 2q 3q 3q"
+_NORM = "7q d 15q 2q"
+_NORM_BACKWARD = _NORM + " 15q 2q"
+_PACK = {name: struct.Struct("=" + fmt.replace(" ", "")).pack for name, fmt in (
+    ("dwp_causal_conv", _CONV), ("dwp_causal_conv_backward", _CONV_BACKWARD),
+    ("dwp_causal_conv_step", _CONV_STEP), ("dwp_selective_scan", _SCAN),
+    ("dwp_selective_scan_backward", _SCAN_BACKWARD), ("dwp_selective_scan_step", _SCAN_STEP),
+    ("dwp_block_norm", _NORM), ("dwp_block_norm_backward", _NORM_BACKWARD))}
+_WITH_SCRATCH = ("dwp_causal_conv_backward", "dwp_selective_scan", "dwp_selective_scan_backward",
+                 "dwp_block_norm_backward")
+
+
+def scratch_bytes(name: str, packed: bytes) -> int:
+    """Scratch a call needs, for its packed argument structure."""
+    need = ctypes.c_size_t(0)
+    _dwp._check(getattr(_dwp.load(), name)(packed, None, ctypes.byref(need), None), name)
+    return need.value
+
+
+def _launch(name, fields, device, stream, scratch=None):
+    packed = _PACK[name](*fields)
+    entry = getattr(_dwp.load(), name)
+    handle = (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+    with _on(device):
+        if name in _WITH_SCRATCH:
+            size = ctypes.c_size_t(0)
+            if scratch is None:
+                st = entry(packed, None, ctypes.byref(size), None)
+                _dwp._check(st, name)
+                with _allocating(stream):
+                    scratch = torch.empty(max(size.value, 16), dtype=torch.uint8, device=device)
+            size.value = scratch.numel()
+            st = entry(packed, scratch.data_ptr(), ctypes.byref(size), handle)
+        else:
+            st = entry(packed, handle)
+    _dwp._check(st, name)
+
+
+_NOTHING = contextlib.nullcontext()
+
+
+def _on(device):
+    return _NOTHING if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+
+
+def _allocating(stream):
+    """Memory made here belongs to the stream the call runs on."""
+    return _NOTHING if stream is None else torch.cuda.stream(stream)
+
+
+def _need(ok, what: str) -> None:
+    if not ok:
+        raise ValueError(what)
+
+
+def _main(x, what, ndims=(2, 3)):
+    """The tensor that sets a call's type, device and row shape."""
+    _need(x.is_cuda and x.dtype in _DTYPES and x.dim() in ndims,
+          "%s must be a CUDA tensor of float32, bfloat16 or float16 rows" % what)
+    return _rows(x, what)
+
+
+def _rows(t, what):
+    """(address, batch stride, row stride) of a tensor of rows."""
+    s = t.stride()
+    _need(s[-1] == 1 or t.shape[-1] <= 1 or t.numel() == 0, "%s must have contiguous channels" % what)
+    return (t.data_ptr(), s[0], s[1]) if len(s) == 3 else (t.data_ptr(), 0, s[0])
+
+
+def _like(t, x, what):
+    """Rows of a tensor of the shape, type and device of x; zeros for None."""
+    if t is None:
+        return _NO_ROWS
+    _need(t.shape == x.shape and t.dtype == x.dtype and t.device == x.device,
+          "%s must have the shape, type and device of the call's main input" % what)
+    return _rows(t, what)
+
+
+def _dense(t, shape, dtype, device, what):
+    """Address of a contiguous tensor; 0 for None."""
+    if t is None:
+        return 0
+    _need(t.dtype == dtype and t.device == device and t.is_contiguous() and tuple(t.shape) == tuple(shape),
+          "%s must be a contiguous %s tensor of shape %s on %s" % (what, dtype, tuple(shape), device))
+    return t.data_ptr()
+
+
+def _sequences(x, offsets):
+    """(batch, rows, offsets' address, segments, sequences)."""
+    if offsets is not None:
+        _need(x.dim() == 2 and offsets.is_cuda and offsets.device == x.device and offsets.is_contiguous()
+              and offsets.dim() == 1 and offsets.numel() >= 1 and offsets.element_size() == 4
+              and not offsets.is_floating_point(),
+              "offsets must be a contiguous CUDA tensor of 4-byte integers, for packed (rows, channels) inputs")
+        n = offsets.numel() - 1
+        return 1, x.shape[0], offsets.data_ptr(), n, n
+    return (1, x.shape[0], 0, 0, 1) if x.dim() == 2 else (x.shape[0], x.shape[1], 0, 0, x.shape[0])
+
+
+def _weight(weight, x, shape, what):
+    _need(weight.dtype == x.dtype or weight.dtype == torch.float32,
+          "%s must be float32 or of x's type" % what)
+    return _dense(weight, shape, weight.dtype, x.device, what)
+
+
+def _output(out, x, stream, what="out"):
+    if out is None:
+        with _allocating(stream):
+            return torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    _like(out, x, what)
+    return out
+
+
+def _empty(shape, dtype, device, stream):
+    with _allocating(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+# ---------------------------------------------------------------------------
+# causal convolution
+
+
+def _conv_fields(x, xr, out, weight, bias, offsets, initial_state, final_state, silu):
+    _need(weight.dim() == 2 and weight.shape[0] == x.shape[-1], "weight must have shape (channels, width)")
+    width, ch = weight.shape[1], x.shape[-1]
+    batch, rows, off, nseg, seqs = _sequences(x, offsets)
+    state = (seqs, width - 1, ch)
+    return [_DTYPES[x.dtype], _DTYPES.get(weight.dtype, -1), 1 if silu else 0, width, ch, batch, rows, nseg, *xr, *out,
+            _weight(weight, x, (ch, width), "weight"), _dense(bias, (ch,), weight.dtype, x.device, "bias"), off,
+            _dense(initial_state, state, x.dtype, x.device, "initial_state"),
+            _dense(final_state, state, x.dtype, x.device, "final_state")], state
+
+
+def causal_conv(x, weight, bias=None, offsets=None, initial_state=None, silu=True, return_state=False, out=None,
+                final_state=None, stream=None):
+    """Causal depthwise convolution of rows `x` with `weight` (channels, width),
+    through x * sigmoid(x) if `silu`.  `initial_state` (sequences, width - 1,
+    channels) holds the inputs before each sequence's first row (None: zeros).
+    Returns out, or (out, final_state) with `return_state` or a `final_state`
+    to write."""
+    xr = _main(x, "x")
+    out = _output(out, x, stream)
+    if return_state and final_state is None:
+        _need(weight.dim() == 2, "weight must have shape (channels, width)")
+        final_state = _empty((_sequences(x, offsets)[4], weight.shape[1] - 1, x.shape[-1]), x.dtype, x.device, stream)
+    fields, _ = _conv_fields(x, xr, _rows(out, "out"), weight, bias, offsets, initial_state, final_state, silu)
+    _launch("dwp_causal_conv", fields, x.device, stream)
+    return out if final_state is None else (out, final_state)
+
+
+def causal_conv_backward(grad_out, x, weight, bias=None, offsets=None, initial_state=None, silu=True,
+                         grad_final_state=None, scratch=None, stream=None):
+    """Gradients of causal_conv: a dict of "x", "weight" and, where given,
+    "bias" and "initial_state" (the last also with a `grad_final_state`)."""
+    xr = _main(x, "x")
+    gr = _like(grad_out, x, "grad_out")
+    fields, state = _conv_fields(x, xr, _NO_ROWS, weight, bias, offsets, initial_state, None, silu)
+    f32, dev = torch.float32, x.device
+    grads = {"x": _output(None, x, stream), "weight": _empty(weight.shape, f32, dev, stream)}
+    if bias is not None:
+        grads["bias"] = _empty(bias.shape, f32, dev, stream)
+    if initial_state is not None or grad_final_state is not None:
+        grads["initial_state"] = _empty(state, x.dtype, dev, stream)
+    at = lambda k: grads[k].data_ptr() if k in grads else 0  # noqa: E731
+    fields += [*gr, *_rows(grads["x"], "grad_x"), _dense(grad_final_state, state, x.dtype, dev, "grad_final_state"),
+               at("weight"), at("bias"), at("initial_state")]
+    _launch("dwp_causal_conv_backward", fields, dev, stream, scratch)
+    return grads
+
+
+def _slots(slots, batch, device):
+    if slots is None:
+        return 0
+    _need(slots.dtype == torch.int32, "slots must be int32")
+    return _dense(slots, (batch,), torch.int32, device, "slots")
+
+
+def causal_conv_step(x, state, weight, bias=None, slots=None, silu=True, out=None, stream=None):
+    """causal_conv of one new row of each of `batch` sequences: x (batch,
+    channels), `state` (num_slots, width - 1, channels) updated in place.
+    `slots` (int32, batch) names each row's state; a slot outside the cache
+    marks a padding row (output 0).  None: row i has state i.  Returns out."""
+    xr = _main(x, "x", (2,))
+    out = _output(out, x, stream)
+    batch, ch = x.shape
+    _need(weight.dim() == 2 and weight.shape[0] == ch, "weight must have shape (channels, width)")
+    width = weight.shape[1]
+    _need(state.dim() == 3 and state.shape[1:] == (width - 1, ch) and state.dtype == x.dtype
+          and state.device == x.device and (state.numel() == 0 or state[0].is_contiguous()),
+          "state must have shape (slots, width - 1, channels), each slot contiguous, and x's type and device")
+    fields = [_DTYPES[x.dtype], _DTYPES.get(weight.dtype, -1), 1 if silu else 0, width, ch, batch, state.shape[0],
+              *xr, *_rows(out, "out"), _weight(weight, x, (ch, width), "weight"),
+              _dense(bias, (ch,), weight.dtype, x.device, "bias"), state.data_ptr(), state.stride(0),
+              _slots(slots, batch, x.device)]
+    _launch("dwp_causal_conv_step", fields, x.device, stream)
+    return out
+
+
+# ---------------------------------------------------------------------------
+# selective scan
+
+
+def _bc(t, u, what):
+    """(rows triple, group stride, groups, states) of B or C: (..., groups, states) or (..., states)."""
+    lead = u.dim() - 1
+    _need(t.dtype == u.dtype and t.device == u.device and t.dim() in (lead + 1, lead + 2)
+          and t.shape[:lead] == u.shape[:lead],
+          "%s must have u's rows, type and device, and shape (..., groups, states)" % what)
+    s = t.stride()
+    _need(s[-1] == 1 or t.shape[-1] <= 1 or t.numel() == 0, "%s must have contiguous states" % what)
+    batch, row = (s[0], s[1]) if lead == 2 else (0, s[0])
+    grouped = t.dim() == lead + 2
+    return ((t.data_ptr(), batch, row), s[-2] if grouped else 0, t.shape[-2] if grouped else 1, t.shape[-1])
+
+
+def _scan_parts(u, dt, A, B, C, D, z, dt_bias, out):
+    """The fields that the prompt and the token form share."""
+    ch, dev, f32 = u.shape[-1], u.device, torch.float32
+    br, bg, groups, n = _bc(B, u, "B")
+    cr, cg, cgroups, cn = _bc(C, u, "C")
+    _need((groups, n) == (cgroups, cn), "B and C must have the same groups and states")
+    rows = [*_main(u, "u"), *_like(dt, u, "dt"), *_like(z, u, "z"), *br, *cr, *out, bg, cg,
+            _dense(A, (ch, n), f32, dev, "A"), _dense(D, (ch,), f32, dev, "D"),
+            _dense(dt_bias, (ch,), f32, dev, "dt_bias")]
+    return rows, groups, n
+
+
+def _scan_fields(u, dt, A, B, C, D, z, dt_bias, out, offsets, initial, final, checkpoints, dt_softplus):
+    parts, groups, n = _scan_parts(u, dt, A, B, C, D, z, dt_bias, out)
+    batch, rows, off, nseg, seqs = _sequences(u, offsets)
+    ch, dev, f32 = u.shape[-1], u.device, torch.float32
+    state = (seqs, ch, n)
+    points = (batch, -(-rows // CHECKPOINT_ROWS), ch, n)
+    return [_DTYPES[u.dtype], 1 if dt_softplus else 0, ch, n, groups, batch, rows, nseg, *parts, off,
+            _dense(initial, state, f32, dev, "initial_state"), _dense(final, state, f32, dev, "final_state"),
+            _dense(checkpoints, points, f32, dev, "checkpoints")], state
+
+
+def selective_scan(u, dt, A, B, C, D=None, z=None, dt_bias=None, offsets=None, initial_state=None, dt_softplus=True,
+                   return_state=False, return_checkpoints=False, out=None, final_state=None, checkpoints=None,
+                   scratch=None, stream=None):
+    """Selective state space scan.  u, dt, z: rows of channels; B, C: rows of
+    (groups, states), or of states; A (channels, states), D, dt_bias
+    (channels): float32.  `initial_state` (sequences, channels, states) is
+    float32 (None: zeros).  Returns out, or a tuple of out and then, where
+    asked for, the final state and the checkpoints that the gradient needs."""
+    _main(u, "u")
+    out = _output(out, u, stream)
+    batch, rows, _, _, seqs = _sequences(u, offsets)
+    ch, n = u.shape[-1], A.shape[-1]
+    if return_state and final_state is None:
+        final_state = _empty((seqs, ch, n), torch.float32, u.device, stream)
+    if return_checkpoints and checkpoints is None:
+        checkpoints = _empty((batch, -(-rows // CHECKPOINT_ROWS), ch, n), torch.float32, u.device, stream)
+    fields, _ = _scan_fields(u, dt, A, B, C, D, z, dt_bias, _rows(out, "out"), offsets, initial_state, final_state,
+                             checkpoints, dt_softplus)
+    _launch("dwp_selective_scan", fields, u.device, stream, scratch)
+    if final_state is None and checkpoints is None:
+        return out
+    return (out, *(t for t in (final_state, checkpoints) if t is not None))
+
+
+def selective_scan_backward(grad_out, u, dt, A, B, C, checkpoints, D=None, z=None, dt_bias=None, offsets=None,
+                            initial_state=None, dt_softplus=True, grad_final_state=None, scratch=None, stream=None):
+    """Gradients of selective_scan: a dict of "u", "dt", "A", "B", "C" and,
+    where given, "D", "z", "dt_bias" and "initial_state" (the last also with a
+    `grad_final_state`).  `checkpoints` are the forward's."""
+    _main(u, "u")
+    gr = _like(grad_out, u, "grad_out")
+    _need(checkpoints is not None, "the gradient needs the forward's checkpoints")
+    fields, state = _scan_fields(u, dt, A, B, C, D, z, dt_bias, _NO_ROWS, offsets, initial_state, None, checkpoints,
+                                 dt_softplus)
+    f32, dev = torch.float32, u.device
+    grads = {"u": _output(None, u, stream), "dt": _output(None, u, stream), "A": _empty(A.shape, f32, dev, stream),
+             "B": _empty(B.shape, u.dtype, dev, stream), "C": _empty(C.shape, u.dtype, dev, stream)}
+    if D is not None:
+        grads["D"] = _empty(D.shape, f32, dev, stream)
+    if z is not None:
+        grads["z"] = _output(None, u, stream)
+    if dt_bias is not None:
+        grads["dt_bias"] = _empty(dt_bias.shape, f32, dev, stream)
+    if initial_state is not None or grad_final_state is not None:
+        grads["initial_state"] = _empty(state, f32, dev, stream)
+    at = lambda k: grads[k].data_ptr() if k in grads else 0  # noqa: E731
+    fields += [*gr, _dense(grad_final_state, state, f32, dev, "grad_final_state"), at("u"), at("dt"), at("z"), at("B"),
+               at("C"), at("A"), at("D"), at("dt_bias"), at("initial_state")]
+    _launch("dwp_selective_scan_backward", fields, dev, stream, scratch)
+    return grads
+
+
+def selective_scan_step(u, dt, A, B, C, state, D=None, z=None, dt_bias=None, slots=None, dt_softplus=True, out=None,
+                        stream=None):
+    """selective_scan of one new row of each of `batch` sequences: u, dt, z
+    (batch, channels), B, C (batch, groups, states) or (batch, states),
+    `state` float32 (num_slots, channels, states) updated in place; `slots` as
+    for causal_conv_step.  Returns out."""
+    _main(u, "u", (2,))
+    out = _output(out, u, stream)
+    parts, groups, n = _scan_parts(u, dt, A, B, C, D, z, dt_bias, _rows(out, "out"))
+    batch, ch = u.shape
+    _need(state.dim() == 3 and state.shape[1:] == (ch, n) and state.dtype == torch.float32
+          and state.device == u.device and (state.numel() == 0 or state[0].is_contiguous()),
+          "state must be float32 of shape (slots, channels, states), each slot contiguous, on u's device")
+    fields = [_DTYPES[u.dtype], 1 if dt_softplus else 0, ch, n, groups, batch, state.shape[0], *parts,
+              state.data_ptr(), state.stride(0), _slots(slots, batch, u.device)]
+    _launch("dwp_selective_scan_step", fields, u.device, stream)
+    return out
+
+
+# ---------------------------------------------------------------------------
+# block norm
+
+
+def _norm_fields(x, xr, residual, gate, total, out, weight, scale, gate_after, groups, eps, rdtype):
+    ch = x.shape[-1]
+    return [_DTYPES[x.dtype], _DTYPES.get(weight.dtype, -1), rdtype, 1 if gate_after else 0, ch, groups, x.shape[0],
+            float(eps), *xr, *residual, *gate, *total, *out, _weight(weight, x, (ch,), "weight"),
+            _dense(scale, (ch,), weight.dtype, x.device, "scale")]
+
+
+def _residual(t, x, what):
+    _need(t.shape == x.shape and t.device == x.device and t.dtype in (x.dtype, torch.float32),
+          "%s must have x's shape and device, and be float32 or of x's type" % what)
+    return _rows(t, what)
+
+
+def _flat_rows(t):
+    """A (batch, rows, channels) tensor as (batch * rows, channels)."""
+    return t if t is None or t.dim() == 2 else t.view(-1, t.shape[-1])
+
+
+def block_norm(x, weight, residual=None, scale=None, gate=None, gate_after=False, groups=1, eps=1e-5, out=None,
+               sum_out=None, stream=None):
+    """Root-mean-square norm over each of `groups` parts of a row, times
+    `weight`: of x; of residual + scale * x with a `residual` (scale (channels)
+    or None for 1), which is also returned; of x * silu(gate) with a `gate`, or
+    times silu(gate) afterwards if `gate_after`.  `out` may be x and `sum_out`
+    may be residual, in place.  Returns (out, sum), sum None without a residual."""
+    shape = x.shape
+    _need(x.dim() in (2, 3), "x must be (rows, channels) or (batch, rows, channels)")
+    x2 = _flat_rows(x)
+    xr = _main(x2, "x", (2,))
+    out = _output(out, x, stream)
+    rr, total, rdtype = _NO_ROWS, None, _DTYPES[x.dtype]
+    if residual is not None:
+        _need(residual.shape == shape, "residual must have x's shape")
+        residual = _flat_rows(residual)
+        rr, rdtype = _residual(residual, x2, "residual"), _DTYPES[residual.dtype]
+        total = _empty(shape, residual.dtype, x.device, stream) if sum_out is None else sum_out
+        _need(total.shape == shape and total.dtype == residual.dtype, "sum_out must have residual's shape and type")
+    fields = _norm_fields(x2, xr, rr, _like(_flat_rows(gate), x2, "gate"),
+                          _NO_ROWS if total is None else _residual(_flat_rows(total), x2, "sum_out"),
+                          _rows(_flat_rows(out), "out"), weight, scale, gate_after, groups, eps, rdtype)
+    _launch("dwp_block_norm", fields, x.device, stream)
+    return out, total
+
+
+def block_norm_backward(grad_out, v, weight, x=None, scale=None, gate=None, gate_after=False, grad_residual=None,
+                        groups=1, eps=1e-5, residual=None, scratch=None, stream=None):
+    """Gradients of block_norm.  `v` is what was normed: the returned sum where
+    there was a residual, else x.  `residual` says whether there was one (None:
+    there was if `scale`, `grad_residual` or v's type says so); `x` is needed
+    with a `scale`; `grad_residual` is the returned sum's gradient.  A dict of
+    "x", "weight" and, where they apply, "residual", "scale" and "gate"; "x"
+    and "residual" are one tensor where they are equal."""
+    shape = v.shape
+    _need(grad_out.shape == shape and v.dim() in (2, 3), "grad_out must have v's shape")
+    if residual is None:
+        residual = scale is not None or grad_residual is not None or v.dtype != grad_out.dtype
+    _need(scale is None or (x is not None and residual), "the scale's gradient needs x, and a residual")
+    flat = [_flat_rows(t) for t in (grad_out, v, x, gate, grad_residual)]
+    g2, v2, x2, z2, s2 = flat
+    gr = _main(g2, "grad_out", (2,))
+    dev, f32 = g2.device, torch.float32
+    vr = _residual(v2, g2, "v")
+    _need(residual or v2.dtype == g2.dtype, "v must have grad_out's type without a residual")
+    if s2 is not None:
+        _need(residual and s2.dtype == v2.dtype, "grad_residual must have v's type, with a residual")
+    grads = {"weight": _empty(weight.shape, f32, dev, stream), "x": _output(None, grad_out, stream)}
+    gx = _flat_rows(grads["x"])
+    gres = _NO_ROWS
+    if residual:
+        if scale is None and v.dtype == grad_out.dtype:
+            grads["residual"] = grads["x"]  # the same numbers
+        else:
+            grads["residual"] = _empty(shape, v.dtype, dev, stream)
+            gres = _rows(_flat_rows(grads["residual"]), "grad_residual")
+    if scale is not None:
+        grads["scale"] = _empty(scale.shape, f32, dev, stream)
+    gz = _NO_ROWS
+    if gate is not None:
+        grads["gate"] = _output(None, grad_out, stream)
+        gz = _rows(_flat_rows(grads["gate"]), "grad_gate")
+    xr = (_NO_ROWS if scale is None else _like(x2, g2, "x")) if residual else vr
+    fields = _norm_fields(g2, xr, _NO_ROWS, _like(z2, g2, "gate"), vr if residual else _NO_ROWS, _NO_ROWS, weight,
+                          scale, gate_after, groups, eps, _DTYPES[v2.dtype])
+    fields += [*gr, *(_NO_ROWS if s2 is None else _residual(s2, g2, "grad_residual")), *_rows(gx, "grad_x"), *gres,
+               *gz, grads["weight"].data_ptr(), grads["scale"].data_ptr() if scale is not None else 0]
+    _launch("dwp_block_norm_backward", fields, dev, stream, scratch)
+    return grads

@@ -286,6 +286,226 @@ dwp_status dwp_linear_recurrence_f32(const float *d_a, const float *d_b, float *
                                      dwp_stream stream);
 
 /*
+ * Sequence operators.
+ *
+ * The linear recurrence above in the form a state space layer uses it, with
+ * what stands around it there: the short causal convolution before it, the
+ * selective scan, and the norm around the block, each with its gradient, and
+ * the first two with a form for single tokens.
+ *
+ * Layout.  Rows are tokens; a row's channels are contiguous.  A tensor of
+ * rows is [batch, rows, channels], given by its address, batch stride and row
+ * stride, in elements: a column range of a wider tensor (half of a
+ * projection's output) needs no copy.  With `offsets` the batch is 1 and the
+ * rows are num_segments sequences packed one after another, by CSR offsets as
+ * for dwp_segmented_scan_u32: uint32[num_segments + 1], non-decreasing, empty
+ * segments allowed, trusted (other offsets give unspecified values but no
+ * access out of range); rows outside [offsets[0], offsets[num_segments]) are
+ * left unwritten in every output and add nothing to any sum.  Without it each
+ * batch entry is one sequence.  "Sequence s" below is segment s or batch
+ * entry s, and the number of sequences is num_segments or batch.
+ *
+ * Types.  Activations have one type per call (dwp_dtype).  Arithmetic, sums,
+ * norms and states of the scan are f32; an activation is rounded once, when
+ * it is written.
+ *
+ * Pointers need their element's alignment only.  Rows that start on 16-byte
+ * boundaries (address, strides and channel count) take wider accesses.
+ *
+ * Outputs overlap neither inputs nor one another nor the scratch
+ * (DWP_ERR_ALIASING), except where a call says so; column ranges of one wider
+ * tensor that share no element do not overlap.  Sizes: batch * rows < 2^31,
+ * at most 2^20 channels.  DWP_ERR_INVALID_VALUE for a NULL required pointer,
+ * a size or type out of range, or a stride below the row it spans.
+ *
+ * No wait on the device: these calls keep no status word.  Results are
+ * deterministic, bit for bit from run to run.  Scratch follows the two-call
+ * pattern above, 16-byte aligned; its contents on entry do not matter.
+ */
+typedef enum dwp_dtype { DWP_F32 = 0, DWP_BF16 = 1, DWP_F16 = 2 } dwp_dtype;
+
+/* Rows of a tensor: element strides between batch entries and rows. */
+typedef struct dwp_rows {
+    void *data;
+    int64_t batch_stride;
+    int64_t row_stride;
+} dwp_rows;
+
+/*
+ * Causal depthwise convolution, per channel:
+ *   p[t] = bias + sum_k weight[k] * x[t - (width-1) + k],  out = p, or p * sigmoid(p)
+ * where the rows before a sequence's first are its initial state's.
+ *   dtype          of x, out and the states; weight_dtype: dtype or DWP_F32,
+ *                  of weight and bias
+ *   width          1 .. 8
+ *   weight         [channels, width];   bias  [channels] or NULL
+ *   offsets        NULL, or see above
+ *   initial_state  [sequences, width - 1, channels], or NULL for zeros: the
+ *                  inputs before each sequence's first row, oldest first
+ *   final_state    NULL, or the same for the rows after its last (may not
+ *                  overlap initial_state)
+ */
+typedef struct dwp_conv_args {
+    int64_t dtype, weight_dtype, silu, width;
+    int64_t channels, batch, rows, num_segments;
+    dwp_rows x, out;
+    const void *weight, *bias;
+    const uint32_t *offsets;
+    const void *initial_state;
+    void *final_state;
+} dwp_conv_args;
+dwp_status dwp_causal_conv(const dwp_conv_args *args, dwp_stream stream);
+
+/*
+ * Gradient of dwp_causal_conv.
+ *   conv                the forward's arguments (out, final_state unused)
+ *   grad_out            of the output;  grad_final_state  NULL for zeros
+ *   grad_x              of x (dtype)
+ *   grad_weight         f32 [channels, width];  grad_bias  f32 [channels] or NULL
+ *   grad_initial_state  NULL, or as initial_state
+ */
+typedef struct dwp_conv_backward_args {
+    dwp_conv_args conv;
+    dwp_rows grad_out, grad_x;
+    const void *grad_final_state;
+    float *grad_weight, *grad_bias;
+    void *grad_initial_state;
+} dwp_conv_backward_args;
+dwp_status dwp_causal_conv_backward(const dwp_conv_backward_args *args, void *d_scratch,
+                                    size_t *scratch_bytes, dwp_stream stream);
+
+/*
+ * dwp_causal_conv for one new row of each of `batch` sequences, the states
+ * updated in place.
+ *   x, out   [batch, channels] (batch_stride unused)
+ *   state    [num_slots, width - 1, channels], slot_stride elements apart
+ *   slots    int32[batch]: the slot of each row; a row whose slot lies outside
+ *            [0, num_slots) is padding: its output is 0 and no state changes.
+ *            NULL: row i has slot i.  No two rows may name one slot.
+ */
+typedef struct dwp_conv_step_args {
+    int64_t dtype, weight_dtype, silu, width;
+    int64_t channels, batch, num_slots;
+    dwp_rows x, out;
+    const void *weight, *bias;
+    void *state;
+    int64_t slot_stride;
+    const int32_t *slots;
+} dwp_conv_step_args;
+dwp_status dwp_causal_conv_step(const dwp_conv_step_args *args, dwp_stream stream);
+
+/* Rows between the states that the selective scan keeps for its gradient. */
+#define DWP_SCAN_CHECKPOINT_ROWS 32
+
+/*
+ * Selective state space scan: per channel d (group g) and state n,
+ *   delta = dt + dt_bias, through log(1 + exp()) if softplus
+ *   h[t]  = exp(delta A[d,n]) h[t-1] + delta u B[t,g,n]
+ *   y[t]  = sum_n C[t,g,n] h[t] + D[d] u,   out = y, or y * silu(z)
+ *   u, dt, z, out  rows of `channels`; z.data may be NULL
+ *   B, C           rows of [groups, states], group_stride elements apart;
+ *                  groups divides channels, and channel d has group
+ *                  d / (channels / groups)
+ *   states         1 .. 128
+ *   A              f32 [channels, states];  D, dt_bias  f32 [channels] or NULL
+ *   initial_state  f32 [sequences, channels, states], or NULL for zeros
+ *   final_state    NULL, or the same after each sequence's last row
+ *   checkpoints    NULL, or f32 [batch, ceil(rows / DWP_SCAN_CHECKPOINT_ROWS),
+ *                  channels, states]: states kept for the gradient
+ */
+typedef struct dwp_selective_scan_args {
+    int64_t dtype, softplus;
+    int64_t channels, states, groups, batch, rows, num_segments;
+    dwp_rows u, dt, z, B, C, out;
+    int64_t b_group_stride, c_group_stride;
+    const float *A, *D, *dt_bias;
+    const uint32_t *offsets;
+    const float *initial_state;
+    float *final_state, *checkpoints;
+} dwp_selective_scan_args;
+dwp_status dwp_selective_scan(const dwp_selective_scan_args *args, void *d_scratch,
+                              size_t *scratch_bytes, dwp_stream stream);
+
+/*
+ * Gradient of dwp_selective_scan.
+ *   scan        the forward's arguments, checkpoints as the forward wrote them
+ *               (out, final_state unused)
+ *   grad_out    of the output;  grad_final_state  NULL for zeros
+ *   grad_u, grad_dt, grad_z  [batch, rows, channels], dense, dtype (grad_z
+ *               NULL without z);  grad_B, grad_C  [batch, rows, groups,
+ *               states], dense, dtype
+ *   grad_A f32 [channels, states];  grad_D, grad_dt_bias f32 [channels], or
+ *               NULL;  grad_initial_state  NULL, or as initial_state
+ */
+typedef struct dwp_selective_scan_backward_args {
+    dwp_selective_scan_args scan;
+    dwp_rows grad_out;
+    const float *grad_final_state;
+    void *grad_u, *grad_dt, *grad_z, *grad_B, *grad_C;
+    float *grad_A, *grad_D, *grad_dt_bias, *grad_initial_state;
+} dwp_selective_scan_backward_args;
+dwp_status dwp_selective_scan_backward(const dwp_selective_scan_backward_args *args,
+                                       void *d_scratch, size_t *scratch_bytes, dwp_stream stream);
+
+/*
+ * dwp_selective_scan for one new row of each of `batch` sequences, the states
+ * updated in place; slots as for dwp_causal_conv_step, `state` f32
+ * [num_slots, channels, states], slot_stride elements apart.
+ */
+typedef struct dwp_selective_scan_step_args {
+    int64_t dtype, softplus;
+    int64_t channels, states, groups, batch, num_slots;
+    dwp_rows u, dt, z, B, C, out;
+    int64_t b_group_stride, c_group_stride;
+    const float *A, *D, *dt_bias;
+    float *state;
+    int64_t slot_stride;
+    const int32_t *slots;
+} dwp_selective_scan_step_args;
+dwp_status dwp_selective_scan_step(const dwp_selective_scan_step_args *args, dwp_stream stream);
+
+/*
+ * Root-mean-square norm around a block, over each of `groups` equal parts of
+ * a row of `channels` (channels / groups at most DWP_NORM_MAX_GROUP):
+ *   v   = residual + scale * x, written to `sum`; or x without a residual
+ *   t   = v * silu(gate) (gate given, gate_after 0), else v
+ *   out = t / sqrt(mean(t^2) + eps) * weight, times silu(gate) if gate_after
+ *   x, gate, out    dtype; gate.data may be NULL.  out may be x exactly.
+ *   residual, sum   residual_dtype: dtype or DWP_F32; both or neither.  sum
+ *                   may be residual exactly.
+ *   weight, scale   [channels], weight_dtype: dtype or DWP_F32; scale NULL
+ *                   for 1, and only with a residual
+ * Tensors are [rows, channels] (batch_stride unused).
+ */
+#define DWP_NORM_MAX_GROUP 16384
+typedef struct dwp_norm_args {
+    int64_t dtype, weight_dtype, residual_dtype, gate_after;
+    int64_t channels, groups, rows;
+    double eps;
+    dwp_rows x, residual, gate, sum, out;
+    const void *weight, *scale;
+} dwp_norm_args;
+dwp_status dwp_block_norm(const dwp_norm_args *args, dwp_stream stream);
+
+/*
+ * Gradient of dwp_block_norm.
+ *   norm           the forward's arguments: x where scale is given, `sum` as
+ *                  the forward wrote it where residual was given (residual
+ *                  and out unused)
+ *   grad_out       of the output;  grad_sum  of `sum`, residual_dtype, or NULL
+ *   grad_x         dtype, or NULL;  grad_residual  residual_dtype, with a
+ *                  residual only, or NULL;  grad_gate  dtype, with a gate
+ *   grad_weight    f32 [channels];  grad_scale  f32 [channels], with a scale
+ */
+typedef struct dwp_norm_backward_args {
+    dwp_norm_args norm;
+    dwp_rows grad_out, grad_sum, grad_x, grad_residual, grad_gate;
+    float *grad_weight, *grad_scale;
+} dwp_norm_backward_args;
+dwp_status dwp_block_norm_backward(const dwp_norm_backward_args *args, void *d_scratch,
+                                   size_t *scratch_bytes, dwp_stream stream);
+
+/*
  * Device-side status of the most recent call that used d_scratch.
  * Synchronises `stream`, then reads the status word.  Returns DWP_SUCCESS,
  * DWP_ERR_LOOKBACK_TIMEOUT or DWP_ERR_PIPELINE_TIMEOUT (and, in a library
