@@ -163,6 +163,11 @@ struct ScanParams {
     const float *A, *D, *dt_bias, *initial;
     float *final, *checkpoints;
     const uint32_t *segmap;  // NULL, or a code word per packed row
+    bool wide;         // two neighbouring channels, and four neighbouring states of B and C, are one aligned access
+    bool states_wide;  // four neighbouring states of A and every state array are one aligned access
+    // [batch * (chunks - 1)]: last states, sums of delta per channel, whether a segment began
+    float *carry, *carry_sum;
+    uint32_t *carry_head;
 };
 struct ScanBackwardParams {
     ScanParams f;
@@ -188,9 +193,18 @@ struct ScanStepParams {
 };
 // Channels one block of the selective scan covers at this many states.
 int64_t scan_block_channels(int64_t states);
+// Warps of the forward that an SM holds (168 registers a lane).
+constexpr int kScanWarpsPerSM = 12;
+// Channels one warp of the forward covers.
+int64_t scan_warp_channels(int64_t states);
 cudaError_t launch_segment_map(const uint32_t *offsets, uint32_t nseg, uint32_t rows, uint32_t *map,
                                cudaStream_t s);
 cudaError_t launch_selscan(dwp_dtype t, const ScanParams &p, cudaStream_t s);
+cudaError_t launch_selscan_f32(const ScanParams &p, cudaStream_t s);
+cudaError_t launch_selscan_bf16(const ScanParams &p, cudaStream_t s);
+cudaError_t launch_selscan_f16(const ScanParams &p, cudaStream_t s);
+// States carried over the chunks of the forward.
+cudaError_t launch_carry(const ScanParams &p, cudaStream_t s);
 cudaError_t launch_selscan_backward(dwp_dtype t, const ScanBackwardParams &p, cudaStream_t s);
 cudaError_t launch_selscan_step(dwp_dtype t, const ScanStepParams &p, cudaStream_t s);
 

@@ -7,7 +7,7 @@
 //   du = delta q1 + D dy,      ddelta = u q1 + q2
 //   dA = sum_t dh a h[t-1] delta
 //
-// The states come again from those the forward kept before every kScanTile
+// The states come again from those the forward kept before every kCheckpointRows
 // rows: a tile is first walked forward to its kSub-row boundaries, then each
 // kSub rows are walked forward once more with the states kept in registers
 // and backward.
@@ -18,7 +18,7 @@ namespace dwp {
 namespace {
 
 constexpr int kSub = 8;
-constexpr int kSubs = kScanTile / kSub;
+constexpr int kSubs = kCheckpointRows / kSub;
 
 template <class T, int NL>
 __global__ void __launch_bounds__(kScanThreads) scan_backward_kernel(ScanBackwardParams q) {
@@ -28,13 +28,13 @@ __global__ void __launch_bounds__(kScanThreads) scan_backward_kernel(ScanBackwar
     const ScanParams &p = q.f;
     extern __shared__ float4 smem4[];
     float2 *sd = reinterpret_cast<float2 *>(smem4);               // (delta, delta u)
-    float *sg = reinterpret_cast<float *>(sd + kScanTile * kCh);  // dy
-    float *s1 = sg + kScanTile * kCh;                             // q1
-    float *s2 = s1 + kScanTile * kCh;                             // q2
-    float *sy = s2 + kScanTile * kCh;                             // y
-    float *sb = sy + kScanTile * kCh;
-    float *sc = sb + kScanTile * kNP;
-    float *sr = sc + kScanTile * kNP;                             // [warp][kSub][2 kNP]
+    float *sg = reinterpret_cast<float *>(sd + kCheckpointRows * kCh);  // dy
+    float *s1 = sg + kCheckpointRows * kCh;                             // q1
+    float *s2 = s1 + kCheckpointRows * kCh;                             // q2
+    float *sy = s2 + kCheckpointRows * kCh;                             // y
+    float *sb = sy + kCheckpointRows * kCh;
+    float *sc = sb + kCheckpointRows * kNP;
+    float *sr = sc + kCheckpointRows * kNP;                             // [warp][kSub][2 kNP]
     uint32_t *sf = reinterpret_cast<uint32_t *>(sr + kWarps * kSub * 2 * kNP);
     pdl_trigger();
     pdl_wait();
@@ -81,17 +81,17 @@ __global__ void __launch_bounds__(kScanThreads) scan_backward_kernel(ScanBackwar
     T *gz = q.grad_z ? static_cast<T *>(q.grad_z) + out0 : nullptr;
     float acc_D = 0.0f, acc_bias = 0.0f;  // of channel tid % kCh
 
-    const int64_t last = t0 + (t1 - 1 - t0) / kScanTile * kScanTile;
-    for (int64_t s0 = last; s0 >= t0; s0 -= kScanTile) {
-        const int rows = int(min(int64_t(kScanTile), t1 - s0));
-        for (int i = tid; i < kScanTile * kCh; i += kScanThreads) {
+    const int64_t last = t0 + (t1 - 1 - t0) / kCheckpointRows * kCheckpointRows;
+    for (int64_t s0 = last; s0 >= t0; s0 -= kCheckpointRows) {
+        const int rows = int(min(int64_t(kCheckpointRows), t1 - s0));
+        for (int i = tid; i < kCheckpointRows * kCh; i += kScanThreads) {
             const int r = i / kCh, k = i % kCh;
             float2 v = make_float2(0.0f, 0.0f);
             float dy = 0.0f;
             if (k < live && r < rows) {
                 v.x = to_f32<T>(dt[(s0 + r) * p.dt_row + k]);
                 if (p.dt_bias) v.x += p.dt_bias[cb + k];
-                if (p.softplus) v.x = softplus(v.x);
+                if (p.softplus) v.x = softplus_poly(v.x);
                 v.y = v.x * to_f32<T>(u[(s0 + r) * p.u_row + k]);
                 dy = to_f32<T>(go[(s0 + r) * q.grad_row + k]);
                 if (z) dy *= silu(to_f32<T>(z[(s0 + r) * p.z_row + k]));
@@ -99,15 +99,15 @@ __global__ void __launch_bounds__(kScanThreads) scan_backward_kernel(ScanBackwar
             sd[i] = v;
             sg[i] = dy;
         }
-        for (int i = tid; i < kScanTile * kNP; i += kScanThreads) {
+        for (int i = tid; i < kCheckpointRows * kNP; i += kScanThreads) {
             const int r = i / kNP, n = i % kNP;
             sb[i] = r < rows && n < p.states ? to_f32<T>(B[(s0 + r) * p.b_row + n]) : 0.0f;
             sc[i] = r < rows && n < p.states ? to_f32<T>(C[(s0 + r) * p.c_row + n]) : 0.0f;
         }
-        if (tid < kScanTile) sf[tid] = tid >= rows ? kRowOutside : p.segmap ? p.segmap[s0 + tid] : 0u;
+        if (tid < kCheckpointRows) sf[tid] = tid >= rows ? kRowOutside : p.segmap ? p.segmap[s0 + tid] : 0u;
         __syncthreads();
 
-        load_state(h, p.checkpoints, int64_t(b) * p.tiles + s0 / kScanTile);
+        load_state(h, p.checkpoints, int64_t(b) * p.tiles + s0 / kCheckpointRows);
         auto step = [&](int r) {  // the state past row r
             const uint32_t f = sf[r];
             if (f == kRowOutside) return;
@@ -271,7 +271,7 @@ cudaError_t backward_nl(ScanBackwardParams q, cudaStream_t s) {
     ScanParams &p = q.f;
     p.group_blocks = uint32_t((p.group + kCh - 1) / kCh);
     const size_t smem =
-        sizeof(float) * (kScanTile * (6 * kCh + 2 * kNP + 1) + kScanThreads / 32 * kSub * 2 * kNP);
+        sizeof(float) * (kCheckpointRows * (6 * kCh + 2 * kNP + 1) + kScanThreads / 32 * kSub * 2 * kNP);
     if (device_blocks(reinterpret_cast<const void *>(scan_backward_kernel<T, NL>), kScanThreads, smem) == 0)
         return cudaErrorInvalidConfiguration;
     const dim3 grid(uint32_t(p.batch * p.chunks), uint32_t(p.groups * p.group_blocks));

@@ -70,10 +70,11 @@ struct Regions {
     }
 };
 
-// Checks and wide-access alignment, collected over a call's tensors.
+// Checks, and the alignment that a call's tensors have in common.
 struct Check {
     dwp_status status = DWP_SUCCESS;
-    bool wide = true;  // every row of every tensor seen starts on 16 bytes
+    // every address and byte stride seen, or-ed: of the rows, of B and C, of f32 states
+    uintptr_t bits = 0, bits_bc = 0, bits_state = 0;
     Regions regions;
 
     void fail(dwp_status s) {
@@ -95,21 +96,23 @@ struct Check {
         if (output && batch > 1 && n > 1)
             require(step >= (n - 1) * row + inner || row >= (batch - 1) * step + inner);
         if (status != DWP_SUCCESS) return;
-        wide = wide && aligned(x.data, 16) && row * e % 16 == 0 && step * e % 16 == 0;
+        bits |= reinterpret_cast<uintptr_t>(x.data) | uintptr_t(row * e) | uintptr_t(step * e);
         if (track) {
             const Region r{reinterpret_cast<uintptr_t>(x.data), batch, n, inner * e, step * e, row * e};
             output ? regions.output(r) : regions.in(r);
         }
     }
     // dense array of `count` elements of type t; NULL allowed if optional
-    void dense(const void *p, int64_t t, int64_t count, bool output, bool optional, bool counts_wide = false) {
+    void dense(const void *p, int64_t t, int64_t count, bool output, bool optional, uintptr_t *seen = nullptr) {
         if (!optional && count > 0) require(p != nullptr);
         if (status != DWP_SUCCESS || !p) return;
         if (!aligned(p, size_of(t))) return fail(DWP_ERR_MISALIGNED);
-        if (counts_wide) wide = wide && aligned(p, 16);
+        if (seen) *seen |= reinterpret_cast<uintptr_t>(p);
         const Region r = flat(p, count * size_of(t));
         output ? regions.output(r) : regions.in(r);
     }
+    // Rows of `inner` elements of type t are whole 16-byte pieces.
+    bool wide(int64_t inner, int64_t t) const { return ((bits | uintptr_t(inner * size_of(t))) & 15u) == 0; }
     // The scratch of the two-call pattern; true: go on and launch.
     bool scratch(void *p, size_t *bytes, size_t need, dwp_status *st) {
         if (status != DWP_SUCCESS) return *st = status, false;
@@ -159,9 +162,8 @@ int64_t check_conv(Check &c, const dwp_conv_args &a, bool backward) {
     }
     c.dense(a.weight, a.weight_dtype, a.channels * a.width, false, false);
     c.dense(a.bias, a.weight_dtype, a.channels, false, true);
-    c.dense(a.initial_state, a.dtype, seqs * halo * a.channels, false, true, true);
-    if (!backward) c.dense(a.final_state, a.dtype, seqs * halo * a.channels, true, true, true);
-    c.wide = c.wide && a.channels * size_of(a.dtype) % 16 == 0;
+    c.dense(a.initial_state, a.dtype, seqs * halo * a.channels, false, true, &c.bits);
+    if (!backward) c.dense(a.final_state, a.dtype, seqs * halo * a.channels, true, true, &c.bits);
     return seqs;
 }
 
@@ -190,7 +192,7 @@ dwp_status conv_forward(const dwp_conv_args &a, cudaStream_t s) {
         if (err != cudaSuccess) return launched(err);
     }
     if (a.batch * a.rows == 0 || seqs == 0) return DWP_SUCCESS;
-    return launched(launch_conv(t, conv_params(a, conv_strip_rows()), c.wide, s));
+    return launched(launch_conv(t, conv_params(a, conv_strip_rows()), c.wide(a.channels, a.dtype), s));
 }
 
 // Rows of a strip of the gradient: long enough that the taps' partial sums
@@ -209,8 +211,8 @@ dwp_status conv_backward(const dwp_conv_backward_args &a, void *scratch, size_t 
         c.rows(a.grad_out, f.dtype, f.batch, f.rows, f.channels, false);
         c.rows(a.grad_x, f.dtype, f.batch, f.rows, f.channels, true);
     }
-    c.dense(a.grad_final_state, f.dtype, seqs * halo * f.channels, false, true, true);
-    c.dense(a.grad_initial_state, f.dtype, seqs * halo * f.channels, true, true, true);
+    c.dense(a.grad_final_state, f.dtype, seqs * halo * f.channels, false, true, &c.bits);
+    c.dense(a.grad_initial_state, f.dtype, seqs * halo * f.channels, true, true, &c.bits);
     c.dense(a.grad_weight, DWP_F32, f.channels * f.width, true, false);
     c.dense(a.grad_bias, DWP_F32, f.channels, true, true);
     const int64_t strips = ceil_div(f.rows, kGradStrip);
@@ -232,7 +234,7 @@ dwp_status conv_backward(const dwp_conv_backward_args &a, void *scratch, size_t 
     p.grad_x = a.grad_x.data, p.gx_batch = a.grad_x.batch_stride, p.gx_row = a.grad_x.row_stride;
     p.grad_final = a.grad_final_state, p.grad_initial = a.grad_initial_state;
     p.partial = static_cast<float *>(scratch);
-    cudaError_t err = launch_conv_backward(t, p, c.wide, s);
+    cudaError_t err = launch_conv_backward(t, p, c.wide(f.channels, f.dtype), s);
     if (err != cudaSuccess) return launched(err);
     const ColumnOut o{{a.grad_weight, a.grad_bias, nullptr},
                       {f.channels * f.width, f.channels * (f.width + 1), 0},
@@ -271,8 +273,7 @@ dwp_status conv_step(const dwp_conv_step_args &a, cudaStream_t s) {
     p.width = int(a.width), p.silu = int(a.silu), p.weight_f32 = a.weight_dtype == DWP_F32;
     p.x = a.x.data, p.x_row = a.x.row_stride, p.y = a.out.data, p.y_row = a.out.row_stride;
     p.weight = a.weight, p.bias = a.bias, p.state = a.state, p.state_slot = a.slot_stride, p.slots = a.slots;
-    const bool wide = c.wide && a.channels * size_of(a.dtype) % 16 == 0;
-    return launched(launch_conv_step(static_cast<dwp_dtype>(a.dtype), p, wide, s));
+    return launched(launch_conv_step(static_cast<dwp_dtype>(a.dtype), p, c.wide(a.channels, a.dtype), s));
 }
 
 // ---------------------------------------------------------------------------
@@ -282,8 +283,12 @@ dwp_status conv_step(const dwp_conv_step_args &a, cudaStream_t s) {
 void check_bc(Check &c, const dwp_rows &x, int64_t group_stride, int64_t t, int64_t batch, int64_t rows,
               int64_t groups, int64_t states) {
     c.require(groups == 1 || (group_stride >= states && group_stride <= kMaxStride));
-    if (c.status == DWP_SUCCESS)
-        c.rows(x, t, batch, rows, (groups - 1) * group_stride * (groups > 1) + states, false);
+    if (c.status != DWP_SUCCESS) return;
+    const uintptr_t others = c.bits;
+    c.bits = 0;
+    c.rows(x, t, batch, rows, (groups - 1) * group_stride * (groups > 1) + states, false);
+    c.bits_bc |= c.bits | uintptr_t(groups > 1 ? group_stride * size_of(t) : 0);
+    c.bits = others;
 }
 
 bool scan_sizes_ok(int64_t dtype, int64_t softplus, int64_t channels, int64_t states, int64_t groups) {
@@ -305,13 +310,27 @@ int64_t check_scan(Check &c, const dwp_selective_scan_args &a, bool backward) {
         check_bc(c, a.C, a.c_group_stride, a.dtype, a.batch, a.rows, a.groups, a.states);
         if (!backward) c.rows(a.out, a.dtype, a.batch, a.rows, a.channels, true);
     }
-    c.dense(a.A, DWP_F32, state, false, false);
+    c.dense(a.A, DWP_F32, state, false, false, &c.bits_state);
     c.dense(a.D, DWP_F32, a.channels, false, true);
     c.dense(a.dt_bias, DWP_F32, a.channels, false, true);
-    c.dense(a.initial_state, DWP_F32, seqs * state, false, true);
-    if (!backward) c.dense(a.final_state, DWP_F32, seqs * state, true, true);
-    c.dense(a.checkpoints, DWP_F32, a.batch * tiles * state, !backward, !backward);
+    c.dense(a.initial_state, DWP_F32, seqs * state, false, true, &c.bits_state);
+    if (!backward) c.dense(a.final_state, DWP_F32, seqs * state, true, true, &c.bits_state);
+    c.dense(a.checkpoints, DWP_F32, a.batch * tiles * state, !backward, !backward, &c.bits_state);
     return seqs;
+}
+
+// Chunks of rows for the forward: as many as fill the GPU's warps once, where
+// the channels alone fill less than half of them.  A cut costs a second walk
+// over the rows, about 0.65 of the first; a warp alone on its scheduler runs
+// at a third of the rate of three.  Measured at 8192 rows x 4096 channels x 16
+// states (256 warps): 1 chunk 1013 us, 4 516, 7 339, 14 342; at 65536 x 2048
+// (32 warps): 38 chunks 1726 us, 56 1218, 112 1276.
+int64_t scan_chunks(const dwp_selective_scan_args &a) {
+    const int64_t units = a.batch * a.groups * ceil_div(a.channels / a.groups, scan_warp_channels(a.states));
+    const int64_t slots = 152 * kScanWarpsPerSM;
+    if (2 * units >= slots) return 1;
+    const int64_t most = ceil_div(a.rows, 2 * DWP_SCAN_CHECKPOINT_ROWS);
+    return slots / units < most ? slots / units : most;
 }
 
 ScanParams scan_params(const dwp_selective_scan_args &a, uint32_t *segmap) {
@@ -332,11 +351,28 @@ ScanParams scan_params(const dwp_selective_scan_args &a, uint32_t *segmap) {
     return p;
 }
 
+// How wide the scan's accesses may be.
+void set_scan_access(ScanParams &p, const Check &c, const dwp_selective_scan_args &a) {
+    const uintptr_t e = uintptr_t(size_of(a.dtype));
+    p.wide = (c.bits & (2 * e - 1)) == 0 && p.group % 2 == 0 && (c.bits_bc & (4 * e - 1)) == 0 && a.states % 4 == 0;
+    p.states_wide = (c.bits_state & 15u) == 0 && a.states % 4 == 0;
+}
+
 dwp_status scan_forward(const dwp_selective_scan_args &a, void *scratch, size_t *bytes, cudaStream_t s) {
     Check c;
     const int64_t seqs = check_scan(c, a, false);
-    const size_t need = a.offsets ? round16(size_t(a.rows > 0 ? a.rows : 0) * 4u) : 0u;
-    dwp_status st;
+    dwp_status st = c.status;
+    if (st != DWP_SUCCESS) return st;
+    ScanParams p = scan_params(a, static_cast<uint32_t *>(scratch));
+    if (a.batch * a.rows > 0) {  // whole tiles of rows to each chunk
+        p.chunk_rows = ceil_div(p.tiles, scan_chunks(a)) * DWP_SCAN_CHECKPOINT_ROWS;
+        p.chunks = ceil_div(a.rows, p.chunk_rows);
+    }
+    const int64_t carries = a.batch * (p.chunks - 1);
+    const size_t map = a.offsets ? round16(size_t(a.rows) * 4u) : 0u;
+    const size_t ends = round16(size_t(carries * a.channels * a.states) * 4u);
+    const size_t sums = round16(size_t(carries * a.channels) * 4u);
+    const size_t need = map + ends + sums + round16(size_t(carries) * 4u);
     if (!c.scratch(scratch, bytes, need, &st)) return st;
     const int64_t state = a.channels * a.states;
     if (a.final_state && (a.offsets || a.rows == 0)) {
@@ -345,12 +381,17 @@ dwp_status scan_forward(const dwp_selective_scan_args &a, void *scratch, size_t 
         if (err != cudaSuccess) return launched(err);
     }
     if (a.batch * a.rows == 0 || seqs == 0) return DWP_SUCCESS;
-    auto *map = static_cast<uint32_t *>(scratch);
     if (a.offsets) {
-        const cudaError_t err = launch_segment_map(a.offsets, uint32_t(seqs), uint32_t(a.rows), map, s);
+        const cudaError_t err = launch_segment_map(a.offsets, uint32_t(seqs), uint32_t(a.rows),
+                                                   static_cast<uint32_t *>(scratch), s);
         if (err != cudaSuccess) return launched(err);
     }
-    return launched(launch_selscan(static_cast<dwp_dtype>(a.dtype), scan_params(a, map), s));
+    char *at = static_cast<char *>(scratch);
+    p.carry = reinterpret_cast<float *>(at + map);
+    p.carry_sum = reinterpret_cast<float *>(at + map + ends);
+    p.carry_head = reinterpret_cast<uint32_t *>(at + map + ends + sums);
+    set_scan_access(p, c, a);
+    return launched(launch_selscan(static_cast<dwp_dtype>(a.dtype), p, s));
 }
 
 dwp_status scan_backward(const dwp_selective_scan_backward_args &a, void *scratch, size_t *bytes, cudaStream_t s) {
@@ -455,7 +496,6 @@ void check_norm(Check &c, const dwp_norm_args &a) {
     if (c.status != DWP_SUCCESS) return;
     c.dense(a.weight, a.weight_dtype, a.channels, false, false);
     c.dense(a.scale, a.weight_dtype, a.channels, false, true);
-    c.wide = c.wide && a.channels / a.groups * size_of(a.dtype) % 16 == 0;
 }
 
 NormParams norm_params(const dwp_norm_args &a) {
@@ -487,7 +527,7 @@ dwp_status norm_forward(const dwp_norm_args &a, cudaStream_t s) {
     c.rows(a.out, a.dtype, 1, a.rows, a.channels, true);
     if (c.status != DWP_SUCCESS) return c.status;
     if (c.regions.clash()) return DWP_ERR_ALIASING;
-    return launched(launch_norm(static_cast<dwp_dtype>(a.dtype), norm_params(a), c.wide, s));
+    return launched(launch_norm(static_cast<dwp_dtype>(a.dtype), norm_params(a), c.wide(a.channels / a.groups, a.dtype), s));
 }
 
 // Blocks that share a group's rows in the gradient: enough to fill the GPU's
@@ -536,7 +576,7 @@ dwp_status norm_backward(const dwp_norm_backward_args &a, void *scratch, size_t 
     p.grad_residual = a.grad_residual.data, p.gres_row = a.grad_residual.row_stride;
     p.grad_gate = a.grad_gate.data, p.ggate_row = a.grad_gate.row_stride;
     p.partial = static_cast<float *>(scratch);
-    cudaError_t err = launch_norm_backward(static_cast<dwp_dtype>(f.dtype), p, c.wide, s);
+    cudaError_t err = launch_norm_backward(static_cast<dwp_dtype>(f.dtype), p, c.wide(f.channels / f.groups, f.dtype), s);
     if (err != cudaSuccess) return launched(err);
     const ColumnOut o{{a.grad_weight, a.grad_scale, nullptr}, {f.channels, planes * f.channels, 0}, 1};
     return launched(launch_column_sums(p.partial, blocks, planes * f.channels, o, s));
