@@ -191,7 +191,8 @@ struct ScanStepParams {
     int64_t state_slot;
     const int32_t *slots;
 };
-// Channels one block of the selective scan covers at this many states.
+// Warps of the gradient that an SM holds, and channels one covers.
+constexpr int kScanBackWarpsPerSM = 8;
 int64_t scan_block_channels(int64_t states);
 // Warps of the forward that an SM holds (168 registers a lane).
 constexpr int kScanWarpsPerSM = 12;
@@ -206,6 +207,15 @@ cudaError_t launch_selscan_f16(const ScanParams &p, cudaStream_t s);
 // States carried over the chunks of the forward.
 cudaError_t launch_carry(const ScanParams &p, cudaStream_t s);
 cudaError_t launch_selscan_backward(dwp_dtype t, const ScanBackwardParams &p, cudaStream_t s);
+cudaError_t launch_selscan_backward_f32(const ScanBackwardParams &p, cudaStream_t s);
+cudaError_t launch_selscan_backward_bf16(const ScanBackwardParams &p, cudaStream_t s);
+cudaError_t launch_selscan_backward_f16(const ScanBackwardParams &p, cudaStream_t s);
+// The gradient's recurrence over the chunks, from the last (chunk 0 of the
+// carry) to the second.
+cudaError_t launch_scan_walk_back(dwp_dtype t, const ScanParams &p, cudaStream_t s);
+cudaError_t launch_scan_walk_back_f32(const ScanParams &p, cudaStream_t s);
+cudaError_t launch_scan_walk_back_bf16(const ScanParams &p, cudaStream_t s);
+cudaError_t launch_scan_walk_back_f16(const ScanParams &p, cudaStream_t s);
 cudaError_t launch_selscan_step(dwp_dtype t, const ScanStepParams &p, cudaStream_t s);
 
 struct NormParams {

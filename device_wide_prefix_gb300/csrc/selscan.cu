@@ -60,6 +60,22 @@ int64_t scan_warp_channels(int64_t states) {
     return states <= 16 ? 64 : states <= 32 ? 32 : states <= 64 ? 16 : 8;
 }
 
+int64_t scan_block_channels(int64_t states) {
+    return states <= 16 ? 32 : states <= 32 ? 16 : states <= 64 ? 8 : 4;
+}
+
+cudaError_t launch_scan_walk_back(dwp_dtype t, const ScanParams &p, cudaStream_t s) {
+    if (t == DWP_F32) return launch_scan_walk_back_f32(p, s);
+    if (t == DWP_BF16) return launch_scan_walk_back_bf16(p, s);
+    return launch_scan_walk_back_f16(p, s);
+}
+
+cudaError_t launch_selscan_backward(dwp_dtype t, const ScanBackwardParams &q, cudaStream_t s) {
+    if (t == DWP_F32) return launch_selscan_backward_f32(q, s);
+    if (t == DWP_BF16) return launch_selscan_backward_bf16(q, s);
+    return launch_selscan_backward_f16(q, s);
+}
+
 cudaError_t launch_selscan(dwp_dtype t, const ScanParams &p, cudaStream_t s) {
     if (t == DWP_F32) return launch_selscan_f32(p, s);
     if (t == DWP_BF16) return launch_selscan_bf16(p, s);

@@ -49,6 +49,9 @@ __device__ __forceinline__ float rcp(float x) {
     return y;
 }
 
+// z * sigmoid(z); for z far below 0 the exponential is +inf and the product 0.
+__device__ __forceinline__ float gate_of(float z) { return z * rcp(1.0f + ex2(z * -kLog2e)); }
+
 // log(1 + e^x) = max(x, 0) + log1p(e^-|x|).  log1p(e) / e on [0, 1] is a
 // degree-8 polynomial fitted for the least relative error (3.0e-8; 1.8e-7
 // evaluated in f32); with the exponential's own error the result is within

@@ -51,15 +51,19 @@ struct Two<float> {
 
 __device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
-// z * sigmoid(z); for z far below 0 the exponential is +inf and the product 0.
-__device__ __forceinline__ float gate_of(float z) { return z * rcp(1.0f + ex2(z * -kLog2e)); }
+// What a walk computes.  kWalkOut: the scan.  kWalkStates: the first pass
+// over chunks, last states and sums of delta only.  kWalkBack: the same for
+// the gradient, whose recurrence runs from the last row to the first:
+// e = exp(delta A) (e + dout silu(z) C), with u standing for dout, B for C,
+// initial for the final state's gradient, and a segment's last row in the
+// place of its first.
+enum : int { kWalkStates = 0, kWalkOut = 1, kWalkBack = 2 };
 
-// kOut: the scan.  Otherwise the first pass over chunks: last states and
-// sums of delta only.  kWide: two neighbouring channels, and four neighbouring
-// states of B and C, are one aligned access, so that the loads are straight
+// kWide: two neighbouring channels, and four neighbouring states of B and C,
+// are one aligned access, so that the loads are straight
 // code: a load under a branch is waited for where the branch ends, and the
 // rows ahead of their use would buy nothing.
-template <class T, int NT, int NL, bool kOut, bool kWide>
+template <class T, int NT, int NL, int kMode, bool kWide>
 __global__ void __launch_bounds__(32, kScanWarpsPerSM) selscan_kernel(ScanParams p) {
     constexpr int kC = 64 / NL, kN = NT * NL, kP = NT / 2;
     constexpr int kRows = kN <= 16 ? 16 : kN <= 32 ? 8 : 4;  // rows of B and C staged at once
@@ -69,9 +73,11 @@ __global__ void __launch_bounds__(32, kScanWarpsPerSM) selscan_kernel(ScanParams
     pdl_trigger();
     pdl_wait();
 
+    constexpr bool kOut = kMode == kWalkOut, kBack = kMode == kWalkBack, kGate = kMode != kWalkStates;
+    constexpr uint32_t kFirst = kBack ? kRowTail : kRowHead;
     const uint32_t chunks = kOut ? uint32_t(p.chunks) : uint32_t(p.chunks - 1);
     const uint32_t b = blockIdx.x / chunks, chunk = blockIdx.x % chunks;
-    const int64_t t0 = int64_t(chunk) * p.chunk_rows;
+    const int64_t t0 = int64_t(kBack ? uint32_t(p.chunks) - 1u - chunk : chunk) * p.chunk_rows;
     const int64_t t1 = min(t0 + p.chunk_rows, p.rows);
     const uint32_t g = blockIdx.y / p.group_blocks;
     const int64_t cg = int64_t(blockIdx.y % p.group_blocks) * kC;  // first channel within the group
@@ -138,7 +144,8 @@ __global__ void __launch_bounds__(32, kScanWarpsPerSM) selscan_kernel(ScanParams
 
     const T *u = static_cast<const T *>(p.u) + int64_t(b) * p.u_batch + cb;
     const T *dt = static_cast<const T *>(p.dt) + int64_t(b) * p.dt_batch + cb;
-    const bool gate = kOut && p.z;
+    auto place = [&](int64_t s) { return kBack ? t0 + t1 - 1 - s : s; };  // the row that the walk meets as row s
+    const bool gate = kGate && p.z;
     const T *z = gate ? static_cast<const T *>(p.z) + int64_t(b) * p.z_batch + cb : u;
     const int64_t z_row = gate ? p.z_row : p.u_row;
     const T *B = static_cast<const T *>(p.B) + int64_t(b) * p.b_batch + g * p.b_group;
@@ -156,7 +163,7 @@ __global__ void __launch_bounds__(32, kScanWarpsPerSM) selscan_kernel(ScanParams
 #pragma unroll
         for (int i = 0; i < kEach; ++i) {
             const int q = lane + 32 * i, r = q / (kN / 4), n = q % (kN / 4) * 4;
-            const int64_t t = min(s0 + min(r, kRows - 1), t1 - 1);
+            const int64_t t = place(min(s0 + r, t1 - 1));
             if constexpr (kWide) {
                 const int m = min(n, p.states - 4);
                 rb[i] = *reinterpret_cast<const Pack<T, 4> *>(B + t * p.b_row + m);
@@ -207,16 +214,16 @@ __global__ void __launch_bounds__(32, kScanWarpsPerSM) selscan_kernel(ScanParams
     auto load = [&](int64_t s) {  // rows past the last are read as the last
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
-            const int64_t t = min(s + i, t1 - 1);
+            const int64_t t = place(min(s + i, t1 - 1));
             const T *pd = dt + t * p.dt_row, *pu = u + t * p.u_row, *pz = z + t * z_row;
             if constexpr (kWide) {
                 raw.dt[i].load(pd + c0);
                 raw.u[i].load(pu + c0);
-                if (kOut) raw.z[i].load(pz + c0);
+                if (kGate) raw.z[i].load(pz + c0);
             } else {
                 raw.dt[i].load(pd + c0, pd + c1);
                 raw.u[i].load(pu + c0, pu + c1);
-                if (kOut) raw.z[i].load(pz + c0, pz + c1);
+                if (kGate) raw.z[i].load(pz + c0, pz + c1);
             }
         }
     };
@@ -224,10 +231,10 @@ __global__ void __launch_bounds__(32, kScanWarpsPerSM) selscan_kernel(ScanParams
     // few rows in flight to cover the way from HBM.
     auto prefetch = [&](int64_t s) {
         if (s + kRows > t1) return;
-        const int r = lane % kRows;
+        const int64_t t = place(s + lane % kRows);
         if (kRows == 16) {
-            prefetch_l2((lane < 16 ? dt + (s + r) * p.dt_row : u + (s + r) * p.u_row));
-            if (kOut && lane < 16) prefetch_l2(z + (s + r) * z_row);
+            prefetch_l2(lane < 16 ? dt + t * p.dt_row : u + t * p.u_row);
+            if (kGate && lane < 16) prefetch_l2(z + t * z_row);
         }
     };
     auto convert = [&](Ready &to) {
@@ -238,7 +245,15 @@ __global__ void __launch_bounds__(32, kScanWarpsPerSM) selscan_kernel(ScanParams
             d.x += bias.x, d.y += bias.y;
             if (p.softplus) d.x = softplus_poly(d.x), d.y = softplus_poly(d.y);
             to.d[0][i] = d.x, to.d[1][i] = d.y;
-            to.x[0][i] = d.x * uv.x, to.x[1][i] = d.y * uv.y;
+            if constexpr (kBack) {
+                to.x[0][i] = uv.x, to.x[1][i] = uv.y;
+                if (gate) {
+                    const float2 zv = raw.z[i].f32();
+                    to.x[0][i] *= gate_of(zv.x), to.x[1][i] *= gate_of(zv.y);
+                }
+            } else {
+                to.x[0][i] = d.x * uv.x, to.x[1][i] = d.y * uv.y;
+            }
             to.u[i] = raw.u[i], to.z[i] = raw.z[i];
         }
     };
@@ -259,7 +274,8 @@ __global__ void __launch_bounds__(32, kScanWarpsPerSM) selscan_kernel(ScanParams
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     const float2 e = unpack(mul2(f2(in.d[c][i], in.d[c][i]), A2[c][j + q]));
-                    h[c][j + q] = fma2(f2(ex2(e.x), ex2(e.y)), h[c][j + q], mul2(f2(in.x[c][i], in.x[c][i]), Bv[q]));
+                    const F2 a = f2(ex2(e.x), ex2(e.y)), x = f2(in.x[c][i], in.x[c][i]);
+                    h[c][j + q] = kBack ? mul2(a, fma2(x, Bv[q], h[c][j + q])) : fma2(a, h[c][j + q], mul2(x, Bv[q]));
                     if (kOut) acc[c] = j + q == 0 ? mul2(Cv[q], h[c][0]) : fma2(Cv[q], h[c][j + q], acc[c]);
                 }
         }
@@ -296,7 +312,7 @@ __global__ void __launch_bounds__(32, kScanWarpsPerSM) selscan_kernel(ScanParams
                 if (f == kRowOutside) {
                     skip |= 1u << i;
                 } else {
-                    if (f & kRowHead) {
+                    if (f & kFirst) {
                         load_state(p.initial, f & kRowSegment);
                         head_seen = true;
                     }
@@ -359,7 +375,7 @@ __global__ void __launch_bounds__(32, kScanWarpsPerSM) selscan_kernel(ScanParams
         if (s0 + kRows < t1) fetch(s0 + kRows);
         prefetch(s0 + 2 * kRows);
         if (map) {  // heads, tails and rows outside need a look
-            code = lane < rows ? map[s0 + lane] : 0u;
+            code = lane < rows ? map[place(s0 + lane)] : 0u;
             plain = __all_sync(0xffffffffu, (code & (kRowHead | kRowTail)) == 0u);
         }
         if (kOut && p.checkpoints && s0 % kCheckpointRows == 0)
@@ -396,13 +412,13 @@ cudaError_t scan_v(ScanParams p, cudaStream_t s) {
     p.group_blocks = uint32_t((p.group + kC - 1) / kC);
     const uint32_t units = uint32_t(p.groups * p.group_blocks);
     if (p.chunks > 1) {
-        cudaError_t err = launch_pdl(selscan_kernel<T, NT, NL, false, kWide>,
+        cudaError_t err = launch_pdl(selscan_kernel<T, NT, NL, kWalkStates, kWide>,
                                      dim3(uint32_t(p.batch * (p.chunks - 1)), units), dim3(32), 0, s, p);
         if (err != cudaSuccess) return err;
         err = launch_carry(p, s);
         if (err != cudaSuccess) return err;
     }
-    return launch_pdl(selscan_kernel<T, NT, NL, true, kWide>, dim3(uint32_t(p.batch * p.chunks), units), dim3(32), 0, s,
+    return launch_pdl(selscan_kernel<T, NT, NL, kWalkOut, kWide>, dim3(uint32_t(p.batch * p.chunks), units), dim3(32), 0, s,
                       p);
 }
 
@@ -418,6 +434,27 @@ cudaError_t scan_t(const ScanParams &p, cudaStream_t s) {
     if (p.states <= 32) return scan_w<T, 16, 2>(p, s);
     if (p.states <= 64) return scan_w<T, 16, 4>(p, s);
     return scan_w<T, 16, 8>(p, s);
+}
+
+// The walk back over all chunks but the first, and the carry over them.
+template <class T, int NT, int NL>
+cudaError_t back_w(ScanParams p, cudaStream_t s) {
+    constexpr int kC = 64 / NL;
+    p.group_blocks = uint32_t((p.group + kC - 1) / kC);
+    const dim3 grid(uint32_t(p.batch * (p.chunks - 1)), uint32_t(p.groups * p.group_blocks));
+    const cudaError_t err =
+        p.wide ? launch_pdl(selscan_kernel<T, NT, NL, kWalkBack, true>, grid, dim3(32), 0, s, p)
+               : launch_pdl(selscan_kernel<T, NT, NL, kWalkBack, false>, grid, dim3(32), 0, s, p);
+    return err == cudaSuccess ? launch_carry(p, s) : err;
+}
+
+template <class T>
+cudaError_t back_t(const ScanParams &p, cudaStream_t s) {
+    if (p.states <= 8) return back_w<T, 8, 1>(p, s);
+    if (p.states <= 16) return back_w<T, 16, 1>(p, s);
+    if (p.states <= 32) return back_w<T, 16, 2>(p, s);
+    if (p.states <= 64) return back_w<T, 16, 4>(p, s);
+    return back_w<T, 16, 8>(p, s);
 }
 
 }  // namespace

@@ -325,13 +325,36 @@ int64_t check_scan(Check &c, const dwp_selective_scan_args &a, bool backward) {
 // at a third of the rate of three.  Measured at 8192 rows x 4096 channels x 16
 // states (256 warps): 1 chunk 1013 us, 4 516, 7 339, 14 342; at 65536 x 2048
 // (32 warps): 38 chunks 1726 us, 56 1218, 112 1276.
-int64_t scan_chunks(const dwp_selective_scan_args &a) {
-    const int64_t units = a.batch * a.groups * ceil_div(a.channels / a.groups, scan_warp_channels(a.states));
-    const int64_t slots = 152 * kScanWarpsPerSM;
+int64_t chunks_of(const dwp_selective_scan_args &a, int64_t units, int64_t slots) {
     if (2 * units >= slots) return 1;
-    const int64_t most = ceil_div(a.rows, 2 * DWP_SCAN_CHECKPOINT_ROWS);
+    const int64_t most = ceil_div(a.rows, 4 * DWP_SCAN_CHECKPOINT_ROWS);
     return slots / units < most ? slots / units : most;
 }
+
+int64_t scan_units(const dwp_selective_scan_args &a, int64_t channels) {
+    return a.batch * a.groups * ceil_div(a.channels / a.groups, channels);
+}
+
+// Whole tiles of rows to each chunk.
+void set_chunks(ScanParams &p, int64_t chunks) {
+    p.chunk_rows = ceil_div(p.tiles, chunks) * DWP_SCAN_CHECKPOINT_ROWS;
+    p.chunks = ceil_div(p.rows, p.chunk_rows);
+}
+
+// Scratch of the states carried over chunks.
+struct CarrySpace {
+    size_t ends, sums, heads;
+    explicit CarrySpace(const ScanParams &p)
+        : ends(round16(size_t(p.batch * (p.chunks - 1) * p.channels * p.states) * 4u)),
+          sums(round16(size_t(p.batch * (p.chunks - 1) * p.channels) * 4u)),
+          heads(round16(size_t(p.batch * (p.chunks - 1)) * 4u)) {}
+    size_t bytes() const { return ends + sums + heads; }
+    void place(ScanParams &p, char *at) const {
+        p.carry = reinterpret_cast<float *>(at);
+        p.carry_sum = reinterpret_cast<float *>(at + ends);
+        p.carry_head = reinterpret_cast<uint32_t *>(at + ends + sums);
+    }
+};
 
 ScanParams scan_params(const dwp_selective_scan_args &a, uint32_t *segmap) {
     ScanParams p = {};
@@ -364,15 +387,11 @@ dwp_status scan_forward(const dwp_selective_scan_args &a, void *scratch, size_t 
     dwp_status st = c.status;
     if (st != DWP_SUCCESS) return st;
     ScanParams p = scan_params(a, static_cast<uint32_t *>(scratch));
-    if (a.batch * a.rows > 0) {  // whole tiles of rows to each chunk
-        p.chunk_rows = ceil_div(p.tiles, scan_chunks(a)) * DWP_SCAN_CHECKPOINT_ROWS;
-        p.chunks = ceil_div(a.rows, p.chunk_rows);
-    }
-    const int64_t carries = a.batch * (p.chunks - 1);
+    if (a.batch * a.rows > 0)
+        set_chunks(p, chunks_of(a, scan_units(a, scan_warp_channels(a.states)), 152 * kScanWarpsPerSM));
+    const CarrySpace carry(p);
     const size_t map = a.offsets ? round16(size_t(a.rows) * 4u) : 0u;
-    const size_t ends = round16(size_t(carries * a.channels * a.states) * 4u);
-    const size_t sums = round16(size_t(carries * a.channels) * 4u);
-    const size_t need = map + ends + sums + round16(size_t(carries) * 4u);
+    const size_t need = map + carry.bytes();
     if (!c.scratch(scratch, bytes, need, &st)) return st;
     const int64_t state = a.channels * a.states;
     if (a.final_state && (a.offsets || a.rows == 0)) {
@@ -386,10 +405,7 @@ dwp_status scan_forward(const dwp_selective_scan_args &a, void *scratch, size_t 
                                                    static_cast<uint32_t *>(scratch), s);
         if (err != cudaSuccess) return launched(err);
     }
-    char *at = static_cast<char *>(scratch);
-    p.carry = reinterpret_cast<float *>(at + map);
-    p.carry_sum = reinterpret_cast<float *>(at + map + ends);
-    p.carry_head = reinterpret_cast<uint32_t *>(at + map + ends + sums);
+    carry.place(p, static_cast<char *>(scratch) + map);
     set_scan_access(p, c, a);
     return launched(launch_selscan(static_cast<dwp_dtype>(a.dtype), p, s));
 }
@@ -413,16 +429,18 @@ dwp_status scan_backward(const dwp_selective_scan_backward_args &a, void *scratc
     c.dense(a.grad_A, DWP_F32, state, true, false);
     c.dense(a.grad_D, DWP_F32, f.channels, true, true);
     c.dense(a.grad_dt_bias, DWP_F32, f.channels, true, true);
-    c.dense(a.grad_final_state, DWP_F32, seqs * state, false, true);
+    c.dense(a.grad_final_state, DWP_F32, seqs * state, false, true, &c.bits_state);
     c.dense(a.grad_initial_state, DWP_F32, seqs * state, true, true);
 
     ScanBackwardParams p = {};
     p.f = scan_params(f, nullptr);
-    const int64_t blocks = ceil_div(p.f.group, scan_block_channels(f.states));
+    const int64_t per = scan_block_channels(f.states), blocks = ceil_div(p.f.group, per);
+    if (n > 0) set_chunks(p.f, chunks_of(f, scan_units(f, per), 152 * kScanBackWarpsPerSM));
+    const CarrySpace carry(p.f);
     const size_t map = f.offsets ? round16(size_t(f.rows) * 4u) : 0u;
     const size_t part = round16(size_t(f.batch * p.f.chunks * f.channels * (f.states + 2)) * 4u);
     const size_t bc = round16(size_t(blocks * n * f.groups * 2 * f.states) * 4u);
-    if (!c.scratch(scratch, bytes, map + part + bc, &st)) return st;
+    if (!c.scratch(scratch, bytes, map + part + bc + carry.bytes(), &st)) return st;
     if (a.grad_initial_state && (f.offsets || f.rows == 0)) {
         const cudaError_t err = launch_empty_states(DWP_F32, f.offsets, seqs, state, a.grad_final_state,
                                                     a.grad_initial_state, s);
@@ -445,7 +463,18 @@ dwp_status scan_backward(const dwp_selective_scan_backward_args &a, void *scratc
     p.grad_out = a.grad_out.data, p.grad_batch = a.grad_out.batch_stride, p.grad_row = a.grad_out.row_stride;
     p.grad_final = a.grad_final_state, p.grad_initial = a.grad_initial_state;
     p.grad_u = a.grad_u, p.grad_dt = a.grad_dt, p.grad_z = a.grad_z, p.grad_B = a.grad_B, p.grad_C = a.grad_C;
-    cudaError_t err = launch_selscan_backward(static_cast<dwp_dtype>(f.dtype), p, s);
+    set_scan_access(p.f, c, f);
+    carry.place(p.f, at + map + part + bc);
+    const auto t = static_cast<dwp_dtype>(f.dtype);
+    if (p.f.chunks > 1) {
+        ScanParams r = p.f;  // as the walk back reads it
+        r.u = p.grad_out, r.u_batch = p.grad_batch, r.u_row = p.grad_row;
+        r.B = p.f.C, r.b_batch = p.f.c_batch, r.b_row = p.f.c_row, r.b_group = p.f.c_group;
+        r.initial = p.grad_final;
+        const cudaError_t err = launch_scan_walk_back(t, r, s);
+        if (err != cudaSuccess) return launched(err);
+    }
+    cudaError_t err = launch_selscan_backward(t, p, s);
     if (err != cudaSuccess) return launched(err);
     const ColumnOut o{{a.grad_A, a.grad_D, a.grad_dt_bias},
                       {state, state + f.channels, state + 2 * f.channels},

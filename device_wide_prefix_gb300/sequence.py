@@ -22,7 +22,7 @@ import torch
 import device_wide_prefix_gb300 as _dwp
 
 DWP_F32, DWP_BF16, DWP_F16 = 0, 1, 2
-CHECKPOINT_ROWS = 32  # DWP_SCAN_CHECKPOINT_ROWS
+CHECKPOINT_ROWS = 16  # DWP_SCAN_CHECKPOINT_ROWS
 NORM_MAX_GROUP = 16384  # DWP_NORM_MAX_GROUP
 
 _DTYPES = {torch.float32: DWP_F32, torch.bfloat16: DWP_BF16, torch.float16: DWP_F16}

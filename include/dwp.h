@@ -395,7 +395,7 @@ typedef struct dwp_conv_step_args {
 dwp_status dwp_causal_conv_step(const dwp_conv_step_args *args, dwp_stream stream);
 
 /* Rows between the states that the selective scan keeps for its gradient. */
-#define DWP_SCAN_CHECKPOINT_ROWS 32
+#define DWP_SCAN_CHECKPOINT_ROWS 16
 
 /*
  * Selective state space scan: per channel d (group g) and state n,
