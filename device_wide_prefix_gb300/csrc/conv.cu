@@ -30,6 +30,60 @@ __device__ __forceinline__ Span span_at(const uint32_t *offsets, uint32_t nseg, 
     return {s, int64_t(offsets[s]), min(int64_t(offsets[s + 1]), rows)};
 }
 
+// Taps and bias of V channels: w[j][i] is channel i's for j rows before the
+// row itself, 0 past the width.
+template <class T, int V, int W>
+__device__ __forceinline__ void load_taps(const ConvParams &p, int64_t c0, float (&w)[W][V], float (&bias)[V]) {
+    const int halo = p.width - 1;
+    if (W == 4 && p.width == 4 && p.weight_f32 && p.weight_wide) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const float4 v = reinterpret_cast<const float4 *>(p.weight)[c0 + i];
+            w[0][i] = v.w, w[1][i] = v.z, w[2][i] = v.y, w[W - 1][i] = v.x;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+#pragma unroll
+            for (int j = 0; j < W; ++j)
+                w[j][i] = j <= halo ? load_param<T>(p.weight, (c0 + i) * p.width + (halo - j), p.weight_f32) : 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) bias[i] = p.bias ? load_param<T>(p.bias, c0 + i, p.weight_f32) : 0.0f;
+}
+
+// The W - 1 inputs before row t of span `sp`: win[j - 1] is row t - j, or the
+// state row that stands for it.
+template <class T, int V, int W>
+__device__ __forceinline__ void load_window(const ConvParams &p, const Span &sp, const T *x, int64_t t, int64_t c0,
+                                            float (&win)[W][V]) {
+    const int halo = p.width - 1;
+    const T *init = static_cast<const T *>(p.initial_state);
+#pragma unroll
+    for (int j = 1; j < W; ++j) {
+        const int64_t r = t - j;
+#pragma unroll
+        for (int i = 0; i < V; ++i) win[j - 1][i] = 0.0f;
+        if (j <= halo) {
+            if (r >= sp.begin) load_f32<V>(win[j - 1], x + r * p.x_row);
+            else if (init)
+                load_f32<V>(win[j - 1], init + (int64_t(sp.seg) * halo + (r - sp.begin + halo)) * p.channels + c0);
+        }
+    }
+}
+
+template <int V, int W>
+__device__ __forceinline__ void push(float (&win)[W][V], const float (&x)[V]) {
+#pragma unroll
+    for (int j = W - 1; j > 0; --j)
+#pragma unroll
+        for (int i = 0; i < V; ++i) win[j][i] = win[j - 1][i];
+#pragma unroll
+    for (int i = 0; i < V; ++i) win[0][i] = x[i];
+}
+
+constexpr int kConvGroup = 4;  // rows loaded together, one group ahead of their use
+
 // Forward.  A thread walks kConvStrip rows of V channels with the last W - 1
 // inputs and the taps in registers, so each input is read once (plus W - 1
 // rows per strip).
@@ -43,60 +97,52 @@ __global__ void __launch_bounds__(kConvThreads) conv_kernel(ConvParams p) {
     const int64_t t0 = int64_t(blockIdx.x % p.strips) * kConvStrip;
     const int64_t t1 = min(t0 + kConvStrip, p.rows);
     const int halo = p.width - 1;
-
-    // taps w[W-1] for the row itself, w[W-1-j] for j rows before; 0 past the width
-    float w[W][V], bias[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-#pragma unroll
-        for (int j = 0; j < W; ++j)
-            w[j][i] = j <= halo ? load_param<T>(p.weight, (c0 + i) * p.width + (halo - j), p.weight_f32) : 0.0f;
-        bias[i] = p.bias ? load_param<T>(p.bias, c0 + i, p.weight_f32) : 0.0f;
-    }
     const T *x = static_cast<const T *>(p.x) + int64_t(b) * p.x_batch + c0;
     T *y = static_cast<T *>(p.y) + int64_t(b) * p.y_batch + c0;
-    const T *init = static_cast<const T *>(p.initial_state);
     T *fin = static_cast<T *>(p.final_state);
 
-    float win[W][V];  // win[j]: the input j rows before the current one
+    Pack<T, V> next[kConvGroup];
+    auto load = [&](int64_t t) {  // rows past the last are read as the last
+#pragma unroll
+        for (int i = 0; i < kConvGroup; ++i)
+            next[i] = *reinterpret_cast<const Pack<T, V> *>(x + min(t + i, t1 - 1) * p.x_row);
+    };
+    load(t0);
+    float w[W][V], bias[V], win[W][V];
+    load_taps<T, V, W>(p, c0, w, bias);
     Span sp{0, p.rows, 0};
-    for (int64_t t = t0; t < t1; ++t) {
-        if (t == t0 || t >= sp.end) {
-            sp = span_at(p.offsets, p.num_segments, b, p.rows, t);
-            if (sp.begin <= t) {
+    for (int64_t s = t0; s < t1; s += kConvGroup) {
+        Pack<T, V> now[kConvGroup];
 #pragma unroll
-                for (int j = 1; j < W; ++j) {  // row t - j, or the state row that stands for it
-                    const int64_t r = t - j;
+        for (int i = 0; i < kConvGroup; ++i) now[i] = next[i];
+        if (s + kConvGroup < t1) load(s + kConvGroup);
 #pragma unroll
-                    for (int i = 0; i < V; ++i) win[j - 1][i] = 0.0f;
-                    if (j <= halo) {
-                        if (r >= sp.begin) load_f32<V>(win[j - 1], x + r * p.x_row);
-                        else if (init)
-                            load_f32<V>(win[j - 1], init + (int64_t(sp.seg) * halo + (r - sp.begin + halo)) * p.channels + c0);
-                    }
-                }
+        for (int i = 0; i < kConvGroup; ++i) {
+            const int64_t t = s + i;
+            if (t >= t1) break;
+            if (t == t0 || t >= sp.end) {
+                sp = span_at(p.offsets, p.num_segments, b, p.rows, t);
+                if (sp.begin <= t) load_window<T, V, W>(p, sp, x, t, c0, win);
             }
-        }
-        if (sp.begin > t) continue;  // outside every segment: left unwritten
+            if (sp.begin > t) continue;  // outside every segment: left unwritten
+            float o[V];
 #pragma unroll
-        for (int j = W - 1; j > 0; --j)
+            for (int k = 0; k < V; ++k) o[k] = to_f32<T>(now[i].e[k]);
+            push<V, W>(win, o);
 #pragma unroll
-            for (int i = 0; i < V; ++i) win[j][i] = win[j - 1][i];
-        load_f32<V>(win[0], x + t * p.x_row);
-        float o[V];
+            for (int k = 0; k < V; ++k) {
+                float a = bias[k];
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            float a = bias[i];
+                for (int j = 0; j < W; ++j) a = fmaf(w[j][k], win[j][k], a);
+                o[k] = p.silu ? silu(a) : a;
+            }
+            store_f32<V>(y + t * p.y_row, o);
+            if (fin && t == sp.end - 1) {
 #pragma unroll
-            for (int j = 0; j < W; ++j) a = fmaf(w[j][i], win[j][i], a);
-            o[i] = p.silu ? silu(a) : a;
-        }
-        store_f32<V>(y + t * p.y_row, o);
-        if (fin && t == sp.end - 1) {
-#pragma unroll
-            for (int j = 0; j < W; ++j)
-                if (j < halo)
-                    store_f32<V>(fin + (int64_t(sp.seg) * halo + (halo - 1 - j)) * p.channels + c0, win[j]);
+                for (int j = 0; j < W; ++j)
+                    if (j < halo)
+                        store_f32<V>(fin + (int64_t(sp.seg) * halo + (halo - 1 - j)) * p.channels + c0, win[j]);
+            }
         }
     }
 }
@@ -107,9 +153,9 @@ __global__ void __launch_bounds__(kConvThreads)
     empty_state_kernel(const uint32_t *offsets, int64_t count, const T *src, T *dst) {
     pdl_trigger();
     pdl_wait();
-    const uint32_t s = blockIdx.x;
+    const int64_t s = blockIdx.x;
     if (offsets && offsets[s] < offsets[s + 1]) return;
-    for (int64_t i = threadIdx.x; i < count; i += kConvThreads)
+    for (int64_t i = int64_t(blockIdx.y) * kConvThreads + threadIdx.x; i < count; i += int64_t(gridDim.y) * kConvThreads)
         dst[s * count + i] = src ? src[s * count + i] : from_f32<T>(0.0f);
 }
 
@@ -133,21 +179,24 @@ __global__ void __launch_bounds__(kConvThreads) conv_backward_kernel(ConvBackwar
     const int64_t te = min(t1 + p.width - 1, p.rows);
     const int halo = p.width - 1;
 
-    float w[W][V], bias[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-#pragma unroll
-        for (int j = 0; j < W; ++j)
-            w[j][i] = j <= halo ? load_param<T>(p.weight, (c0 + i) * p.width + (halo - j), p.weight_f32) : 0.0f;
-        bias[i] = p.bias ? load_param<T>(p.bias, c0 + i, p.weight_f32) : 0.0f;
-    }
     const T *x = static_cast<const T *>(p.x) + int64_t(b) * p.x_batch + c0;
     const T *dy = static_cast<const T *>(q.grad_out) + int64_t(b) * q.grad_batch + c0;
     T *dx = static_cast<T *>(q.grad_x) + int64_t(b) * q.gx_batch + c0;
-    const T *init = static_cast<const T *>(p.initial_state);
     T *dinit = static_cast<T *>(q.grad_initial);
     const T *dfin = static_cast<const T *>(q.grad_final);
 
+    Pack<T, V> nx[kConvGroup], ng[kConvGroup];
+    auto load = [&](int64_t t) {  // rows past the last are read as the last
+#pragma unroll
+        for (int i = 0; i < kConvGroup; ++i) {
+            const int64_t r = min(t + i, te - 1);
+            nx[i] = *reinterpret_cast<const Pack<T, V> *>(x + r * p.x_row);
+            ng[i] = *reinterpret_cast<const Pack<T, V> *>(dy + r * q.grad_row);
+        }
+    };
+    load(t0);
+    float w[W][V], bias[V];
+    load_taps<T, V, W>(p, c0, w, bias);
     float win[W][V], acc[W][V], dw[W][V], db[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -165,64 +214,66 @@ __global__ void __launch_bounds__(kConvThreads) conv_backward_kernel(ConvBackwar
             store_f32<V>(dinit + (int64_t(sp.seg) * halo + (r - sp.begin + halo)) * p.channels + c0, v);
         }
     };
-    for (int64_t t = t0; t < te; ++t) {
-        if (t == t0 || t >= sp.end) {
-            sp = span_at(p.offsets, p.num_segments, b, p.rows, t);
-            if (sp.begin <= t) {
-                if (t >= t1) {
-                    if (sp.begin == t) break;  // a segment of the next strip
-                }
+    bool over = false;  // a segment of the next strip begins
+    for (int64_t s = t0; s < te && !over; s += kConvGroup) {
+        Pack<T, V> cx[kConvGroup], cg[kConvGroup];
 #pragma unroll
-                for (int j = 1; j < W; ++j) {
-                    const int64_t r = t - j;
+        for (int i = 0; i < kConvGroup; ++i) cx[i] = nx[i], cg[i] = ng[i];
+        if (s + kConvGroup < te) load(s + kConvGroup);
 #pragma unroll
-                    for (int i = 0; i < V; ++i) win[j - 1][i] = 0.0f, acc[j - 1][i] = 0.0f;
-                    if (j <= halo) {
-                        if (r >= sp.begin) load_f32<V>(win[j - 1], x + r * p.x_row);
-                        else if (init)
-                            load_f32<V>(win[j - 1], init + (int64_t(sp.seg) * halo + (r - sp.begin + halo)) * p.channels + c0);
+        for (int i = 0; i < kConvGroup; ++i) {
+            const int64_t t = s + i;
+            if (t >= te || over) break;
+            if (t == t0 || t >= sp.end) {
+                sp = span_at(p.offsets, p.num_segments, b, p.rows, t);
+                if (sp.begin <= t) {
+                    if (t >= t1 && sp.begin == t) {
+                        over = true;
+                        break;
                     }
+                    load_window<T, V, W>(p, sp, x, t, c0, win);
+#pragma unroll
+                    for (int j = 0; j < W; ++j)
+#pragma unroll
+                        for (int k = 0; k < V; ++k) acc[j][k] = 0.0f;
                 }
             }
-        }
-        if (sp.begin > t) continue;
+            if (sp.begin > t) continue;
+            float xv[V], g[V], none[V];
 #pragma unroll
-        for (int j = W - 1; j > 0; --j)
+            for (int k = 0; k < V; ++k) xv[k] = to_f32<T>(cx[i].e[k]), g[k] = to_f32<T>(cg[i].e[k]), none[k] = 0.0f;
+            push<V, W>(win, xv);
+            push<V, W>(acc, none);
 #pragma unroll
-            for (int i = 0; i < V; ++i) win[j][i] = win[j - 1][i], acc[j][i] = acc[j - 1][i];
-        load_f32<V>(win[0], x + t * p.x_row);
-        float g[V];
-        load_f32<V>(g, dy + t * q.grad_row);
+            for (int k = 0; k < V; ++k) {
+                float a = bias[k];
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            float a = bias[i];
+                for (int j = 0; j < W; ++j) a = fmaf(w[j][k], win[j][k], a);
+                if (p.silu) g[k] *= silu_slope(a);
 #pragma unroll
-            for (int j = 0; j < W; ++j) a = fmaf(w[j][i], win[j][i], a);
-            if (p.silu) g[i] *= silu_slope(a);
-            acc[0][i] = 0.0f;
+                for (int j = 0; j < W; ++j) acc[j][k] = fmaf(w[j][k], g[k], acc[j][k]);
+                if (t < t1) {
+                    db[k] += g[k];
 #pragma unroll
-            for (int j = 0; j < W; ++j) acc[j][i] = fmaf(w[j][i], g[i], acc[j][i]);
-            if (t < t1) {
-                db[i] += g[i];
-#pragma unroll
-                for (int j = 0; j < W; ++j) dw[j][i] = fmaf(g[i], win[j][i], dw[j][i]);
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < W; ++j)
-            if (j == halo) put(t - j, acc[j]);
-        if (t == sp.end - 1) {  // the rows that no later row of the segment reaches
-#pragma unroll
-            for (int j = 0; j < W - 1; ++j)
-                if (j < halo) {
-                    float v[V];
-#pragma unroll
-                    for (int i = 0; i < V; ++i) v[i] = 0.0f;
-                    if (dfin) load_f32<V>(v, dfin + (int64_t(sp.seg) * halo + (halo - 1 - j)) * p.channels + c0);
-#pragma unroll
-                    for (int i = 0; i < V; ++i) v[i] += acc[j][i];
-                    put(t - j, v);
+                    for (int j = 0; j < W; ++j) dw[j][k] = fmaf(g[k], win[j][k], dw[j][k]);
                 }
+            }
+#pragma unroll
+            for (int j = 0; j < W; ++j)
+                if (j == halo) put(t - j, acc[j]);
+            if (t == sp.end - 1) {  // the rows that no later row of the segment reaches
+#pragma unroll
+                for (int j = 0; j < W - 1; ++j)
+                    if (j < halo) {
+                        float v[V];
+#pragma unroll
+                        for (int k = 0; k < V; ++k) v[k] = 0.0f;
+                        if (dfin) load_f32<V>(v, dfin + (int64_t(sp.seg) * halo + (halo - 1 - j)) * p.channels + c0);
+#pragma unroll
+                        for (int k = 0; k < V; ++k) v[k] += acc[j][k];
+                        put(t - j, v);
+                    }
+            }
         }
     }
     float *part = q.partial + (int64_t(blockIdx.x) * (p.width + 1)) * p.channels + c0;
@@ -300,7 +351,9 @@ cudaError_t conv_step_w(const ConvStepParams &p, cudaStream_t s) {
 template <class T>
 cudaError_t empty_states(const uint32_t *offsets, int64_t segments, int64_t count, const void *src, void *dst,
                          cudaStream_t s) {
-    return launch_pdl(empty_state_kernel<T>, dim3(uint32_t(segments)), dim3(kConvThreads), 0, s, offsets, count,
+    const int64_t spread = (count + kConvThreads - 1) / kConvThreads;  // few segments: many blocks to each
+    const uint32_t per = uint32_t(segments >= 1024 ? 1 : spread < 1024 / segments ? spread : 1024 / segments);
+    return launch_pdl(empty_state_kernel<T>, dim3(uint32_t(segments), per), dim3(kConvThreads), 0, s, offsets, count,
                       static_cast<const T *>(src), static_cast<T *>(dst));
 }
 

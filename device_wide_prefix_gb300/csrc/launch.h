@@ -108,7 +108,7 @@ cudaError_t launch_recurrence(const float *a, const float *b, float *h, uint64_t
 struct ConvParams {
     int64_t channels, batch, rows, strips;  // strips: blocks of rows per batch entry
     int width, silu;
-    bool weight_f32;
+    bool weight_f32, weight_wide;  // wide: weight starts on 16 bytes
     const void *x, *weight, *bias, *initial_state;
     void *y, *final_state;
     int64_t x_batch, x_row, y_batch, y_row;

@@ -48,8 +48,8 @@ __device__ __forceinline__ void store_residual(void *p, int64_t i, const float (
     else store_f32<V>(static_cast<T *>(p) + i, f);
 }
 
-template <class T, int V, int K>
-__global__ void __launch_bounds__(1024) norm_kernel(NormParams p) {
+template <class T, int V, int K, int kMost>
+__global__ void __launch_bounds__(kMost, 1) norm_kernel(NormParams p) {
     __shared__ float sh[32];
     pdl_trigger();
     pdl_wait();
@@ -58,7 +58,8 @@ __global__ void __launch_bounds__(1024) norm_kernel(NormParams p) {
     const T *x = static_cast<const T *>(p.x) + row * p.x_row + g0;
     const T *z = p.gate ? static_cast<const T *>(p.gate) + row * p.gate_row + g0 : nullptr;
     T *y = static_cast<T *>(p.y) + row * p.y_row + g0;
-    float v[K][V], gt[K][V], ss[1] = {0.0f};
+    // every load first: a store between them would hold the later ones back
+    float v[K][V], gt[K][V], sc[K][V], w[K][V], ss[1] = {0.0f};
 #pragma unroll
     for (int k = 0; k < K; ++k) {
         const int64_t i = (int64_t(k) * blockDim.x + threadIdx.x) * V;
@@ -66,17 +67,25 @@ __global__ void __launch_bounds__(1024) norm_kernel(NormParams p) {
         for (int j = 0; j < V; ++j) v[k][j] = 0.0f, gt[k][j] = 1.0f;
         if (i < p.group) {
             load_f32<V>(v[k], x + i);
-            if (p.residual) {
-                float r[V];
-                load_residual<T, V>(r, p.residual, row * p.residual_row + g0 + i, p.residual_f32);
+            if (p.residual) load_residual<T, V>(sc[k], p.residual, row * p.residual_row + g0 + i, p.residual_f32);
+            if (z) load_f32<V>(gt[k], z + i);
+            load_params<T, V>(w[k], p.weight, g0 + i, p.weight_f32);
+        }
+    }
 #pragma unroll
-                for (int j = 0; j < V; ++j)
-                    v[k][j] = p.scale ? fmaf(load_param<T>(p.scale, g0 + i + j, p.weight_f32), v[k][j], r[j])
-                                      : v[k][j] + r[j];
+    for (int k = 0; k < K; ++k) {
+        const int64_t i = (int64_t(k) * blockDim.x + threadIdx.x) * V;
+        if (i < p.group) {
+            if (p.residual) {
+                float s[V];
+#pragma unroll
+                for (int j = 0; j < V; ++j) s[j] = 1.0f;
+                if (p.scale) load_params<T, V>(s, p.scale, g0 + i, p.weight_f32);
+#pragma unroll
+                for (int j = 0; j < V; ++j) v[k][j] = fmaf(s[j], v[k][j], sc[k][j]);
                 store_residual<T, V>(p.sum, row * p.sum_row + g0 + i, v[k], p.residual_f32);
             }
             if (z) {
-                load_f32<V>(gt[k], z + i);
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
                     gt[k][j] = silu(gt[k][j]);
@@ -96,7 +105,7 @@ __global__ void __launch_bounds__(1024) norm_kernel(NormParams p) {
             float o[V];
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                o[j] = v[k][j] * r * load_param<T>(p.weight, g0 + i + j, p.weight_f32);
+                o[j] = v[k][j] * r * w[k][j];
                 if (p.gate_after) o[j] *= gt[k][j];
             }
             store_f32<V>(y + i, o);
@@ -111,97 +120,111 @@ __global__ void __launch_bounds__(1024) norm_kernel(NormParams p) {
 // group's columns and walks rows blockIdx.x, + gridDim.x, ..., so the column
 // sums stay in registers; each block writes its share and a second kernel
 // adds the shares in a fixed order.
+//
+// A thread holds the raw values of its columns of one row, and loads the next
+// row's before it waits for the block's sums.
 template <class T, int V, int K>
-__global__ void __launch_bounds__(K *V >= 16 ? 512 : 1024) norm_backward_kernel(NormBackwardParams q) {
+struct NormRow {
+    Pack<float, V> v32[K];  // the norm's input in f32, or
+    Pack<T, V> v[K];        // in the activations' type
+    Pack<T, V> dy[K], gate[K];
+};
+
+template <class T, int V, int K, bool kWideV>
+__global__ void __launch_bounds__(512, 1) norm_backward_kernel(NormBackwardParams q) {
     __shared__ float sh[64];
     pdl_trigger();
     pdl_wait();
     const NormParams &p = q.n;
     const int64_t g0 = int64_t(blockIdx.y) * p.group;
-    float dw[K][V], ds[K][V];
+    const bool gated = p.gate != nullptr;
+    float dw[K][V], ds[K][V], w[K][V];
+    int at[K];  // this thread's columns; past the group they are read from its start and not used
+    bool in[K];
 #pragma unroll
-    for (int k = 0; k < K; ++k)
+    for (int k = 0; k < K; ++k) {
+        const int i = (k * int(blockDim.x) + int(threadIdx.x)) * V;
+        in[k] = i < p.group, at[k] = int(g0) + (in[k] ? i : 0);
+        load_params<T, V>(w[k], p.weight, at[k], p.weight_f32);
 #pragma unroll
         for (int j = 0; j < V; ++j) dw[k][j] = ds[k][j] = 0.0f;
-    for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
-        const T *dy = static_cast<const T *>(q.grad_out) + row * q.grad_row + g0;
-        const T *z = p.gate ? static_cast<const T *>(p.gate) + row * p.gate_row + g0 : nullptr;
-        float t[K][V], gw[K][V], red[2] = {0.0f, 0.0f};
+    }
+    auto load = [&](NormRow<T, V, K> &r, int64_t row) {
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int64_t i = (int64_t(k) * blockDim.x + threadIdx.x) * V;
-#pragma unroll
-            for (int j = 0; j < V; ++j) t[k][j] = gw[k][j] = 0.0f;
-            if (i < p.group) {
-                load_residual<T, V>(t[k], q.v, row * q.v_row + g0 + i, q.v_f32);
-                load_f32<V>(gw[k], dy + i);
-                float gt[V];
-                if (z) load_f32<V>(gt, z + i);
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    const float s = z ? silu(gt[j]) : 1.0f;
-                    if (z && !p.gate_after) t[k][j] *= s;
-                    if (z && p.gate_after) gw[k][j] *= s;
-                    gw[k][j] *= load_param<T>(p.weight, g0 + i + j, p.weight_f32);
-                    red[0] = fmaf(t[k][j], t[k][j], red[0]);
-                    red[1] = fmaf(gw[k][j], t[k][j], red[1]);
-                }
-            }
+            if (kWideV)
+                r.v32[k] = *reinterpret_cast<const Pack<float, V> *>(static_cast<const float *>(q.v) + row * q.v_row + at[k]);
+            else r.v[k] = *reinterpret_cast<const Pack<T, V> *>(static_cast<const T *>(q.v) + row * q.v_row + at[k]);
+            r.dy[k] = *reinterpret_cast<const Pack<T, V> *>(static_cast<const T *>(q.grad_out) + row * q.grad_row + at[k]);
+            if (gated)
+                r.gate[k] = *reinterpret_cast<const Pack<T, V> *>(static_cast<const T *>(p.gate) + row * p.gate_row + at[k]);
         }
+    };
+    NormRow<T, V, K> now, next;
+    if (int64_t(blockIdx.x) < p.rows) load(next, blockIdx.x);
+    for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+        now = next;
+        load(next, min(row + gridDim.x, p.rows - 1));
+        auto vin = [&](int k, int j) { return kWideV ? now.v32[k].e[j] : to_f32<T>(now.v[k].e[j]); };
+        float red[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                float t = in[k] ? vin(k, j) : 0.0f, gw = to_f32<T>(now.dy[k].e[j]) * w[k][j];
+                if (gated) (p.gate_after ? gw : t) *= silu(to_f32<T>(now.gate[k].e[j]));
+                red[0] = fmaf(t, t, red[0]);
+                red[1] = fmaf(gw, t, red[1]);
+            }
         block_sums(red, sh);
         const float r = rsqrtf(red[0] / float(p.group) + p.eps);
         const float m = red[1] * r / float(p.group) * r;  // mean(gw h) r: dt = r gw - t r m
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int64_t i = (int64_t(k) * blockDim.x + threadIdx.x) * V;
-            if (i < p.group) {
-                float g[V], gt[V], dz[V], xs[V], dv[V];
-                load_f32<V>(g, dy + i);
-                if (z) load_f32<V>(gt, z + i);
-                float vin[V];
-                if (z && !p.gate_after) load_residual<T, V>(vin, q.v, row * q.v_row + g0 + i, q.v_f32);
-                if (q.x_in) load_f32<V>(xs, static_cast<const T *>(q.x_in) + row * q.xin_row + g0 + i);
-                float dr[V];
-                if (q.grad_sum) load_residual<T, V>(dr, q.grad_sum, row * q.gsum_row + g0 + i, q.v_f32);
+            if (!in[k]) continue;
+            float dz[V], dv[V], add[V], xs[V];
+            if (q.grad_sum) load_residual<T, V>(add, q.grad_sum, row * q.gsum_row + at[k], q.v_f32);
+            if (q.x_in) load_f32<V>(xs, static_cast<const T *>(q.x_in) + row * q.xin_row + at[k]);
 #pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    const float w = load_param<T>(p.weight, g0 + i + j, p.weight_f32);
-                    const float h = t[k][j] * r;
-                    float d = r * fmaf(-t[k][j], m, gw[k][j]);
-                    if (z && p.gate_after) {
-                        dz[j] = g[j] * h * w * silu_slope(gt[j]);
-                        dw[k][j] = fmaf(g[j] * silu(gt[j]), h, dw[k][j]);
-                    } else {
-                        dw[k][j] = fmaf(g[j], h, dw[k][j]);
-                    }
-                    if (z && !p.gate_after) {
-                        dz[j] = d * vin[j] * silu_slope(gt[j]);
-                        d *= silu(gt[j]);
-                    }
-                    if (q.grad_sum) d += dr[j];
-                    dv[j] = d;
-                    if (q.x_in) ds[k][j] = fmaf(d, xs[j], ds[k][j]);
+            for (int j = 0; j < V; ++j) {
+                const float v = vin(k, j), zv = gated ? to_f32<T>(now.gate[k].e[j]) : 0.0f;
+                const float s = gated ? silu(zv) : 1.0f;
+                float g = to_f32<T>(now.dy[k].e[j]), t = v;
+                if (gated && !p.gate_after) t *= s;
+                const float h = t * r;
+                if (gated && p.gate_after) {
+                    dz[j] = g * h * w[k][j] * silu_slope(zv);
+                    g *= s;
                 }
-                if (z) store_f32<V>(static_cast<T *>(q.grad_gate) + row * q.ggate_row + g0 + i, dz);
-                if (q.grad_residual)
-                    store_residual<T, V>(q.grad_residual, row * q.gres_row + g0 + i, dv, q.v_f32);
-                if (q.grad_x) {
+                dw[k][j] = fmaf(g, h, dw[k][j]);
+                float d = r * fmaf(-t, m, g * w[k][j]);
+                if (gated && !p.gate_after) {
+                    dz[j] = d * v * silu_slope(zv);
+                    d *= s;
+                }
+                if (q.grad_sum) d += add[j];
+                dv[j] = d;
+                if (q.x_in) ds[k][j] = fmaf(d, xs[j], ds[k][j]);
+            }
+            if (gated) store_f32<V>(static_cast<T *>(q.grad_gate) + row * q.ggate_row + at[k], dz);
+            if (q.grad_residual) store_residual<T, V>(q.grad_residual, row * q.gres_row + at[k], dv, q.v_f32);
+            if (q.grad_x) {
+                if (p.scale) {
+                    float s[V];
+                    load_params<T, V>(s, p.scale, at[k], p.weight_f32);
 #pragma unroll
-                    for (int j = 0; j < V; ++j)
-                        if (p.scale) dv[j] *= load_param<T>(p.scale, g0 + i + j, p.weight_f32);
-                    store_f32<V>(static_cast<T *>(q.grad_x) + row * q.gx_row + g0 + i, dv);
+                    for (int j = 0; j < V; ++j) dv[j] *= s[j];
                 }
+                store_f32<V>(static_cast<T *>(q.grad_x) + row * q.gx_row + at[k], dv);
             }
         }
     }
-    float *part = q.partial + int64_t(blockIdx.x) * (q.x_in ? 2 : 1) * p.channels + g0;
+    float *part = q.partial + int64_t(blockIdx.x) * (q.x_in ? 2 : 1) * p.channels;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-        const int64_t i = (int64_t(k) * blockDim.x + threadIdx.x) * V;
-        if (i < p.group) {
-            store_f32<V>(part + i, dw[k]);
-            if (q.x_in) store_f32<V>(part + p.channels + i, ds[k]);
-        }
+        if (!in[k]) continue;
+        store_f32<V>(part + at[k], dw[k]);
+        if (q.x_in) store_f32<V>(part + p.channels + at[k], ds[k]);
     }
 }
 
@@ -211,25 +234,48 @@ uint32_t threads_for(int64_t n, int v, int k) {
     return uint32_t((need + 31) / 32 * 32);
 }
 
-template <class T, int V>
-cudaError_t norm_v(const NormParams &p, cudaStream_t s) {
-    const dim3 grid(uint32_t(p.rows * p.groups));
-    if (threads_for(p.group, V, 2) <= 512)
-        return launch_pdl(norm_kernel<T, V, 2>, grid, dim3(threads_for(p.group, V, 2)), 0, s, p);
-    if (threads_for(p.group, V, 4) <= 1024)
-        return launch_pdl(norm_kernel<T, V, 4>, grid, dim3(threads_for(p.group, V, 4)), 0, s, p);
-    return launch_pdl(norm_kernel<T, V, 16>, grid, dim3(threads_for(p.group, V, 16)), 0, s, p);
+// The fewest accesses a thread that a block of kMost threads allows.
+template <class T, int V, int K, int kMost>
+cudaError_t norm_k(const NormParams &p, cudaStream_t s) {
+    return launch_pdl(norm_kernel<T, V, K, kMost>, dim3(uint32_t(p.rows * p.groups)), dim3(threads_for(p.group, V, K)), 0,
+                      s, p);
 }
 
 template <class T, int V>
+cudaError_t norm_v(const NormParams &p, cudaStream_t s) {
+    if constexpr (V == 1) {
+        if (p.group <= 1024) return norm_k<T, 1, 2, 512>(p, s);
+        if (p.group <= 4096) return norm_k<T, 1, 8, 512>(p, s);
+        return norm_k<T, 1, 16, 1024>(p, s);
+    } else {
+        if (p.group <= 512 * V) return norm_k<T, V, 1, 512>(p, s);
+        if (p.group <= 1024 * V) return norm_k<T, V, 2, 512>(p, s);
+        return norm_k<T, V, 32 / V, 512>(p, s);
+    }
+}
+
+template <class T, int V, bool kWideV>
 cudaError_t norm_backward_v(const NormBackwardParams &q, cudaStream_t s) {
     const NormParams &p = q.n;
     const dim3 grid(uint32_t(q.blocks), uint32_t(p.groups));
-    const uint32_t most = V * 2 >= 16 ? 512 : 1024;
-    if (threads_for(p.group, V, 2) <= most)
-        return launch_pdl(norm_backward_kernel<T, V, 2>, grid, dim3(threads_for(p.group, V, 2)), 0, s, q);
-    return launch_pdl(norm_backward_kernel<T, V, 4 * (8 / V)>, grid, dim3(threads_for(p.group, V, 4 * (8 / V))), 0, s,
-                      q);
+    auto go = [&](auto kernel, int k) {
+        return launch_pdl(kernel, grid, dim3(threads_for(p.group, V, k)), 0, s, q);
+    };
+    if constexpr (V == 1) {
+        if (p.group <= 1024) return go(norm_backward_kernel<T, 1, 2, kWideV>, 2);
+        if (p.group <= 4096) return go(norm_backward_kernel<T, 1, 8, kWideV>, 8);
+        return go(norm_backward_kernel<T, 1, 32, kWideV>, 32);
+    } else {
+        if (p.group <= 512 * V) return go(norm_backward_kernel<T, V, 1, kWideV>, 1);
+        if (p.group <= 1024 * V) return go(norm_backward_kernel<T, V, 2, kWideV>, 2);
+        return go(norm_backward_kernel<T, V, 32 / V, kWideV>, 32 / V);
+    }
+}
+
+template <class T, int V>
+cudaError_t norm_backward_t(const NormBackwardParams &q, cudaStream_t s) {
+    if (sizeof(T) == 4 || !q.v_f32) return norm_backward_v<T, V, false>(q, s);
+    return norm_backward_v<T, V, true>(q, s);
 }
 
 constexpr int kColThreads = 256;
@@ -277,9 +323,9 @@ cudaError_t launch_norm(dwp_dtype t, const NormParams &p, bool vec, cudaStream_t
 }
 
 cudaError_t launch_norm_backward(dwp_dtype t, const NormBackwardParams &p, bool vec, cudaStream_t s) {
-    if (t == DWP_F32) return vec ? norm_backward_v<float, 4>(p, s) : norm_backward_v<float, 1>(p, s);
-    if (t == DWP_BF16) return vec ? norm_backward_v<__nv_bfloat16, 8>(p, s) : norm_backward_v<__nv_bfloat16, 1>(p, s);
-    return vec ? norm_backward_v<__half, 8>(p, s) : norm_backward_v<__half, 1>(p, s);
+    if (t == DWP_F32) return vec ? norm_backward_t<float, 4>(p, s) : norm_backward_t<float, 1>(p, s);
+    if (t == DWP_BF16) return vec ? norm_backward_t<__nv_bfloat16, 8>(p, s) : norm_backward_t<__nv_bfloat16, 1>(p, s);
+    return vec ? norm_backward_t<__half, 8>(p, s) : norm_backward_t<__half, 1>(p, s);
 }
 
 }  // namespace dwp

@@ -49,6 +49,8 @@ __device__ __forceinline__ float rcp(float x) {
     return y;
 }
 
+__device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 // z * sigmoid(z); for z far below 0 the exponential is +inf and the product 0.
 __device__ __forceinline__ float gate_of(float z) { return z * rcp(1.0f + ex2(z * -kLog2e)); }
 

@@ -57,17 +57,34 @@ __global__ void __launch_bounds__(32, 8) selscan_backward_kernel(ScanBackwardPar
     // state pair j of this lane is pair j ^ flip of its NT states
     const int flip = kP == 4 ? (pair & 1) * 2 + (pair >> 1 & 1) : pair & 1;
 
-    F2 A[2][kP], e[2][kP], dA[2][kP], h[2][kP];
+    F2 A2[2][kP], e[2][kP], dA[2][kP], h[2][kP];
+    const F2 zero = f2(0.0f, 0.0f);
+    const bool whole = p.states == kN && p.states_wide;  // every state is live, in aligned pairs
     auto load_state = [&](F2(&v)[2][kP], const float *from, int64_t i) {
+        if (!from) {
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
+            for (int c = 0; c < 2; ++c)
 #pragma unroll
-            for (int j = 0; j < kP; ++j) {
-                const int n = n0 + 2 * (j ^ flip), ch = c ? other : own;
-                const float *x = from + (i * p.channels + cb + ch) * p.states + n;
-                v[c][j] = f2(from && ch < live && n < p.states ? x[0] : 0.0f,
-                             from && ch < live && n + 1 < p.states ? x[1] : 0.0f);
+                for (int j = 0; j < kP; ++j) v[c][j] = zero;
+            return;
+        }
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {  // a channel past the last takes the last's
+            const float *x = from + (i * p.channels + cb + min(c ? other : own, live - 1)) * p.states + n0;
+            if (whole) {
+#pragma unroll
+                for (int j = 0; j < kP; ++j) {
+                    const float2 s = *reinterpret_cast<const float2 *>(x + 2 * (j ^ flip));
+                    v[c][j] = f2(s.x, s.y);
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < kP; ++j) {
+                    const int n = 2 * (j ^ flip);
+                    v[c][j] = f2(n0 + n < p.states ? x[n] : 0.0f, n0 + n + 1 < p.states ? x[n + 1] : 0.0f);
+                }
             }
+        }
     };
     auto save_state = [&](float *to, int64_t i, const F2(&v)[2][kP]) {
 #pragma unroll
@@ -81,10 +98,13 @@ __global__ void __launch_bounds__(32, 8) selscan_backward_kernel(ScanBackwardPar
                 if (ch < live && n + 1 < p.states) x[1] = s.y;
             }
     };
-    load_state(A, p.A, 0);
+    load_state(A2, p.A, 0);
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int j = 0; j < kP; ++j) A2[c][j] = mul2(A2[c][j], f2(kLog2e, kLog2e));
     if (chunk + 1 < p.chunks) load_state(e, p.carry, int64_t(b) * (p.chunks - 1) + (p.chunks - 2 - chunk));
     else load_state(e, p.segmap ? nullptr : q.grad_final, b);
-    const F2 zero = f2(0.0f, 0.0f);
 #pragma unroll
     for (int c = 0; c < 2; ++c)
 #pragma unroll
@@ -129,7 +149,7 @@ __global__ void __launch_bounds__(32, 8) selscan_backward_kernel(ScanBackwardPar
                 if (with_y) cv = sbc[r * kN + kN / 2 + (n0 / 2 + (j ^ flip))];
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    const float2 ar = unpack(mul2(dd[c], mul2(A[c][j], f2(kLog2e, kLog2e))));
+                    const float2 ar = unpack(mul2(dd[c], A2[c][j]));
                     h[c][j] = fma2(f2(ex2(ar.x), ex2(ar.y)), h[c][j], mul2(xx[c], f2(bv.x, bv.y)));
                     if (with_y) acc[c] = fma2(f2(cv.x, cv.y), h[c][j], acc[c]);
                 }
@@ -202,17 +222,19 @@ __global__ void __launch_bounds__(32, 8) selscan_backward_kernel(ScanBackwardPar
                     const F2 Bv = f2(bv.x, bv.y), Cv = f2(cv.x, cv.y);
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        const float2 ar = unpack(mul2(dd[c], mul2(A[c][j], f2(kLog2e, kLog2e))));
+                        const float2 ar = unpack(mul2(dd[c], A2[c][j]));
                         const F2 a = f2(ex2(ar.x), ex2(ar.y));
-                        // the state past the row, as the walk forward had it
-                        const F2 hr = fma2(a, hist[i][c][j], mul2(xx[c], Bv));
+                        // the state past the row: the next row's, unless that begins a segment
+                        const F2 hr = kLook         ? fma2(a, hist[i][c][j], mul2(xx[c], Bv))
+                                      : i + 1 < kSub ? hist[i + 1 < kSub ? i + 1 : i][c][j]
+                                                     : h[c][j];
                         const F2 dh = fma2(dy[c], Cv, e[c][j]);
                         vc[j] = c ? fma2(dy[c], hr, vc[j]) : mul2(dy[c], hr);
                         vb[j] = c ? fma2(dh, xx[c], vb[j]) : mul2(dh, xx[c]);
                         a1[c] = fma2(dh, Bv, a1[c]);
                         e[c][j] = mul2(dh, a);
                         const F2 w = mul2(e[c][j], hist[i][c][j]);
-                        a2[c] = fma2(w, A[c][j], a2[c]);
+                        a2[c] = fma2(w, A2[c][j], a2[c]);
                         dA[c][j] = fma2(w, dd[c], dA[c][j]);
                     }
                 }
@@ -228,7 +250,8 @@ __global__ void __launch_bounds__(32, 8) selscan_backward_kernel(ScanBackwardPar
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     const float2 v1 = unpack(a1[c]), v2 = unpack(a2[c]);
-                    sums[0][c] = v1.x + v1.y, sums[1][c] = v2.x + v2.y, sums[2][c] = y[i][c];
+                    sums[0][c] = v1.x + v1.y, sums[2][c] = y[i][c];
+                    sums[1][c] = (v2.x + v2.y) * 0.6931471805599453f;  // A = A2 ln 2
                 }
 #pragma unroll
                 for (int m = 0; m < 3; ++m) {
@@ -304,8 +327,17 @@ __global__ void __launch_bounds__(32, 8) selscan_backward_kernel(ScanBackwardPar
         uint32_t code = kRowOutside;
         if (lane < rows) code = p.segmap ? p.segmap[s0 + lane] : 0u;
         const bool plain = __all_sync(0xffffffffu, lane >= kTile || (code & (kRowHead | kRowTail)) == 0u);
+        if (s0 - kTile >= t0) {  // ask L2 for the rows of the next tile, and the state before it
+            const int64_t t = s0 - kTile + lane % kTile;
+            prefetch_l2(lane < kTile ? dt + t * p.dt_row : u + t * p.u_row);
+            prefetch_l2(lane < kTile ? z + t * z_row : go + t * q.grad_row);
+            prefetch_l2(lane < kTile ? B + t * p.b_row : C + t * p.c_row);
+            const float *x = p.checkpoints +
+                             ((int64_t(b) * p.tiles + s0 / kTile - 1) * p.channels + cb) * p.states;
+            for (int i = lane * 32; i < live * p.states; i += 32 * 32) prefetch_l2(x + i);
+        }
         // rows past the last are read as the last, and not used
-#pragma unroll
+#pragma unroll 8
         for (int m = 0; m < kMine; ++m) {
             const int r = mine_row + m * kMineRows;
             const int64_t t = min(s0 + r, t1 - 1);

@@ -49,8 +49,6 @@ struct Two<float> {
     __device__ __forceinline__ void load(const float *p, const float *q) { v = make_float2(*p, *q); }
 };
 
-__device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
-
 // What a walk computes.  kWalkOut: the scan.  kWalkStates: the first pass
 // over chunks, last states and sums of delta only.  kWalkBack: the same for
 // the gradient, whose recurrence runs from the last row to the first:

@@ -64,6 +64,13 @@ __device__ __forceinline__ float load_param(const void *p, uint64_t i, bool is_f
     return is_f32 ? static_cast<const float *>(p)[i] : to_f32<T>(static_cast<const T *>(p)[i]);
 }
 
+// V neighbouring parameters from i on, as one access.
+template <class T, int V>
+__device__ __forceinline__ void load_params(float (&f)[V], const void *p, uint64_t i, bool is_f32) {
+    if (is_f32) load_f32<V>(f, static_cast<const float *>(p) + i);
+    else load_f32<V>(f, static_cast<const T *>(p) + i);
+}
+
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

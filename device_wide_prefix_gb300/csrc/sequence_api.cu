@@ -171,6 +171,7 @@ ConvParams conv_params(const dwp_conv_args &a, int64_t strip) {
     ConvParams p = {};
     p.channels = a.channels, p.batch = a.batch, p.rows = a.rows, p.strips = ceil_div(a.rows, strip);
     p.width = int(a.width), p.silu = int(a.silu), p.weight_f32 = a.weight_dtype == DWP_F32;
+    p.weight_wide = aligned(a.weight, 16);
     p.x = a.x.data, p.weight = a.weight, p.bias = a.bias;
     p.initial_state = a.initial_state, p.final_state = a.final_state;
     p.y = a.out.data;
@@ -197,7 +198,7 @@ dwp_status conv_forward(const dwp_conv_args &a, cudaStream_t s) {
 
 // Rows of a strip of the gradient: long enough that the taps' partial sums
 // are a small share of the traffic.
-constexpr int64_t kGradStrip = 32;
+constexpr int64_t kGradStrip = 64;
 
 dwp_status conv_backward(const dwp_conv_backward_args &a, void *scratch, size_t *bytes, cudaStream_t s) {
     Check c;
@@ -523,8 +524,8 @@ void check_norm(Check &c, const dwp_norm_args &a) {
               a.channels / a.groups <= DWP_NORM_MAX_GROUP && a.rows >= 0 && a.rows <= kMaxRows &&
               a.rows * a.groups <= kMaxRows && a.eps >= 0.0);
     if (c.status != DWP_SUCCESS) return;
-    c.dense(a.weight, a.weight_dtype, a.channels, false, false);
-    c.dense(a.scale, a.weight_dtype, a.channels, false, true);
+    c.dense(a.weight, a.weight_dtype, a.channels, false, false, &c.bits);
+    c.dense(a.scale, a.weight_dtype, a.channels, false, true, &c.bits);
 }
 
 NormParams norm_params(const dwp_norm_args &a) {
@@ -559,10 +560,15 @@ dwp_status norm_forward(const dwp_norm_args &a, cudaStream_t s) {
     return launched(launch_norm(static_cast<dwp_dtype>(a.dtype), norm_params(a), c.wide(a.channels / a.groups, a.dtype), s));
 }
 
-// Blocks that share a group's rows in the gradient: enough to fill the GPU's
-// 152 SMs a few times over, few enough that their column sums are a small
-// share of the traffic.
-constexpr int64_t kNormBlocks = 608;
+// Blocks that share a group's rows in the gradient: enough threads to keep an
+// SM's registers busy (about 768 of them), few enough that the blocks' column
+// sums are a small share of the traffic.
+int64_t norm_blocks(const dwp_norm_args &a) {
+    const int64_t threads = ceil_div(ceil_div(a.channels / a.groups, 8), 32) * 32;
+    int64_t blocks = ceil_div(152 * 768, a.groups * (threads > 512 ? 512 : threads));
+    if (8 * blocks > a.rows) blocks = ceil_div(a.rows, 8);  // eight rows or more to each
+    return blocks;
+}
 
 dwp_status norm_backward(const dwp_norm_backward_args &a, void *scratch, size_t *bytes, cudaStream_t s) {
     Check c;
@@ -586,8 +592,7 @@ dwp_status norm_backward(const dwp_norm_backward_args &a, void *scratch, size_t 
     }
     c.dense(a.grad_weight, DWP_F32, f.channels, true, false);
     c.dense(a.grad_scale, DWP_F32, f.channels, true, true);
-    int64_t blocks = ceil_div(kNormBlocks, f.groups);
-    if (blocks > f.rows) blocks = f.rows;
+    const int64_t blocks = norm_blocks(f);
     const int64_t planes = f.scale ? 2 : 1;
     const size_t need = round16(size_t(blocks * planes * f.channels) * 4u);
     if (!c.scratch(scratch, bytes, need, &st)) return st;
