@@ -116,18 +116,10 @@ __global__ void __launch_bounds__(kConvThreads) conv_kernel(ConvParams p) {
 #pragma unroll
         for (int i = 0; i < kConvGroup; ++i) now[i] = next[i];
         if (s + kConvGroup < t1) load(s + kConvGroup);
-#pragma unroll
-        for (int i = 0; i < kConvGroup; ++i) {
-            const int64_t t = s + i;
-            if (t >= t1) break;
-            if (t == t0 || t >= sp.end) {
-                sp = span_at(p.offsets, p.num_segments, b, p.rows, t);
-                if (sp.begin <= t) load_window<T, V, W>(p, sp, x, t, c0, win);
-            }
-            if (sp.begin > t) continue;  // outside every segment: left unwritten
+        auto row = [&](int64_t t, const Pack<T, V> &xv) {
             float o[V];
 #pragma unroll
-            for (int k = 0; k < V; ++k) o[k] = to_f32<T>(now[i].e[k]);
+            for (int k = 0; k < V; ++k) o[k] = to_f32<T>(xv.e[k]);
             push<V, W>(win, o);
 #pragma unroll
             for (int k = 0; k < V; ++k) {
@@ -137,12 +129,29 @@ __global__ void __launch_bounds__(kConvThreads) conv_kernel(ConvParams p) {
                 o[k] = p.silu ? silu(a) : a;
             }
             store_f32<V>(y + t * p.y_row, o);
-            if (fin && t == sp.end - 1) {
+        };
+        if (s > t0 && s + kConvGroup <= t1 && sp.begin <= s && s + kConvGroup < sp.end) {  // inside one segment
 #pragma unroll
-                for (int j = 0; j < W; ++j)
-                    if (j < halo)
-                        store_f32<V>(fin + (int64_t(sp.seg) * halo + (halo - 1 - j)) * p.channels + c0, win[j]);
+            for (int i = 0; i < kConvGroup; ++i) row(s + i, now[i]);
+            continue;
+        }
+#pragma unroll 1
+        for (int64_t t = s; t < min(s + kConvGroup, t1); ++t) {
+            if (t == t0 || t >= sp.end) {
+                sp = span_at(p.offsets, p.num_segments, b, p.rows, t);
+                if (sp.begin <= t) load_window<T, V, W>(p, sp, x, t, c0, win);
             }
+            if (sp.begin <= t) {  // else outside every segment: left unwritten
+                row(t, now[0]);
+                if (fin && t == sp.end - 1) {
+#pragma unroll
+                    for (int j = 0; j < W; ++j)
+                        if (j < halo)
+                            store_f32<V>(fin + (int64_t(sp.seg) * halo + (halo - 1 - j)) * p.channels + c0, win[j]);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i + 1 < kConvGroup; ++i) now[i] = now[i + 1];
         }
     }
 }
@@ -220,10 +229,41 @@ __global__ void __launch_bounds__(kConvThreads) conv_backward_kernel(ConvBackwar
 #pragma unroll
         for (int i = 0; i < kConvGroup; ++i) cx[i] = nx[i], cg[i] = ng[i];
         if (s + kConvGroup < te) load(s + kConvGroup);
+        // row t: its p and g, and what g adds to the rows and taps; `mine`: a row of this strip
+        auto row = [&](const Pack<T, V> &xr, const Pack<T, V> &gr, bool mine) {
+            float xv[V], g[V], none[V];
 #pragma unroll
-        for (int i = 0; i < kConvGroup; ++i) {
-            const int64_t t = s + i;
-            if (t >= te || over) break;
+            for (int k = 0; k < V; ++k) xv[k] = to_f32<T>(xr.e[k]), g[k] = to_f32<T>(gr.e[k]), none[k] = 0.0f;
+            push<V, W>(win, xv);
+            push<V, W>(acc, none);
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+                float a = bias[k];
+#pragma unroll
+                for (int j = 0; j < W; ++j) a = fmaf(w[j][k], win[j][k], a);
+                if (p.silu) g[k] *= silu_slope(a, sigmoid(a));
+#pragma unroll
+                for (int j = 0; j < W; ++j) acc[j][k] = fmaf(w[j][k], g[k], acc[j][k]);
+                if (mine) {
+                    db[k] += g[k];
+#pragma unroll
+                    for (int j = 0; j < W; ++j) dw[j][k] = fmaf(g[k], win[j][k], dw[j][k]);
+                }
+            }
+        };
+        if (s - halo >= t0 && s + kConvGroup <= t1 && sp.begin <= s - halo && s + kConvGroup < sp.end) {
+            // inside one segment, and every finished row is this strip's
+#pragma unroll
+            for (int i = 0; i < kConvGroup; ++i) {
+                row(cx[i], cg[i], true);
+#pragma unroll
+                for (int j = 0; j < W; ++j)
+                    if (j == halo) store_f32<V>(dx + (s + i - j) * q.gx_row, acc[j]);
+            }
+            continue;
+        }
+#pragma unroll 1
+        for (int64_t t = s; t < min(s + kConvGroup, te); ++t) {
             if (t == t0 || t >= sp.end) {
                 sp = span_at(p.offsets, p.num_segments, b, p.rows, t);
                 if (sp.begin <= t) {
@@ -238,42 +278,27 @@ __global__ void __launch_bounds__(kConvThreads) conv_backward_kernel(ConvBackwar
                         for (int k = 0; k < V; ++k) acc[j][k] = 0.0f;
                 }
             }
-            if (sp.begin > t) continue;
-            float xv[V], g[V], none[V];
+            if (sp.begin <= t) {
+                row(cx[0], cg[0], t < t1);
 #pragma unroll
-            for (int k = 0; k < V; ++k) xv[k] = to_f32<T>(cx[i].e[k]), g[k] = to_f32<T>(cg[i].e[k]), none[k] = 0.0f;
-            push<V, W>(win, xv);
-            push<V, W>(acc, none);
+                for (int j = 0; j < W; ++j)
+                    if (j == halo) put(t - j, acc[j]);
+                if (t == sp.end - 1) {  // the rows that no later row of the segment reaches
 #pragma unroll
-            for (int k = 0; k < V; ++k) {
-                float a = bias[k];
+                    for (int j = 0; j < W - 1; ++j)
+                        if (j < halo) {
+                            float v[V];
 #pragma unroll
-                for (int j = 0; j < W; ++j) a = fmaf(w[j][k], win[j][k], a);
-                if (p.silu) g[k] *= silu_slope(a);
+                            for (int k = 0; k < V; ++k) v[k] = 0.0f;
+                            if (dfin) load_f32<V>(v, dfin + (int64_t(sp.seg) * halo + (halo - 1 - j)) * p.channels + c0);
 #pragma unroll
-                for (int j = 0; j < W; ++j) acc[j][k] = fmaf(w[j][k], g[k], acc[j][k]);
-                if (t < t1) {
-                    db[k] += g[k];
-#pragma unroll
-                    for (int j = 0; j < W; ++j) dw[j][k] = fmaf(g[k], win[j][k], dw[j][k]);
+                            for (int k = 0; k < V; ++k) v[k] += acc[j][k];
+                            put(t - j, v);
+                        }
                 }
             }
 #pragma unroll
-            for (int j = 0; j < W; ++j)
-                if (j == halo) put(t - j, acc[j]);
-            if (t == sp.end - 1) {  // the rows that no later row of the segment reaches
-#pragma unroll
-                for (int j = 0; j < W - 1; ++j)
-                    if (j < halo) {
-                        float v[V];
-#pragma unroll
-                        for (int k = 0; k < V; ++k) v[k] = 0.0f;
-                        if (dfin) load_f32<V>(v, dfin + (int64_t(sp.seg) * halo + (halo - 1 - j)) * p.channels + c0);
-#pragma unroll
-                        for (int k = 0; k < V; ++k) v[k] += acc[j][k];
-                        put(t - j, v);
-                    }
-            }
+            for (int i = 0; i + 1 < kConvGroup; ++i) cx[i] = cx[i + 1], cg[i] = cg[i + 1];
         }
     }
     float *part = q.partial + (int64_t(blockIdx.x) * (p.width + 1)) * p.channels + c0;

@@ -130,8 +130,8 @@ struct NormRow {
     Pack<T, V> dy[K], gate[K];
 };
 
-template <class T, int V, int K, bool kWideV>
-__global__ void __launch_bounds__(512, 1) norm_backward_kernel(NormBackwardParams q) {
+template <class T, int V, int K, bool kWideV, int kMost, int kBlocks>
+__global__ void __launch_bounds__(kMost, kBlocks) norm_backward_kernel(NormBackwardParams q) {
     __shared__ float sh[64];
     pdl_trigger();
     pdl_wait();
@@ -166,13 +166,17 @@ __global__ void __launch_bounds__(512, 1) norm_backward_kernel(NormBackwardParam
         now = next;
         load(next, min(row + gridDim.x, p.rows - 1));
         auto vin = [&](int k, int j) { return kWideV ? now.v32[k].e[j] : to_f32<T>(now.v[k].e[j]); };
-        float red[2] = {0.0f, 0.0f};
+        float red[2] = {0.0f, 0.0f}, sg[K][V];  // sg: sigmoid of the gate
 #pragma unroll
         for (int k = 0; k < K; ++k)
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 float t = in[k] ? vin(k, j) : 0.0f, gw = to_f32<T>(now.dy[k].e[j]) * w[k][j];
-                if (gated) (p.gate_after ? gw : t) *= silu(to_f32<T>(now.gate[k].e[j]));
+                if (gated) {
+                    const float zv = to_f32<T>(now.gate[k].e[j]);
+                    sg[k][j] = sigmoid(zv);
+                    (p.gate_after ? gw : t) *= zv * sg[k][j];
+                }
                 red[0] = fmaf(t, t, red[0]);
                 red[1] = fmaf(gw, t, red[1]);
             }
@@ -188,18 +192,18 @@ __global__ void __launch_bounds__(512, 1) norm_backward_kernel(NormBackwardParam
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 const float v = vin(k, j), zv = gated ? to_f32<T>(now.gate[k].e[j]) : 0.0f;
-                const float s = gated ? silu(zv) : 1.0f;
+                const float s = gated ? zv * sg[k][j] : 1.0f;
                 float g = to_f32<T>(now.dy[k].e[j]), t = v;
                 if (gated && !p.gate_after) t *= s;
                 const float h = t * r;
                 if (gated && p.gate_after) {
-                    dz[j] = g * h * w[k][j] * silu_slope(zv);
+                    dz[j] = g * h * w[k][j] * silu_slope(zv, sg[k][j]);
                     g *= s;
                 }
                 dw[k][j] = fmaf(g, h, dw[k][j]);
                 float d = r * fmaf(-t, m, g * w[k][j]);
                 if (gated && !p.gate_after) {
-                    dz[j] = d * v * silu_slope(zv);
+                    dz[j] = d * v * silu_slope(zv, sg[k][j]);
                     d *= s;
                 }
                 if (q.grad_sum) d += add[j];
@@ -262,13 +266,14 @@ cudaError_t norm_backward_v(const NormBackwardParams &q, cudaStream_t s) {
         return launch_pdl(kernel, grid, dim3(threads_for(p.group, V, k)), 0, s, q);
     };
     if constexpr (V == 1) {
-        if (p.group <= 1024) return go(norm_backward_kernel<T, 1, 2, kWideV>, 2);
-        if (p.group <= 4096) return go(norm_backward_kernel<T, 1, 8, kWideV>, 8);
-        return go(norm_backward_kernel<T, 1, 32, kWideV>, 32);
+        if (p.group <= 1024) return go(norm_backward_kernel<T, 1, 2, kWideV, 512, 1>, 2);
+        if (p.group <= 4096) return go(norm_backward_kernel<T, 1, 8, kWideV, 512, 1>, 8);
+        return go(norm_backward_kernel<T, 1, 32, kWideV, 512, 1>, 32);
     } else {
-        if (p.group <= 512 * V) return go(norm_backward_kernel<T, V, 1, kWideV>, 1);
-        if (p.group <= 1024 * V) return go(norm_backward_kernel<T, V, 2, kWideV>, 2);
-        return go(norm_backward_kernel<T, V, 32 / V, kWideV>, 32 / V);
+        if (p.group <= 128 * V) return go(norm_backward_kernel<T, V, 1, kWideV, 128, 6>, 1);
+        if (p.group <= 512 * V) return go(norm_backward_kernel<T, V, 1, kWideV, 512, 1>, 1);
+        if (p.group <= 1024 * V) return go(norm_backward_kernel<T, V, 2, kWideV, 512, 1>, 2);
+        return go(norm_backward_kernel<T, V, 32 / V, kWideV, 512, 1>, 32 / V);
     }
 }
 

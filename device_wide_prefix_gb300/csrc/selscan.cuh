@@ -43,16 +43,7 @@ __device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
     return r;
 }
 
-__device__ __forceinline__ float rcp(float x) {
-    float y;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 __device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
-
-// z * sigmoid(z); for z far below 0 the exponential is +inf and the product 0.
-__device__ __forceinline__ float gate_of(float z) { return z * rcp(1.0f + ex2(z * -kLog2e)); }
 
 // log(1 + e^x) = max(x, 0) + log1p(e^-|x|).  log1p(e) / e on [0, 1] is a
 // degree-8 polynomial fitted for the least relative error (3.0e-8; 1.8e-7

@@ -346,7 +346,7 @@ __global__ void __launch_bounds__(32, 8) selscan_backward_kernel(ScanBackwardPar
             const float x = d * to_f32<T>((u + t * p.u_row)[mine_at]);
             float dy = to_f32<T>((go + t * q.grad_row)[mine_at]);
             const float zv = to_f32<T>((z + t * z_row)[mine_at]);
-            if (p.z) dy *= gate_of(zv);
+            if (p.z) dy *= silu(zv);
             // a channel past the last adds nothing to dB and dC
             sd[r * kC + mine] = mine < live ? make_float2(d, x) : make_float2(0.0f, 0.0f);
             sg[r * kC + mine] = mine < live ? dy : 0.0f;
@@ -374,14 +374,14 @@ __global__ void __launch_bounds__(32, 8) selscan_backward_kernel(ScanBackwardPar
             const float uv = to_f32<T>((u + t * p.u_row)[mine]), q1 = s1[r * kC + mine], dy = sg[r * kC + mine];
             float dd = fmaf(q1, uv, s2[r * kC + mine]);
             // the slope of softplus
-            if (p.softplus) dd *= rcp(1.0f + ex2((to_f32<T>((dt + t * p.dt_row)[mine]) + bias) * -kLog2e));
+            if (p.softplus) dd *= sigmoid(to_f32<T>((dt + t * p.dt_row)[mine]) + bias);
             gu[t * p.channels + mine] = from_f32<T>(fmaf(q1, sd[r * kC + mine].x, Dv * dy));
             gdt[t * p.channels + mine] = from_f32<T>(dd);
             if (p.z) {
                 const float zv = to_f32<T>((z + t * z_row)[mine]), gv = to_f32<T>((go + t * q.grad_row)[mine]);
-                const float s = rcp(1.0f + ex2(zv * -kLog2e));
+                const float s = silu_slope(zv, sigmoid(zv));
                 gz[t * p.channels + mine] =
-                    from_f32<T>(gv * fmaf(Dv, uv, sy[r * kC + mine]) * (s * fmaf(zv, 1.0f - s, 1.0f)));
+                    from_f32<T>(gv * fmaf(Dv, uv, sy[r * kC + mine]) * s);
             }
             acc_D = fmaf(dy, uv, acc_D);
             acc_bias += dd;

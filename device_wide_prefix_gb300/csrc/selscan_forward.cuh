@@ -247,7 +247,7 @@ __global__ void __launch_bounds__(32, kScanWarpsPerSM) selscan_kernel(ScanParams
                 to.x[0][i] = uv.x, to.x[1][i] = uv.y;
                 if (gate) {
                     const float2 zv = raw.z[i].f32();
-                    to.x[0][i] *= gate_of(zv.x), to.x[1][i] *= gate_of(zv.y);
+                    to.x[0][i] *= silu(zv.x), to.x[1][i] *= silu(zv.y);
                 }
             } else {
                 to.x[0][i] = d.x * uv.x, to.x[1][i] = d.y * uv.y;
@@ -341,7 +341,7 @@ __global__ void __launch_bounds__(32, kScanWarpsPerSM) selscan_kernel(ScanParams
                 y[i][0] = fmaf(Dv.x, uv.x, y[i][0]), y[i][1] = fmaf(Dv.y, uv.y, y[i][1]);
                 if (gate) {
                     const float2 zv = now.z[i].f32();
-                    y[i][0] *= gate_of(zv.x), y[i][1] *= gate_of(zv.y);
+                    y[i][0] *= silu(zv.x), y[i][1] *= silu(zv.y);
                 }
             }
             if ((NL == 1 || nl == 0) && ch < live) {

@@ -29,7 +29,7 @@ __global__ void __launch_bounds__(kScanThreads) scan_step_kernel(ScanStepParams 
         u = to_f32<T>(static_cast<const T *>(p.u)[b * p.u_row + c]);
         float d = to_f32<T>(static_cast<const T *>(p.dt)[b * p.dt_row + c]);
         if (p.dt_bias) d += p.dt_bias[c];
-        if (p.softplus) d = softplus(d);
+        if (p.softplus) d = softplus_poly(d);
         float *st = p.state + slot * p.state_slot + c * p.states;
         const T *B = static_cast<const T *>(p.B) + b * p.b_row + g * p.b_group;
         const T *C = static_cast<const T *>(p.C) + b * p.c_row + g * p.c_group;

@@ -79,21 +79,18 @@ __device__ __forceinline__ float ex2(float x) {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
+__device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // Logistic function 1 / (1 + e^-x); for large -x the exponential is +inf and
 // the quotient 0, the limit.
-__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.0f, 1.0f + __expf(-x)); }
-// x * sigmoid(x); below -88 the product is under the smallest normal f32, and
-// an infinite x would give inf * 0.
-__device__ __forceinline__ float silu(float x) { return x < -88.0f ? 0.0f : x * sigmoid(x); }
-// d/dx of x * sigmoid(x), with its limits 0 and 1.
-__device__ __forceinline__ float silu_slope(float x) {
-    if (x < -88.0f) return 0.0f;
-    if (x > 88.0f) return 1.0f;
-    const float s = sigmoid(x);
-    return s * (1.0f + x * (1.0f - s));
-}
-// log(1 + e^x); above 20 it equals x to f32 rounding.
-__device__ __forceinline__ float softplus(float x) { return x > 20.0f ? x : log1pf(expf(x)); }
+__device__ __forceinline__ float sigmoid(float x) { return rcp(1.0f + ex2(x * -kLog2e)); }
+__device__ __forceinline__ float silu(float x) { return x * sigmoid(x); }
+// d/dx of x * sigmoid(x), from x and s = sigmoid(x).
+__device__ __forceinline__ float silu_slope(float x, float s) { return s * fmaf(x, 1.0f - s, 1.0f); }
 
 // Segment of packed row `t` by CSR offsets (num_segments + 1 entries): the
 // first s with offsets[s + 1] > t, or num_segments if there is none.  Empty

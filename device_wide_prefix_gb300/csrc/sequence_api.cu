@@ -561,7 +561,7 @@ dwp_status norm_forward(const dwp_norm_args &a, cudaStream_t s) {
 }
 
 // Blocks that share a group's rows in the gradient: enough threads to keep an
-// SM's registers busy (about 768 of them), few enough that the blocks' column
+// SM's registers busy (about 512 of them), few enough that the blocks' column
 // sums are a small share of the traffic.
 int64_t norm_blocks(const dwp_norm_args &a) {
     const int64_t threads = ceil_div(ceil_div(a.channels / a.groups, 8), 32) * 32;
