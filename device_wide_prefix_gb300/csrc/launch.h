@@ -176,6 +176,7 @@ struct ScanBackwardParams {
     const float *grad_final;
     void *grad_u, *grad_dt, *grad_z, *grad_B, *grad_C;
     float *grad_initial;
+    int64_t carry_chunks, carry_per;  // the walk back's chunks, in all and to each chunk here
     float *partial;     // [batch * chunks][channels * (states + 2)]
     float *partial_bc;  // [channel blocks of a group][batch * rows][groups][2][states]
 };
@@ -190,6 +191,7 @@ struct ScanStepParams {
     float *state;
     int64_t state_slot;
     const int32_t *slots;
+    bool wide;  // four neighbouring states of A, B, C and the state are one aligned access
 };
 // Warps of the gradient that an SM holds, and channels one covers.
 constexpr int kScanBackWarpsPerSM = 8;

@@ -2,12 +2,12 @@
 // smooth functions of a row's step, and the rows' staging.
 #pragma once
 
+#include <type_traits>
+
 #include "sequence.cuh"
 
 namespace dwp {
 
-constexpr int kScanThreads = 128;
-constexpr int kNT = 4;  // states of a channel in one thread
 constexpr int kCheckpointRows = DWP_SCAN_CHECKPOINT_ROWS;
 
 // Code words of the segment map.

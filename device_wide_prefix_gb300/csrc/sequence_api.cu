@@ -328,7 +328,7 @@ int64_t check_scan(Check &c, const dwp_selective_scan_args &a, bool backward) {
 // (32 warps): 38 chunks 1726 us, 56 1218, 112 1276.
 int64_t chunks_of(const dwp_selective_scan_args &a, int64_t units, int64_t slots) {
     if (2 * units >= slots) return 1;
-    const int64_t most = ceil_div(a.rows, 4 * DWP_SCAN_CHECKPOINT_ROWS);
+    const int64_t most = ceil_div(a.rows, DWP_SCAN_CHECKPOINT_ROWS);
     return slots / units < most ? slots / units : most;
 }
 
@@ -436,8 +436,20 @@ dwp_status scan_backward(const dwp_selective_scan_backward_args &a, void *scratc
     ScanBackwardParams p = {};
     p.f = scan_params(f, nullptr);
     const int64_t per = scan_block_channels(f.states), blocks = ceil_div(p.f.group, per);
-    if (n > 0) set_chunks(p.f, chunks_of(f, scan_units(f, per), 152 * kScanBackWarpsPerSM));
-    const CarrySpace carry(p.f);
+    // the walk back has half as many warps to a chunk and needs fewer
+    // registers: its chunks are finer, a whole number of them to each chunk
+    ScanParams r = p.f;
+    if (n > 0) {
+        const int64_t chunks = chunks_of(f, scan_units(f, per), 152 * kScanBackWarpsPerSM);
+        const int64_t want = chunks_of(f, scan_units(f, scan_warp_channels(f.states)), 152 * kScanWarpsPerSM);
+        const int64_t finer = chunks > 1 && want > chunks ? ceil_div(want, chunks) : 1;
+        set_chunks(r, chunks * finer);
+        p.carry_per = finer;
+        p.f.chunk_rows = r.chunk_rows * finer;
+        p.f.chunks = ceil_div(f.rows, p.f.chunk_rows);
+    }
+    p.carry_chunks = r.chunks;
+    const CarrySpace carry(r);
     const size_t map = f.offsets ? round16(size_t(f.rows) * 4u) : 0u;
     const size_t part = round16(size_t(f.batch * p.f.chunks * f.channels * (f.states + 2)) * 4u);
     const size_t bc = round16(size_t(blocks * n * f.groups * 2 * f.states) * 4u);
@@ -468,7 +480,9 @@ dwp_status scan_backward(const dwp_selective_scan_backward_args &a, void *scratc
     carry.place(p.f, at + map + part + bc);
     const auto t = static_cast<dwp_dtype>(f.dtype);
     if (p.f.chunks > 1) {
-        ScanParams r = p.f;  // as the walk back reads it
+        const int64_t chunks = r.chunks, chunk_rows = r.chunk_rows;
+        r = p.f;  // as the walk back reads it
+        r.chunks = chunks, r.chunk_rows = chunk_rows;
         r.u = p.grad_out, r.u_batch = p.grad_batch, r.u_row = p.grad_row;
         r.B = p.f.C, r.b_batch = p.f.c_batch, r.b_row = p.f.c_row, r.b_group = p.f.c_group;
         r.initial = p.grad_final;
@@ -495,7 +509,8 @@ dwp_status scan_step(const dwp_selective_scan_step_args &a, cudaStream_t s) {
     check_bc(c, a.B, a.b_group_stride, a.dtype, 1, a.batch, a.groups, a.states);
     check_bc(c, a.C, a.c_group_stride, a.dtype, 1, a.batch, a.groups, a.states);
     c.rows(a.out, a.dtype, 1, a.batch, a.channels, true);
-    c.dense(a.A, DWP_F32, a.channels * a.states, false, false);
+    c.dense(a.A, DWP_F32, a.channels * a.states, false, false, &c.bits_state);
+    c.bits_state |= reinterpret_cast<uintptr_t>(a.state);
     c.dense(a.D, DWP_F32, a.channels, false, true);
     c.dense(a.dt_bias, DWP_F32, a.channels, false, true);
     check_slots(c, a.state, DWP_F32, a.batch, a.num_slots, a.slot_stride, a.channels * a.states, a.slots);
@@ -510,6 +525,9 @@ dwp_status scan_step(const dwp_selective_scan_step_args &a, cudaStream_t s) {
     p.C = a.C.data, p.c_row = a.C.row_stride, p.c_group = a.c_group_stride;
     p.A = a.A, p.D = a.D, p.dt_bias = a.dt_bias;
     p.state = a.state, p.state_slot = a.slot_stride, p.slots = a.slots;
+    const uintptr_t e = uintptr_t(size_of(a.dtype));
+    p.wide = a.states % 4 == 0 && (c.bits_bc & (4 * e - 1)) == 0 &&
+             ((c.bits_state | uintptr_t(a.slot_stride * 4)) & 15u) == 0;
     return launched(launch_selscan_step(static_cast<dwp_dtype>(a.dtype), p, s));
 }
 

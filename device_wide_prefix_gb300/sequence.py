@@ -13,7 +13,6 @@ each function; gradients of parameters are float32.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import struct
 
@@ -46,60 +45,75 @@ _WITH_SCRATCH = ("dwp_causal_conv_backward", "dwp_selective_scan", "dwp_selectiv
                  "dwp_block_norm_backward")
 
 
+_ENTRY = {}  # entry points by name, once the library is loaded
+
+
+def _entry(name):
+    f = _ENTRY.get(name)
+    if f is None:
+        f = _ENTRY[name] = getattr(_dwp.load(), name)
+    return f
+
+
 def scratch_bytes(name: str, packed: bytes) -> int:
     """Scratch a call needs, for its packed argument structure."""
     need = ctypes.c_size_t(0)
-    _dwp._check(getattr(_dwp.load(), name)(packed, None, ctypes.byref(need), None), name)
+    _dwp._check(_entry(name)(packed, None, ctypes.byref(need), None), name)
     return need.value
 
 
-def _launch(name, fields, device, stream, scratch=None):
+def _launch(name, fields, x, stream, scratch=None):
+    index = x.get_device()
+    if index != torch._C._cuda_getDevice():
+        with torch.cuda.device(index):
+            return _launch(name, fields, x, stream, scratch)
     packed = _PACK[name](*fields)
-    entry = getattr(_dwp.load(), name)
-    handle = (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
-    with _on(device):
-        if name in _WITH_SCRATCH:
-            size = ctypes.c_size_t(0)
-            if scratch is None:
-                st = entry(packed, None, ctypes.byref(size), None)
+    handle = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    if name in _WITH_SCRATCH:
+        size = ctypes.c_size_t(0)
+        at = ctypes.byref(size)
+        if scratch is None:
+            st = _entry(name)(packed, None, at, None)
+            if st:
                 _dwp._check(st, name)
-                with _allocating(stream):
-                    scratch = torch.empty(max(size.value, 16), dtype=torch.uint8, device=device)
-            size.value = scratch.numel()
-            st = entry(packed, scratch.data_ptr(), ctypes.byref(size), handle)
-        else:
-            st = entry(packed, handle)
-    _dwp._check(st, name)
+            scratch = _empty((size.value or 16,), torch.uint8, x, stream)
+        size.value = scratch.numel()
+        st = _entry(name)(packed, scratch.data_ptr(), at, handle)
+    else:
+        st = _entry(name)(packed, handle)
+    if st:
+        _dwp._check(st, name)
 
 
-_NOTHING = contextlib.nullcontext()
+def _empty(shape, dtype, x, stream):
+    """Memory on x's device that belongs to the stream the call runs on."""
+    if stream is None:
+        return x.new_empty(shape, dtype=dtype)
+    with torch.cuda.stream(stream):
+        return x.new_empty(shape, dtype=dtype)
 
 
-def _on(device):
-    return _NOTHING if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+def _refuse(what, *about):
+    raise ValueError(what % about)
 
 
-def _allocating(stream):
-    """Memory made here belongs to the stream the call runs on."""
-    return _NOTHING if stream is None else torch.cuda.stream(stream)
-
-
-def _need(ok, what: str) -> None:
+def _need(ok, what):
     if not ok:
         raise ValueError(what)
 
 
 def _main(x, what, ndims=(2, 3)):
-    """The tensor that sets a call's type, device and row shape."""
-    _need(x.is_cuda and x.dtype in _DTYPES and x.dim() in ndims,
-          "%s must be a CUDA tensor of float32, bfloat16 or float16 rows" % what)
+    """Rows of the tensor that sets a call's type, device and row shape."""
+    if not x.is_cuda or x.dtype not in _DTYPES or x.dim() not in ndims:
+        _refuse("%s must be a CUDA tensor of float32, bfloat16 or float16 rows", what)
     return _rows(x, what)
 
 
 def _rows(t, what):
     """(address, batch stride, row stride) of a tensor of rows."""
     s = t.stride()
-    _need(s[-1] == 1 or t.shape[-1] <= 1 or t.numel() == 0, "%s must have contiguous channels" % what)
+    if s[-1] != 1 and t.shape[-1] > 1 and t.numel():
+        _refuse("%s must have contiguous channels", what)
     return (t.data_ptr(), s[0], s[1]) if len(s) == 3 else (t.data_ptr(), 0, s[0])
 
 
@@ -107,49 +121,42 @@ def _like(t, x, what):
     """Rows of a tensor of the shape, type and device of x; zeros for None."""
     if t is None:
         return _NO_ROWS
-    _need(t.shape == x.shape and t.dtype == x.dtype and t.device == x.device,
-          "%s must have the shape, type and device of the call's main input" % what)
+    if t.shape != x.shape or t.dtype != x.dtype or t.get_device() != x.get_device():
+        _refuse("%s must have the shape, type and device of the call's main input", what)
     return _rows(t, what)
 
 
-def _dense(t, shape, dtype, device, what):
-    """Address of a contiguous tensor; 0 for None."""
+def _dense(t, shape, dtype, x, what):
+    """Address of a contiguous tensor on x's device; 0 for None."""
     if t is None:
         return 0
-    _need(t.dtype == dtype and t.device == device and t.is_contiguous() and tuple(t.shape) == tuple(shape),
-          "%s must be a contiguous %s tensor of shape %s on %s" % (what, dtype, tuple(shape), device))
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != x.get_device():
+        _refuse("%s must be a contiguous %s tensor of shape %s on %s", what, dtype, tuple(shape), x.device)
     return t.data_ptr()
 
 
 def _sequences(x, offsets):
     """(batch, rows, offsets' address, segments, sequences)."""
     if offsets is not None:
-        _need(x.dim() == 2 and offsets.is_cuda and offsets.device == x.device and offsets.is_contiguous()
-              and offsets.dim() == 1 and offsets.numel() >= 1 and offsets.element_size() == 4
-              and not offsets.is_floating_point(),
-              "offsets must be a contiguous CUDA tensor of 4-byte integers, for packed (rows, channels) inputs")
+        if (x.dim() != 2 or offsets.get_device() != x.get_device() or offsets.dim() != 1 or offsets.numel() < 1
+                or not offsets.is_contiguous() or offsets.element_size() != 4 or offsets.is_floating_point()):
+            _refuse("offsets must be a contiguous CUDA tensor of 4-byte integers, for packed (rows, channels) inputs")
         n = offsets.numel() - 1
         return 1, x.shape[0], offsets.data_ptr(), n, n
     return (1, x.shape[0], 0, 0, 1) if x.dim() == 2 else (x.shape[0], x.shape[1], 0, 0, x.shape[0])
 
 
 def _weight(weight, x, shape, what):
-    _need(weight.dtype == x.dtype or weight.dtype == torch.float32,
-          "%s must be float32 or of x's type" % what)
-    return _dense(weight, shape, weight.dtype, x.device, what)
+    if weight.dtype != x.dtype and weight.dtype != torch.float32:
+        _refuse("%s must be float32 or of x's type", what)
+    return _dense(weight, shape, weight.dtype, x, what)
 
 
 def _output(out, x, stream, what="out"):
     if out is None:
-        with _allocating(stream):
-            return torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        return _empty(x.shape, x.dtype, x, stream)
     _like(out, x, what)
     return out
-
-
-def _empty(shape, dtype, device, stream):
-    with _allocating(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
 
 
 # ---------------------------------------------------------------------------
@@ -162,9 +169,9 @@ def _conv_fields(x, xr, out, weight, bias, offsets, initial_state, final_state, 
     batch, rows, off, nseg, seqs = _sequences(x, offsets)
     state = (seqs, width - 1, ch)
     return [_DTYPES[x.dtype], _DTYPES.get(weight.dtype, -1), 1 if silu else 0, width, ch, batch, rows, nseg, *xr, *out,
-            _weight(weight, x, (ch, width), "weight"), _dense(bias, (ch,), weight.dtype, x.device, "bias"), off,
-            _dense(initial_state, state, x.dtype, x.device, "initial_state"),
-            _dense(final_state, state, x.dtype, x.device, "final_state")], state
+            _weight(weight, x, (ch, width), "weight"), _dense(bias, (ch,), weight.dtype, x, "bias"), off,
+            _dense(initial_state, state, x.dtype, x, "initial_state"),
+            _dense(final_state, state, x.dtype, x, "final_state")], state
 
 
 def causal_conv(x, weight, bias=None, offsets=None, initial_state=None, silu=True, return_state=False, out=None,
@@ -178,9 +185,9 @@ def causal_conv(x, weight, bias=None, offsets=None, initial_state=None, silu=Tru
     out = _output(out, x, stream)
     if return_state and final_state is None:
         _need(weight.dim() == 2, "weight must have shape (channels, width)")
-        final_state = _empty((_sequences(x, offsets)[4], weight.shape[1] - 1, x.shape[-1]), x.dtype, x.device, stream)
+        final_state = _empty((_sequences(x, offsets)[4], weight.shape[1] - 1, x.shape[-1]), x.dtype, x, stream)
     fields, _ = _conv_fields(x, xr, _rows(out, "out"), weight, bias, offsets, initial_state, final_state, silu)
-    _launch("dwp_causal_conv", fields, x.device, stream)
+    _launch("dwp_causal_conv", fields, x, stream)
     return out if final_state is None else (out, final_state)
 
 
@@ -191,24 +198,31 @@ def causal_conv_backward(grad_out, x, weight, bias=None, offsets=None, initial_s
     xr = _main(x, "x")
     gr = _like(grad_out, x, "grad_out")
     fields, state = _conv_fields(x, xr, _NO_ROWS, weight, bias, offsets, initial_state, None, silu)
-    f32, dev = torch.float32, x.device
-    grads = {"x": _output(None, x, stream), "weight": _empty(weight.shape, f32, dev, stream)}
+    f32 = torch.float32
+    grads = {"x": _output(None, x, stream), "weight": _empty(weight.shape, f32, x, stream)}
     if bias is not None:
-        grads["bias"] = _empty(bias.shape, f32, dev, stream)
+        grads["bias"] = _empty(bias.shape, f32, x, stream)
     if initial_state is not None or grad_final_state is not None:
-        grads["initial_state"] = _empty(state, x.dtype, dev, stream)
+        grads["initial_state"] = _empty(state, x.dtype, x, stream)
     at = lambda k: grads[k].data_ptr() if k in grads else 0  # noqa: E731
-    fields += [*gr, *_rows(grads["x"], "grad_x"), _dense(grad_final_state, state, x.dtype, dev, "grad_final_state"),
+    fields += [*gr, *_rows(grads["x"], "grad_x"), _dense(grad_final_state, state, x.dtype, x, "grad_final_state"),
                at("weight"), at("bias"), at("initial_state")]
-    _launch("dwp_causal_conv_backward", fields, dev, stream, scratch)
+    _launch("dwp_causal_conv_backward", fields, x, stream, scratch)
     return grads
 
 
-def _slots(slots, batch, device):
+def _slots(slots, batch, x):
     if slots is None:
         return 0
     _need(slots.dtype == torch.int32, "slots must be int32")
-    return _dense(slots, (batch,), torch.int32, device, "slots")
+    return _dense(slots, (batch,), torch.int32, x, "slots")
+
+
+def _cache(state, shape, x):
+    """Whether `state` is (slots, *shape) on x's device, each slot contiguous."""
+    s = state.stride()
+    return (len(s) == 3 and state.shape[1:] == shape and state.get_device() == x.get_device()
+            and (state.numel() == 0 or ((s[2] == 1 or shape[1] == 1) and (s[1] == shape[1] or shape[0] == 1))))
 
 
 def causal_conv_step(x, state, weight, bias=None, slots=None, silu=True, out=None, stream=None):
@@ -221,14 +235,13 @@ def causal_conv_step(x, state, weight, bias=None, slots=None, silu=True, out=Non
     batch, ch = x.shape
     _need(weight.dim() == 2 and weight.shape[0] == ch, "weight must have shape (channels, width)")
     width = weight.shape[1]
-    _need(state.dim() == 3 and state.shape[1:] == (width - 1, ch) and state.dtype == x.dtype
-          and state.device == x.device and (state.numel() == 0 or state[0].is_contiguous()),
+    _need(state.dtype == x.dtype and _cache(state, (width - 1, ch), x),
           "state must have shape (slots, width - 1, channels), each slot contiguous, and x's type and device")
     fields = [_DTYPES[x.dtype], _DTYPES.get(weight.dtype, -1), 1 if silu else 0, width, ch, batch, state.shape[0],
               *xr, *_rows(out, "out"), _weight(weight, x, (ch, width), "weight"),
-              _dense(bias, (ch,), weight.dtype, x.device, "bias"), state.data_ptr(), state.stride(0),
-              _slots(slots, batch, x.device)]
-    _launch("dwp_causal_conv_step", fields, x.device, stream)
+              _dense(bias, (ch,), weight.dtype, x, "bias"), state.data_ptr(), state.stride(0),
+              _slots(slots, batch, x)]
+    _launch("dwp_causal_conv_step", fields, x, stream)
     return out
 
 
@@ -239,37 +252,39 @@ def causal_conv_step(x, state, weight, bias=None, slots=None, silu=True, out=Non
 def _bc(t, u, what):
     """(rows triple, group stride, groups, states) of B or C: (..., groups, states) or (..., states)."""
     lead = u.dim() - 1
-    _need(t.dtype == u.dtype and t.device == u.device and t.dim() in (lead + 1, lead + 2)
-          and t.shape[:lead] == u.shape[:lead],
-          "%s must have u's rows, type and device, and shape (..., groups, states)" % what)
-    s = t.stride()
-    _need(s[-1] == 1 or t.shape[-1] <= 1 or t.numel() == 0, "%s must have contiguous states" % what)
+    s, shape = t.stride(), t.shape
+    if (t.dtype != u.dtype or t.get_device() != u.get_device() or not lead + 1 <= len(s) <= lead + 2
+            or shape[:lead] != u.shape[:lead]):
+        _refuse("%s must have u's rows, type and device, and shape (..., groups, states)", what)
+    if s[-1] != 1 and shape[-1] > 1 and t.numel():
+        _refuse("%s must have contiguous states", what)
     batch, row = (s[0], s[1]) if lead == 2 else (0, s[0])
-    grouped = t.dim() == lead + 2
-    return ((t.data_ptr(), batch, row), s[-2] if grouped else 0, t.shape[-2] if grouped else 1, t.shape[-1])
+    if len(s) == lead + 2:
+        return (t.data_ptr(), batch, row), s[-2], shape[-2], shape[-1]
+    return (t.data_ptr(), batch, row), 0, 1, shape[-1]
 
 
 def _scan_parts(u, dt, A, B, C, D, z, dt_bias, out):
     """The fields that the prompt and the token form share."""
-    ch, dev, f32 = u.shape[-1], u.device, torch.float32
+    ch, f32 = u.shape[-1], torch.float32
     br, bg, groups, n = _bc(B, u, "B")
     cr, cg, cgroups, cn = _bc(C, u, "C")
     _need((groups, n) == (cgroups, cn), "B and C must have the same groups and states")
     rows = [*_main(u, "u"), *_like(dt, u, "dt"), *_like(z, u, "z"), *br, *cr, *out, bg, cg,
-            _dense(A, (ch, n), f32, dev, "A"), _dense(D, (ch,), f32, dev, "D"),
-            _dense(dt_bias, (ch,), f32, dev, "dt_bias")]
+            _dense(A, (ch, n), f32, u, "A"), _dense(D, (ch,), f32, u, "D"),
+            _dense(dt_bias, (ch,), f32, u, "dt_bias")]
     return rows, groups, n
 
 
 def _scan_fields(u, dt, A, B, C, D, z, dt_bias, out, offsets, initial, final, checkpoints, dt_softplus):
     parts, groups, n = _scan_parts(u, dt, A, B, C, D, z, dt_bias, out)
     batch, rows, off, nseg, seqs = _sequences(u, offsets)
-    ch, dev, f32 = u.shape[-1], u.device, torch.float32
+    ch, f32 = u.shape[-1], torch.float32
     state = (seqs, ch, n)
     points = (batch, -(-rows // CHECKPOINT_ROWS), ch, n)
     return [_DTYPES[u.dtype], 1 if dt_softplus else 0, ch, n, groups, batch, rows, nseg, *parts, off,
-            _dense(initial, state, f32, dev, "initial_state"), _dense(final, state, f32, dev, "final_state"),
-            _dense(checkpoints, points, f32, dev, "checkpoints")], state
+            _dense(initial, state, f32, u, "initial_state"), _dense(final, state, f32, u, "final_state"),
+            _dense(checkpoints, points, f32, u, "checkpoints")], state
 
 
 def selective_scan(u, dt, A, B, C, D=None, z=None, dt_bias=None, offsets=None, initial_state=None, dt_softplus=True,
@@ -285,12 +300,12 @@ def selective_scan(u, dt, A, B, C, D=None, z=None, dt_bias=None, offsets=None, i
     batch, rows, _, _, seqs = _sequences(u, offsets)
     ch, n = u.shape[-1], A.shape[-1]
     if return_state and final_state is None:
-        final_state = _empty((seqs, ch, n), torch.float32, u.device, stream)
+        final_state = _empty((seqs, ch, n), torch.float32, u, stream)
     if return_checkpoints and checkpoints is None:
-        checkpoints = _empty((batch, -(-rows // CHECKPOINT_ROWS), ch, n), torch.float32, u.device, stream)
+        checkpoints = _empty((batch, -(-rows // CHECKPOINT_ROWS), ch, n), torch.float32, u, stream)
     fields, _ = _scan_fields(u, dt, A, B, C, D, z, dt_bias, _rows(out, "out"), offsets, initial_state, final_state,
                              checkpoints, dt_softplus)
-    _launch("dwp_selective_scan", fields, u.device, stream, scratch)
+    _launch("dwp_selective_scan", fields, u, stream, scratch)
     if final_state is None and checkpoints is None:
         return out
     return (out, *(t for t in (final_state, checkpoints) if t is not None))
@@ -306,21 +321,21 @@ def selective_scan_backward(grad_out, u, dt, A, B, C, checkpoints, D=None, z=Non
     _need(checkpoints is not None, "the gradient needs the forward's checkpoints")
     fields, state = _scan_fields(u, dt, A, B, C, D, z, dt_bias, _NO_ROWS, offsets, initial_state, None, checkpoints,
                                  dt_softplus)
-    f32, dev = torch.float32, u.device
-    grads = {"u": _output(None, u, stream), "dt": _output(None, u, stream), "A": _empty(A.shape, f32, dev, stream),
-             "B": _empty(B.shape, u.dtype, dev, stream), "C": _empty(C.shape, u.dtype, dev, stream)}
+    f32 = torch.float32
+    grads = {"u": _output(None, u, stream), "dt": _output(None, u, stream), "A": _empty(A.shape, f32, u, stream),
+             "B": _empty(B.shape, u.dtype, u, stream), "C": _empty(C.shape, u.dtype, u, stream)}
     if D is not None:
-        grads["D"] = _empty(D.shape, f32, dev, stream)
+        grads["D"] = _empty(D.shape, f32, u, stream)
     if z is not None:
         grads["z"] = _output(None, u, stream)
     if dt_bias is not None:
-        grads["dt_bias"] = _empty(dt_bias.shape, f32, dev, stream)
+        grads["dt_bias"] = _empty(dt_bias.shape, f32, u, stream)
     if initial_state is not None or grad_final_state is not None:
-        grads["initial_state"] = _empty(state, f32, dev, stream)
+        grads["initial_state"] = _empty(state, f32, u, stream)
     at = lambda k: grads[k].data_ptr() if k in grads else 0  # noqa: E731
-    fields += [*gr, _dense(grad_final_state, state, f32, dev, "grad_final_state"), at("u"), at("dt"), at("z"), at("B"),
+    fields += [*gr, _dense(grad_final_state, state, f32, u, "grad_final_state"), at("u"), at("dt"), at("z"), at("B"),
                at("C"), at("A"), at("D"), at("dt_bias"), at("initial_state")]
-    _launch("dwp_selective_scan_backward", fields, dev, stream, scratch)
+    _launch("dwp_selective_scan_backward", fields, u, stream, scratch)
     return grads
 
 
@@ -334,12 +349,11 @@ def selective_scan_step(u, dt, A, B, C, state, D=None, z=None, dt_bias=None, slo
     out = _output(out, u, stream)
     parts, groups, n = _scan_parts(u, dt, A, B, C, D, z, dt_bias, _rows(out, "out"))
     batch, ch = u.shape
-    _need(state.dim() == 3 and state.shape[1:] == (ch, n) and state.dtype == torch.float32
-          and state.device == u.device and (state.numel() == 0 or state[0].is_contiguous()),
+    _need(state.dtype == torch.float32 and _cache(state, (ch, n), u),
           "state must be float32 of shape (slots, channels, states), each slot contiguous, on u's device")
     fields = [_DTYPES[u.dtype], 1 if dt_softplus else 0, ch, n, groups, batch, state.shape[0], *parts,
-              state.data_ptr(), state.stride(0), _slots(slots, batch, u.device)]
-    _launch("dwp_selective_scan_step", fields, u.device, stream)
+              state.data_ptr(), state.stride(0), _slots(slots, batch, u)]
+    _launch("dwp_selective_scan_step", fields, u, stream)
     return out
 
 
@@ -351,12 +365,12 @@ def _norm_fields(x, xr, residual, gate, total, out, weight, scale, gate_after, g
     ch = x.shape[-1]
     return [_DTYPES[x.dtype], _DTYPES.get(weight.dtype, -1), rdtype, 1 if gate_after else 0, ch, groups, x.shape[0],
             float(eps), *xr, *residual, *gate, *total, *out, _weight(weight, x, (ch,), "weight"),
-            _dense(scale, (ch,), weight.dtype, x.device, "scale")]
+            _dense(scale, (ch,), weight.dtype, x, "scale")]
 
 
 def _residual(t, x, what):
-    _need(t.shape == x.shape and t.device == x.device and t.dtype in (x.dtype, torch.float32),
-          "%s must have x's shape and device, and be float32 or of x's type" % what)
+    if t.shape != x.shape or t.get_device() != x.get_device() or (t.dtype != x.dtype and t.dtype != torch.float32):
+        _refuse("%s must have x's shape and device, and be float32 or of x's type", what)
     return _rows(t, what)
 
 
@@ -382,12 +396,12 @@ def block_norm(x, weight, residual=None, scale=None, gate=None, gate_after=False
         _need(residual.shape == shape, "residual must have x's shape")
         residual = _flat_rows(residual)
         rr, rdtype = _residual(residual, x2, "residual"), _DTYPES[residual.dtype]
-        total = _empty(shape, residual.dtype, x.device, stream) if sum_out is None else sum_out
+        total = _empty(shape, residual.dtype, x, stream) if sum_out is None else sum_out
         _need(total.shape == shape and total.dtype == residual.dtype, "sum_out must have residual's shape and type")
     fields = _norm_fields(x2, xr, rr, _like(_flat_rows(gate), x2, "gate"),
                           _NO_ROWS if total is None else _residual(_flat_rows(total), x2, "sum_out"),
                           _rows(_flat_rows(out), "out"), weight, scale, gate_after, groups, eps, rdtype)
-    _launch("dwp_block_norm", fields, x.device, stream)
+    _launch("dwp_block_norm", fields, x, stream)
     return out, total
 
 
@@ -407,22 +421,22 @@ def block_norm_backward(grad_out, v, weight, x=None, scale=None, gate=None, gate
     flat = [_flat_rows(t) for t in (grad_out, v, x, gate, grad_residual)]
     g2, v2, x2, z2, s2 = flat
     gr = _main(g2, "grad_out", (2,))
-    dev, f32 = g2.device, torch.float32
+    f32 = torch.float32
     vr = _residual(v2, g2, "v")
     _need(residual or v2.dtype == g2.dtype, "v must have grad_out's type without a residual")
     if s2 is not None:
         _need(residual and s2.dtype == v2.dtype, "grad_residual must have v's type, with a residual")
-    grads = {"weight": _empty(weight.shape, f32, dev, stream), "x": _output(None, grad_out, stream)}
+    grads = {"weight": _empty(weight.shape, f32, g2, stream), "x": _output(None, grad_out, stream)}
     gx = _flat_rows(grads["x"])
     gres = _NO_ROWS
     if residual:
         if scale is None and v.dtype == grad_out.dtype:
             grads["residual"] = grads["x"]  # the same numbers
         else:
-            grads["residual"] = _empty(shape, v.dtype, dev, stream)
+            grads["residual"] = _empty(shape, v.dtype, g2, stream)
             gres = _rows(_flat_rows(grads["residual"]), "grad_residual")
     if scale is not None:
-        grads["scale"] = _empty(scale.shape, f32, dev, stream)
+        grads["scale"] = _empty(scale.shape, f32, g2, stream)
     gz = _NO_ROWS
     if gate is not None:
         grads["gate"] = _output(None, grad_out, stream)
@@ -432,5 +446,5 @@ def block_norm_backward(grad_out, v, weight, x=None, scale=None, gate=None, gate
                           scale, gate_after, groups, eps, _DTYPES[v2.dtype])
     fields += [*gr, *(_NO_ROWS if s2 is None else _residual(s2, g2, "grad_residual")), *_rows(gx, "grad_x"), *gres,
                *gz, grads["weight"].data_ptr(), grads["scale"].data_ptr() if scale is not None else 0]
-    _launch("dwp_block_norm_backward", fields, dev, stream, scratch)
+    _launch("dwp_block_norm_backward", fields, g2, stream, scratch)
     return grads
