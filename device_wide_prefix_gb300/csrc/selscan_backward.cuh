@@ -368,26 +368,38 @@ __global__ void __launch_bounds__(32, 8) selscan_backward_kernel(ScanBackwardPar
         if (plain) tile(s0, rows, code, std::false_type());
         else tile(s0, rows, code, std::true_type());
         __syncwarp();
-#pragma unroll 4
-        for (int m = 0; m < kMine; ++m) {
-            const int r = mine_row + m * kMineRows;
-            const uint32_t f = __shfl_sync(0xffffffffu, code, r);
-            if (mine >= live || f == kRowOutside) continue;
-            const int64_t t = s0 + r;
-            const float uv = to_f32<T>((u + t * p.u_row)[mine]), q1 = s1[r * kC + mine], dy = sg[r * kC + mine];
-            float dd = fmaf(q1, uv, s2[r * kC + mine]);
-            // the slope of softplus
-            if (p.softplus) dd *= sigmoid(to_f32<T>((dt + t * p.dt_row)[mine]) + bias);
-            gu[t * p.channels + mine] = from_f32<T>(fmaf(q1, sd[r * kC + mine].x, Dv * dy));
-            gdt[t * p.channels + mine] = from_f32<T>(dd);
-            if (p.z) {
-                const float zv = to_f32<T>((z + t * z_row)[mine]), gv = to_f32<T>((go + t * q.grad_row)[mine]);
-                const float s = silu_slope(zv, sigmoid(zv));
-                gz[t * p.channels + mine] =
-                    from_f32<T>(gv * fmaf(Dv, uv, sy[r * kC + mine]) * s);
+        // loads of several rows before the first store, which would hold them back
+        constexpr int kBatch = kMine < 8 ? kMine : 8;
+#pragma unroll 1
+        for (int m0 = 0; m0 < kMine; m0 += kBatch) {
+            T ru[kBatch], rd[kBatch], rz[kBatch], rg[kBatch];
+#pragma unroll
+            for (int m = 0; m < kBatch; ++m) {
+                const int64_t t = min(s0 + mine_row + (m0 + m) * kMineRows, t1 - 1);
+                ru[m] = (u + t * p.u_row)[mine_at];
+                rd[m] = (dt + t * p.dt_row)[mine_at];
+                rz[m] = (z + t * z_row)[mine_at];
+                rg[m] = (go + t * q.grad_row)[mine_at];
             }
-            acc_D = fmaf(dy, uv, acc_D);
-            acc_bias += dd;
+#pragma unroll
+            for (int m = 0; m < kBatch; ++m) {
+                const int r = mine_row + (m0 + m) * kMineRows;
+                const uint32_t f = __shfl_sync(0xffffffffu, code, r);
+                const int64_t t = s0 + r;
+                const float uv = to_f32<T>(ru[m]), q1 = s1[r * kC + mine], dy = sg[r * kC + mine];
+                float dd = fmaf(q1, uv, s2[r * kC + mine]);
+                if (p.softplus) dd *= sigmoid(to_f32<T>(rd[m]) + bias);  // the slope of softplus
+                const float du = fmaf(q1, sd[r * kC + mine].x, Dv * dy);
+                const float zv = to_f32<T>(rz[m]);
+                const float dz = to_f32<T>(rg[m]) * fmaf(Dv, uv, sy[r * kC + mine]) * silu_slope(zv, sigmoid(zv));
+                if (mine < live && f != kRowOutside) {
+                    gu[t * p.channels + mine] = from_f32<T>(du);
+                    gdt[t * p.channels + mine] = from_f32<T>(dd);
+                    if (p.z) gz[t * p.channels + mine] = from_f32<T>(dz);
+                    acc_D = fmaf(dy, uv, acc_D);
+                    acc_bias += dd;
+                }
+            }
         }
         __syncwarp();
     }
