@@ -239,6 +239,8 @@ struct NormBackwardParams {
     float *partial;  // [blocks][1 or 2][channels]
 };
 cudaError_t launch_norm(dwp_dtype t, const NormParams &p, bool vec, cudaStream_t s);
+// Threads of one block of the gradient.
+int64_t norm_backward_threads(dwp_dtype t, int64_t group, bool vec);
 cudaError_t launch_norm_backward(dwp_dtype t, const NormBackwardParams &p, bool vec, cudaStream_t s);
 
 }  // namespace dwp

@@ -258,22 +258,27 @@ cudaError_t norm_v(const NormParams &p, cudaStream_t s) {
     }
 }
 
+// Accesses a thread of the gradient makes for a group of `n` elements, V each.
+int64_t backward_accesses(int64_t n, int v) {
+    if (v == 1) return n <= 1024 ? 2 : n <= 4096 ? 8 : 32;
+    return n <= 512 * v ? 1 : n <= 1024 * v ? 2 : 32 / v;
+}
+
 template <class T, int V, bool kWideV>
 cudaError_t norm_backward_v(const NormBackwardParams &q, cudaStream_t s) {
     const NormParams &p = q.n;
     const dim3 grid(uint32_t(q.blocks), uint32_t(p.groups));
-    auto go = [&](auto kernel, int k) {
-        return launch_pdl(kernel, grid, dim3(threads_for(p.group, V, k)), 0, s, q);
-    };
+    const int64_t k = backward_accesses(p.group, V);
+    auto go = [&](auto kernel) { return launch_pdl(kernel, grid, dim3(threads_for(p.group, V, int(k))), 0, s, q); };
     if constexpr (V == 1) {
-        if (p.group <= 1024) return go(norm_backward_kernel<T, 1, 2, kWideV, 512, 1>, 2);
-        if (p.group <= 4096) return go(norm_backward_kernel<T, 1, 8, kWideV, 512, 1>, 8);
-        return go(norm_backward_kernel<T, 1, 32, kWideV, 512, 1>, 32);
+        if (k == 2) return go(norm_backward_kernel<T, 1, 2, kWideV, 512, 1>);
+        if (k == 8) return go(norm_backward_kernel<T, 1, 8, kWideV, 512, 1>);
+        return go(norm_backward_kernel<T, 1, 32, kWideV, 512, 1>);
     } else {
-        if (p.group <= 128 * V) return go(norm_backward_kernel<T, V, 1, kWideV, 128, 6>, 1);
-        if (p.group <= 512 * V) return go(norm_backward_kernel<T, V, 1, kWideV, 512, 1>, 1);
-        if (p.group <= 1024 * V) return go(norm_backward_kernel<T, V, 2, kWideV, 512, 1>, 2);
-        return go(norm_backward_kernel<T, V, 32 / V, kWideV, 512, 1>, 32 / V);
+        if (p.group <= 128 * V) return go(norm_backward_kernel<T, V, 1, kWideV, 128, 4>);
+        if (k == 1) return go(norm_backward_kernel<T, V, 1, kWideV, 512, 1>);
+        if (k == 2) return go(norm_backward_kernel<T, V, 2, kWideV, 512, 1>);
+        return go(norm_backward_kernel<T, V, 32 / V, kWideV, 512, 1>);
     }
 }
 
@@ -319,6 +324,11 @@ __global__ void __launch_bounds__(kColThreads)
 cudaError_t launch_column_sums(const float *part, int64_t blocks, int64_t cols, const ColumnOut &o, cudaStream_t s) {
     return launch_pdl(column_sums_kernel, dim3(uint32_t((cols + 31) / 32)), dim3(kColThreads), 0, s, part, blocks,
                       cols, o);
+}
+
+int64_t norm_backward_threads(dwp_dtype t, int64_t group, bool vec) {
+    const int v = !vec ? 1 : t == DWP_F32 ? 4 : 8;
+    return threads_for(group, v, int(backward_accesses(group, v)));
 }
 
 cudaError_t launch_norm(dwp_dtype t, const NormParams &p, bool vec, cudaStream_t s) {

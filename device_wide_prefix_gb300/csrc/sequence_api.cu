@@ -578,14 +578,15 @@ dwp_status norm_forward(const dwp_norm_args &a, cudaStream_t s) {
     return launched(launch_norm(static_cast<dwp_dtype>(a.dtype), norm_params(a), c.wide(a.channels / a.groups, a.dtype), s));
 }
 
-// Blocks that share a group's rows in the gradient: enough threads to keep an
-// SM's registers busy (about 512 of them), few enough that the blocks' column
-// sums are a small share of the traffic.
-int64_t norm_blocks(const dwp_norm_args &a) {
-    const int64_t threads = ceil_div(ceil_div(a.channels / a.groups, 8), 32) * 32;
-    int64_t blocks = ceil_div(152 * 768, a.groups * (threads > 512 ? 512 : threads));
+// Blocks that share a group's rows in the gradient: those that run at once
+// (512 threads of 128 registers fill an SM), so that none waits for another's
+// end.  Gated norm of 4096 x 8192 f16 in 8 groups: 512 threads an SM 97 us,
+// 768 122, 1024 102.
+int64_t norm_blocks(const dwp_norm_args &a, bool wide) {
+    const int64_t threads = norm_backward_threads(static_cast<dwp_dtype>(a.dtype), a.channels / a.groups, wide);
+    int64_t blocks = 152 * (512 / threads) / a.groups;
     if (8 * blocks > a.rows) blocks = ceil_div(a.rows, 8);  // eight rows or more to each
-    return blocks;
+    return blocks < 1 && a.rows > 0 ? 1 : blocks;
 }
 
 dwp_status norm_backward(const dwp_norm_backward_args &a, void *scratch, size_t *bytes, cudaStream_t s) {
@@ -610,7 +611,7 @@ dwp_status norm_backward(const dwp_norm_backward_args &a, void *scratch, size_t 
     }
     c.dense(a.grad_weight, DWP_F32, f.channels, true, false);
     c.dense(a.grad_scale, DWP_F32, f.channels, true, true);
-    const int64_t blocks = norm_blocks(f);
+    const int64_t blocks = norm_blocks(f, c.wide(f.channels / f.groups, f.dtype));
     const int64_t planes = f.scale ? 2 : 1;
     const size_t need = round16(size_t(blocks * planes * f.channels) * 4u);
     if (!c.scratch(scratch, bytes, need, &st)) return st;
