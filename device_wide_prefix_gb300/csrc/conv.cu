@@ -32,8 +32,8 @@ __device__ __forceinline__ Span span_at(const uint32_t *offsets, uint32_t nseg, 
 
 // Taps and bias of V channels: w[j][i] is channel i's for j rows before the
 // row itself, 0 past the width.
-template <class T, int V, int W>
-__device__ __forceinline__ void load_taps(const ConvParams &p, int64_t c0, float (&w)[W][V], float (&bias)[V]) {
+template <class T, int V, int W, class Params>
+__device__ __forceinline__ void load_taps(const Params &p, int64_t c0, float (&w)[W][V], float (&bias)[V]) {
     const int halo = p.width - 1;
     if (W == 4 && p.width == 4 && p.weight_f32 && p.weight_wide) {
 #pragma unroll
@@ -322,32 +322,27 @@ __global__ void __launch_bounds__(kConvThreads) conv_step_kernel(ConvStepParams 
     const int halo = p.width - 1;
     T *y = static_cast<T *>(p.y) + b * p.y_row + c0;
     const int64_t slot = p.slots ? p.slots[b] : b;
-    float o[V];
-    if (slot < 0 || slot >= p.num_slots) {  // a padding row
-#pragma unroll
-        for (int i = 0; i < V; ++i) o[i] = 0.0f;
-        store_f32<V>(y, o);
-        return;
-    }
-    T *st = static_cast<T *>(p.state) + slot * p.state_slot + c0;
-    float win[W][V];
+    const bool live = slot >= 0 && slot < p.num_slots;  // else a padding row
+    // the taps do not wait for the slot
+    float w[W][V], o[V], win[W][V];
+    load_taps<T, V, W>(p, c0, w, o);
+    T *st = static_cast<T *>(p.state) + (live ? slot : 0) * p.state_slot + c0;
     load_f32<V>(win[0], static_cast<const T *>(p.x) + b * p.x_row + c0);
 #pragma unroll
     for (int j = 1; j < W; ++j) {
 #pragma unroll
         for (int i = 0; i < V; ++i) win[j][i] = 0.0f;
-        if (j <= halo) load_f32<V>(win[j], st + int64_t(halo - j) * p.channels);
+        if (live && j <= halo) load_f32<V>(win[j], st + int64_t(halo - j) * p.channels);
     }
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        float a = p.bias ? load_param<T>(p.bias, c0 + i, p.weight_f32) : 0.0f;
 #pragma unroll
-        for (int j = 0; j < W; ++j)
-            if (j <= halo)
-                a = fmaf(load_param<T>(p.weight, (c0 + i) * p.width + (halo - j), p.weight_f32), win[j][i], a);
-        o[i] = p.silu ? silu(a) : a;
+        for (int j = 0; j < W; ++j) o[i] = fmaf(w[j][i], win[j][i], o[i]);
+        if (p.silu) o[i] = silu(o[i]);
+        if (!live) o[i] = 0.0f;
     }
     store_f32<V>(y, o);
+    if (!live) return;
 #pragma unroll
     for (int j = 0; j < W - 1; ++j)
         if (j < halo) store_f32<V>(st + int64_t(halo - 1 - j) * p.channels, win[j]);
@@ -410,9 +405,9 @@ cudaError_t launch_conv_backward(dwp_dtype t, const ConvBackwardParams &p, bool 
 }
 
 cudaError_t launch_conv_step(dwp_dtype t, const ConvStepParams &p, bool vec, cudaStream_t s) {
-    if (t == DWP_F32) return vec ? conv_step_w<float, 4>(p, s) : conv_step_w<float, 1>(p, s);
-    if (t == DWP_BF16) return vec ? conv_step_w<__nv_bfloat16, 8>(p, s) : conv_step_w<__nv_bfloat16, 1>(p, s);
-    return vec ? conv_step_w<__half, 8>(p, s) : conv_step_w<__half, 1>(p, s);
+    if (t == DWP_F32) return vec ? conv_step_w<float, 2>(p, s) : conv_step_w<float, 1>(p, s);
+    if (t == DWP_BF16) return vec ? conv_step_w<__nv_bfloat16, 2>(p, s) : conv_step_w<__nv_bfloat16, 1>(p, s);
+    return vec ? conv_step_w<__half, 2>(p, s) : conv_step_w<__half, 1>(p, s);
 }
 
 }  // namespace dwp

@@ -126,7 +126,7 @@ struct ConvBackwardParams {
 struct ConvStepParams {
     int64_t channels, batch, num_slots;
     int width, silu;
-    bool weight_f32;
+    bool weight_f32, weight_wide;
     const void *x, *weight, *bias;
     void *y, *state;
     int64_t x_row, y_row, state_slot;

@@ -272,6 +272,7 @@ dwp_status conv_step(const dwp_conv_step_args &a, cudaStream_t s) {
     ConvStepParams p = {};
     p.channels = a.channels, p.batch = a.batch, p.num_slots = a.num_slots;
     p.width = int(a.width), p.silu = int(a.silu), p.weight_f32 = a.weight_dtype == DWP_F32;
+    p.weight_wide = aligned(a.weight, 16);
     p.x = a.x.data, p.x_row = a.x.row_stride, p.y = a.out.data, p.y_row = a.out.row_stride;
     p.weight = a.weight, p.bias = a.bias, p.state = a.state, p.state_slot = a.slot_stride, p.slots = a.slots;
     return launched(launch_conv_step(static_cast<dwp_dtype>(a.dtype), p, c.wide(a.channels, a.dtype), s));

@@ -361,22 +361,37 @@ def selective_scan_step(u, dt, A, B, C, state, D=None, z=None, dt_bias=None, slo
 # block norm
 
 
-def _norm_fields(x, xr, residual, gate, total, out, weight, scale, gate_after, groups, eps, rdtype):
+def _norm_rows(t, x, what, f32=False):
+    """(address, 0, row stride) of a tensor of x's shape, (rows, channels) or
+    (batch, rows, channels) with evenly spaced rows; of x's type, or float32
+    where `f32` allows it.  Zeros for None."""
+    if t is None:
+        return _NO_ROWS
+    if t is not x and (t.shape != x.shape or t.get_device() != x.get_device()
+                       or (t.dtype != x.dtype and not (f32 and t.dtype == torch.float32))):
+        _refuse("%s must have the shape and device of the call's main input, and its type (a residual or sum: or float32)",
+                what)
+    s, shape = t.stride(), t.shape
+    if s[-1] != 1 and shape[-1] > 1 and t.numel():
+        _refuse("%s must have contiguous channels", what)
+    if len(s) == 2:
+        return t.data_ptr(), 0, s[0]
+    if shape[0] > 1 and shape[1] > 1 and s[0] != shape[1] * s[1]:
+        _refuse("%s must have evenly spaced rows", what)
+    return t.data_ptr(), 0, s[1] if shape[1] > 1 else s[0]
+
+
+def _norm_main(x, what):
+    if not x.is_cuda or x.dtype not in _DTYPES or not 2 <= x.dim() <= 3:
+        _refuse("%s must be a CUDA tensor of float32, bfloat16 or float16 rows", what)
+    return _norm_rows(x, x, what)
+
+
+def _norm_fields(x, weight, scale, rdtype, gate_after, groups, eps, *rows):
     ch = x.shape[-1]
-    return [_DTYPES[x.dtype], _DTYPES.get(weight.dtype, -1), rdtype, 1 if gate_after else 0, ch, groups, x.shape[0],
-            float(eps), *xr, *residual, *gate, *total, *out, _weight(weight, x, (ch,), "weight"),
+    return [_DTYPES[x.dtype], _DTYPES.get(weight.dtype, -1), rdtype, 1 if gate_after else 0, ch, groups,
+            x.numel() // ch if ch else 0, float(eps), *rows, _weight(weight, x, (ch,), "weight"),
             _dense(scale, (ch,), weight.dtype, x, "scale")]
-
-
-def _residual(t, x, what):
-    if t.shape != x.shape or t.get_device() != x.get_device() or (t.dtype != x.dtype and t.dtype != torch.float32):
-        _refuse("%s must have x's shape and device, and be float32 or of x's type", what)
-    return _rows(t, what)
-
-
-def _flat_rows(t):
-    """A (batch, rows, channels) tensor as (batch * rows, channels)."""
-    return t if t is None or t.dim() == 2 else t.view(-1, t.shape[-1])
 
 
 def block_norm(x, weight, residual=None, scale=None, gate=None, gate_after=False, groups=1, eps=1e-5, out=None,
@@ -386,21 +401,17 @@ def block_norm(x, weight, residual=None, scale=None, gate=None, gate_after=False
     or None for 1), which is also returned; of x * silu(gate) with a `gate`, or
     times silu(gate) afterwards if `gate_after`.  `out` may be x and `sum_out`
     may be residual, in place.  Returns (out, sum), sum None without a residual."""
-    shape = x.shape
-    _need(x.dim() in (2, 3), "x must be (rows, channels) or (batch, rows, channels)")
-    x2 = _flat_rows(x)
-    xr = _main(x2, "x", (2,))
-    out = _output(out, x, stream)
-    rr, total, rdtype = _NO_ROWS, None, _DTYPES[x.dtype]
+    xr = _norm_main(x, "x")
+    if out is None:
+        out = _empty(x.shape, x.dtype, x, stream)
+    total, rr, tr, rdtype = None, _NO_ROWS, _NO_ROWS, _DTYPES[x.dtype]
     if residual is not None:
-        _need(residual.shape == shape, "residual must have x's shape")
-        residual = _flat_rows(residual)
-        rr, rdtype = _residual(residual, x2, "residual"), _DTYPES[residual.dtype]
-        total = _empty(shape, residual.dtype, x, stream) if sum_out is None else sum_out
-        _need(total.shape == shape and total.dtype == residual.dtype, "sum_out must have residual's shape and type")
-    fields = _norm_fields(x2, xr, rr, _like(_flat_rows(gate), x2, "gate"),
-                          _NO_ROWS if total is None else _residual(_flat_rows(total), x2, "sum_out"),
-                          _rows(_flat_rows(out), "out"), weight, scale, gate_after, groups, eps, rdtype)
+        rr, rdtype = _norm_rows(residual, x, "residual", True), _DTYPES[residual.dtype]
+        total = _empty(x.shape, residual.dtype, x, stream) if sum_out is None else sum_out
+        _need(total.dtype == residual.dtype, "sum_out must have residual's type")
+        tr = _norm_rows(total, x, "sum_out", True)
+    fields = _norm_fields(x, weight, scale, rdtype, gate_after, groups, eps, *xr, *rr, *_norm_rows(gate, x, "gate"), *tr,
+                          *_norm_rows(out, x, "out"))
     _launch("dwp_block_norm", fields, x, stream)
     return out, total
 
@@ -413,38 +424,32 @@ def block_norm_backward(grad_out, v, weight, x=None, scale=None, gate=None, gate
     with a `scale`; `grad_residual` is the returned sum's gradient.  A dict of
     "x", "weight" and, where they apply, "residual", "scale" and "gate"; "x"
     and "residual" are one tensor where they are equal."""
-    shape = v.shape
-    _need(grad_out.shape == shape and v.dim() in (2, 3), "grad_out must have v's shape")
+    gr = _norm_main(grad_out, "grad_out")
     if residual is None:
         residual = scale is not None or grad_residual is not None or v.dtype != grad_out.dtype
     _need(scale is None or (x is not None and residual), "the scale's gradient needs x, and a residual")
-    flat = [_flat_rows(t) for t in (grad_out, v, x, gate, grad_residual)]
-    g2, v2, x2, z2, s2 = flat
-    gr = _main(g2, "grad_out", (2,))
-    f32 = torch.float32
-    vr = _residual(v2, g2, "v")
-    _need(residual or v2.dtype == g2.dtype, "v must have grad_out's type without a residual")
-    if s2 is not None:
-        _need(residual and s2.dtype == v2.dtype, "grad_residual must have v's type, with a residual")
-    grads = {"weight": _empty(weight.shape, f32, g2, stream), "x": _output(None, grad_out, stream)}
-    gx = _flat_rows(grads["x"])
-    gres = _NO_ROWS
+    _need(residual or v.dtype == grad_out.dtype, "v must have grad_out's type without a residual")
+    _need(grad_residual is None or (residual and grad_residual.dtype == v.dtype),
+          "grad_residual must have v's type, with a residual")
+    vr = _norm_rows(v, grad_out, "v", True)
+    shape, f32 = grad_out.shape, torch.float32
+    grads = {"weight": _empty(weight.shape, f32, grad_out, stream), "x": _empty(shape, grad_out.dtype, grad_out, stream)}
+    gx, gres, gz = _norm_rows(grads["x"], grad_out, "grad_x"), _NO_ROWS, _NO_ROWS
     if residual:
         if scale is None and v.dtype == grad_out.dtype:
             grads["residual"] = grads["x"]  # the same numbers
         else:
-            grads["residual"] = _empty(shape, v.dtype, g2, stream)
-            gres = _rows(_flat_rows(grads["residual"]), "grad_residual")
+            grads["residual"] = _empty(shape, v.dtype, grad_out, stream)
+            gres = _norm_rows(grads["residual"], grad_out, "grad_residual", True)
     if scale is not None:
-        grads["scale"] = _empty(scale.shape, f32, g2, stream)
-    gz = _NO_ROWS
+        grads["scale"] = _empty(scale.shape, f32, grad_out, stream)
     if gate is not None:
-        grads["gate"] = _output(None, grad_out, stream)
-        gz = _rows(_flat_rows(grads["gate"]), "grad_gate")
-    xr = (_NO_ROWS if scale is None else _like(x2, g2, "x")) if residual else vr
-    fields = _norm_fields(g2, xr, _NO_ROWS, _like(z2, g2, "gate"), vr if residual else _NO_ROWS, _NO_ROWS, weight,
-                          scale, gate_after, groups, eps, _DTYPES[v2.dtype])
-    fields += [*gr, *(_NO_ROWS if s2 is None else _residual(s2, g2, "grad_residual")), *_rows(gx, "grad_x"), *gres,
-               *gz, grads["weight"].data_ptr(), grads["scale"].data_ptr() if scale is not None else 0]
-    _launch("dwp_block_norm_backward", fields, g2, stream, scratch)
+        grads["gate"] = _empty(shape, grad_out.dtype, grad_out, stream)
+        gz = _norm_rows(grads["gate"], grad_out, "grad_gate")
+    xr = vr if not residual else _norm_rows(x, grad_out, "x") if scale is not None else _NO_ROWS
+    fields = _norm_fields(grad_out, weight, scale, _DTYPES[v.dtype], gate_after, groups, eps, *xr, *_NO_ROWS,
+                          *_norm_rows(gate, grad_out, "gate"), *(vr if residual else _NO_ROWS), *_NO_ROWS)
+    fields += [*gr, *_norm_rows(grad_residual, grad_out, "grad_residual", True), *gx, *gres, *gz,
+               grads["weight"].data_ptr(), grads["scale"].data_ptr() if scale is not None else 0]
+    _launch("dwp_block_norm_backward", fields, grad_out, stream, scratch)
     return grads
