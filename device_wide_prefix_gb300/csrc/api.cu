@@ -322,7 +322,7 @@ const char *dwp_status_string(dwp_status status) {
     return "DWP_UNKNOWN_STATUS";
 }
 
-int dwp_version(void) { return 100; }
+int dwp_version(void) { return 200; }
 
 dwp_status dwp_set_lookback_window(uint32_t tiles) {
     set_lookback_window(tiles);
