@@ -83,11 +83,12 @@ __device__ __forceinline__ void push(float (&win)[W][V], const float (&x)[V]) {
 }
 
 constexpr int kConvGroup = 4;  // rows loaded together, one group ahead of their use
+constexpr int kConvAhead = 4;  // rows between a load and the prefetch beside it
 
 // Forward.  A thread walks kConvStrip rows of V channels with the last W - 1
 // inputs and the taps in registers, so each input is read once (plus W - 1
 // rows per strip).  Four 16-bit channels a thread and 85 registers (24 warps an
-// SM) carry 16384 x 5120 bf16 in 91 us; eight channels and 12 warps took 110,
+// SM) carry 16384 x 5120 bf16 in 88 us (91 without the prefetch); eight channels and 12 warps took 110,
 // 64 registers 117.
 template <class T, int V, int W>
 __global__ void __launch_bounds__(kConvThreads, W == 4 ? 6 : 2) conv_kernel(ConvParams p) {
@@ -108,7 +109,14 @@ __global__ void __launch_bounds__(kConvThreads, W == 4 ? 6 : 2) conv_kernel(Conv
 #pragma unroll
         for (int i = 0; i < kConvGroup; ++i)
             next[i] = *reinterpret_cast<const Pack<T, V> *>(x + min(t + i, t1 - 1) * p.x_row);
+        // the registers hold too few rows in flight for HBM: the groups after
+        // this one are on their way to L2
+#pragma unroll
+        for (int i = 0; i < kConvGroup; ++i)
+            if (t + kConvAhead + i < t1) prefetch_l2(x + (t + kConvAhead + i) * p.x_row);
     };
+    for (int i = kConvGroup; i < kConvAhead; ++i)
+        if (t0 + i < t1) prefetch_l2(x + (t0 + i) * p.x_row);
     load(t0);
     float w[W][V], bias[V], win[W][V];
     load_taps<T, V, W>(p, c0, w, bias);
@@ -124,11 +132,12 @@ __global__ void __launch_bounds__(kConvThreads, W == 4 ? 6 : 2) conv_kernel(Conv
             for (int k = 0; k < V; ++k) o[k] = to_f32<T>(xv.e[k]);
             push<V, W>(win, o);
 #pragma unroll
-            for (int k = 0; k < V; ++k) {
-                float a = bias[k];
+            for (int k = 0; k < V; ++k) o[k] = bias[k];
 #pragma unroll
-                for (int j = 0; j < W; ++j) a = fmaf(w[j][k], win[j][k], a);
-                o[k] = p.silu ? silu(a) : a;
+            for (int j = 0; j < W; ++j) fma_to<V>(o, w[j], win[j]);
+            if (p.silu) {
+#pragma unroll
+                for (int k = 0; k < V; ++k) o[k] = silu(o[k]);
             }
             store_f32<V>(y + t * p.y_row, o);
         };
@@ -238,19 +247,22 @@ __global__ void __launch_bounds__(kConvThreads, W == 4 ? 7 : 3) conv_backward_ke
             for (int k = 0; k < V; ++k) xv[k] = to_f32<T>(xr.e[k]), g[k] = to_f32<T>(gr.e[k]), none[k] = 0.0f;
             push<V, W>(win, xv);
             push<V, W>(acc, none);
+            if (p.silu) {
+                float a[V];
 #pragma unroll
-            for (int k = 0; k < V; ++k) {
-                float a = bias[k];
+                for (int k = 0; k < V; ++k) a[k] = bias[k];
 #pragma unroll
-                for (int j = 0; j < W; ++j) a = fmaf(w[j][k], win[j][k], a);
-                if (p.silu) g[k] *= silu_slope(a, sigmoid(a));
+                for (int j = 0; j < W; ++j) fma_to<V>(a, w[j], win[j]);
 #pragma unroll
-                for (int j = 0; j < W; ++j) acc[j][k] = fmaf(w[j][k], g[k], acc[j][k]);
-                if (mine) {
-                    db[k] += g[k];
+                for (int k = 0; k < V; ++k) g[k] *= silu_slope(a[k], sigmoid(a[k]));
+            }
 #pragma unroll
-                    for (int j = 0; j < W; ++j) dw[j][k] = fmaf(g[k], win[j][k], dw[j][k]);
-                }
+            for (int j = 0; j < W; ++j) fma_to<V>(acc[j], w[j], g);
+            if (mine) {
+#pragma unroll
+                for (int k = 0; k < V; ++k) db[k] += g[k];
+#pragma unroll
+                for (int j = 0; j < W; ++j) fma_to<V>(dw[j], g, win[j]);
             }
         };
         if (s - halo >= t0 && s + kConvGroup <= t1 && sp.begin <= s - halo && s + kConvGroup < sp.end) {

@@ -71,6 +71,8 @@ __device__ __forceinline__ void load_params(float (&f)[V], const void *p, uint64
     else load_f32<V>(f, static_cast<const T *>(p) + i);
 }
 
+__device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -91,6 +93,48 @@ __device__ __forceinline__ float sigmoid(float x) { return rcp(1.0f + ex2(x * -k
 __device__ __forceinline__ float silu(float x) { return x * sigmoid(x); }
 // d/dx of x * sigmoid(x), from x and s = sigmoid(x).
 __device__ __forceinline__ float silu_slope(float x, float s) { return s * fmaf(x, 1.0f - s, 1.0f); }
+
+// Two f32 in one 64-bit register pair.  One packed instruction does two
+// multiply-adds at the same rate as two scalar ones but takes one issue slot
+// (measured: 2.1-2.4 cycles a warp and scheduler against 1.04 each).
+struct F2 {
+    unsigned long long v;
+};
+__device__ __forceinline__ F2 f2(float lo, float hi) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 unpack(F2 a) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+    return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+
+// acc += a * b of V values, in pairs where V is even.
+template <int V>
+__device__ __forceinline__ void fma_to(float (&acc)[V], const float (&a)[V], const float (&b)[V]) {
+    if constexpr (V % 2 == 0) {
+#pragma unroll
+        for (int i = 0; i < V; i += 2) {
+            const float2 r = unpack(fma2(f2(a[i], a[i + 1]), f2(b[i], b[i + 1]), f2(acc[i], acc[i + 1])));
+            acc[i] = r.x, acc[i + 1] = r.y;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[i] = fmaf(a[i], b[i], acc[i]);
+    }
+}
 
 // Segment of packed row `t` by CSR offsets (num_segments + 1 entries): the
 // first s with offsets[s + 1] > t, or num_segments if there is none.  Empty
