@@ -300,8 +300,10 @@ __global__ void __launch_bounds__(kColThreads)
     const int lane = threadIdx.x % 32, strand = threadIdx.x / 32;
     const int64_t c = int64_t(blockIdx.x) * 32 + lane;
     float s = 0.0f;
-    if (c < cols)
+    if (c < cols) {
+#pragma unroll 8
         for (int64_t b = strand; b < blocks; b += 8) s += part[b * cols + c];
+    }
     sh[strand][lane] = s;
     __syncthreads();
     if (strand == 0 && c < cols) {

@@ -24,7 +24,7 @@ namespace dwp {
 
 namespace {
 
-constexpr int kAhead = 4;  // rows loaded ahead of their use
+constexpr int kAhead = 2;  // rows loaded ahead of their use
 
 // Two neighbouring channels of a row, as loaded: the bits are taken apart at
 // their first use only, so that a load is waited for there and not before.
@@ -62,7 +62,7 @@ enum : int { kWalkStates = 0, kWalkOut = 1, kWalkBack = 2 };
 // code: a load under a branch is waited for where the branch ends, and the
 // rows ahead of their use would buy nothing.
 template <class T, int NT, int NL, int kMode, bool kWide>
-__global__ void __launch_bounds__(32, kScanWarpsPerSM) selscan_kernel(ScanParams p) {
+__global__ void __launch_bounds__(32, 10) selscan_kernel(ScanParams p) {
     constexpr int kC = 64 / NL, kN = NT * NL, kP = NT / 2;
     constexpr int kRows = kN <= 16 ? 16 : kN <= 32 ? 8 : 4;  // rows of B and C staged at once
     static_assert(kRows % kAhead == 0 && kCheckpointRows % kRows == 0, "");

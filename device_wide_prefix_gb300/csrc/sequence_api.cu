@@ -323,10 +323,10 @@ int64_t check_scan(Check &c, const dwp_selective_scan_args &a, bool backward) {
 
 // Chunks of rows for the forward: as many as fill the GPU's warps once, where
 // the channels alone fill less than half of them.  A cut costs a second walk
-// over the rows, about 0.65 of the first; a warp alone on its scheduler runs
-// at a third of the rate of three.  Measured at 8192 rows x 4096 channels x 16
-// states (256 warps): 1 chunk 1013 us, 4 516, 7 339, 14 342; at 65536 x 2048
-// (32 warps): 38 chunks 1726 us, 56 1218, 112 1276.
+// over the rows, about 0.6 of the first; a warp alone on its scheduler runs at
+// a third of the rate of three.  Measured at 8192 rows x 4096 channels x 16
+// states (256 warps): 1 chunk 1013 us, 6 391, 7 293, 9 345, 14 309; at 65536 x
+// 2048 (32 warps): 47 chunks 1311 us, 57 1086, 114 1107.
 int64_t chunks_of(const dwp_selective_scan_args &a, int64_t units, int64_t slots) {
     if (2 * units >= slots) return 1;
     const int64_t most = ceil_div(a.rows, DWP_SCAN_CHECKPOINT_ROWS);
