@@ -183,9 +183,11 @@ __global__ void __launch_bounds__(kConvThreads)
 // row t - j of the segment (or the state row that stands for it) receives
 // w[W-1-j] g[t].  A thread walks its strip and W - 1 rows past it with the
 // unfinished sums in registers, and writes a row's sum once the last tap
-// reached it.  Each row's g also adds to the taps' gradients, which are
-// summed over the block's strips in shared memory, written per block, and
-// summed over the blocks in a fixed order by a second kernel.
+// reached it.  Each row's g also adds to the taps' gradients, which a thread
+// sums over its strip and a second kernel over the strips, in a fixed order.
+// 4 x 2048 x 4096 bf16: 201 MB in 92 us, 11 of them the second kernel; about 70
+// instructions for two channels of a row, issue 0.64 a cycle.  Two channels a
+// thread and 28 warps an SM; four and 16 took 103.
 template <class T, int V, int W>
 __global__ void __launch_bounds__(kConvThreads, W == 4 ? 7 : 3) conv_backward_kernel(ConvBackwardParams q) {
     pdl_trigger();

@@ -87,10 +87,10 @@ def _launch(name, fields, x, stream, scratch=None):
 
 def _empty(shape, dtype, x, stream):
     """Memory on x's device that belongs to the stream the call runs on."""
-    if stream is None:
-        return x.new_empty(shape, dtype=dtype)
+    if stream is None:  # torch.empty: half of new_empty's time on the host
+        return torch.empty(shape, dtype=dtype, device=x.device)
     with torch.cuda.stream(stream):
-        return x.new_empty(shape, dtype=dtype)
+        return torch.empty(shape, dtype=dtype, device=x.device)
 
 
 def _refuse(what, *about):
@@ -367,8 +367,8 @@ def _norm_rows(t, x, what, f32=False):
     where `f32` allows it.  Zeros for None."""
     if t is None:
         return _NO_ROWS
-    if t is not x and (t.shape != x.shape or t.get_device() != x.get_device()
-                       or (t.dtype != x.dtype and not (f32 and t.dtype == torch.float32))):
+    if t is not x and (t.shape != x.shape or (t.dtype != x.dtype and not (f32 and t.dtype == torch.float32))
+                       or t.get_device() != x.get_device()):
         _refuse("%s must have the shape and device of the call's main input, and its type (a residual or sum: or float32)",
                 what)
     s, shape = t.stride(), t.shape
