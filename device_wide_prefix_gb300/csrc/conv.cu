@@ -83,7 +83,6 @@ __device__ __forceinline__ void push(float (&win)[W][V], const float (&x)[V]) {
 }
 
 constexpr int kConvGroup = 4;  // rows loaded together, one group ahead of their use
-constexpr int kConvAhead = 4;  // rows between a load and the prefetch beside it
 
 // Forward.  A thread walks kConvStrip rows of V channels with the last W - 1
 // inputs and the taps in registers, so each input is read once (plus W - 1
@@ -109,14 +108,12 @@ __global__ void __launch_bounds__(kConvThreads, W == 4 ? 6 : 2) conv_kernel(Conv
 #pragma unroll
         for (int i = 0; i < kConvGroup; ++i)
             next[i] = *reinterpret_cast<const Pack<T, V> *>(x + min(t + i, t1 - 1) * p.x_row);
-        // the registers hold too few rows in flight for HBM: the groups after
-        // this one are on their way to L2
+        // the registers hold too few rows in flight for HBM: the group after
+        // this one is on its way to L2
 #pragma unroll
         for (int i = 0; i < kConvGroup; ++i)
-            if (t + kConvAhead + i < t1) prefetch_l2(x + (t + kConvAhead + i) * p.x_row);
+            if (t + kConvGroup + i < t1) prefetch_l2(x + (t + kConvGroup + i) * p.x_row);
     };
-    for (int i = kConvGroup; i < kConvAhead; ++i)
-        if (t0 + i < t1) prefetch_l2(x + (t0 + i) * p.x_row);
     load(t0);
     float w[W][V], bias[V], win[W][V];
     load_taps<T, V, W>(p, c0, w, bias);

@@ -176,7 +176,6 @@ struct ScanBackwardParams {
     const float *grad_final;
     void *grad_u, *grad_dt, *grad_z, *grad_B, *grad_C;
     float *grad_initial;
-    int64_t carry_chunks, carry_per;  // the walk back's chunks, in all and to each chunk here
     float *partial;     // [batch * chunks][channels * (states + 2)]
     float *partial_bc;  // [channel blocks of a group][batch * rows][groups][2][states]
 };
@@ -193,9 +192,10 @@ struct ScanStepParams {
     const int32_t *slots;
     bool wide;  // four neighbouring states of A, B, C and the state are one aligned access
 };
-// Warps of the gradient that its chunks are made for: three times the eight
-// that an SM holds (255 registers a lane).  Training step of 2 x 2048 rows x
-// 4096 channels: one time 780 us, two 755, three 715, seven 694.
+// Warps an SM that the gradient's chunks are made for: three times the eight
+// that it holds at once (255 registers a lane), so that the last ones to run
+// are a small part.  Training step of 2 x 2048 rows x 4096 channels: made for
+// eight 780 us, 16 755, 24 715, 56 694 (in 3.5 times the scratch).
 constexpr int kScanBackWarpsPerSM = 24;
 // Channels one warp of the gradient covers.
 int64_t scan_block_channels(int64_t states);

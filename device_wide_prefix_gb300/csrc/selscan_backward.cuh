@@ -103,10 +103,8 @@ __global__ void __launch_bounds__(32, 8) selscan_backward_kernel(ScanBackwardPar
     for (int c = 0; c < 2; ++c)
 #pragma unroll
         for (int j = 0; j < kP; ++j) A2[c][j] = mul2(A2[c][j], f2(kLog2e, kLog2e));
-    if (chunk + 1 < p.chunks) {  // after the walk back's chunk that begins where this one ends
-        const int64_t begins = (int64_t(chunk) + 1) * q.carry_per;
-        load_state(e, p.carry, int64_t(b) * (q.carry_chunks - 1) + (q.carry_chunks - 1 - begins));
-    }
+    // the walk back's entry k is the state after it left the last chunk but k
+    if (chunk + 1 < p.chunks) load_state(e, p.carry, int64_t(b) * (p.chunks - 1) + (p.chunks - 2 - chunk));
     else load_state(e, p.segmap ? nullptr : q.grad_final, b);
 #pragma unroll
     for (int c = 0; c < 2; ++c)

@@ -67,9 +67,9 @@ struct Two<float> {
 enum : int { kWalkStates = 0, kWalkOut = 1, kWalkBack = 2 };
 
 // kWide: two neighbouring channels, and four neighbouring states of B and C,
-// are one aligned access, so that the loads are straight
-// code: a load under a branch is waited for where the branch ends, and the
-// rows ahead of their use would buy nothing.
+// are one aligned access, so that the loads are straight code: a load under a
+// branch is waited for where the branch ends, and the rows ahead of their use
+// would buy nothing.
 template <class T, int NT, int NL, int kMode, bool kWide>
 __global__ void __launch_bounds__(32, 10) selscan_kernel(ScanParams p) {
     constexpr int kC = 64 / NL, kN = NT * NL, kP = NT / 2;
@@ -91,8 +91,8 @@ __global__ void __launch_bounds__(32, 10) selscan_kernel(ScanParams p) {
     const int64_t cb = int64_t(g) * p.group + cg;
     const int live = int(min(int64_t(kC), p.group - cg));
     // Where the lane loads: its channels, or live ones in place of those past
-    // the last, so that no load needs a predicate.  Pairs (one access for both
-    // channels): live is even, and so is every first channel.
+    // the last, so that no load needs a predicate.  One access for both
+    // channels: live is even, and so is every first channel.
     const int ch = lane / NL * 2;
     const uint32_t c0 = uint32_t(min(ch, kWide ? live - 2 : live - 1)), c1 = uint32_t(min(ch + 1, live - 1));
 

@@ -437,20 +437,8 @@ dwp_status scan_backward(const dwp_selective_scan_backward_args &a, void *scratc
     ScanBackwardParams p = {};
     p.f = scan_params(f, nullptr);
     const int64_t per = scan_block_channels(f.states), blocks = ceil_div(p.f.group, per);
-    // the walk back has half as many warps to a chunk and needs fewer
-    // registers: its chunks are finer, a whole number of them to each chunk
-    ScanParams r = p.f;
-    if (n > 0) {
-        const int64_t chunks = chunks_of(f, scan_units(f, per), 152 * kScanBackWarpsPerSM);
-        const int64_t want = chunks_of(f, scan_units(f, scan_warp_channels(f.states)), 152 * kScanWarpsPerSM);
-        const int64_t finer = chunks > 1 && want > chunks ? ceil_div(want, chunks) : 1;
-        set_chunks(r, chunks * finer);
-        p.carry_per = finer;
-        p.f.chunk_rows = r.chunk_rows * finer;
-        p.f.chunks = ceil_div(f.rows, p.f.chunk_rows);
-    }
-    p.carry_chunks = r.chunks;
-    const CarrySpace carry(r);
+    if (n > 0) set_chunks(p.f, chunks_of(f, scan_units(f, per), 152 * kScanBackWarpsPerSM));
+    const CarrySpace carry(p.f);
     const size_t map = f.offsets ? round16(size_t(f.rows) * 4u) : 0u;
     const size_t part = round16(size_t(f.batch * p.f.chunks * f.channels * (f.states + 2)) * 4u);
     const size_t bc = round16(size_t(blocks * n * f.groups * 2 * f.states) * 4u);
@@ -481,9 +469,7 @@ dwp_status scan_backward(const dwp_selective_scan_backward_args &a, void *scratc
     carry.place(p.f, at + map + part + bc);
     const auto t = static_cast<dwp_dtype>(f.dtype);
     if (p.f.chunks > 1) {
-        const int64_t chunks = r.chunks, chunk_rows = r.chunk_rows;
-        r = p.f;  // as the walk back reads it
-        r.chunks = chunks, r.chunk_rows = chunk_rows;
+        ScanParams r = p.f;  // as the walk back reads it
         r.u = p.grad_out, r.u_batch = p.grad_batch, r.u_row = p.grad_row;
         r.B = p.f.C, r.b_batch = p.f.c_batch, r.b_row = p.f.c_row, r.b_group = p.f.c_group;
         r.initial = p.grad_final;
