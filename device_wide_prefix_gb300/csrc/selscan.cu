@@ -17,14 +17,25 @@ __global__ void __launch_bounds__(256) carry_kernel(ScanParams p) {
     const float A2 = p.A[i] * kLog2e;
     const int64_t first = int64_t(blockIdx.y) * (p.chunks - 1);
     float *st = p.carry + first * per + i;
+    const float *sum = p.carry_sum + first * p.channels + c;
+    const uint32_t *head = p.carry_head + first;
+    const int64_t entries = p.chunks - 1;
+    constexpr int kBatch = 16;  // loads in flight: the stores between them would hold the later ones back
     float h = 0.0f;
-#pragma unroll 8
-    for (int64_t k = 0; k < p.chunks - 1; ++k) {
-        const float e = st[k * per];
-        const float s = p.carry_sum[(first + k) * p.channels + c];
-        // a chunk with a head takes nothing from before it
-        h = p.carry_head[first + k] ? e : fmaf(ex2(A2 * s), h, e);
-        st[k * per] = h;
+    for (int64_t k0 = 0; k0 < entries; k0 += kBatch) {
+        float e[kBatch], d[kBatch];
+        bool cut[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int64_t k = min(k0 + i, entries - 1);
+            e[i] = st[k * per], d[i] = sum[k * p.channels], cut[i] = head[k] != 0u;
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            // a chunk with a head takes nothing from before it
+            h = cut[i] ? e[i] : fmaf(ex2(A2 * d[i]), h, e[i]);
+            if (k0 + i < entries) st[(k0 + i) * per] = h;
+        }
     }
 }
 

@@ -522,6 +522,46 @@ def test_results_repeat_bit_for_bit_and_on_another_stream():
         assert torch.equal(a, b) and torch.equal(a, d)
 
 
+def test_token_forms_in_a_graph():
+    """A generation step captured once and replayed: the calls allocate through torch's graph pool and wait for nothing."""
+    c = Scan(61, "bf16", (6, 1), None, 72, 16, 1)
+    pos, kw = c.args()
+    z = kw.pop("z")[:, 0]
+    one = [p if p is pos[2] else p[:, 0] for p in pos]
+    d = Draw(62, torch.bfloat16)
+    taps, _ = d.act(6, 3, 72)
+    w, _ = d.f32(72, 4)
+    g, _ = d.f32(72)
+
+    def step(conv_state, state):
+        u = dwp.causal_conv_step(one[0], conv_state, w)
+        y = dwp.selective_scan_step(u, *one[1:], state, z=z, **kw)
+        return dwp.block_norm(y, g)[0]
+
+    eager = [taps.clone(), c.t["init"].clone()]
+    want = [step(*eager).clone() for _ in range(3)]
+    state = [taps.clone(), c.t["init"].clone()]
+    step(*[t.clone() for t in state])  # the library's first calls, outside the capture
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step(*state)
+    for t, s in zip(state, (taps, c.t["init"])):
+        t.copy_(s)
+    for k in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[k])
+    assert all(torch.equal(a, b) for a, b in zip(state, eager))
+
+
+@pytest.mark.parametrize("states", [16, 40, 128])
+def test_one_step_of_many_sequences(states):
+    """More sequences than warps: nothing is cut, and every row is a sequence's first and last."""
+    c = Scan(71, "f32", (900, 1), None, 6, states, 1)
+    check_scan(c)
+
+
 def test_places_past_32_bits():
     """Rows and slots whose element offsets pass 2^32: the same numbers as in a small tensor."""
     ch = 32768
