@@ -50,8 +50,8 @@ __device__ __forceinline__ void store_residual(void *p, int64_t i, const float (
     else store_f32<V>(static_cast<T *>(p) + i, f);
 }
 
-template <class T, int V, int K, int kMost>
-__global__ void __launch_bounds__(kMost, 1) norm_kernel(NormParams p) {
+template <class T, int V, int K, int kMost, int kBlocks>
+__global__ void __launch_bounds__(kMost, kBlocks) norm_kernel(NormParams p) {
     __shared__ float sh[32];
     pdl_trigger();
     pdl_wait();
@@ -61,7 +61,7 @@ __global__ void __launch_bounds__(kMost, 1) norm_kernel(NormParams p) {
     const T *z = p.gate ? static_cast<const T *>(p.gate) + row * p.gate_row + g0 : nullptr;
     T *y = static_cast<T *>(p.y) + row * p.y_row + g0;
     // every load first: a store between them would hold the later ones back
-    float v[K][V], gt[K][V], sc[K][V], w[K][V], ss[1] = {0.0f};
+    float v[K][V], gt[K][V], sc[K][V], ss[1] = {0.0f};
 #pragma unroll
     for (int k = 0; k < K; ++k) {
         const int64_t i = (int64_t(k) * blockDim.x + threadIdx.x) * V;
@@ -71,7 +71,6 @@ __global__ void __launch_bounds__(kMost, 1) norm_kernel(NormParams p) {
             load_f32<V>(v[k], x + i);
             if (p.residual) load_residual<T, V>(sc[k], p.residual, row * p.residual_row + g0 + i, p.residual_f32);
             if (z) load_f32<V>(gt[k], z + i);
-            load_params<T, V>(w[k], p.weight, g0 + i, p.weight_f32);
         }
     }
 #pragma unroll
@@ -104,10 +103,11 @@ __global__ void __launch_bounds__(kMost, 1) norm_kernel(NormParams p) {
     for (int k = 0; k < K; ++k) {
         const int64_t i = (int64_t(k) * blockDim.x + threadIdx.x) * V;
         if (i < p.group) {
-            float o[V];
+            float o[V], w[V];
+            load_params<T, V>(w, p.weight, g0 + i, p.weight_f32);
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                o[j] = v[k][j] * r * w[k][j];
+                o[j] = v[k][j] * r * w[j];
                 if (p.gate_after) o[j] *= gt[k][j];
             }
             store_f32<V>(y + i, o);
@@ -124,7 +124,9 @@ __global__ void __launch_bounds__(kMost, 1) norm_kernel(NormParams p) {
 // adds the shares in a fixed order.
 //
 // A thread holds the raw values of its columns of one row, and loads the next
-// row's before it waits for the block's sums.  4096 x 8192 f16 in 8 groups with
+// row's before it waits for the block's sums.  The widest groups (kWideRow)
+// leave no registers for that: there the column sums are in shared memory, each
+// word one thread's own, and the weights are read again for each row.  4096 x 8192 f16 in 8 groups with
 // a gate: 336 MB in 97 us; issue (0.65 a cycle) and the wait for the sums bound
 // it.
 template <class T, int V, int K>
@@ -134,24 +136,35 @@ struct NormRow {
     Pack<T, V> dy[K], gate[K];
 };
 
-template <class T, int V, int K, bool kWideV, int kMost, int kBlocks>
+template <class T, int V, int K, bool kWideV, int kMost, int kBlocks, bool kWideRow>
 __global__ void __launch_bounds__(kMost, kBlocks) norm_backward_kernel(NormBackwardParams q) {
     __shared__ float sh[64];
+    extern __shared__ float sums[];  // kWideRow: [2][threads * K * V], a thread's own words threads apart
     pdl_trigger();
     pdl_wait();
     const NormParams &p = q.n;
     const int64_t g0 = int64_t(blockIdx.y) * p.group;
     const bool gated = p.gate != nullptr;
-    float dw[K][V], ds[K][V], w[K][V];
+    constexpr bool kW = kWideRow;
+    constexpr int kKept = kW ? 1 : K;
+    float dw[kKept][V], ds[kKept][V], w[kKept][V];
+    auto slot = [&](int which, int k, int j) -> float & {
+        return sums[((which * K + k) * V + j) * int(blockDim.x) + int(threadIdx.x)];
+    };
     int at[K];  // this thread's columns; past the group they are read from its start and not used
     bool in[K];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
         const int i = (k * int(blockDim.x) + int(threadIdx.x)) * V;
         in[k] = i < p.group, at[k] = int(g0) + (in[k] ? i : 0);
-        load_params<T, V>(w[k], p.weight, at[k], p.weight_f32);
+        if constexpr (kWideRow) {
 #pragma unroll
-        for (int j = 0; j < V; ++j) dw[k][j] = ds[k][j] = 0.0f;
+            for (int j = 0; j < V; ++j) slot(0, k, j) = slot(1, k, j) = 0.0f;
+        } else {
+            load_params<T, V>(w[k], p.weight, at[k], p.weight_f32);
+#pragma unroll
+            for (int j = 0; j < V; ++j) dw[k][j] = ds[k][j] = 0.0f;
+        }
     }
     auto load = [&](NormRow<T, V, K> &r, int64_t row) {
 #pragma unroll
@@ -165,25 +178,31 @@ __global__ void __launch_bounds__(kMost, kBlocks) norm_backward_kernel(NormBackw
         }
     };
     NormRow<T, V, K> now, next;
-    if (int64_t(blockIdx.x) < p.rows) load(next, blockIdx.x);
+    if (!kWideRow && int64_t(blockIdx.x) < p.rows) load(next, blockIdx.x);
     for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
-        now = next;
-        load(next, min(row + gridDim.x, p.rows - 1));
+        if constexpr (kWideRow) {
+            load(now, row);
+        } else {
+            now = next;
+            load(next, min(row + gridDim.x, p.rows - 1));
+        }
         auto vin = [&](int k, int j) { return kWideV ? now.v32[k].e[j] : to_f32<T>(now.v[k].e[j]); };
-        float red[2] = {0.0f, 0.0f}, sg[K][V];  // sg: sigmoid of the gate
+        float red[2] = {0.0f, 0.0f}, sg[kKept][V];  // sg: sigmoid of the gate
 #pragma unroll
-        for (int k = 0; k < K; ++k)
+        for (int k = 0; k < K; ++k) {
+            if constexpr (kWideRow) load_params<T, V>(w[0], p.weight, at[k], p.weight_f32);
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                float t = in[k] ? vin(k, j) : 0.0f, gw = to_f32<T>(now.dy[k].e[j]) * w[k][j];
+                float t = in[k] ? vin(k, j) : 0.0f, gw = to_f32<T>(now.dy[k].e[j]) * w[kWideRow ? 0 : k][j];
                 if (gated) {
-                    const float zv = to_f32<T>(now.gate[k].e[j]);
-                    sg[k][j] = sigmoid(zv);
-                    (p.gate_after ? gw : t) *= zv * sg[k][j];
+                    const float zv = to_f32<T>(now.gate[k].e[j]), s = sigmoid(zv);
+                    if (!kWideRow) sg[kWideRow ? 0 : k][j] = s;
+                    (p.gate_after ? gw : t) *= zv * s;
                 }
                 red[0] = fmaf(t, t, red[0]);
                 red[1] = fmaf(gw, t, red[1]);
             }
+        }
         block_sums(red, sh);
         const float r = rsqrtf(red[0] / float(p.group) + p.eps);
         const float m = red[1] * r / float(p.group) * r;  // mean(gw h) r: dt = r gw - t r m
@@ -191,28 +210,34 @@ __global__ void __launch_bounds__(kMost, kBlocks) norm_backward_kernel(NormBackw
         for (int k = 0; k < K; ++k) {
             if (!in[k]) continue;
             float dz[V], dv[V], add[V], xs[V];
+            if constexpr (kW) load_params<T, V>(w[0], p.weight, at[k], p.weight_f32);
             if (q.grad_sum) load_residual<T, V>(add, q.grad_sum, row * q.gsum_row + at[k], q.v_f32);
             if (q.x_in) load_f32<V>(xs, static_cast<const T *>(q.x_in) + row * q.xin_row + at[k]);
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 const float v = vin(k, j), zv = gated ? to_f32<T>(now.gate[k].e[j]) : 0.0f;
-                const float s = gated ? zv * sg[k][j] : 1.0f;
+                const float sig = !gated ? 0.0f : kW ? sigmoid(zv) : sg[kW ? 0 : k][j];
+                const float s = gated ? zv * sig : 1.0f, wj = w[kW ? 0 : k][j];
                 float g = to_f32<T>(now.dy[k].e[j]), t = v;
                 if (gated && !p.gate_after) t *= s;
                 const float h = t * r;
                 if (gated && p.gate_after) {
-                    dz[j] = g * h * w[k][j] * silu_slope(zv, sg[k][j]);
+                    dz[j] = g * h * wj * silu_slope(zv, sig);
                     g *= s;
                 }
-                dw[k][j] = fmaf(g, h, dw[k][j]);
-                float d = r * fmaf(-t, m, g * w[k][j]);
+                if constexpr (kW) slot(0, k, j) = fmaf(g, h, slot(0, k, j));
+                else dw[k][j] = fmaf(g, h, dw[k][j]);
+                float d = r * fmaf(-t, m, g * wj);
                 if (gated && !p.gate_after) {
-                    dz[j] = d * v * silu_slope(zv, sg[k][j]);
+                    dz[j] = d * v * silu_slope(zv, sig);
                     d *= s;
                 }
                 if (q.grad_sum) d += add[j];
                 dv[j] = d;
-                if (q.x_in) ds[k][j] = fmaf(d, xs[j], ds[k][j]);
+                if (q.x_in) {
+                    if constexpr (kW) slot(1, k, j) = fmaf(d, xs[j], slot(1, k, j));
+                    else ds[k][j] = fmaf(d, xs[j], ds[k][j]);
+                }
             }
             if (gated) store_f32<V>(static_cast<T *>(q.grad_gate) + row * q.ggate_row + at[k], dz);
             if (q.grad_residual) store_residual<T, V>(q.grad_residual, row * q.gres_row + at[k], dv, q.v_f32);
@@ -231,8 +256,12 @@ __global__ void __launch_bounds__(kMost, kBlocks) norm_backward_kernel(NormBackw
 #pragma unroll
     for (int k = 0; k < K; ++k) {
         if (!in[k]) continue;
-        store_f32<V>(part + at[k], dw[k]);
-        if (q.x_in) store_f32<V>(part + p.channels + at[k], ds[k]);
+        if constexpr (kWideRow) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) dw[0][j] = slot(0, k, j), ds[0][j] = slot(1, k, j);
+        }
+        store_f32<V>(part + at[k], dw[kWideRow ? 0 : k]);
+        if (q.x_in) store_f32<V>(part + p.channels + at[k], ds[kWideRow ? 0 : k]);
     }
 }
 
@@ -243,24 +272,27 @@ uint32_t threads_for(int64_t n, int v, int k) {
 }
 
 // The fewest accesses a thread that a block of kMost threads allows.
-template <class T, int V, int K, int kMost>
+template <class T, int V, int K, int kMost, int kBlocks>
 cudaError_t norm_k(const NormParams &p, cudaStream_t s) {
-    return launch_pdl(norm_kernel<T, V, K, kMost>, dim3(uint32_t(p.rows * p.groups)), dim3(threads_for(p.group, V, K)), 0,
+    return launch_pdl(norm_kernel<T, V, K, kMost, kBlocks>, dim3(uint32_t(p.rows * p.groups)), dim3(threads_for(p.group, V, K)), 0,
                       s, p);
 }
 
 template <class T, int V>
 cudaError_t norm_v(const NormParams &p, cudaStream_t s) {
     if constexpr (V == 1) {
-        if (p.group <= 1024) return norm_k<T, 1, 2, 512>(p, s);
-        if (p.group <= 4096) return norm_k<T, 1, 8, 512>(p, s);
-        return norm_k<T, 1, 16, 1024>(p, s);
+        if (p.group <= 1024) return norm_k<T, 1, 2, 512, 2>(p, s);
+        if (p.group <= 4096) return norm_k<T, 1, 8, 512, 2>(p, s);
+        return norm_k<T, 1, 16, 1024, 1>(p, s);
     } else {
-        if (p.group <= 512 * V) return norm_k<T, V, 1, 512>(p, s);
-        if (p.group <= 1024 * V) return norm_k<T, V, 2, 512>(p, s);
-        return norm_k<T, V, 32 / V, 512>(p, s);
+        if (p.group <= 512 * V) return norm_k<T, V, 1, 512, 2>(p, s);
+        if (p.group <= 1024 * V) return norm_k<T, V, 2, 512, 2>(p, s);
+        return norm_k<T, V, 32 / V, 512, 1>(p, s);
     }
 }
+
+// Shared memory for two sums of the widest group's columns.
+constexpr size_t kWideRowBytes = size_t(512) * 32 * 2 * sizeof(float);
 
 // Accesses a thread of the gradient makes for a group of `n` elements, V each.
 int64_t backward_accesses(int64_t n, int v) {
@@ -273,16 +305,23 @@ cudaError_t norm_backward_v(const NormBackwardParams &q, cudaStream_t s) {
     const NormParams &p = q.n;
     const dim3 grid(uint32_t(q.blocks), uint32_t(p.groups));
     const int64_t k = backward_accesses(p.group, V);
-    auto go = [&](auto kernel) { return launch_pdl(kernel, grid, dim3(threads_for(p.group, V, int(k))), 0, s, q); };
+    const uint32_t threads = threads_for(p.group, V, int(k));
+    auto go = [&](auto kernel) { return launch_pdl(kernel, grid, dim3(threads), 0, s, q); };
+    auto wide = [&](auto kernel) {
+        const size_t smem = size_t(threads) * k * V * 2 * sizeof(float);
+        if (device_blocks(reinterpret_cast<const void *>(kernel), 512, kWideRowBytes) == 0)
+            return cudaErrorInvalidConfiguration;
+        return launch_pdl(kernel, grid, dim3(threads), smem, s, q);
+    };
     if constexpr (V == 1) {
-        if (k == 2) return go(norm_backward_kernel<T, 1, 2, kWideV, 512, 1>);
-        if (k == 8) return go(norm_backward_kernel<T, 1, 8, kWideV, 512, 1>);
-        return go(norm_backward_kernel<T, 1, 32, kWideV, 512, 1>);
+        if (k == 2) return go(norm_backward_kernel<T, 1, 2, kWideV, 512, 1, false>);
+        if (k == 8) return go(norm_backward_kernel<T, 1, 8, kWideV, 512, 1, false>);
+        return wide(norm_backward_kernel<T, 1, 32, kWideV, 512, 1, true>);
     } else {
-        if (p.group <= 128 * V) return go(norm_backward_kernel<T, V, 1, kWideV, 128, 4>);
-        if (k == 1) return go(norm_backward_kernel<T, V, 1, kWideV, 512, 1>);
-        if (k == 2) return go(norm_backward_kernel<T, V, 2, kWideV, 512, 1>);
-        return go(norm_backward_kernel<T, V, 32 / V, kWideV, 512, 1>);
+        if (p.group <= 128 * V) return go(norm_backward_kernel<T, V, 1, kWideV, 128, 4, false>);
+        if (k == 1) return go(norm_backward_kernel<T, V, 1, kWideV, 512, 1, false>);
+        if (k == 2) return go(norm_backward_kernel<T, V, 2, kWideV, 512, 1, false>);
+        return wide(norm_backward_kernel<T, V, 32 / V, kWideV, 512, 1, true>);
     }
 }
 
