@@ -124,11 +124,12 @@ __global__ void __launch_bounds__(kMost, kBlocks) norm_kernel(NormParams p) {
 // adds the shares in a fixed order.
 //
 // A thread holds the raw values of its columns of one row, and loads the next
-// row's before it waits for the block's sums.  The widest groups (kWideRow)
-// leave no registers for that: there the column sums are in shared memory, each
-// word one thread's own, and the weights are read again for each row.  4096 x 8192 f16 in 8 groups with
-// a gate: 336 MB in 97 us; issue (0.65 a cycle) and the wait for the sums bound
-// it.
+// row's before it waits for the block's sums.  Wide groups (kWideRow) leave no
+// registers for that: there the column sums are in shared memory, each word one
+// thread's own, and the weights are read again for each row (8192 x 8192 bf16
+// with a gate: 223 us, against 472 with spilled sums).  4096 x 8192 f16 in 8
+// groups with a gate: 336 MB in 97 us; issue (0.65 a cycle) and the wait for the
+// sums bound it.
 template <class T, int V, int K>
 struct NormRow {
     Pack<float, V> v32[K];  // the norm's input in f32, or
@@ -287,6 +288,7 @@ cudaError_t norm_v(const NormParams &p, cudaStream_t s) {
     } else {
         if (p.group <= 512 * V) return norm_k<T, V, 1, 512, 2>(p, s);
         if (p.group <= 1024 * V) return norm_k<T, V, 2, 512, 2>(p, s);
+        if (p.group <= 2048 * V) return norm_k<T, V, 2, 1024, 1>(p, s);
         return norm_k<T, V, 32 / V, 512, 1>(p, s);
     }
 }
@@ -320,7 +322,7 @@ cudaError_t norm_backward_v(const NormBackwardParams &q, cudaStream_t s) {
     } else {
         if (p.group <= 128 * V) return go(norm_backward_kernel<T, V, 1, kWideV, 128, 4, false>);
         if (k == 1) return go(norm_backward_kernel<T, V, 1, kWideV, 512, 1, false>);
-        if (k == 2) return go(norm_backward_kernel<T, V, 2, kWideV, 512, 1, false>);
+        if (k == 2) return wide(norm_backward_kernel<T, V, 2, kWideV, 512, 1, true>);
         return wide(norm_backward_kernel<T, V, 32 / V, kWideV, 512, 1, true>);
     }
 }
