@@ -87,6 +87,7 @@ SHAPES = [
     ((1, 1), None), ((2, 3), None), ((37,), None), ((3, 0), None), ((0, 5), None), ((1, 130), None),
     ((70,), [0, 70]), ((70,), [0, 0, 1, 1, 33, 64, 65, 70, 70]), ((70,), [5, 5, 20, 50]), ((40,), [7, 7, 7]),
     ((100,), [0, 31, 32, 33, 96, 97, 100]), ((9,), list(range(10))), ((5,), [0]),
+    ((70,), [5, 20, 50]), ((200,), [66, 67, 140]),
 ]
 IDS = ["%s-%s" % ("x".join(map(str, s)), "batch" if o is None else "o%d_%d" % (len(o), o[0])) for s, o in SHAPES]
 
