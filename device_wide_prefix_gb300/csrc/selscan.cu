@@ -32,8 +32,9 @@ __global__ void __launch_bounds__(256) carry_kernel(ScanParams p) {
         }
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
-            // a chunk with a head takes nothing from before it
-            h = cut[i] ? e[i] : fmaf(ex2(A2 * d[i]), h, e[i]);
+            // a chunk with a head takes nothing from before it, and from a zero
+            // state nothing comes even where the product of decays overflows
+            h = cut[i] || h == 0.0f ? e[i] : fmaf(ex2(A2 * d[i]), h, e[i]);
             if (k0 + i < entries) st[(k0 + i) * per] = h;
         }
     }
@@ -53,7 +54,6 @@ __global__ void __launch_bounds__(256)
         code = s | (offsets[s] == t ? kRowHead : 0u) | (min(offsets[s + 1], rows) == t + 1u ? kRowTail : 0u);
     map[t] = code;
 }
-
 
 }  // namespace
 

@@ -481,6 +481,18 @@ def test_norm_in_place_and_batched_rows():
     assert o2 is x2 and t2 is r2 and torch.equal(o2, out) and torch.equal(t2, total)
 
 
+def test_scan_of_zeros_with_growing_states_is_zero():
+    # A > 0: a chunk's product of decays overflows, a zero state stays zero
+    rows, ch, n = 4096, 4, 16
+    z, one = torch.zeros(1, rows, ch, device="cuda"), torch.ones(1, rows, 1, n, device="cuda")
+    args = (z, torch.full_like(z, 8.0), torch.ones(ch, n, device="cuda"), one, one)
+    out, fin, points = dwp.selective_scan(*args, dt_softplus=False, return_state=True, return_checkpoints=True)
+    assert (out == 0).all() and (fin == 0).all()
+    g = dwp.selective_scan_backward(z, *args, points, dt_softplus=False)
+    for k, v in g.items():
+        assert v is None or (v == 0).all(), k
+
+
 def test_norm_of_a_row_of_zeros_is_zero():
     x = torch.zeros(2, 64, device="cuda")
     w = torch.ones(64, device="cuda")
