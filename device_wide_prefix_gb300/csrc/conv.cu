@@ -138,7 +138,8 @@ __global__ void __launch_bounds__(kConvThreads, W == 4 ? 6 : 2) conv_kernel(Conv
             }
             store_f32<V>(y + t * p.y_row, o);
         };
-        if (s > t0 && s + kConvGroup <= t1 && sp.begin <= s && s + kConvGroup < sp.end) {  // inside one segment
+        // inside one segment, and past its first row: that one loads the window
+        if (s > t0 && s + kConvGroup <= t1 && sp.begin < s && s + kConvGroup < sp.end) {
 #pragma unroll
             for (int i = 0; i < kConvGroup; ++i) row(s + i, now[i]);
             continue;
