@@ -5,11 +5,17 @@
 //
 // per channel, where rows before a segment's first come from its state rows.
 // Every element is read and written once: the work is HBM traffic.
+#include <type_traits>
+
 #include "sequence.cuh"
 
 namespace dwp {
 
 namespace {
+
+// Every kernel below is made for its width W.  One for widths up to W, with
+// taps of 0 past the width, would multiply rows that the definition does not
+// reach, and 0 times an infinity there is NaN.
 
 constexpr int kConvThreads = 128;
 constexpr int kConvStrip = 64;  // rows one thread walks
@@ -31,22 +37,23 @@ __device__ __forceinline__ Span span_at(const uint32_t *offsets, uint32_t nseg, 
 }
 
 // Taps and bias of V channels: w[j][i] is channel i's for j rows before the
-// row itself, 0 past the width.
+// row itself.
 template <class T, int V, int W, class Params>
 __device__ __forceinline__ void load_taps(const Params &p, int64_t c0, float (&w)[W][V], float (&bias)[V]) {
-    const int halo = p.width - 1;
-    if (W == 4 && p.width == 4 && p.weight_f32 && p.weight_wide) {
+    if (W == 4 && p.weight_f32 && p.weight_wide) {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const float4 v = reinterpret_cast<const float4 *>(p.weight)[c0 + i];
-            w[0][i] = v.w, w[1][i] = v.z, w[2][i] = v.y, w[W - 1][i] = v.x;
+            const float taps[4] = {v.w, v.z, v.y, v.x};
+#pragma unroll
+            for (int j = 0; j < W; ++j) w[j][i] = taps[j % 4];
         }
     } else {
 #pragma unroll
         for (int i = 0; i < V; ++i)
 #pragma unroll
             for (int j = 0; j < W; ++j)
-                w[j][i] = j <= halo ? load_param<T>(p.weight, (c0 + i) * p.width + (halo - j), p.weight_f32) : 0.0f;
+                w[j][i] = load_param<T>(p.weight, (c0 + i) * W + (W - 1 - j), p.weight_f32);
     }
 #pragma unroll
     for (int i = 0; i < V; ++i) bias[i] = p.bias ? load_param<T>(p.bias, c0 + i, p.weight_f32) : 0.0f;
@@ -57,18 +64,16 @@ __device__ __forceinline__ void load_taps(const Params &p, int64_t c0, float (&w
 template <class T, int V, int W>
 __device__ __forceinline__ void load_window(const ConvParams &p, const Span &sp, const T *x, int64_t t, int64_t c0,
                                             float (&win)[W][V]) {
-    const int halo = p.width - 1;
+    constexpr int halo = W - 1;
     const T *init = static_cast<const T *>(p.initial_state);
 #pragma unroll
     for (int j = 1; j < W; ++j) {
         const int64_t r = t - j;
 #pragma unroll
         for (int i = 0; i < V; ++i) win[j - 1][i] = 0.0f;
-        if (j <= halo) {
-            if (r >= sp.begin) load_f32<V>(win[j - 1], x + r * p.x_row);
-            else if (init)
-                load_f32<V>(win[j - 1], init + (int64_t(sp.seg) * halo + (r - sp.begin + halo)) * p.channels + c0);
-        }
+        if (r >= sp.begin) load_f32<V>(win[j - 1], x + r * p.x_row);
+        else if (init)
+            load_f32<V>(win[j - 1], init + (int64_t(sp.seg) * halo + (r - sp.begin + halo)) * p.channels + c0);
     }
 }
 
@@ -87,10 +92,10 @@ constexpr int kConvGroup = 4;  // rows loaded together, one group ahead of their
 // Forward.  A thread walks kConvStrip rows of V channels with the last W - 1
 // inputs and the taps in registers, so each input is read once (plus W - 1
 // rows per strip).  Four 16-bit channels a thread and 85 registers (24 warps an
-// SM) carry 16384 x 5120 bf16 in 84-86 us; without the prefetch it took 3 us
-// more, with eight channels and 12 warps 22, with 64 registers 29.
+// SM) carry 16384 x 5120 bf16 in 82 us; without the prefetch it took 3 us more,
+// with eight channels and 12 warps 22, with 64 registers 29.
 template <class T, int V, int W>
-__global__ void __launch_bounds__(kConvThreads, W == 4 ? 6 : 2) conv_kernel(ConvParams p) {
+__global__ void __launch_bounds__(kConvThreads, W <= 4 ? 6 : 2) conv_kernel(ConvParams p) {
     pdl_trigger();
     pdl_wait();
     const int64_t c0 = (int64_t(blockIdx.y) * kConvThreads + threadIdx.x) * V;
@@ -98,7 +103,7 @@ __global__ void __launch_bounds__(kConvThreads, W == 4 ? 6 : 2) conv_kernel(Conv
     const uint32_t b = blockIdx.x / p.strips;
     const int64_t t0 = int64_t(blockIdx.x % p.strips) * kConvStrip;
     const int64_t t1 = min(t0 + kConvStrip, p.rows);
-    const int halo = p.width - 1;
+    constexpr int halo = W - 1;
     const T *x = static_cast<const T *>(p.x) + int64_t(b) * p.x_batch + c0;
     T *y = static_cast<T *>(p.y) + int64_t(b) * p.y_batch + c0;
     T *fin = static_cast<T *>(p.final_state);
@@ -154,9 +159,8 @@ __global__ void __launch_bounds__(kConvThreads, W == 4 ? 6 : 2) conv_kernel(Conv
                 row(t, now[0]);
                 if (fin && t == sp.end - 1) {
 #pragma unroll
-                    for (int j = 0; j < W; ++j)
-                        if (j < halo)
-                            store_f32<V>(fin + (int64_t(sp.seg) * halo + (halo - 1 - j)) * p.channels + c0, win[j]);
+                    for (int j = 0; j < halo; ++j)
+                        store_f32<V>(fin + (int64_t(sp.seg) * halo + (halo - 1 - j)) * p.channels + c0, win[j]);
                 }
             }
 #pragma unroll
@@ -183,11 +187,11 @@ __global__ void __launch_bounds__(kConvThreads)
 // unfinished sums in registers, and writes a row's sum once the last tap
 // reached it.  Each row's g also adds to the taps' gradients, which a thread
 // sums over its strip and a second kernel over the strips, in a fixed order.
-// 4 x 2048 x 4096 bf16: 201 MB in 92 us, 11 of them the second kernel; about 70
-// instructions for two channels of a row, issue 0.64 a cycle.  Two channels a
-// thread and 28 warps an SM; four and 16 took 103.
+// 4 x 2048 x 4096 bf16: 201 MB in 74 us, 11 of them the second kernel (92 when
+// one kernel served every width up to four).  Two channels a thread and 28
+// warps an SM; four and 16 took 11 us more.
 template <class T, int V, int W>
-__global__ void __launch_bounds__(kConvThreads, W == 4 ? 7 : 3) conv_backward_kernel(ConvBackwardParams q) {
+__global__ void __launch_bounds__(kConvThreads, W <= 4 ? 7 : 3) conv_backward_kernel(ConvBackwardParams q) {
     pdl_trigger();
     pdl_wait();
     const ConvParams &p = q.c;
@@ -196,8 +200,8 @@ __global__ void __launch_bounds__(kConvThreads, W == 4 ? 7 : 3) conv_backward_ke
     const uint32_t b = blockIdx.x / p.strips;
     const int64_t t0 = int64_t(blockIdx.x % p.strips) * q.strip_rows;
     const int64_t t1 = min(t0 + q.strip_rows, p.rows);
-    const int64_t te = min(t1 + p.width - 1, p.rows);
-    const int halo = p.width - 1;
+    constexpr int halo = W - 1;
+    const int64_t te = min(t1 + halo, p.rows);
 
     const T *x = static_cast<const T *>(p.x) + int64_t(b) * p.x_batch + c0;
     const T *dy = static_cast<const T *>(q.grad_out) + int64_t(b) * q.grad_batch + c0;
@@ -270,9 +274,7 @@ __global__ void __launch_bounds__(kConvThreads, W == 4 ? 7 : 3) conv_backward_ke
 #pragma unroll
             for (int i = 0; i < kConvGroup; ++i) {
                 row(cx[i], cg[i], true);
-#pragma unroll
-                for (int j = 0; j < W; ++j)
-                    if (j == halo) store_f32<V>(dx + (s + i - j) * q.gx_row, acc[j]);
+                store_f32<V>(dx + (s + i - halo) * q.gx_row, acc[halo]);
             }
             continue;
         }
@@ -294,32 +296,28 @@ __global__ void __launch_bounds__(kConvThreads, W == 4 ? 7 : 3) conv_backward_ke
             }
             if (sp.begin <= t) {
                 row(cx[0], cg[0], t < t1);
-#pragma unroll
-                for (int j = 0; j < W; ++j)
-                    if (j == halo) put(t - j, acc[j]);
+                put(t - halo, acc[halo]);
                 if (t == sp.end - 1) {  // the rows that no later row of the segment reaches
 #pragma unroll
-                    for (int j = 0; j < W - 1; ++j)
-                        if (j < halo) {
-                            float v[V];
+                    for (int j = 0; j < halo; ++j) {
+                        float v[V];
 #pragma unroll
-                            for (int k = 0; k < V; ++k) v[k] = 0.0f;
-                            if (dfin) load_f32<V>(v, dfin + (int64_t(sp.seg) * halo + (halo - 1 - j)) * p.channels + c0);
+                        for (int k = 0; k < V; ++k) v[k] = 0.0f;
+                        if (dfin) load_f32<V>(v, dfin + (int64_t(sp.seg) * halo + (halo - 1 - j)) * p.channels + c0);
 #pragma unroll
-                            for (int k = 0; k < V; ++k) v[k] += acc[j][k];
-                            put(t - j, v);
-                        }
+                        for (int k = 0; k < V; ++k) v[k] += acc[j][k];
+                        put(t - j, v);
+                    }
                 }
             }
 #pragma unroll
             for (int i = 0; i + 1 < kConvGroup; ++i) cx[i] = cx[i + 1], cg[i] = cg[i + 1];
         }
     }
-    float *part = q.partial + (int64_t(blockIdx.x) * (p.width + 1)) * p.channels + c0;
+    float *part = q.partial + (int64_t(blockIdx.x) * (W + 1)) * p.channels + c0;
 #pragma unroll
-    for (int j = 0; j < W; ++j)
-        if (j <= halo) store_f32<V>(part + int64_t(halo - j) * p.channels, dw[j]);
-    store_f32<V>(part + int64_t(p.width) * p.channels, db);
+    for (int j = 0; j < W; ++j) store_f32<V>(part + int64_t(halo - j) * p.channels, dw[j]);
+    store_f32<V>(part + int64_t(W) * p.channels, db);
 }
 
 // One token for each row of a batch: the slot's W - 1 state rows and the new
@@ -331,7 +329,7 @@ __global__ void __launch_bounds__(kConvThreads) conv_step_kernel(ConvStepParams 
     const int64_t c0 = (int64_t(blockIdx.y) * kConvThreads + threadIdx.x) * V;
     if (c0 >= p.channels) return;
     const int64_t b = blockIdx.x;
-    const int halo = p.width - 1;
+    constexpr int halo = W - 1;
     T *y = static_cast<T *>(p.y) + b * p.y_row + c0;
     const int64_t slot = p.slots ? p.slots[b] : b;
     const bool live = slot >= 0 && slot < p.num_slots;  // else a padding row
@@ -344,7 +342,7 @@ __global__ void __launch_bounds__(kConvThreads) conv_step_kernel(ConvStepParams 
     for (int j = 1; j < W; ++j) {
 #pragma unroll
         for (int i = 0; i < V; ++i) win[j][i] = 0.0f;
-        if (live && j <= halo) load_f32<V>(win[j], st + int64_t(halo - j) * p.channels);
+        if (live) load_f32<V>(win[j], st + int64_t(halo - j) * p.channels);
     }
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -356,30 +354,48 @@ __global__ void __launch_bounds__(kConvThreads) conv_step_kernel(ConvStepParams 
     store_f32<V>(y, o);
     if (!live) return;
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j)
-        if (j < halo) store_f32<V>(st + int64_t(halo - 1 - j) * p.channels, win[j]);
+    for (int j = 0; j < halo; ++j) store_f32<V>(st + int64_t(halo - 1 - j) * p.channels, win[j]);
+}
+
+// go(W) for W = width, which the entry points hold to 1 .. 8.
+template <class F>
+cudaError_t by_width(int width, F go) {
+    switch (width) {
+        case 1: return go(std::integral_constant<int, 1>());
+        case 2: return go(std::integral_constant<int, 2>());
+        case 3: return go(std::integral_constant<int, 3>());
+        case 4: return go(std::integral_constant<int, 4>());
+        case 5: return go(std::integral_constant<int, 5>());
+        case 6: return go(std::integral_constant<int, 6>());
+        case 7: return go(std::integral_constant<int, 7>());
+        case 8: return go(std::integral_constant<int, 8>());
+    }
+    return cudaErrorInvalidValue;
 }
 
 template <class T, int V>
 cudaError_t conv_forward_w(const ConvParams &p, cudaStream_t s) {
     const dim3 grid(uint32_t(p.batch * p.strips), uint32_t((p.channels + kConvThreads * V - 1) / (kConvThreads * V)));
-    if (p.width <= 4) return launch_pdl(conv_kernel<T, V, 4>, grid, dim3(kConvThreads), 0, s, p);
-    return launch_pdl(conv_kernel<T, V, 8>, grid, dim3(kConvThreads), 0, s, p);
+    return by_width(p.width, [&](auto w) {
+        return launch_pdl(conv_kernel<T, V, decltype(w)::value>, grid, dim3(kConvThreads), 0, s, p);
+    });
 }
 
 template <class T, int V>
 cudaError_t conv_backward_w(const ConvBackwardParams &q, cudaStream_t s) {
     const ConvParams &p = q.c;
     const dim3 grid(uint32_t(p.batch * p.strips), uint32_t((p.channels + kConvThreads * V - 1) / (kConvThreads * V)));
-    if (p.width <= 4) return launch_pdl(conv_backward_kernel<T, V, 4>, grid, dim3(kConvThreads), 0, s, q);
-    return launch_pdl(conv_backward_kernel<T, V, 8>, grid, dim3(kConvThreads), 0, s, q);
+    return by_width(p.width, [&](auto w) {
+        return launch_pdl(conv_backward_kernel<T, V, decltype(w)::value>, grid, dim3(kConvThreads), 0, s, q);
+    });
 }
 
 template <class T, int V>
 cudaError_t conv_step_w(const ConvStepParams &p, cudaStream_t s) {
     const dim3 grid(uint32_t(p.batch), uint32_t((p.channels + kConvThreads * V - 1) / (kConvThreads * V)));
-    if (p.width <= 4) return launch_pdl(conv_step_kernel<T, V, 4>, grid, dim3(kConvThreads), 0, s, p);
-    return launch_pdl(conv_step_kernel<T, V, 8>, grid, dim3(kConvThreads), 0, s, p);
+    return by_width(p.width, [&](auto w) {
+        return launch_pdl(conv_step_kernel<T, V, decltype(w)::value>, grid, dim3(kConvThreads), 0, s, p);
+    });
 }
 
 template <class T>

@@ -1,5 +1,6 @@
 """The sequence operators at the edges of what they accept: segments that
-begin at any row.  The bar and the helpers are test_sequence_gpu's."""
+begin at any row, values that are not finite.  The bar and the helpers are test_sequence_gpu's."""
+import numpy as np
 import pytest
 
 pytestmark = pytest.mark.gpu
@@ -9,6 +10,7 @@ if not torch.cuda.is_available():
     pytest.skip("needs a CUDA GPU", allow_module_level=True)
 
 import device_wide_prefix_gb300 as dwp  # noqa: E402
+import sequence_ref as ref  # noqa: E402
 import test_sequence_gpu as base  # noqa: E402
 from device_wide_prefix_gb300 import build as dwp_build  # noqa: E402
 
@@ -30,3 +32,81 @@ def lib():
 def test_conv_of_a_segment_that_begins_after_rows_outside(rows, offsets, dtype, ch, width, pad):
     """At every place within the rows that are loaded together, and at a strip's edge."""
     base.test_conv((rows,), offsets, dtype, ch, width, pad)
+
+
+# ---------------------------------------------------------------------------
+# values that are not finite
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("act", [True, False])
+@pytest.mark.parametrize("dtype,ch", [("f32", 12), ("bf16", 16), ("f16", 7)])
+@pytest.mark.parametrize("width", [1, 2, 3, 4, 5, 6, 7, 8])
+def test_conv_keeps_bad_values_to_the_taps(width, dtype, ch, act, bad):
+    """A value in row t reaches the rows t .. t + width - 1 of its channel and segment, and no others."""
+    d = base.Draw(width, base.TYPES[dtype])
+    x, _ = d.act(150, ch)
+    w, _ = d.f32(ch, width, lo=0.5, hi=1.0)
+    dy, _ = d.act(150, ch)
+    init, _ = d.act(3, width - 1, ch)
+    cuts = [2, 90, 93, 148]
+    off, halo, c = base.offs(cuts), width - 1, 5
+
+    def run(x, init):
+        y, fin = dwp.causal_conv(x, w, None, off, init, act, return_state=True)
+        g = dwp.causal_conv_backward(dy, x, w, None, off, init, act)
+        return y, fin, g
+
+    y0, f0, g0 = run(x, init)
+    for t in (9, 62, 63, 64, 70, 87, 91, 120, 147):
+        x1 = x.clone()
+        x1[t, c] = bad
+        y1, f1, g1 = run(x1, init)
+        end = min(e for e in cuts if e > t)
+        lo, hi = max(b for b in cuts if b <= t), min(t + width, end)
+        hit = torch.zeros(150, ch, dtype=torch.bool, device="cuda")
+        hit[t:hi, c] = True
+        inside = slice(2, 148)
+        assert not torch.isfinite(y1[hit]).any() or (act and bad == -float("inf"))
+        assert torch.equal(y1[inside][~hit[inside]], y0[inside][~hit[inside]]), t
+        # the activation's slope is taken at the rows hit, and each goes back to its width - 1 rows before
+        hit[max(lo, t - halo):hi, c] = act
+        if not act:
+            hit[:] = False
+        assert torch.equal(g1["x"][inside][~hit[inside]], g0["x"][inside][~hit[inside]]), t
+        others = [i for i in range(ch) if i != c]
+        assert torch.equal(g1["weight"][others], g0["weight"][others])
+        for s in range(3):
+            for j in range(halo):
+                r = cuts[s + 1] - halo + j
+                if not (r == t and cuts[s] <= t < cuts[s + 1]):
+                    assert torch.equal(f1[s, j], f0[s, j])
+                else:
+                    assert not torch.isfinite(f1[s, j, c])
+    if halo:
+        i1 = init.clone()
+        i1[1, 0, c] = bad  # the oldest state row reaches the first row only
+        y1, _, _ = run(x, i1)
+        keep = torch.ones(150, ch, dtype=torch.bool, device="cuda")
+        keep[:2] = keep[148:] = False
+        keep[90, c] = False
+        assert torch.equal(y1[keep], y0[keep])
+
+
+@pytest.mark.parametrize("width", [1, 2, 3, 4, 5, 6, 7, 8])
+def test_conv_step_is_the_prompt_next_to_an_infinity(width):
+    """Where the prompt's output is finite so is the token's, and the same within the bar; the states are equal."""
+    d = base.Draw(40 + width, torch.float32)
+    x, xv = d.act(1, 12, 8)
+    x[0, 3, 2] = float("inf")
+    w, _ = d.f32(8, width, lo=0.5, hi=1.0)
+    y, fin = dwp.causal_conv(x, w, return_state=True)
+    cache = torch.zeros(1, width - 1, 8, device="cuda")
+    z = torch.stack([dwp.causal_conv_step(x[:, t], cache, w) for t in range(12)], 1)
+    assert torch.equal(torch.isfinite(y), torch.isfinite(z)) and int((~torch.isfinite(y)).sum()) == width
+    ok = torch.isfinite(y)
+    p, _ = ref.conv_pre(abs(np.where(np.isfinite(x[0].cpu().numpy()), xv[0], 0.0)), w.double().cpu().numpy(), np.zeros(8),
+                        np.zeros((width - 1, 8)))
+    bound = torch.from_numpy(2 * base.U * (64 + width) * (p + 1)).cuda()[None]
+    assert ((y - z).abs()[ok] <= bound[ok]).all()
+    assert torch.equal(fin, cache)
