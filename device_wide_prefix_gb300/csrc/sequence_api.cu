@@ -113,8 +113,11 @@ struct Check {
     }
     // Rows of `inner` elements of type t are whole 16-byte pieces.
     bool wide(int64_t inner, int64_t t) const { return ((bits | uintptr_t(inner * size_of(t))) & 15u) == 0; }
-    // The scratch of the two-call pattern; true: go on and launch.
+    // The scratch of the two-call pattern; true: go on and launch.  A call that
+    // needs none asks for 16 bytes: of 0 a caller's allocation may be NULL, and
+    // the second call would be taken for another query.
     bool scratch(void *p, size_t *bytes, size_t need, dwp_status *st) {
+        if (need < 16u) need = 16u;
         if (status != DWP_SUCCESS) return *st = status, false;
         if (!p) return *bytes = need, *st = DWP_SUCCESS, false;
         if (*bytes < need) return *st = DWP_ERR_SCRATCH_TOO_SMALL, false;

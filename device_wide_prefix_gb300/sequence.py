@@ -76,7 +76,7 @@ def _launch(name, fields, x, stream, scratch=None):
             st = _entry(name)(packed, None, at, None)
             if st:
                 _dwp._check(st, name)
-            scratch = _empty((size.value or 16,), torch.uint8, x, stream)
+            scratch = _empty((size.value,), torch.uint8, x, stream)
         size.value = scratch.numel()
         st = _entry(name)(packed, scratch.data_ptr(), at, handle)
     else:

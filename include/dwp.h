@@ -320,7 +320,8 @@ dwp_status dwp_linear_recurrence_f32(const float *d_a, const float *d_b, float *
  *
  * No wait on the device: these calls keep no status word.  Results are
  * deterministic, bit for bit from run to run.  Scratch follows the two-call
- * pattern above, 16-byte aligned; its contents on entry do not matter.
+ * pattern above, 16-byte aligned and never less than 16 bytes; its contents on
+ * entry do not matter.
  */
 typedef enum dwp_dtype { DWP_F32 = 0, DWP_BF16 = 1, DWP_F16 = 2 } dwp_dtype;
 
