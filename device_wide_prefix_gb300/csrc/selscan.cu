@@ -6,6 +6,19 @@ namespace dwp {
 
 namespace {
 
+// 2^x as part * lo * hi, lo and hi powers of two on the same side of 1 and
+// part in (1/2, 1] (up to |x| = 252, past which a state's product with it is
+// all but out of range).  A chunk's product of decays may be past f32's range
+// where its product with the state is not; one factor after another, the state
+// leaves the range only where the result does.
+struct Power {
+    float part, lo, hi;
+};
+__device__ __forceinline__ Power power(float x) {
+    const int n = int(ceilf(fminf(fmaxf(x, -252.0f), 252.0f))), half = n / 2;
+    return {ex2(x - float(n)), __int_as_float((half + 127) << 23), __int_as_float((n - half + 127) << 23)};
+}
+
 // Carries the states over the chunks of a batch entry, in place: entry k
 // becomes the state after chunk k.
 __global__ void __launch_bounds__(256) carry_kernel(ScanParams p) {
@@ -34,7 +47,8 @@ __global__ void __launch_bounds__(256) carry_kernel(ScanParams p) {
         for (int i = 0; i < kBatch; ++i) {
             // a chunk with a head takes nothing from before it, and from a zero
             // state nothing comes even where the product of decays overflows
-            h = cut[i] || h == 0.0f ? e[i] : fmaf(ex2(A2 * d[i]), h, e[i]);
+            const Power a = power(A2 * d[i]);
+            h = cut[i] || h == 0.0f ? e[i] : fmaf(h * a.part * a.lo, a.hi, e[i]);
             if (k0 + i < entries) st[(k0 + i) * per] = h;
         }
     }

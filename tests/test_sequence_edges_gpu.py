@@ -1,5 +1,6 @@
 """The sequence operators at the edges of what they accept: segments that
-begin at any row, values that are not finite.  The bar and the helpers are test_sequence_gpu's."""
+begin at any row, values that are not finite, growth and decay past the range
+of one f32 factor.  The bar and the helpers are test_sequence_gpu's."""
 import numpy as np
 import pytest
 
@@ -110,3 +111,33 @@ def test_conv_step_is_the_prompt_next_to_an_infinity(width):
     bound = torch.from_numpy(2 * base.U * (64 + width) * (p + 1)).cuda()[None]
     assert ((y - z).abs()[ok] <= bound[ok]).all()
     assert torch.equal(fin, cache)
+
+
+# ---------------------------------------------------------------------------
+# the scan past the range of one f32 factor
+
+
+@pytest.mark.parametrize("grow", [True, False])
+@pytest.mark.parametrize("ch,n", [(4, 16), (3, 5)])
+def test_scan_carries_a_state_over_a_chunk_past_one_factors_range(ch, n, grow):
+    """The product of a chunk's decays is past f32's range, what it does to the state is not.
+
+    Rows 16 to 31 have delta 1 and A = +-5.6: e^89.6 over them, for a state of 1e-37 (or e^-89.6 for 1e37);
+    the other rows have delta 0, so the walks on both sides keep the state as it is.
+    """
+    rows = 48
+    A = torch.full((ch, n), 5.6 if grow else -5.6, device="cuda")
+    dt = torch.zeros(1, rows, ch, device="cuda")
+    dt[:, 16:32] = 1.0
+    size = 1e-37 if grow else 1e37
+    init = torch.linspace(1.0, 2.0, ch * n, device="cuda").view(1, ch, n) * size
+    zero, B = torch.zeros(1, rows, ch, device="cuda"), torch.zeros(1, rows, n, device="cuda")
+    factor = np.exp(16 * A.double().cpu().numpy())[None]
+    want = init.double().cpu().numpy() * factor
+    # the exponent's rounding (8.08 in base 2) and the exponential's, for each of 16 rows, as in the bar
+    _, fin, points = dwp.selective_scan(zero, dt, A, B, B, initial_state=init, dt_softplus=False, return_state=True,
+                                        return_checkpoints=True)
+    base.near(fin, want, abs(want), 64 + 16 * rows, "final_state")
+    g = dwp.selective_scan_backward(zero, zero, dt, A, B, B, points, initial_state=init, dt_softplus=False,
+                                    grad_final_state=init)
+    base.near(g["initial_state"], want, abs(want), 2 * (64 + 16 * rows), "grad initial_state")
