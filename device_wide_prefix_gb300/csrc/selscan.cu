@@ -27,7 +27,7 @@ __global__ void __launch_bounds__(256) carry_kernel(ScanParams p) {
     const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x, per = p.channels * p.states;
     if (i >= per) return;
     const int64_t c = i / p.states;
-    const float A2 = p.A[i] * kLog2e;
+    const float A2 = decay_rate(p.A[i]);
     const int64_t first = int64_t(blockIdx.y) * (p.chunks - 1);
     float *st = p.carry + first * per + i;
     const float *sum = p.carry_sum + first * p.channels + c;

@@ -16,6 +16,19 @@ constexpr uint32_t kRowTail = 0x40000000u;
 constexpr uint32_t kRowSegment = 0x3fffffffu;
 constexpr uint32_t kRowOutside = 0xffffffffu;
 
+// A log2(e), held to finite values.  Past |A| = 2.4e38 it would be infinite,
+// and 0 times that (a delta of 0; a lane past the last channel) NaN, where
+// exp(0 A) is 1.
+__device__ __forceinline__ float decay_rate(float A) {
+    float r;  // the forms that hand a NaN on; a test of the infinite cost the scan 4%
+    asm("{.reg .f32 t; max.NaN.f32 t, %1, 0fFF7FFFFF; min.NaN.f32 %0, t, 0f7F7FFFFF;}" : "=f"(r) : "f"(A * kLog2e));
+    return r;
+}
+__device__ __forceinline__ F2 decay_rate(F2 A) {
+    const float2 v = unpack(A);
+    return f2(decay_rate(v.x), decay_rate(v.y));
+}
+
 // log(1 + e^x) = max(x, 0) + log1p(e^-|x|).  log1p(e) / e on [0, 1] is a
 // degree-8 polynomial fitted for the least relative error (3.0e-8; 1.8e-7
 // evaluated in f32); with the exponential's own error the result is within

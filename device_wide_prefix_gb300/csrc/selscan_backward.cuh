@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(32, 8) selscan_backward_kernel(ScanBackwardPar
 #pragma unroll
     for (int c = 0; c < 2; ++c)
 #pragma unroll
-        for (int j = 0; j < kP; ++j) A2[c][j] = mul2(A2[c][j], f2(kLog2e, kLog2e));
+        for (int j = 0; j < kP; ++j) A2[c][j] = decay_rate(A2[c][j]);
     // the walk back's entry k is the state after it left the last chunk but k
     if (chunk + 1 < p.chunks) load_state(e, p.carry, int64_t(b) * (p.chunks - 1) + (p.chunks - 2 - chunk));
     else load_state(e, p.segmap ? nullptr : q.grad_final, b);

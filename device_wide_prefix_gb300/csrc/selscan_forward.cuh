@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(32, 10) selscan_kernel(ScanParams p) {
 
     F2 A2[2][kP], h[2][kP];
     const bool whole = p.states == kN && p.states_wide;  // every lane's states are live, in 16-byte pieces
-    auto load_states = [&](F2(&v)[2][kP], const float *from, int64_t i, float scale) {
+    auto load_states = [&](F2(&v)[2][kP], const float *from, int64_t i) {
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
             const float *x = from + (i * p.channels + cb + min(ch + c, live - 1)) * p.states + n0;
@@ -106,19 +106,18 @@ __global__ void __launch_bounds__(32, 10) selscan_kernel(ScanParams p) {
 #pragma unroll
                 for (int j = 0; j < kP; j += 2) {
                     const float4 q = reinterpret_cast<const float4 *>(x)[j / 2];
-                    v[c][j] = f2(q.x * scale, q.y * scale), v[c][j + 1] = f2(q.z * scale, q.w * scale);
+                    v[c][j] = f2(q.x, q.y), v[c][j + 1] = f2(q.z, q.w);
                 }
             } else {
 #pragma unroll
                 for (int j = 0; j < kP; ++j)
-                    v[c][j] = f2(n0 + 2 * j < p.states ? x[2 * j] * scale : 0.0f,
-                                 n0 + 2 * j + 1 < p.states ? x[2 * j + 1] * scale : 0.0f);
+                    v[c][j] = f2(n0 + 2 * j < p.states ? x[2 * j] : 0.0f, n0 + 2 * j + 1 < p.states ? x[2 * j + 1] : 0.0f);
             }
         }
     };
     auto load_state = [&](const float *from, int64_t i) {
         if (from) {
-            load_states(h, from, i, 1.0f);
+            load_states(h, from, i);
         } else {
 #pragma unroll
             for (int c = 0; c < 2; ++c)
@@ -145,7 +144,11 @@ __global__ void __launch_bounds__(32, 10) selscan_kernel(ScanParams p) {
             }
         }
     };
-    load_states(A2, p.A, 0, kLog2e);
+    load_states(A2, p.A, 0);
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int j = 0; j < kP; ++j) A2[c][j] = decay_rate(A2[c][j]);
     if (kOut && chunk > 0) load_state(p.carry, int64_t(b) * (p.chunks - 1) + chunk - 1);
     else load_state(!p.segmap && chunk == 0 ? p.initial : nullptr, b);
 

@@ -83,11 +83,12 @@ __global__ void __launch_bounds__(kStepThreads, 8) scan_step_kernel(ScanStepPara
     for (int i = 0; i < kStepRows; ++i) {
         float delta = d[i] + bias;
         if (p.softplus) delta = softplus_poly(delta);
-        const float x = delta * u[i];
+        // delta, not A, times log2(e): 0 times any finite A is then 0
+        const float x = delta * u[i], rate = delta * kLog2e;
         float y = 0.0f;
 #pragma unroll
         for (int j = 0; j < kN; ++j) {
-            h[i][j] = fmaf(ex2(delta * (A[j] * kLog2e)), h[i][j], x * B[i][j]);
+            h[i][j] = fmaf(ex2(rate * A[j]), h[i][j], x * B[i][j]);
             y = fmaf(C[i][j], h[i][j], y);
         }
 #pragma unroll

@@ -141,3 +141,30 @@ def test_scan_carries_a_state_over_a_chunk_past_one_factors_range(ch, n, grow):
     g = dwp.selective_scan_backward(zero, zero, dt, A, B, B, points, initial_state=init, dt_softplus=False,
                                     grad_final_state=init)
     base.near(g["initial_state"], want, abs(want), 2 * (64 + 16 * rows), "grad initial_state")
+
+
+@pytest.mark.parametrize("ch,n", [(40, 16), (33, 5), (6, 128), (9, 24)])
+@pytest.mark.parametrize("size", [-3.4028234663852886e38, -2.5e38])
+def test_scan_of_the_lowest_decay_rate(size, ch, n):
+    """A at its type's lowest value: such a state is its last input, exp(0 A) is 1, and no other is touched."""
+    c = base.Scan(77, "f32", (1, 40), None, ch, n, 1)
+    c.t["A"][:, 1] = size
+    c.t["A"][ch - 1, :] = size
+    c.v["A"] = c.t["A"].double().cpu().numpy()
+    base.check_scan(c)
+    c.t["dt"][:, 7:9] = -200.0  # softplus gives 0 there in 32 bits; the gradient in 32 bits is then 0 times infinity
+    c.v["dt"] = c.t["dt"].double().cpu().numpy()
+    pos, kw = c.args()
+    out, fin = dwp.selective_scan(*pos, **kw, initial_state=c.t["init"], return_state=True)
+    (y, last), (ym, lastm) = ref.scan(*c.ref(0))
+    base.near(out[0], y, ym, 64 + 16 * 40, "out")
+    base.near(fin[0], last, lastm, 64 + 16 * 40, "final_state")
+    for row in (3, 8):
+        step = [c.t[k][:, row] for k in ("u", "dt")] + [c.t["A"]] + [c.t[k][:, row] for k in "BC"]
+        cache = c.t["init"].clone()
+        out = dwp.selective_scan_step(*step, cache, D=c.t["D"], z=c.t["z"][:, row], dt_bias=c.t["dt_bias"])
+        args = [v[row:row + 1] if i != 2 else v for i, v in enumerate(c.ref(0)[:5])] + [
+            c.v["D"], c.v["z"].reshape(-1, ch)[row:row + 1], c.v["dt_bias"], True, c.v["init"][0]]
+        (y, last), (ym, lastm) = ref.scan(*args)
+        base.near(out, y, ym, 80, "token out")
+        base.near(cache[0], last, lastm, 80, "token state")
