@@ -6,19 +6,6 @@ namespace dwp {
 
 namespace {
 
-// 2^x as part * lo * hi, lo and hi powers of two on the same side of 1 and
-// part in (1/2, 1] (up to |x| = 252, past which a state's product with it is
-// all but out of range).  A chunk's product of decays may be past f32's range
-// where its product with the state is not; one factor after another, the state
-// leaves the range only where the result does.
-struct Power {
-    float part, lo, hi;
-};
-__device__ __forceinline__ Power power(float x) {
-    const int n = int(ceilf(fminf(fmaxf(x, -252.0f), 252.0f))), half = n / 2;
-    return {ex2(x - float(n)), __int_as_float((half + 127) << 23), __int_as_float((n - half + 127) << 23)};
-}
-
 // Carries the states over the chunks of a batch entry, in place: entry k
 // becomes the state after chunk k.
 __global__ void __launch_bounds__(256) carry_kernel(ScanParams p) {
@@ -27,7 +14,7 @@ __global__ void __launch_bounds__(256) carry_kernel(ScanParams p) {
     const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x, per = p.channels * p.states;
     if (i >= per) return;
     const int64_t c = i / p.states;
-    const float A2 = decay_rate(p.A[i]);
+    const float A2 = 0.5f * decay_rate(p.A[i]);
     const int64_t first = int64_t(blockIdx.y) * (p.chunks - 1);
     float *st = p.carry + first * per + i;
     const float *sum = p.carry_sum + first * p.channels + c;
@@ -47,8 +34,10 @@ __global__ void __launch_bounds__(256) carry_kernel(ScanParams p) {
         for (int i = 0; i < kBatch; ++i) {
             // a chunk with a head takes nothing from before it, and from a zero
             // state nothing comes even where the product of decays overflows
-            const Power a = power(A2 * d[i]);
-            h = cut[i] || h == 0.0f ? e[i] : fmaf(h * a.part * a.lo, a.hi, e[i]);
+            // the exponential of half the sum, twice: the product of a chunk's
+            // decays may be past f32's range where the state times it is not
+            const float a = ex2(A2 * d[i]);
+            h = cut[i] || h == 0.0f ? e[i] : fmaf(h * a, a, e[i]);
             if (k0 + i < entries) st[(k0 + i) * per] = h;
         }
     }
