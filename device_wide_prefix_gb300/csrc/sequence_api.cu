@@ -32,6 +32,12 @@ bool aligned(const void *p, int64_t n) { return (reinterpret_cast<uintptr_t>(p) 
 struct Region {
     uintptr_t at;
     int64_t batch, rows, width, step, row;
+    // The same bytes, the smaller stride (or the only one) going by rows: one
+    // row a batch entry, and rows that lie outside the batch, are compared too.
+    Region by_rows() const {
+        if (rows > 1 && (batch == 1 || row <= step)) return *this;
+        return {at, rows, batch, width, row, step};
+    }
     bool empty() const { return at == 0 || batch <= 0 || rows <= 0 || width <= 0; }
     uintptr_t end() const { return at + uintptr_t((batch - 1) * step + (rows - 1) * row + width); }
     bool regular() const { return batch == 1 || step % row == 0; }
@@ -99,7 +105,7 @@ struct Check {
         bits |= reinterpret_cast<uintptr_t>(x.data) | uintptr_t(row * e) | uintptr_t(step * e);
         if (track) {
             const Region r{reinterpret_cast<uintptr_t>(x.data), batch, n, inner * e, step * e, row * e};
-            output ? regions.output(r) : regions.in(r);
+            output ? regions.output(r.by_rows()) : regions.in(r.by_rows());
         }
     }
     // dense array of `count` elements of type t; NULL allowed if optional

@@ -58,3 +58,54 @@ def test_a_size_query_never_answers_zero(name, names, good, change):
     status, size = query(name, names, good, **change)
     assert status == dwp.DWP_SUCCESS and size >= 16 and size % 16 == 0
     assert abi.call(name, names, good, size=size - 1, **change) == SMALL
+
+
+def halves(rows, batch, *, row, step):
+    """x and out as the two halves of one tensor of 2 x 64 channels."""
+    return {"batch": batch, "rows": rows, "x.data": A, "x.row_stride": row, "x.batch_stride": step,
+            "out.data": A + 64 * 4, "out.row_stride": row, "out.batch_stride": step, "initial": 0, "final": 0}
+
+
+# The calls below are accepted on the host and get as far as the launch, which reports that there is no GPU.
+ACCEPTED = dwp.DWP_ERR_CUDA
+
+
+@pytest.mark.parametrize("rows,batch,row,step", [
+    (100, 2, 128, 12800), (1, 8, 128, 128), (1, 8, 77, 128), (8, 1, 128, 99),
+    (100, 4, 512, 128),  # rows first: [rows, batch, 2 x 64]
+    (100, 4, 640, 128), (1, 1, 128, 128)])
+def test_column_ranges_of_one_tensor_do_not_overlap(rows, batch, row, step):
+    change = halves(rows, batch, row=row, step=step)
+    assert abi.call("dwp_causal_conv", abi.CONV, abi.conv_good(), **change) == ACCEPTED
+    if rows * batch > 1:  # one element into the other half
+        change["out.data"] -= 4
+        assert abi.call("dwp_causal_conv", abi.CONV, abi.conv_good(), **change) == ALIASING
+        change["out.data"] += 8
+        assert abi.call("dwp_causal_conv", abi.CONV, abi.conv_good(), **change) == ALIASING
+
+
+def test_overlap_is_never_missed():
+    """Random strides of x and out: whenever they share an element the call is refused."""
+    import random
+    rng = random.Random(1)
+    shared = 0
+    for _ in range(4000):
+        ch, rows, batch = rng.choice([1, 2, 3, 8]), rng.choice([1, 1, 2, 3, 5]), rng.choice([1, 1, 2, 4])
+        def strides():
+            row = rng.choice([ch, 2 * ch, 2 * ch + 1, 4 * ch, batch * 2 * ch])
+            step = rng.choice([ch, 2 * ch, rows * row, rows * row + ch, 2 * rows * row])
+            return row, step
+        (xr, xs), (orow, ostep) = strides(), strides()
+        if rng.random() < 0.7:
+            orow, ostep = xr, xs
+        at = rng.randrange(0, 4 * ch + 1)
+        places = lambda base, row, step: {base + b * step + t * row + c  # noqa: E731
+                                          for b in range(batch) for t in range(rows) for c in range(ch)}
+        status = abi.call("dwp_causal_conv", abi.CONV, abi.conv_good(), channels=ch, rows=rows, batch=batch, initial=0,
+                          final=0, **{"x.data": A, "x.row_stride": xr, "x.batch_stride": xs, "out.data": A + 4 * at,
+                                      "out.row_stride": orow, "out.batch_stride": ostep})
+        assert status in (INVALID, ALIASING, ACCEPTED)
+        if places(0, xr, xs) & places(at, orow, ostep):
+            shared += 1
+            assert status != ACCEPTED
+    assert shared > 500
