@@ -19,6 +19,7 @@ constexpr int64_t kMaxSegments = (int64_t(1) << 30) - 2;
 constexpr int64_t kMaxStates = 128;
 constexpr int64_t kMaxWidth = 8;
 constexpr int64_t kMaxStride = int64_t(1) << 40;
+constexpr int64_t kMaxSpan = int64_t(1) << 58;  // elements from a tensor's first row to its last, each way
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 size_t round16(size_t n) { return (n + 15u) / 16u * 16u; }
@@ -98,6 +99,9 @@ struct Check {
         // one row (or one batch entry) needs no stride
         const int64_t row = n > 1 ? x.row_stride : inner, step = batch > 1 ? x.batch_stride : inner;
         require(row >= inner && row <= kMaxStride && step >= inner && step <= kMaxStride);
+        // and what they span is counted in 64 bits below
+        if (status == DWP_SUCCESS) require(n - 1 <= kMaxSpan / row && batch - 1 <= kMaxSpan / step);
+        if (status != DWP_SUCCESS) return;
         // rows of an output may not fold onto one another
         if (output && batch > 1 && n > 1)
             require(step >= (n - 1) * row + inner || row >= (batch - 1) * step + inner);

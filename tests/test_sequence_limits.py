@@ -109,3 +109,15 @@ def test_overlap_is_never_missed():
             shared += 1
             assert status != ACCEPTED
     assert shared > 500
+
+
+@pytest.mark.parametrize("change", [
+    {"rows": 1 << 30, "batch": 1, "x.row_stride": 1 << 40}, {"rows": 1 << 30, "batch": 1, "out.row_stride": 1 << 40},
+    {"rows": 1, "batch": 1 << 30, "x.batch_stride": 1 << 40}, {"rows": 1 << 24, "batch": 64, "out.row_stride": 1 << 40,
+                                                              "out.batch_stride": 1 << 40},
+    {"rows": (1 << 31) - 1, "batch": 1, "out.row_stride": 1 << 40}])
+def test_a_span_past_the_address_space_is_refused(change):
+    """rows x stride of these would wrap around 64 bits, and the overlap checks with it."""
+    change = dict({"initial": 0, "final": 0, "x.batch_stride": 1 << 40, "out.batch_stride": 1 << 40,
+                   "x.row_stride": 64, "out.row_stride": 64}, **change)
+    assert abi.call("dwp_causal_conv", abi.CONV, abi.conv_good(), **change) == INVALID
