@@ -315,8 +315,10 @@ dwp_status dwp_linear_recurrence_f32(const float *d_a, const float *d_b, float *
  * Outputs overlap neither inputs nor one another nor the scratch
  * (DWP_ERR_ALIASING), except where a call says so; column ranges of one wider
  * tensor that share no element do not overlap.  Sizes: batch * rows < 2^31,
- * at most 2^20 channels.  DWP_ERR_INVALID_VALUE for a NULL required pointer,
- * a size or type out of range, or a stride below the row it spans.
+ * at most 2^17 channels, 1024 groups and 2^30 - 2 segments, strides up to 2^40
+ * elements, 2^58 elements from a tensor's first row to its last.
+ * DWP_ERR_INVALID_VALUE for a NULL required pointer, a size, stride or type out
+ * of range, or a stride below the row it spans.
  *
  * No wait on the device: these calls keep no status word.  Results are
  * deterministic, bit for bit from run to run.  Scratch follows the two-call
@@ -467,7 +469,8 @@ dwp_status dwp_selective_scan_step(const dwp_selective_scan_step_args *args, dwp
 
 /*
  * Root-mean-square norm around a block, over each of `groups` equal parts of
- * a row of `channels` (channels / groups at most DWP_NORM_MAX_GROUP):
+ * a row of `channels` (channels / groups at most DWP_NORM_MAX_GROUP, rows *
+ * groups < 2^31):
  *   v   = residual + scale * x, written to `sum`; or x without a residual
  *   t   = v * silu(gate) (gate given, gate_after 0), else v
  *   out = t / sqrt(mean(t^2) + eps) * weight, times silu(gate) if gate_after

@@ -121,3 +121,54 @@ def test_a_span_past_the_address_space_is_refused(change):
     change = dict({"initial": 0, "final": 0, "x.batch_stride": 1 << 40, "out.batch_stride": 1 << 40,
                    "x.row_stride": 64, "out.row_stride": 64}, **change)
     assert abi.call("dwp_causal_conv", abi.CONV, abi.conv_good(), **change) == INVALID
+
+
+def many_channels(names, good, channels):
+    """`good` with dense rows of that many channels, every tensor 16 GB from the next."""
+    g, n = good(), 0
+    for k in names:
+        if k.endswith(".data") or k in g and g[k] >= A:
+            g[k] = A + n * (16 << 30) if g.get(k) else 0
+            n += 1
+        if k.endswith(".row_stride"):
+            g[k] = channels
+        if k.endswith(".batch_stride"):
+            g[k] = 100 * channels
+    return dict(g, channels=channels)
+
+
+@pytest.mark.parametrize("name,names,good,most,change", [
+    ("dwp_causal_conv_backward", abi.CONV_BACKWARD, abi.conv_good, {"channels": 1 << 17}, {}),
+    ("dwp_causal_conv_backward", abi.CONV_BACKWARD, abi.conv_good, {"width": 8}, {}),
+    ("dwp_selective_scan", abi.SCAN, abi.scan_good, {"channels": 1 << 17}, {"groups": 1}),
+    ("dwp_selective_scan_backward", abi.SCAN_BACKWARD, abi.scan_good, {"channels": 1 << 17}, {"groups": 1}),
+    ("dwp_selective_scan_backward", abi.SCAN_BACKWARD, abi.scan_good, {"groups": 1024},
+     {"channels": 1 << 17, "b_group": 16, "c_group": 16}),
+    ("dwp_selective_scan_backward", abi.SCAN_BACKWARD, abi.scan_good, {"states": 128},
+     {"groups": 1, "B.row_stride": 129, "C.row_stride": 129, "B.batch_stride": 12900, "C.batch_stride": 12900}),
+    ("dwp_block_norm_backward", abi.NORM_BACKWARD, abi.norm_good, {"channels": 1 << 17}, {"groups": 8}),
+    ("dwp_block_norm_backward", abi.NORM_BACKWARD, abi.norm_good, {"groups": 1024}, {"channels": 1 << 17}),
+    ("dwp_block_norm_backward", abi.NORM_BACKWARD, abi.norm_good, {"rows": (1 << 28) - 1}, {"groups": 8}),
+])
+def test_stated_sizes_are_accepted_up_to_the_last(name, names, good, most, change):
+    """The size query takes the largest size that the header names, and refuses the next."""
+    channels = most.get("channels", change.get("channels", 64))
+    f = dict(many_channels(names, good, channels), **change)
+    key, last = next(iter(most.items()))
+    assert query(name, names, f, **{key: last})[0] == dwp.DWP_SUCCESS
+    # one more; a step that every other size divides
+    more = {"channels": last + f["groups"] if "groups" in f else last + 1, "groups": 2 * last}.get(key, last + 1)
+    f["channels"] = more if key == "channels" else f["channels"]
+    for k in names:
+        if key == "channels" and k.endswith(".row_stride"):
+            f[k] = more
+        if key == "channels" and k.endswith(".batch_stride"):
+            f[k] = 100 * more
+    assert query(name, names, f, **{key: more})[0] == INVALID
+
+
+def test_the_header_states_the_channels_that_the_library_takes():
+    import os
+    with open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "dwp.h")) as f:
+        text = " ".join(line.strip(" *\n") for line in f)
+    assert "at most 2^17 channels, 1024 groups" in text and "2^20 channels" not in text
