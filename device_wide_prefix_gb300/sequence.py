@@ -77,7 +77,9 @@ def _launch(name, fields, x, stream, scratch=None):
             if st:
                 _dwp._check(st, name)
             scratch = _empty((size.value,), torch.uint8, x, stream)
-        size.value = scratch.numel()
+        elif scratch.get_device() != index or not scratch.is_contiguous():
+            _refuse("scratch must be a contiguous CUDA tensor on the inputs' device")
+        size.value = scratch.numel() * scratch.element_size()
         st = _entry(name)(packed, scratch.data_ptr(), at, handle)
     else:
         st = _entry(name)(packed, handle)

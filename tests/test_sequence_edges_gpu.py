@@ -168,3 +168,28 @@ def test_scan_of_the_lowest_decay_rate(size, ch, n):
         (y, last), (ym, lastm) = ref.scan(*args)
         base.near(out, y, ym, 80, "token out")
         base.near(cache[0], last, lastm, 80, "token state")
+
+
+# ---------------------------------------------------------------------------
+# the caller's scratch
+
+
+def test_scratch_of_another_place_or_layout_is_refused():
+    """The kernels would write to where it points: host memory, or past the one byte of an expanded tensor."""
+    x = torch.randn(40, 8, device="cuda")
+    w = torch.randn(8, 4, device="cuda")
+    A, B = -torch.ones(8, 4, device="cuda"), torch.randn(40, 4, device="cuda")
+    ones = torch.ones(8, device="cuda")
+    off = torch.tensor([0, 40], dtype=torch.int32).cuda()
+    points = dwp.selective_scan(x, x, A, B, B, return_checkpoints=True)[1]
+    calls = [lambda s: dwp.causal_conv_backward(x, x, w, scratch=s)["x"],
+             lambda s: dwp.selective_scan(x, x, A, B, B, offsets=off, scratch=s),
+             lambda s: dwp.selective_scan_backward(x, x, x, A, B, B, points, scratch=s)["u"],
+             lambda s: dwp.block_norm_backward(x, x, ones, scratch=s)["x"]]
+    for call in calls:
+        want = call(None)
+        assert torch.equal(call(torch.empty(1 << 20, dtype=torch.uint8, device="cuda")), want)
+        assert torch.equal(call(torch.empty(1 << 18, device="cuda")), want)  # bytes, whatever the type
+        for bad in (torch.empty(1 << 20, dtype=torch.uint8), torch.empty(1, dtype=torch.uint8, device="cuda").expand(1 << 20)):
+            with pytest.raises(ValueError):
+                call(bad)
