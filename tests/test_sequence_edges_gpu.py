@@ -170,6 +170,24 @@ def test_scan_of_the_lowest_decay_rate(size, ch, n):
         base.near(cache[0], last, lastm, 80, "token state")
 
 
+@pytest.mark.parametrize("lo,hi", [(-4, 0), (-12, -4), (-16, -12), (-40, -16), (-80, -40), (0, 4), (4, 40)])
+def test_softplus_of_far_arguments(lo, hi):
+    """delta is the state that one row of u = B = 1 leaves.
+
+    |x| log2(e) is rounded (2^-24) after a constant that is (1.4e-8 off, both relative to |x|), the exponential adds
+    2^-22 and the polynomial, with its f32 evaluation, 1.8e-7; all relative, and for x > 0 relative to less.
+    """
+    x = torch.linspace(lo, hi, 4096, device="cuda")
+    one, B = torch.ones(1, 4096, device="cuda"), torch.ones(1, 1, device="cuda")
+    A = torch.zeros(4096, 1, device="cuda")
+    _, fin = dwp.selective_scan(one, x[None], A, B, B, return_state=True)
+    v = x.double().cpu().numpy()
+    want = np.logaddexp(v, 0.0)
+    bound = (abs(np.minimum(v, 0.0)) * (2.0 ** -24 + 1.4e-8) + 2.0 ** -22 + 1.8e-7 + 2.0 ** -24) * want
+    got = fin[0, :, 0].double().cpu().numpy()
+    assert (abs(got - want) <= bound).all(), (abs(got - want) / want).max()
+
+
 # ---------------------------------------------------------------------------
 # the caller's scratch
 
