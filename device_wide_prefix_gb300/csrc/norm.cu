@@ -288,8 +288,10 @@ cudaError_t norm_v(const NormParams &p, cudaStream_t s) {
     } else {
         if (p.group <= 512 * V) return norm_k<T, V, 1, 512, 2>(p, s);
         if (p.group <= 1024 * V) return norm_k<T, V, 2, 512, 2>(p, s);
-        if (p.group <= 2048 * V) return norm_k<T, V, 2, 1024, 1>(p, s);
-        return norm_k<T, V, 32 / V, 512, 1>(p, s);
+        // 16-bit types have V = 8 and end here; f32 has V = 4
+        if constexpr (2048 * V < DWP_NORM_MAX_GROUP)
+            if (p.group > 2048 * V) return norm_k<T, V, 32 / V, 512, 1>(p, s);
+        return norm_k<T, V, 2, 1024, 1>(p, s);
     }
 }
 
@@ -329,8 +331,9 @@ cudaError_t norm_backward_v(const NormBackwardParams &q, cudaStream_t s) {
 
 template <class T, int V>
 cudaError_t norm_backward_t(const NormBackwardParams &q, cudaStream_t s) {
-    if (sizeof(T) == 4 || !q.v_f32) return norm_backward_v<T, V, false>(q, s);
-    return norm_backward_v<T, V, true>(q, s);
+    if constexpr (sizeof(T) != 4)
+        if (q.v_f32) return norm_backward_v<T, V, true>(q, s);
+    return norm_backward_v<T, V, false>(q, s);
 }
 
 constexpr int kColThreads = 256;

@@ -74,7 +74,7 @@ template <class T, int NT, int NL, int kMode, bool kWide>
 __global__ void __launch_bounds__(32, 10) selscan_kernel(ScanParams p) {
     constexpr int kC = 64 / NL, kN = NT * NL, kP = NT / 2;
     constexpr int kRows = kN <= 16 ? 16 : kN <= 32 ? 8 : 4;  // rows of B and C staged at once
-    static_assert(kRows % kAhead == 0 && kCheckpointRows % kRows == 0, "");
+    static_assert(kRows % (2 * kAhead) == 0 && kCheckpointRows % kRows == 0, "");
     __shared__ float4 bc4[2][kRows * 2 * kN / 4];  // B, then C, of each row
     const int lane = threadIdx.x, nl = lane % NL, n0 = nl * NT;
     pdl_trigger();
@@ -390,15 +390,10 @@ __global__ void __launch_bounds__(32, 10) selscan_kernel(ScanParams p) {
         }
         if (kOut && p.checkpoints && s0 % kCheckpointRows == 0)
             save_state(p.checkpoints, int64_t(b) * p.tiles + s0 / kCheckpointRows);
-        if constexpr (kRows >= 2 * kAhead) {
 #pragma unroll 1
-            for (int r = 0; r < rows; r += 2 * kAhead) {
-                turn(s0, r, even, odd);
-                turn(s0, r + kAhead, odd, even);
-            }
-        } else {
-            turn(s0, 0, even, odd);
-            even = odd;
+        for (int r = 0; r < rows; r += 2 * kAhead) {
+            turn(s0, r, even, odd);
+            turn(s0, r + kAhead, odd, even);
         }
         if (s0 + kRows < t1) keep(k ^ 1);
         __syncwarp();
