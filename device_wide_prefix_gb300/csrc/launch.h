@@ -102,8 +102,13 @@ cudaError_t launch_recurrence(const float *a, const float *b, float *h, uint64_t
                               void *scratch, cudaStream_t stream);
 
 // ---------------------------------------------------------------------------
-// Sequence operators (conv.cu, selscan.cu, selscan_bwd.cu, norm.cu).  Strides
-// are in elements.
+// Sequence operators (conv.cu, norm.cu, selscan.cu, selscan_forward.cuh,
+// selscan_backward.cuh, selscan_step.cu).  Strides are in elements.
+
+// Streaming multiprocessors of a GB300.  Scratch sizes follow from it, and a
+// size query makes no CUDA call: on a GPU with another count the cuts are
+// other than measured, and nothing else.
+constexpr int kSMs = 152;
 
 struct ConvParams {
     int64_t channels, batch, rows, strips;  // strips: blocks of rows per batch entry

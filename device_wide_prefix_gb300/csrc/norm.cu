@@ -16,7 +16,8 @@ namespace dwp {
 
 namespace {
 
-// Sum of `a` and `b` over the block; every thread gets both.
+// Each of the N values of `v` summed over the block; every thread gets the sums.
+// sh: 32 words for each.
 template <int N>
 __device__ __forceinline__ void block_sums(float (&v)[N], float *sh) {
     const int warps = (blockDim.x + 31) / 32, warp = threadIdx.x / 32, lane = threadIdx.x % 32;

@@ -68,7 +68,8 @@ __global__ void __launch_bounds__(kStepThreads, 8) scan_step_kernel(ScanStepPara
 #pragma unroll
     for (int i = 0; i < kStepRows; ++i) {
         const int64_t b = min(b0 + i, p.batch - 1);
-        if (slot[i] < 0 || slot[i] >= p.num_slots) slot[i] = -1;  // a padding row: nothing is read or kept for it
+        // a padding row: slot 0 is read in its place, and nothing is kept
+        if (slot[i] < 0 || slot[i] >= p.num_slots) slot[i] = -1;
         const int64_t s = slot[i] < 0 ? 0 : slot[i];
         if (p.num_slots > 0)
             load_pieces<float, NL, P, kWide>(h[i], p.state + s * p.state_slot + c * p.states, nl, p.states);

@@ -403,7 +403,7 @@ dwp_status scan_forward(const dwp_selective_scan_args &a, void *scratch, size_t 
     if (st != DWP_SUCCESS) return st;
     ScanParams p = scan_params(a, static_cast<uint32_t *>(scratch));
     if (a.batch * a.rows > 0)
-        set_chunks(p, chunks_of(a, scan_units(a, scan_warp_channels(a.states)), 152 * kScanWarpsPerSM));
+        set_chunks(p, chunks_of(a, scan_units(a, scan_warp_channels(a.states)), kSMs * kScanWarpsPerSM));
     const CarrySpace carry(p);
     const size_t map = a.offsets ? round16(size_t(a.rows) * 4u) : 0u;
     const size_t need = map + carry.bytes();
@@ -450,7 +450,7 @@ dwp_status scan_backward(const dwp_selective_scan_backward_args &a, void *scratc
     ScanBackwardParams p = {};
     p.f = scan_params(f, nullptr);
     const int64_t per = scan_block_channels(f.states), blocks = ceil_div(p.f.group, per);
-    if (n > 0) set_chunks(p.f, chunks_of(f, scan_units(f, per), 152 * kScanBackWarpsPerSM));
+    if (n > 0) set_chunks(p.f, chunks_of(f, scan_units(f, per), kSMs * kScanBackWarpsPerSM));
     const CarrySpace carry(p.f);
     const size_t map = f.offsets ? round16(size_t(f.rows) * 4u) : 0u;
     const size_t part = round16(size_t(f.batch * p.f.chunks * f.channels * (f.states + 2)) * 4u);
@@ -584,7 +584,7 @@ dwp_status norm_forward(const dwp_norm_args &a, cudaStream_t s) {
 // 768 122, 1024 102.
 int64_t norm_blocks(const dwp_norm_args &a, bool wide) {
     const int64_t threads = norm_backward_threads(static_cast<dwp_dtype>(a.dtype), a.channels / a.groups, wide);
-    int64_t blocks = 152 * (512 / threads) / a.groups;
+    int64_t blocks = kSMs * (512 / threads) / a.groups;
     if (8 * blocks > a.rows) blocks = ceil_div(a.rows, 8);  // eight rows or more to each
     return blocks < 1 && a.rows > 0 ? 1 : blocks;
 }
