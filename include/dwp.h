@@ -439,6 +439,13 @@ dwp_status dwp_selective_scan(const dwp_selective_scan_args *args, void *d_scrat
  *               states], dense, dtype
  *   grad_A f32 [channels, states];  grad_D, grad_dt_bias f32 [channels], or
  *               NULL;  grad_initial_state  NULL, or as initial_state
+ *   scratch     grows with rows x channels: it holds a share of grad_B and
+ *               grad_C, 8 * states bytes, for each row, group and block of the
+ *               group's channels, a block being 32 channels at up to 16
+ *               states, 16 at up to 32, 8 at up to 64 and 4 above.  That is 4
+ *               bytes a row and channel at 16 states, 16 at 32, 64 at 64 and
+ *               256 at 128.  Beside it up to 17 MB, or 4 * batch * channels *
+ *               (states + 2) bytes where that is more, and 4 bytes a packed row.
  */
 typedef struct dwp_selective_scan_backward_args {
     dwp_selective_scan_args scan;

@@ -172,3 +172,20 @@ def test_the_header_states_the_channels_that_the_library_takes():
     with open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "dwp.h")) as f:
         text = " ".join(line.strip(" *\n") for line in f)
     assert "at most 2^17 channels, 1024 groups" in text and "2^20 channels" not in text
+
+
+@pytest.mark.parametrize("states,block", [(16, 32), (20, 16), (32, 16), (64, 8), (100, 4), (128, 4)])
+@pytest.mark.parametrize("rows,channels,groups", [(2048, 4096, 1), (8192, 4096, 4), (4096, 1000, 1),
+                                                  (7, 64, 2), (1, 4096, 1)])
+@pytest.mark.parametrize("batch", [1, 2, 300])
+def test_the_gradients_scratch_is_what_the_header_says(states, block, batch, rows, channels, groups):
+    f = dict(many_channels(abi.SCAN_BACKWARD, abi.scan_good, channels), states=states, groups=groups, batch=batch, rows=rows,
+             b_group=states, c_group=states)
+    wide = max(channels, groups * states)
+    for k in abi.SCAN_BACKWARD:
+        if k.endswith("_stride"):
+            f[k] = {"batch_stride": rows * wide, "row_stride": wide}.get(k.split(".")[-1], states)
+    status, size = query("dwp_selective_scan_backward", abi.SCAN_BACKWARD, f)
+    shares = 8 * states * batch * rows * groups * -(-channels // groups // block)
+    assert status == dwp.DWP_SUCCESS
+    assert shares <= size <= shares + max(17e6, 4 * batch * channels * (states + 2)) + 64
