@@ -94,6 +94,46 @@ def test_conv_keeps_bad_values_to_the_taps(width, dtype, ch, act, bad):
         assert torch.equal(y1[keep], y0[keep])
 
 
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("key", ["u", "dt", "z", "dout", "B", "C"])
+@pytest.mark.parametrize("ch,n,groups", [(12, 8, 1), (70, 16, 2), (6, 128, 1)])
+def test_scan_gradient_keeps_bad_values_to_their_sequence(ch, n, groups, key, bad):
+    """Rows outside are in no sum; a value inside reaches its sequence, and its channel but for the sums over channels."""
+    c = base.Scan(5, "f32", (700,), [2, 200, 203, 203, 500, 698], ch, n, groups)
+    pos, kw = c.args()
+    off = base.offs(c.offsets)
+
+    def run():
+        out, fin, points = dwp.selective_scan(*pos, **kw, offsets=off, initial_state=c.t["init"], return_state=True,
+                                              return_checkpoints=True)
+        g = dwp.selective_scan_backward(c.t["dout"], *pos, points, **kw, offsets=off, initial_state=c.t["init"],
+                                        grad_final_state=c.t["dfinal"])
+        return dict(g, out=out, fin=fin)
+
+    by_row = ("out", "u", "dt", "z", "B", "C")
+    r0 = run()
+    c.t[key][:2] = bad
+    c.t[key][698:] = bad
+    r1 = run()
+    for k, v in r0.items():
+        rows = slice(2, 698) if k in by_row else slice(None)
+        assert torch.equal(v[rows], r1[k][rows]), k
+    at = (350, 0, 0) if key in "BC" else (350, 5)
+    c.t[key][at] = bad
+    r2 = run()
+    others = [t for t in range(2, 698) if not 203 <= t < 500]
+    for k in by_row:
+        assert torch.equal(r0[k][others], r2[k][others]), k
+    for k in ("fin", "initial_state"):
+        assert torch.equal(r0[k][[0, 1, 2, 4]], r2[k][[0, 1, 2, 4]]), k
+    if key not in "BC":
+        apart = [i for i in range(ch) if i != 5]
+        for k in ("out", "u", "dt", "z"):
+            assert torch.equal(r0[k][2:698][:, apart], r2[k][2:698][:, apart]), k
+        for k in ("A", "D", "dt_bias"):
+            assert torch.equal(r0[k][apart], r2[k][apart]), k
+
+
 @pytest.mark.parametrize("width", [1, 2, 3, 4, 5, 6, 7, 8])
 def test_conv_step_is_the_prompt_next_to_an_infinity(width):
     """Where the prompt's output is finite so is the token's, and the same within the bar; the states are equal."""
