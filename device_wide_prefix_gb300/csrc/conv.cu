@@ -92,8 +92,9 @@ constexpr int kConvGroup = 4;  // rows loaded together, one group ahead of their
 // Forward.  A thread walks kConvStrip rows of V channels with the last W - 1
 // inputs and the taps in registers, so each input is read once (plus W - 1
 // rows per strip).  Four 16-bit channels a thread and 85 registers (24 warps an
-// SM) carry 16384 x 5120 bf16 in 82 us; without the prefetch it took 3 us more,
-// with eight channels and 12 warps 22, with 64 registers 29.
+// SM) carry 16384 x 5120 bf16 in 82 us, 97 warp instructions a row, issue 0.71 a
+// cycle; without the prefetch it took 3 us more, with eight channels and 12
+// warps 22, with 64 registers 29.
 template <class T, int V, int W>
 __global__ void __launch_bounds__(kConvThreads, W <= 4 ? 6 : 2) conv_kernel(ConvParams p) {
     pdl_trigger();
@@ -188,8 +189,9 @@ __global__ void __launch_bounds__(kConvThreads)
 // reached it.  Each row's g also adds to the taps' gradients, which a thread
 // sums over its strip and a second kernel over the strips, in a fixed order.
 // 4 x 2048 x 4096 bf16: 201 MB in 74 us, 11 of them the second kernel (92 when
-// one kernel served every width up to four).  Two channels a thread and 28
-// warps an SM; four and 16 took 11 us more.
+// one kernel served every width up to four); 94 warp instructions a row, issue
+// 0.64 a cycle.  Two channels a thread and 28 warps an SM; four and 16 took 11
+// us more.
 template <class T, int V, int W>
 __global__ void __launch_bounds__(kConvThreads, W <= 4 ? 7 : 3) conv_backward_kernel(ConvBackwardParams q) {
     pdl_trigger();

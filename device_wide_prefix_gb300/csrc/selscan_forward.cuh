@@ -20,8 +20,8 @@
 // What bounds it: per state update 4 multiply-adds' worth of f32 work and one
 // exponential (4 cycles a warp each way), and per row and channel about 45
 // instructions of softplus, gate and accesses, a third of the whole at 16
-// states.  8192 rows x 4096 channels x 16 states bf16: 294 us (first pass 120,
-// second 172), issue 0.62-0.64 a cycle at 2 to 2.5 warps a scheduler.  Packed
+// states.  8192 rows x 4096 channels x 16 states bf16: 295 us (first pass 120,
+// second 172), issue 0.61-0.64 a cycle at 2.4 to 2.6 warps a scheduler.  Packed
 // f32 instructions keep the rate of the scalar ones in half the issue slots.
 // Fewer registers for more warps lost (one channel a lane 331 us; 128 registers
 // 430), so did more rows in flight a lane (four 324, one 356, two 294).
