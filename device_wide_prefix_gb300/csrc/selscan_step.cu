@@ -68,11 +68,11 @@ __global__ void __launch_bounds__(kStepThreads, 8) scan_step_kernel(ScanStepPara
 #pragma unroll
     for (int i = 0; i < kStepRows; ++i) {
         const int64_t b = min(b0 + i, p.batch - 1);
-        // a padding row: slot 0 is read in its place, and nothing is kept
+        // a padding row keeps nothing, and A stands for its state in the loads:
+        // any slot may be another row's to write
         if (slot[i] < 0 || slot[i] >= p.num_slots) slot[i] = -1;
-        const int64_t s = slot[i] < 0 ? 0 : slot[i];
-        if (p.num_slots > 0)
-            load_pieces<float, NL, P, kWide>(h[i], p.state + s * p.state_slot + c * p.states, nl, p.states);
+        const float *from = slot[i] < 0 ? p.A : p.state + slot[i] * p.state_slot;
+        load_pieces<float, NL, P, kWide>(h[i], from + c * p.states, nl, p.states);
         load_pieces<T, NL, P, kWide>(B[i], static_cast<const T *>(p.B) + b * p.b_row + g * p.b_group, nl, p.states);
         load_pieces<T, NL, P, kWide>(C[i], static_cast<const T *>(p.C) + b * p.c_row + g * p.c_group, nl, p.states);
         d[i] = to_f32<T>(static_cast<const T *>(p.dt)[b * p.dt_row + c]);

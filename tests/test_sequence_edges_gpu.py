@@ -251,3 +251,37 @@ def test_scratch_of_another_place_or_layout_is_refused():
         for bad in (torch.empty(1 << 20, dtype=torch.uint8), torch.empty(1, dtype=torch.uint8, device="cuda").expand(1 << 20)):
             with pytest.raises(ValueError):
                 call(bad)
+
+
+# ---------------------------------------------------------------------------
+# padding rows of the token forms
+
+
+@pytest.mark.parametrize("n", [16, 12])
+@pytest.mark.parametrize("slots", [[-1] * 5, [7, -1, 0, 2 ** 31 - 1, -2 ** 31], [0, 0x7000, 1, -1, 2]])
+@pytest.mark.parametrize("cache", [0, 1, 4])
+def test_padding_rows_leave_every_state_as_it_is(cache, slots, n):
+    """A slot outside the cache, whatever its number, and a cache of no slots at all."""
+    c = base.Scan(9, "bf16", (5, 1), None, 72, n, 1, slots=cache or 1)
+    pos, kw = c.args()
+    z = kw.pop("z")[:, 0]
+    one = [p if p is pos[2] else p[:, 0] for p in pos]
+    d = base.Draw(10, torch.bfloat16)
+    taps, _ = d.act(cache, 3, 72)
+    w, _ = d.f32(72, 4)
+    live = [i for i, s in enumerate(slots) if 0 <= s < cache]
+    at = torch.tensor(slots, dtype=torch.int32).cuda()
+    state = c.t["init"][:cache].clone()
+    before, taps0 = state.clone(), taps.clone()
+    out = dwp.selective_scan_step(*one, state, z=z, slots=at, **kw)
+    y = dwp.causal_conv_step(one[0], taps, w, slots=at)
+    dead = [i for i in range(5) if i not in live]
+    assert (out[dead] == 0).all() and (y[dead] == 0).all()
+    if live:  # alone, in the same slots
+        few, ft = before.clone(), taps0.clone()
+        rows = [p if p is pos[2] else p[live] for p in one]
+        assert torch.equal(out[live], dwp.selective_scan_step(*rows, few, z=z[live], slots=at[live], **kw))
+        assert torch.equal(y[live], dwp.causal_conv_step(one[0][live], ft, w, slots=at[live]))
+        assert torch.equal(state, few) and torch.equal(taps, ft)
+    else:
+        assert torch.equal(state, before) and torch.equal(taps, taps0)
