@@ -1,7 +1,7 @@
 // Selective state space scan, the single-token form: each row of a batch
 // moves its sequence's state on by one step and reads it out.  The state is
 // read and written once, and that is nearly all of the traffic: at batch 256 x
-// 4096 channels x 16 states 142 MB in 26 us, 0.82 of the copy rate.  Two batch
+// 4096 channels x 16 states 142 MB in 26 us, 0.81 of the copy rate.  Two batch
 // rows a thread, 32 warps an SM; four states a lane instead of eight took 36
 // us (twice the softplus and addresses), four rows 30, one row 27.
 #include "selscan.cuh"
