@@ -68,6 +68,11 @@ EXPORTS = [
     "dwp_selective_scan_step",
     "dwp_block_norm",
     "dwp_block_norm_backward",
+    "dwp_gated_delta_rule",
+    "dwp_gated_delta_rule_backward",
+    "dwp_gated_delta_rule_step",
+    "dwp_layer_norm",
+    "dwp_layer_norm_backward",
 ]
 
 _lib = None
@@ -129,14 +134,14 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.dwp_scan_static_scratch.restype = c.c_int
     lib.dwp_scan_two_level.argtypes = [c.c_int, c.c_int, P, P, S, P, Z, P]
     lib.dwp_scan_two_level.restype = c.c_int
-    lib.dwp_causal_conv.argtypes = [c.c_char_p, P]
-    lib.dwp_causal_conv_step.argtypes = [c.c_char_p, P]
-    lib.dwp_selective_scan_step.argtypes = [c.c_char_p, P]
-    lib.dwp_block_norm.argtypes = [c.c_char_p, P]
+    for name in ("dwp_causal_conv", "dwp_causal_conv_step", "dwp_selective_scan_step", "dwp_block_norm",
+                 "dwp_gated_delta_rule_step", "dwp_layer_norm"):
+        getattr(lib, name).argtypes = [c.c_char_p, P]
+        getattr(lib, name).restype = c.c_int
     for name in ("dwp_causal_conv_backward", "dwp_selective_scan", "dwp_selective_scan_backward",
-                 "dwp_block_norm_backward"):
+                 "dwp_block_norm_backward", "dwp_gated_delta_rule", "dwp_gated_delta_rule_backward",
+                 "dwp_layer_norm_backward"):
         getattr(lib, name).argtypes = [c.c_char_p, P, Z, P]
-    for name in EXPORTS[-8:]:
         getattr(lib, name).restype = c.c_int
     if path == LIB_PATH:
         _lib = lib
@@ -560,7 +565,8 @@ def read_fallbacks(scratch, stream=None) -> int:
 # sequence operators (their module needs torch, which the C layer does not)
 
 _SEQUENCE = ("causal_conv", "causal_conv_backward", "causal_conv_step", "selective_scan",
-             "selective_scan_backward", "selective_scan_step", "block_norm", "block_norm_backward")
+             "selective_scan_backward", "selective_scan_step", "block_norm", "block_norm_backward", "gated_delta_rule",
+             "gated_delta_rule_backward", "gated_delta_rule_step", "layer_norm", "layer_norm_backward")
 
 
 def __getattr__(name):

@@ -1,0 +1,142 @@
+// The gated delta rule: what its kernels share.
+//
+// Per sequence and head, with a state S of keys x values and a = exp(g):
+//
+//   S' = a S;  u = beta (v - S'^T k);  S = S' + k u^T;  o = scale S^T q
+//
+// Over a chunk of 64 rows that begins at state S0, with G the running sum of
+// g in the chunk (G_C its last) and M_ij = exp(G_i - G_j) k_i.k_j:
+//
+//   T = (1 + strictly lower part of diag(beta) M)^-1
+//   U = T diag(beta) (V - diag(e^G) K S0)
+//   O = scale (diag(e^G) Q S0 + A U),   A_ij = exp(G_i - G_j) q_i.k_j, j <= i
+//   S1 = e^{G_C} S0 + K^T diag(e^{G_C - G}) U
+//
+// T and A depend on the chunk alone (delta_local.cu, all chunks at once); the
+// states go from chunk to chunk (delta_chain.cu).  The gradient walks the
+// chunks back for the states' gradients (delta_chain.cu) and then has all
+// chunks at once again (delta_grad.cu).
+#pragma once
+
+#include "sequence.cuh"
+
+namespace dwp {
+
+constexpr int kChunk = 64;
+
+// Log decays below this count as this: its exponential is 0 in f32 all the
+// same, and sums of it stay finite, so that differences of sums are numbers.
+constexpr float kLeastDecay = -110.0f;
+
+// One chunk: its rows, and the sequence it belongs to.
+struct DeltaChunk {
+    int64_t batch, row;  // batch entry and first row in it
+    int rows;            // rows in it, 0: no chunk here
+    int64_t seq;
+};
+
+// First row and rows of a sequence, for any offsets inside the rows.
+__device__ __forceinline__ void delta_sequence(const DeltaParams &p, int64_t seq, int64_t &batch, int64_t &row,
+                                               int64_t &rows, int64_t &slot) {
+    if (p.offsets) {
+        const int64_t lo = min(int64_t(p.offsets[seq]), p.rows), hi = min(int64_t(p.offsets[seq + 1]), p.rows);
+        batch = 0, row = lo, rows = hi > lo ? hi - lo : 0;
+        slot = lo / kChunk + seq;  // sequences' places are apart: ceil(b/64) <= (a+b)/64 - a/64 + 1
+    } else {
+        batch = seq, row = 0, rows = p.rows, slot = seq * p.chunks;
+    }
+}
+
+// The chunk at a place.
+__device__ __forceinline__ DeltaChunk delta_chunk(const DeltaParams &p, int64_t slot) {
+    DeltaChunk c;
+    int64_t first;
+    if (p.offsets) {
+        // the last sequence whose first place is not past this one
+        int64_t lo = 0, hi = p.sequences;
+        while (hi - lo > 1) {
+            const int64_t mid = (lo + hi) / 2;
+            if (min(int64_t(p.offsets[mid]), p.rows) / kChunk + mid <= slot) lo = mid;
+            else hi = mid;
+        }
+        c.seq = lo;
+    } else {
+        c.seq = slot / p.chunks;
+    }
+    int64_t rows;
+    delta_sequence(p, c.seq, c.batch, c.row, rows, first);
+    const int64_t at = (slot - first) * kChunk;
+    c.row += at;
+    c.rows = at < 0 || at >= rows ? 0 : int(min(rows - at, int64_t(kChunk)));
+    return c;
+}
+
+template <class T>
+__device__ __forceinline__ T *delta_at(const DeltaRows &r, int64_t batch, int64_t row, int head) {
+    return reinterpret_cast<T *>(r.data) + batch * r.batch + row * r.row + head * r.head;
+}
+
+template <class T>
+__device__ __forceinline__ float delta_beta(const DeltaParams &p, int64_t batch, int64_t row, int head) {
+    return p.beta_f32 ? *delta_at<float>(p.beta, batch, row, head) : to_f32<T>(*delta_at<T>(p.beta, batch, row, head));
+}
+
+__device__ __forceinline__ float delta_g(const DeltaRows &g, int64_t batch, int64_t row, int head) {
+    if (!g.data) return 0.0f;
+    const float v = *delta_at<float>(g, batch, row, head);
+    return v < kLeastDecay ? kLeastDecay : v;  // a NaN stays one
+}
+
+// A sum in two f32: differences of sums far from 0 keep their last bits.
+struct Sum2 {
+    float hi, lo;
+};
+__device__ __forceinline__ Sum2 sum2_add(Sum2 a, Sum2 b) {
+    const float s = a.hi + b.hi, t = s - a.hi;
+    const float e = (a.hi - (s - t)) + (b.hi - t) + (a.lo + b.lo);
+    const float h = s + e;
+    return {h, e - (h - s)};
+}
+__device__ __forceinline__ float sum2_less(Sum2 a, Sum2 b) { return (a.hi - b.hi) + (a.lo - b.lo); }
+
+// Running sums of the chunk's log decays, by one warp: lane l has rows l and l + 32.
+template <class F>
+__device__ __forceinline__ void delta_sums(Sum2 *sums, F g) {
+    const int lane = threadIdx.x % 32;
+    Sum2 a = {g(lane), 0.0f}, b = {g(lane + 32), 0.0f};
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+        const Sum2 pa = {__shfl_up_sync(0xffffffffu, a.hi, o), __shfl_up_sync(0xffffffffu, a.lo, o)};
+        const Sum2 pb = {__shfl_up_sync(0xffffffffu, b.hi, o), __shfl_up_sync(0xffffffffu, b.lo, o)};
+        if (lane >= o) a = sum2_add(pa, a), b = sum2_add(pb, b);
+    }
+    const Sum2 half = {__shfl_sync(0xffffffffu, a.hi, 31), __shfl_sync(0xffffffffu, a.lo, 31)};
+    sums[lane] = a;
+    sums[lane + 32] = sum2_add(half, b);
+}
+
+// store(i, j, sum over k < kk of a(i, k) b(k, j)) for i < m, j < n.
+template <class FA, class FB, class FS>
+__device__ __forceinline__ void delta_product(int m, int n, int kk, FA a, FB b, FS store) {
+    const int mt = (m + 3) / 4, nt = (n + 3) / 4;
+    for (int e = threadIdx.x; e < mt * nt; e += blockDim.x) {
+        const int i0 = e / nt * 4, j0 = e % nt * 4;
+        float s[4][4] = {};
+        for (int k = 0; k < kk; ++k) {
+            float x[4], y[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = a(min(i0 + i, m - 1), k), y[i] = b(k, min(j0 + i, n - 1));
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) s[i][j] = fmaf(x[i], y[j], s[i][j]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (i0 + i < m && j0 + j < n) store(i0 + i, j0 + j, s[i][j]);
+    }
+}
+
+}  // namespace dwp

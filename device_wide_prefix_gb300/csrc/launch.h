@@ -228,6 +228,49 @@ cudaError_t launch_scan_walk_back_bf16(const ScanParams &p, cudaStream_t s);
 cudaError_t launch_scan_walk_back_f16(const ScanParams &p, cudaStream_t s);
 cudaError_t launch_selscan_step(dwp_dtype t, const ScanStepParams &p, cudaStream_t s);
 
+// Gated delta rule (delta_local.cu, delta_chain.cu, delta_grad.cu,
+// delta_step.cu).  Rows of [heads, keys] or [heads, values].
+struct DeltaRows {
+    char *data;
+    int64_t batch, row, head;  // strides in elements
+};
+struct DeltaParams {
+    int keys, values, key_heads, heads;
+    int64_t batch, rows, sequences, chunks, slots;  // chunks: of a batch entry; slots: chunk places in all
+    float scale;
+    bool beta_f32;
+    DeltaRows q, k, v, out, g, beta;  // g.data NULL: no decay
+    const uint32_t *offsets;
+    const float *initial;
+    float *final;
+    // [slots][heads]: state before the chunk [keys][values], corrections u
+    // [64][values] (both NULL without a gradient), inverse and weights [64][64]
+    float *states, *u, *inverse, *weights;
+};
+struct DeltaBackwardParams {
+    DeltaParams f;
+    DeltaRows grad_out, grad_q, grad_k, grad_v, grad_g, grad_beta;
+    const float *grad_final;
+    float *grad_initial;
+    float *ends, *dr;  // [slots][heads]: gradient of the state after the chunk, and of the corrections' right sides
+    float *share;      // [slots][heads][2][64][keys]: shares of grad_q and grad_k where key heads are shared
+};
+struct DeltaStepParams {
+    int keys, values, key_heads, heads;
+    int64_t batch, num_slots;
+    float scale;
+    bool beta_f32, wide;  // wide: four neighbouring values of v, out and the states are one aligned access
+    DeltaRows q, k, v, out, g, beta;
+    float *state;
+    int64_t state_slot;
+    const int32_t *slots;
+};
+cudaError_t launch_delta_local(dwp_dtype t, const DeltaParams &p, cudaStream_t s);
+cudaError_t launch_delta_chain(dwp_dtype t, const DeltaParams &p, cudaStream_t s);
+cudaError_t launch_delta_chain_back(dwp_dtype t, const DeltaBackwardParams &p, cudaStream_t s);
+cudaError_t launch_delta_grad(dwp_dtype t, const DeltaBackwardParams &p, cudaStream_t s);
+cudaError_t launch_delta_step(dwp_dtype t, const DeltaStepParams &p, cudaStream_t s);
+
 struct NormParams {
     int64_t channels, group, groups, rows;  // group: elements normed together
     float eps;
@@ -250,5 +293,28 @@ cudaError_t launch_norm(dwp_dtype t, const NormParams &p, bool vec, cudaStream_t
 // Threads of one block of the gradient.
 int64_t norm_backward_threads(dwp_dtype t, int64_t group, bool vec);
 cudaError_t launch_norm_backward(dwp_dtype t, const NormBackwardParams &p, bool vec, cudaStream_t s);
+
+struct LayerNormParams {
+    int64_t channels, group, groups, rows;  // group: elements normed together
+    float eps;
+    int team;  // threads of a row's group (set by the launcher)
+    bool weight_f32, residual_f32;
+    const void *x, *residual, *weight, *bias;
+    void *y, *sum;
+    int64_t x_row, residual_row, y_row, sum_row;
+};
+struct LayerNormBackwardParams {
+    LayerNormParams n;
+    int64_t blocks;  // blocks a group's rows are spread over
+    const void *v, *grad_out, *grad_sum;  // v: the norm's input
+    bool v_f32;
+    void *grad_x, *grad_residual;
+    int64_t v_row, grad_row, gsum_row, gx_row, gres_row;
+    float *partial;  // NULL, or [blocks][weight, bias][channels]
+};
+cudaError_t launch_layer_norm(dwp_dtype t, const LayerNormParams &p, bool vec, cudaStream_t s);
+// Rows that a block of the gradient takes at once.
+int64_t layer_norm_teams(dwp_dtype t, int64_t group, bool vec);
+cudaError_t launch_layer_norm_backward(dwp_dtype t, const LayerNormBackwardParams &p, bool vec, cudaStream_t s);
 
 }  // namespace dwp

@@ -7,158 +7,11 @@
 #include <cstdint>
 
 #include "launch.h"
+#include "sequence_check.h"
 
 namespace {
 
 using namespace dwp;
-
-constexpr int64_t kMaxRows = (int64_t(1) << 31) - 1;  // batch * rows
-constexpr int64_t kMaxChannels = int64_t(1) << 17;
-constexpr int64_t kMaxGroups = 1024;
-constexpr int64_t kMaxSegments = (int64_t(1) << 30) - 2;
-constexpr int64_t kMaxStates = 128;
-constexpr int64_t kMaxWidth = 8;
-constexpr int64_t kMaxStride = int64_t(1) << 40;
-constexpr int64_t kMaxSpan = int64_t(1) << 58;  // elements from a tensor's first row to its last, each way
-
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-size_t round16(size_t n) { return (n + 15u) / 16u * 16u; }
-
-bool dtype_ok(int64_t t) { return t == DWP_F32 || t == DWP_BF16 || t == DWP_F16; }
-int64_t size_of(int64_t t) { return t == DWP_F32 ? 4 : 2; }
-bool aligned(const void *p, int64_t n) { return (reinterpret_cast<uintptr_t>(p) & uintptr_t(n - 1)) == 0; }
-
-// Bytes that a tensor of rows covers: `rows` pieces of `width` bytes, `row`
-// bytes apart, in each of `batch` entries `step` bytes apart.
-struct Region {
-    uintptr_t at;
-    int64_t batch, rows, width, step, row;
-    // The same bytes, the smaller stride (or the only one) going by rows: one
-    // row a batch entry, and rows that lie outside the batch, are compared too.
-    Region by_rows() const {
-        if (rows > 1 && (batch == 1 || row <= step)) return *this;
-        return {at, rows, batch, width, row, step};
-    }
-    bool empty() const { return at == 0 || batch <= 0 || rows <= 0 || width <= 0; }
-    uintptr_t end() const { return at + uintptr_t((batch - 1) * step + (rows - 1) * row + width); }
-    bool regular() const { return batch == 1 || step % row == 0; }
-};
-
-Region flat(const void *p, int64_t bytes) {
-    return {reinterpret_cast<uintptr_t>(p), 1, 1, bytes, bytes, bytes};
-}
-
-bool overlap(const Region &a, const Region &b) {
-    if (a.empty() || b.empty() || a.end() <= b.at || b.end() <= a.at) return false;
-    // column ranges of one wider tensor: apart in every row
-    if (a.row == b.row && a.row > 0 && a.regular() && b.regular() && (a.rows > 1 || a.batch > 1) &&
-        (b.rows > 1 || b.batch > 1)) {
-        const uintptr_t lo = a.at < b.at ? a.at : b.at, hi = a.at < b.at ? b.at : a.at;
-        const int64_t d = int64_t((hi - lo) % uintptr_t(a.row));
-        const int64_t wl = a.at < b.at ? a.width : b.width, wh = a.at < b.at ? b.width : a.width;
-        if (d >= wl && d + wh <= a.row) return false;
-    }
-    return true;
-}
-
-// Regions of one call: outputs must overlap nothing else.
-struct Regions {
-    static constexpr int kMost = 32;
-    Region r[kMost];
-    bool out[kMost];
-    int n = 0;
-    void in(const Region &x) { r[n] = x, out[n++] = false; }
-    void output(const Region &x) { r[n] = x, out[n++] = true; }
-    bool clash() const {
-        for (int i = 0; i < n; ++i)
-            for (int j = i + 1; j < n; ++j)
-                if ((out[i] || out[j]) && overlap(r[i], r[j])) return true;
-        return false;
-    }
-};
-
-// Checks, and the alignment that a call's tensors have in common.
-struct Check {
-    dwp_status status = DWP_SUCCESS;
-    // every address and byte stride seen, or-ed: of the rows, of B and C, of f32 states
-    uintptr_t bits = 0, bits_bc = 0, bits_state = 0;
-    Regions regions;
-
-    void fail(dwp_status s) {
-        if (status == DWP_SUCCESS) status = s;
-    }
-    void require(bool ok) {
-        if (!ok) fail(DWP_ERR_INVALID_VALUE);
-    }
-    // rows of `inner` elements of type t
-    void rows(const dwp_rows &x, int64_t t, int64_t batch, int64_t n, int64_t inner, bool output, bool track = true) {
-        const int64_t e = size_of(t);
-        require(x.data != nullptr);
-        if (status != DWP_SUCCESS) return;
-        if (!aligned(x.data, e)) return fail(DWP_ERR_MISALIGNED);
-        // one row (or one batch entry) needs no stride
-        const int64_t row = n > 1 ? x.row_stride : inner, step = batch > 1 ? x.batch_stride : inner;
-        require(row >= inner && row <= kMaxStride && step >= inner && step <= kMaxStride);
-        // and what they span is counted in 64 bits below
-        if (status == DWP_SUCCESS) require(n - 1 <= kMaxSpan / row && batch - 1 <= kMaxSpan / step);
-        if (status != DWP_SUCCESS) return;
-        // rows of an output may not fold onto one another
-        if (output && batch > 1 && n > 1)
-            require(step >= (n - 1) * row + inner || row >= (batch - 1) * step + inner);
-        if (status != DWP_SUCCESS) return;
-        bits |= reinterpret_cast<uintptr_t>(x.data) | uintptr_t(row * e) | uintptr_t(step * e);
-        if (track) {
-            const Region r{reinterpret_cast<uintptr_t>(x.data), batch, n, inner * e, step * e, row * e};
-            output ? regions.output(r.by_rows()) : regions.in(r.by_rows());
-        }
-    }
-    // dense array of `count` elements of type t; NULL allowed if optional
-    void dense(const void *p, int64_t t, int64_t count, bool output, bool optional, uintptr_t *seen = nullptr) {
-        if (!optional && count > 0) require(p != nullptr);
-        if (status != DWP_SUCCESS || !p) return;
-        if (!aligned(p, size_of(t))) return fail(DWP_ERR_MISALIGNED);
-        if (seen) *seen |= reinterpret_cast<uintptr_t>(p);
-        const Region r = flat(p, count * size_of(t));
-        output ? regions.output(r) : regions.in(r);
-    }
-    // Rows of `inner` elements of type t are whole 16-byte pieces.
-    bool wide(int64_t inner, int64_t t) const { return ((bits | uintptr_t(inner * size_of(t))) & 15u) == 0; }
-    // The scratch of the two-call pattern; true: go on and launch.  A call that
-    // needs none asks for 16 bytes: of 0 a caller's allocation may be NULL, and
-    // the second call would be taken for another query.
-    bool scratch(void *p, size_t *bytes, size_t need, dwp_status *st) {
-        if (need < 16u) need = 16u;
-        if (status != DWP_SUCCESS) return *st = status, false;
-        if (!p) return *bytes = need, *st = DWP_SUCCESS, false;
-        if (*bytes < need) return *st = DWP_ERR_SCRATCH_TOO_SMALL, false;
-        if (!aligned(p, 16)) return *st = DWP_ERR_MISALIGNED, false;
-        regions.output(flat(p, int64_t(need)));
-        if (regions.clash()) return *st = DWP_ERR_ALIASING, false;
-        return true;
-    }
-};
-
-dwp_status launched(cudaError_t err) {
-    if (err == cudaSuccess) return DWP_SUCCESS;
-    cudaGetLastError();
-    return DWP_ERR_CUDA;
-}
-
-// Sizes common to calls over packed or batched rows; the number of sequences.
-int64_t sequences(Check &c, int64_t channels, int64_t batch, int64_t rows, int64_t segments, const void *offsets) {
-    c.require(channels >= 1 && channels <= kMaxChannels && batch >= 0 && rows >= 0 && batch <= kMaxRows &&
-              rows <= kMaxRows);
-    if (c.status != DWP_SUCCESS) return 0;
-    c.require(batch * rows <= kMaxRows);
-    if (offsets) {
-        c.require(batch == 1 && segments >= 0 && segments <= kMaxSegments);
-        if (!aligned(offsets, 4)) c.fail(DWP_ERR_MISALIGNED);
-        if (c.status == DWP_SUCCESS) c.regions.in(flat(offsets, (segments + 1) * 4));
-        return segments;
-    }
-    c.require(segments == 0);
-    return batch;
-}
 
 // ---------------------------------------------------------------------------
 // causal convolution
@@ -254,18 +107,6 @@ dwp_status conv_backward(const dwp_conv_backward_args &a, void *scratch, size_t 
                       {f.channels * f.width, f.channels * (f.width + 1), 0},
                       f.width};
     return launched(launch_column_sums(p.partial, f.batch * strips, f.channels * (f.width + 1), o, s));
-}
-
-// A state cache's slots.
-void check_slots(Check &c, const void *state, int64_t t, int64_t batch, int64_t num_slots, int64_t stride,
-                 int64_t inner, const int32_t *slots) {
-    c.require(num_slots >= 0 && num_slots <= kMaxRows && (slots || num_slots >= batch));
-    if (slots && !aligned(slots, 4)) c.fail(DWP_ERR_MISALIGNED);
-    if (c.status == DWP_SUCCESS && slots) c.regions.in(flat(slots, batch * 4));
-    if (inner > 0 && num_slots > 0) {
-        dwp_rows r{const_cast<void *>(state), 0, stride};
-        c.rows(r, t, 1, num_slots, inner, true);
-    }
 }
 
 dwp_status conv_step(const dwp_conv_step_args &a, cudaStream_t s) {
@@ -635,6 +476,97 @@ dwp_status norm_backward(const dwp_norm_backward_args &a, void *scratch, size_t 
     return launched(launch_column_sums(p.partial, blocks, planes * f.channels, o, s));
 }
 
+// ---------------------------------------------------------------------------
+// layer norm
+
+void check_layer_norm(Check &c, const dwp_layer_norm_args &a) {
+    c.require(dtype_ok(a.dtype) && (a.weight_dtype == a.dtype || a.weight_dtype == DWP_F32) &&
+              (a.residual_dtype == a.dtype || a.residual_dtype == DWP_F32) && a.channels >= 1 &&
+              a.channels <= kMaxChannels && a.groups >= 1 && a.groups <= kMaxGroups && a.channels % a.groups == 0 &&
+              a.channels / a.groups <= DWP_NORM_MAX_GROUP && a.rows >= 0 && a.rows <= kMaxRows &&
+              a.rows * a.groups <= kMaxRows && a.eps >= 0.0);
+    if (c.status != DWP_SUCCESS) return;
+    c.dense(a.weight, a.weight_dtype, a.channels, false, true, &c.bits);
+    c.dense(a.bias, a.weight_dtype, a.channels, false, true, &c.bits);
+}
+
+LayerNormParams layer_norm_params(const dwp_layer_norm_args &a) {
+    LayerNormParams p = {};
+    p.channels = a.channels, p.groups = a.groups, p.group = a.channels / a.groups, p.rows = a.rows;
+    p.eps = float(a.eps), p.weight_f32 = a.weight_dtype == DWP_F32, p.residual_f32 = a.residual_dtype == DWP_F32;
+    p.x = a.x.data, p.x_row = a.x.row_stride, p.residual = a.residual.data, p.residual_row = a.residual.row_stride;
+    p.sum = a.sum.data, p.sum_row = a.sum.row_stride, p.y = a.out.data, p.y_row = a.out.row_stride;
+    p.weight = a.weight, p.bias = a.bias;
+    return p;
+}
+
+dwp_status layer_norm_forward(const dwp_layer_norm_args &a, cudaStream_t s) {
+    Check c;
+    check_layer_norm(c, a);
+    if (c.status != DWP_SUCCESS) return c.status;
+    if (a.rows == 0) return DWP_SUCCESS;  // no data, and maybe no addresses
+    c.require((a.residual.data != nullptr) == (a.sum.data != nullptr));
+    // an output that is its input exactly counts once, as the output
+    c.rows(a.x, a.dtype, 1, a.rows, a.channels, false, !same_rows(a.x, a.out));
+    if (a.residual.data) {
+        c.rows(a.residual, a.residual_dtype, 1, a.rows, a.channels, false, !same_rows(a.residual, a.sum));
+        c.rows(a.sum, a.residual_dtype, 1, a.rows, a.channels, true);
+    }
+    c.rows(a.out, a.dtype, 1, a.rows, a.channels, true);
+    if (c.status != DWP_SUCCESS) return c.status;
+    if (c.regions.clash()) return DWP_ERR_ALIASING;
+    return launched(launch_layer_norm(static_cast<dwp_dtype>(a.dtype), layer_norm_params(a),
+                                      c.wide(a.channels / a.groups, a.dtype), s));
+}
+
+// Blocks that share a group's rows in the gradient: two waves of 256 threads,
+// each team with eight rows or more.
+int64_t layer_norm_blocks(const dwp_layer_norm_args &a, bool wide) {
+    const int64_t teams = layer_norm_teams(static_cast<dwp_dtype>(a.dtype), a.channels / a.groups, wide);
+    int64_t blocks = kSMs * 2 / a.groups;
+    if (8 * blocks * teams > a.rows) blocks = ceil_div(a.rows, 8 * teams);
+    return blocks < 1 && a.rows > 0 ? 1 : blocks;
+}
+
+dwp_status layer_norm_backward(const dwp_layer_norm_backward_args &a, void *scratch, size_t *bytes, cudaStream_t s) {
+    Check c;
+    const dwp_layer_norm_args &f = a.norm;
+    check_layer_norm(c, f);
+    dwp_status st = c.status;
+    if (st != DWP_SUCCESS) return st;
+    const bool resid = f.sum.data != nullptr;
+    if (f.rows > 0) {
+        c.require(resid || (!a.grad_residual.data && !a.grad_sum.data && f.residual_dtype == f.dtype));
+        if (resid) c.rows(f.sum, f.residual_dtype, 1, f.rows, f.channels, false);
+        else c.rows(f.x, f.dtype, 1, f.rows, f.channels, false);
+        c.rows(a.grad_out, f.dtype, 1, f.rows, f.channels, false);
+        if (a.grad_sum.data) c.rows(a.grad_sum, f.residual_dtype, 1, f.rows, f.channels, false);
+        if (a.grad_x.data) c.rows(a.grad_x, f.dtype, 1, f.rows, f.channels, true);
+        if (a.grad_residual.data) c.rows(a.grad_residual, f.residual_dtype, 1, f.rows, f.channels, true);
+    }
+    c.dense(a.grad_weight, DWP_F32, f.channels, true, true);
+    c.dense(a.grad_bias, DWP_F32, f.channels, true, true);
+    const bool wide = c.wide(f.channels / f.groups, f.dtype), sums = a.grad_weight || a.grad_bias;
+    const int64_t blocks = layer_norm_blocks(f, wide);
+    if (!c.scratch(scratch, bytes, sums ? round16(size_t(blocks * 2 * f.channels) * 4u) : 0u, &st)) return st;
+    if (f.rows == 0)
+        return launched(launch_clear(a.grad_weight, size_t(f.channels) * 4u, a.grad_bias, size_t(f.channels) * 4u, s));
+    LayerNormBackwardParams p = {};
+    p.n = layer_norm_params(f);
+    p.blocks = blocks;
+    p.v = resid ? f.sum.data : f.x.data, p.v_row = resid ? f.sum.row_stride : f.x.row_stride;
+    p.v_f32 = resid ? f.residual_dtype == DWP_F32 : f.dtype == DWP_F32;
+    p.grad_out = a.grad_out.data, p.grad_row = a.grad_out.row_stride;
+    p.grad_sum = a.grad_sum.data, p.gsum_row = a.grad_sum.row_stride;
+    p.grad_x = a.grad_x.data, p.gx_row = a.grad_x.row_stride;
+    p.grad_residual = a.grad_residual.data, p.gres_row = a.grad_residual.row_stride;
+    p.partial = sums ? static_cast<float *>(scratch) : nullptr;
+    const cudaError_t err = launch_layer_norm_backward(static_cast<dwp_dtype>(f.dtype), p, wide, s);
+    if (err != cudaSuccess || !sums) return launched(err);
+    const ColumnOut o{{a.grad_weight, a.grad_bias, nullptr}, {f.channels, 2 * f.channels, 0}, 1};
+    return launched(launch_column_sums(p.partial, blocks, 2 * f.channels, o, s));
+}
+
 }  // namespace
 
 extern "C" {
@@ -681,6 +613,17 @@ dwp_status dwp_block_norm_backward(const dwp_norm_backward_args *args, void *d_s
                                    dwp_stream stream) {
     if (!args || !scratch_bytes) return DWP_ERR_INVALID_VALUE;
     return norm_backward(*args, d_scratch, scratch_bytes, reinterpret_cast<cudaStream_t>(stream));
+}
+
+dwp_status dwp_layer_norm(const dwp_layer_norm_args *args, dwp_stream stream) {
+    if (!args) return DWP_ERR_INVALID_VALUE;
+    return layer_norm_forward(*args, reinterpret_cast<cudaStream_t>(stream));
+}
+
+dwp_status dwp_layer_norm_backward(const dwp_layer_norm_backward_args *args, void *d_scratch, size_t *scratch_bytes,
+                                   dwp_stream stream) {
+    if (!args || !scratch_bytes) return DWP_ERR_INVALID_VALUE;
+    return layer_norm_backward(*args, d_scratch, scratch_bytes, reinterpret_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

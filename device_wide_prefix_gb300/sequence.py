@@ -1,5 +1,6 @@
 """Sequence operators of libdwp.so: the causal convolution, the selective
-state space scan and the block norm (include/dwp.h, "Sequence operators").
+state space scan, the block norm, the gated delta rule and the layer norm
+(include/dwp.h, "Sequence operators").
 
 Rows are tokens.  A tensor of rows is (batch, rows, channels), or (rows,
 channels) for one packed stream: cut by CSR `offsets` into segments, or one
@@ -23,6 +24,7 @@ import device_wide_prefix_gb300 as _dwp
 DWP_F32, DWP_BF16, DWP_F16 = 0, 1, 2
 CHECKPOINT_ROWS = 16  # DWP_SCAN_CHECKPOINT_ROWS
 NORM_MAX_GROUP = 16384  # DWP_NORM_MAX_GROUP
+DELTA_CHUNK = 64  # DWP_DELTA_CHUNK
 
 _DTYPES = {torch.float32: DWP_F32, torch.bfloat16: DWP_BF16, torch.float16: DWP_F16}
 _NO_ROWS = (0, 0, 0)
@@ -36,13 +38,22 @@ _SCAN_BACKWARD = _SCAN + " 3q 10q"
 _SCAN_STEP = "7q 18q 2q 3q 3q"
 _NORM = "7q d 15q 2q"
 _NORM_BACKWARD = _NORM + " 15q 2q"
+_DELTA = "9q d 16q 3q 3q 4q"
+_DELTA_BACKWARD = _DELTA + " 4q 7q"
+_DELTA_STEP = "8q d 16q 3q 3q 3q"
+_LAYER_NORM = "6q d 12q 2q"
+_LAYER_NORM_BACKWARD = _LAYER_NORM + " 12q 2q"
 _PACK = {name: struct.Struct("=" + fmt.replace(" ", "")).pack for name, fmt in (
     ("dwp_causal_conv", _CONV), ("dwp_causal_conv_backward", _CONV_BACKWARD),
     ("dwp_causal_conv_step", _CONV_STEP), ("dwp_selective_scan", _SCAN),
     ("dwp_selective_scan_backward", _SCAN_BACKWARD), ("dwp_selective_scan_step", _SCAN_STEP),
-    ("dwp_block_norm", _NORM), ("dwp_block_norm_backward", _NORM_BACKWARD))}
+    ("dwp_block_norm", _NORM), ("dwp_block_norm_backward", _NORM_BACKWARD),
+    ("dwp_gated_delta_rule", _DELTA), ("dwp_gated_delta_rule_backward", _DELTA_BACKWARD),
+    ("dwp_gated_delta_rule_step", _DELTA_STEP), ("dwp_layer_norm", _LAYER_NORM),
+    ("dwp_layer_norm_backward", _LAYER_NORM_BACKWARD))}
 _WITH_SCRATCH = ("dwp_causal_conv_backward", "dwp_selective_scan", "dwp_selective_scan_backward",
-                 "dwp_block_norm_backward")
+                 "dwp_block_norm_backward", "dwp_gated_delta_rule", "dwp_gated_delta_rule_backward",
+                 "dwp_layer_norm_backward")
 
 
 _ENTRY = {}  # entry points by name, once the library is loaded
@@ -454,4 +465,199 @@ def block_norm_backward(grad_out, v, weight, x=None, scale=None, gate=None, gate
     fields += [*gr, *_norm_rows(grad_residual, grad_out, "grad_residual", True), *gx, *gres, *gz,
                grads["weight"].data_ptr(), grads["scale"].data_ptr() if scale is not None else 0]
     _launch("dwp_block_norm_backward", fields, grad_out, stream, scratch)
+    return grads
+
+
+# ---------------------------------------------------------------------------
+# gated delta rule
+
+
+def _heads(t, lead, x, what):
+    """(address, batch, row and head stride) of a tensor of x's type and device, of shape (*lead, heads, size)."""
+    s, shape = t.stride(), t.shape
+    if t.dtype != x.dtype or t.get_device() != x.get_device() or len(s) != len(lead) + 2 or shape[:-2] != lead:
+        _refuse("%s must have shape (..., heads, size) with v's rows, type and device", what)
+    if s[-1] != 1 and shape[-1] > 1 and t.numel():
+        _refuse("%s must have contiguous head entries", what)
+    return (t.data_ptr(), s[0] if len(s) == 4 else 0, s[-3], s[-2])
+
+
+def _gates(t, lead, heads, x, what, f32=True):
+    """(address, batch and row stride) of rows of one number a head; float32, or of x's type where `f32` is false."""
+    if t is None:
+        return _NO_ROWS
+    if (t.shape != (*lead, heads) or t.get_device() != x.get_device()
+            or (t.dtype != torch.float32 and (f32 or t.dtype != x.dtype))):
+        _refuse("%s must be float32%s of shape (..., heads) with v's rows and device", what, "" if f32 else " or v's type,")
+    return _rows(t, what)
+
+
+def _delta_parts(q, k, v, g, beta, scale, out, ndims):
+    """The fields that the prompt and the token form share, in two parts, and the shapes."""
+    if not v.is_cuda or v.dtype not in _DTYPES or v.dim() not in ndims:
+        _refuse("v must be a CUDA tensor of float32, bfloat16 or float16, of shape (..., heads, values)")
+    lead, heads, values = v.shape[:-2], v.shape[-2], v.shape[-1]
+    parts = [*_heads(q, lead, v, "q"), *_heads(k, lead, v, "k"), *_heads(v, lead, v, "v"), *out,
+             *_gates(g, lead, heads, v, "g"), *_gates(beta, lead, heads, v, "beta", False)]
+    _need(q.shape == k.shape, "q and k must have one shape")
+    key_heads, keys = k.shape[-2:]
+    sizes = [_DTYPES[v.dtype], _DTYPES[beta.dtype], keys, values, key_heads, heads]
+    return sizes, float(keys ** -0.5 if scale is None and keys else scale or 0.0), parts
+
+
+def _delta_sequences(v, offsets):
+    """_sequences of (..., heads, values)."""
+    return _sequences(v[..., 0], offsets) if v.shape[-2] and v.shape[-1] else _refuse("v has no heads or values")
+
+
+def _delta_points(batch, rows, nseg, offsets, heads, keys, values):
+    chunks = rows // DELTA_CHUNK + nseg if offsets is not None else batch * -(-rows // DELTA_CHUNK)
+    return chunks, heads, DELTA_CHUNK * (2 * DELTA_CHUNK + values) + keys * values
+
+
+def _delta_fields(q, k, v, g, beta, scale, out, offsets, initial, final, checkpoints):
+    sizes, scale, parts = _delta_parts(q, k, v, g, beta, scale, out, (3, 4))
+    batch, rows, off, nseg, seqs = _delta_sequences(v, offsets)
+    keys, values, heads, f32 = sizes[2], sizes[3], sizes[5], torch.float32
+    state = (seqs, heads, keys, values)
+    points = _delta_points(batch, rows, nseg, offsets, heads, keys, values)
+    return [*sizes, batch, rows, nseg, scale, *parts, off, _dense(initial, state, f32, v, "initial_state"),
+            _dense(final, state, f32, v, "final_state"), _dense(checkpoints, points, f32, v, "checkpoints")], state
+
+
+def gated_delta_rule(q, k, v, g, beta, scale=None, offsets=None, initial_state=None, return_state=False,
+                     return_checkpoints=False, out=None, final_state=None, checkpoints=None, scratch=None, stream=None):
+    """Gated delta rule: a state (keys, values) a head that decays by exp(g)
+    and is corrected toward v at k by beta, read out at q.  q, k: (batch, rows,
+    key heads, keys), v: (batch, rows, heads, values), or without the batch for
+    a packed stream; key heads divide heads.  g (or None for no decay) and beta:
+    (batch, rows, heads), float32; beta may have v's type.  `scale` None:
+    keys ** -0.5.  `initial_state` (sequences, heads, keys, values) is float32
+    (None: zeros).  Returns out, or a tuple of out and then, where asked for,
+    the final state and the checkpoints that the gradient needs."""
+    if not v.is_cuda or v.dim() not in (3, 4):
+        _refuse("v must be a CUDA tensor of shape (batch, rows, heads, values) or (rows, heads, values)")
+    out = _empty(v.shape, v.dtype, v, stream) if out is None else out
+    _need(out.shape == v.shape, "out must have v's shape")
+    if return_state or return_checkpoints:
+        batch, rows, _, nseg, seqs = _delta_sequences(v, offsets)
+        keys, heads, values = k.shape[-1], v.shape[-2], v.shape[-1]
+        if return_state and final_state is None:
+            final_state = _empty((seqs, heads, keys, values), torch.float32, v, stream)
+        if return_checkpoints and checkpoints is None:
+            checkpoints = _empty(_delta_points(batch, rows, nseg, offsets, heads, keys, values), torch.float32, v, stream)
+    fields, _ = _delta_fields(q, k, v, g, beta, scale, _heads(out, v.shape[:-2], v, "out"), offsets, initial_state,
+                              final_state, checkpoints)
+    _launch("dwp_gated_delta_rule", fields, v, stream, scratch)
+    if final_state is None and checkpoints is None:
+        return out
+    return (out, *(t for t in (final_state, checkpoints) if t is not None))
+
+
+def gated_delta_rule_backward(grad_out, q, k, v, g, beta, checkpoints, scale=None, offsets=None, initial_state=None,
+                              grad_final_state=None, scratch=None, stream=None):
+    """Gradients of gated_delta_rule: a dict of "q", "k", "v", "beta" and, where
+    given, "g" and "initial_state" (the last also with a `grad_final_state`).
+    `checkpoints` are the forward's."""
+    _need(checkpoints is not None, "the gradient needs the forward's checkpoints")
+    fields, state = _delta_fields(q, k, v, g, beta, scale, (0, 0, 0, 0), offsets, initial_state, None, checkpoints)
+    _need(grad_out.shape == v.shape, "grad_out must have v's shape")
+    grads = {"q": _empty(q.shape, v.dtype, v, stream), "k": _empty(k.shape, v.dtype, v, stream),
+             "v": _empty(v.shape, v.dtype, v, stream), "beta": _empty(beta.shape, beta.dtype, v, stream)}
+    if g is not None:
+        grads["g"] = _empty(g.shape, torch.float32, v, stream)
+    if initial_state is not None or grad_final_state is not None:
+        grads["initial_state"] = _empty(state, torch.float32, v, stream)
+    at = lambda k: grads[k].data_ptr() if k in grads else 0  # noqa: E731
+    fields += [*_heads(grad_out, v.shape[:-2], v, "grad_out"),
+               _dense(grad_final_state, state, torch.float32, v, "grad_final_state"), at("q"), at("k"), at("v"), at("g"),
+               at("beta"), at("initial_state")]
+    _launch("dwp_gated_delta_rule_backward", fields, v, stream, scratch)
+    return grads
+
+
+def gated_delta_rule_step(q, k, v, g, beta, state, scale=None, slots=None, out=None, stream=None):
+    """gated_delta_rule of one new row of each of `batch` sequences: q, k (batch,
+    key heads, keys), v (batch, heads, values), g, beta (batch, heads), `state`
+    float32 (num_slots, heads, keys, values) updated in place; `slots` as for
+    causal_conv_step.  Returns out."""
+    if not v.is_cuda or v.dim() != 3:
+        _refuse("v must be a CUDA tensor of shape (batch, heads, values)")
+    out = _empty(v.shape, v.dtype, v, stream) if out is None else out
+    _need(out.shape == v.shape, "out must have v's shape")
+    sizes, scale, parts = _delta_parts(q, k, v, g, beta, scale, _heads(out, v.shape[:-2], v, "out"), (3,))
+    keys, values, heads, batch = sizes[2], sizes[3], sizes[5], v.shape[0]
+    s = state.stride()
+    _need(state.dtype == torch.float32 and state.get_device() == v.get_device() and len(s) == 4
+          and state.shape[1:] == (heads, keys, values) and (state.numel() == 0 or state[0].is_contiguous()),
+          "state must be float32 of shape (slots, heads, keys, values), each slot contiguous, on v's device")
+    fields = [*sizes, batch, state.shape[0], scale, *parts, state.data_ptr(), s[0], _slots(slots, batch, v)]
+    _launch("dwp_gated_delta_rule_step", fields, v, stream)
+    return out
+
+
+# ---------------------------------------------------------------------------
+# layer norm
+
+
+def _layer_norm_fields(x, weight, bias, rdtype, groups, eps, *rows):
+    ch = x.shape[-1]
+    like = weight if weight is not None else bias
+    wdtype = _DTYPES[x.dtype] if like is None else _DTYPES.get(like.dtype, -1)
+    return [_DTYPES[x.dtype], wdtype, rdtype, ch, groups, x.numel() // ch if ch else 0, float(eps), *rows,
+            0 if weight is None else _weight(weight, x, (ch,), "weight"),
+            0 if bias is None else _dense(bias, (ch,), like.dtype, x, "bias")]
+
+
+def layer_norm(x, weight=None, bias=None, residual=None, groups=1, eps=1e-5, out=None, sum_out=None, stream=None):
+    """Layer norm over each of `groups` parts of a row, times `weight` plus
+    `bias` (None: ones, zeros): of x, or of residual + x with a `residual`, which
+    is also returned.  `out` may be x and `sum_out` may be residual, in place.
+    Returns (out, sum), sum None without a residual."""
+    xr = _norm_main(x, "x")
+    if out is None:
+        out = _empty(x.shape, x.dtype, x, stream)
+    total, rr, tr, rdtype = None, _NO_ROWS, _NO_ROWS, _DTYPES[x.dtype]
+    if residual is not None:
+        rr, rdtype = _norm_rows(residual, x, "residual", True), _DTYPES[residual.dtype]
+        total = _empty(x.shape, residual.dtype, x, stream) if sum_out is None else sum_out
+        _need(total.dtype == residual.dtype, "sum_out must have residual's type")
+        tr = _norm_rows(total, x, "sum_out", True)
+    fields = _layer_norm_fields(x, weight, bias, rdtype, groups, eps, *xr, *rr, *tr, *_norm_rows(out, x, "out"))
+    _launch("dwp_layer_norm", fields, x, stream)
+    return out, total
+
+
+def layer_norm_backward(grad_out, v, weight=None, bias=None, grad_residual=None, groups=1, eps=1e-5, residual=None,
+                        scratch=None, stream=None):
+    """Gradients of layer_norm.  `v` is what was normed: the returned sum where
+    there was a residual, else x.  `residual` says whether there was one (None:
+    there was if `grad_residual` or v's type says so); `grad_residual` is the
+    returned sum's gradient; `bias` asks for its gradient.  A dict of "x" and,
+    where they apply, "weight", "bias" and "residual"; "x" and "residual" are
+    one tensor where they are equal."""
+    gr = _norm_main(grad_out, "grad_out")
+    if residual is None:
+        residual = grad_residual is not None or v.dtype != grad_out.dtype
+    _need(residual or v.dtype == grad_out.dtype, "v must have grad_out's type without a residual")
+    _need(grad_residual is None or (residual and grad_residual.dtype == v.dtype),
+          "grad_residual must have v's type, with a residual")
+    vr = _norm_rows(v, grad_out, "v", True)
+    shape, f32 = grad_out.shape, torch.float32
+    grads = {"x": _empty(shape, grad_out.dtype, grad_out, stream)}
+    if weight is not None:
+        grads["weight"] = _empty(weight.shape, f32, grad_out, stream)
+    if bias is not None:
+        grads["bias"] = _empty(bias.shape, f32, grad_out, stream)
+    gx, gres = _norm_rows(grads["x"], grad_out, "grad_x"), _NO_ROWS
+    if residual and v.dtype == grad_out.dtype:
+        grads["residual"] = grads["x"]  # the same numbers
+    elif residual:
+        grads["residual"] = _empty(shape, v.dtype, grad_out, stream)
+        gres = _norm_rows(grads["residual"], grad_out, "grad_residual", True)
+    fields = _layer_norm_fields(grad_out, weight, bias, _DTYPES[v.dtype], groups, eps, *(_NO_ROWS if residual else vr),
+                                *_NO_ROWS, *(vr if residual else _NO_ROWS), *_NO_ROWS)
+    at = lambda k: grads[k].data_ptr() if k in grads else 0  # noqa: E731
+    fields += [*gr, *_norm_rows(grad_residual, grad_out, "grad_residual", True), *gx, *gres, at("weight"), at("bias")]
+    _launch("dwp_layer_norm_backward", fields, grad_out, stream, scratch)
     return grads

@@ -290,8 +290,9 @@ dwp_status dwp_linear_recurrence_f32(const float *d_a, const float *d_b, float *
  *
  * The linear recurrence above in the form a state space layer uses it, with
  * what stands around it there: the short causal convolution before it, the
- * selective scan, and the norm around the block, each with its gradient, and
- * the first two with a form for single tokens.
+ * selective scan, and the norm around the block; the recurrence with a matrix
+ * state, the gated delta rule, and the layer norm; each with its gradient, and
+ * the convolution and the recurrences with a form for single tokens.
  *
  * Layout.  Rows are tokens; a row's channels are contiguous.  A tensor of
  * rows is [batch, rows, channels], given by its address, batch stride and row
@@ -475,6 +476,93 @@ typedef struct dwp_selective_scan_step_args {
 dwp_status dwp_selective_scan_step(const dwp_selective_scan_step_args *args, dwp_stream stream);
 
 /*
+ * Gated delta rule: per head, a state S of keys x values decays and is then
+ * corrected toward its new row,
+ *   S' = exp(g[t]) S[t-1],  u = beta[t] (v[t] - S'^T k[t])
+ *   S[t] = S' + k[t] u^T,   out[t] = scale S[t]^T q[t]
+ *   q, k           rows of [key_heads, keys];  v, out  rows of [heads, values].
+ *                  key_heads divides heads, and head h has the queries and keys
+ *                  of key head h / (heads / key_heads).  For overlap a row
+ *                  counts as one piece, from its first head to its last
+ *   keys, values   1 .. 128 each;  heads  at most 1024
+ *   g              f32 rows of [heads], the log of the decay; data NULL for no
+ *                  decay.  Below -110 (-infinity too) it counts as -110, whose
+ *                  exponential is 0 in f32 all the same
+ *   beta           rows of [heads], beta_dtype: dtype or DWP_F32
+ *   initial_state  f32 [sequences, heads, keys, values], or NULL for zeros
+ *   final_state    NULL, or the same after each sequence's last row (may not
+ *                  overlap initial_state)
+ *   checkpoints    NULL, or what the gradient needs, to be handed on as it is:
+ *                  f32 [chunks, heads, DWP_DELTA_CHUNK * (2 * DWP_DELTA_CHUNK
+ *                  + values) + keys * values], 16-byte aligned; chunks is
+ *                  batch * ceil(rows / DWP_DELTA_CHUNK), or with offsets
+ *                  rows / DWP_DELTA_CHUNK + num_segments
+ *   scratch        without checkpoints 8 * DWP_DELTA_CHUNK^2 bytes for each
+ *                  of those chunks and head
+ */
+#define DWP_DELTA_CHUNK 64
+typedef struct dwp_heads {
+    void *data;
+    int64_t batch_stride, row_stride, head_stride; /* elements */
+} dwp_heads;
+typedef struct dwp_delta_args {
+    int64_t dtype, beta_dtype;
+    int64_t keys, values, key_heads, heads, batch, rows, num_segments;
+    double scale;
+    dwp_heads q, k, v, out;
+    dwp_rows g, beta;
+    const uint32_t *offsets;
+    const float *initial_state;
+    float *final_state, *checkpoints;
+} dwp_delta_args;
+dwp_status dwp_gated_delta_rule(const dwp_delta_args *args, void *d_scratch, size_t *scratch_bytes,
+                                dwp_stream stream);
+
+/*
+ * Gradient of dwp_gated_delta_rule.
+ *   delta         the forward's arguments, checkpoints as the forward wrote
+ *                 them (out, final_state unused)
+ *   grad_out      of the output;  grad_final_state  NULL for zeros
+ *   grad_q, grad_k  [batch, rows, key_heads, keys], grad_v  [batch, rows,
+ *                 heads, values], dense, dtype: where heads share a key head,
+ *                 the sum over them, rounded once
+ *   grad_g        f32 [batch, rows, heads], dense, or NULL (always without g);
+ *                 grad_beta  the same, beta_dtype
+ *   grad_initial_state  NULL, or as initial_state
+ *   scratch       4 * (keys + DWP_DELTA_CHUNK) * values bytes for each of the
+ *                 chunks and head, and 8 * DWP_DELTA_CHUNK * keys more where
+ *                 heads share keys
+ */
+typedef struct dwp_delta_backward_args {
+    dwp_delta_args delta;
+    dwp_heads grad_out;
+    const float *grad_final_state;
+    void *grad_q, *grad_k, *grad_v;
+    float *grad_g;
+    void *grad_beta;
+    float *grad_initial_state;
+} dwp_delta_backward_args;
+dwp_status dwp_gated_delta_rule_backward(const dwp_delta_backward_args *args, void *d_scratch,
+                                         size_t *scratch_bytes, dwp_stream stream);
+
+/*
+ * dwp_gated_delta_rule for one new row of each of `batch` sequences, the
+ * states updated in place; slots as for dwp_causal_conv_step, `state` f32
+ * [num_slots, heads, keys, values], slot_stride elements apart.
+ */
+typedef struct dwp_delta_step_args {
+    int64_t dtype, beta_dtype;
+    int64_t keys, values, key_heads, heads, batch, num_slots;
+    double scale;
+    dwp_heads q, k, v, out;
+    dwp_rows g, beta;
+    float *state;
+    int64_t slot_stride;
+    const int32_t *slots;
+} dwp_delta_step_args;
+dwp_status dwp_gated_delta_rule_step(const dwp_delta_step_args *args, dwp_stream stream);
+
+/*
  * Root-mean-square norm around a block, over each of `groups` equal parts of
  * a row of `channels` (channels / groups at most DWP_NORM_MAX_GROUP, rows *
  * groups < 2^31):
@@ -514,6 +602,45 @@ typedef struct dwp_norm_backward_args {
     float *grad_weight, *grad_scale;
 } dwp_norm_backward_args;
 dwp_status dwp_block_norm_backward(const dwp_norm_backward_args *args, void *d_scratch,
+                                   size_t *scratch_bytes, dwp_stream stream);
+
+/*
+ * Layer norm, over each of `groups` equal parts of a row of `channels`
+ * (limits as for dwp_block_norm):
+ *   v   = residual + x, written to `sum`; or x without a residual
+ *   out = (v - mean(v)) / sqrt(mean((v - mean(v))^2) + eps) * weight + bias
+ *   x, out          dtype.  out may be x exactly.
+ *   residual, sum   residual_dtype: dtype or DWP_F32; both or neither.  sum
+ *                   may be residual exactly.
+ *   weight, bias    [channels], weight_dtype: dtype or DWP_F32; NULL for ones,
+ *                   zeros
+ * Tensors are [rows, channels] (batch_stride unused).  Mean and squares about
+ * it are kept together, so a mean far from zero costs no accuracy.
+ */
+typedef struct dwp_layer_norm_args {
+    int64_t dtype, weight_dtype, residual_dtype;
+    int64_t channels, groups, rows;
+    double eps;
+    dwp_rows x, residual, sum, out;
+    const void *weight, *bias;
+} dwp_layer_norm_args;
+dwp_status dwp_layer_norm(const dwp_layer_norm_args *args, dwp_stream stream);
+
+/*
+ * Gradient of dwp_layer_norm.
+ *   norm           the forward's arguments: `sum` as the forward wrote it where
+ *                  residual was given, else x (residual, out and bias unused)
+ *   grad_out       of the output;  grad_sum  of `sum`, residual_dtype, or NULL
+ *   grad_x         dtype, or NULL;  grad_residual  residual_dtype, with a
+ *                  residual only, or NULL
+ *   grad_weight, grad_bias  f32 [channels], or NULL
+ */
+typedef struct dwp_layer_norm_backward_args {
+    dwp_layer_norm_args norm;
+    dwp_rows grad_out, grad_sum, grad_x, grad_residual;
+    float *grad_weight, *grad_bias;
+} dwp_layer_norm_backward_args;
+dwp_status dwp_layer_norm_backward(const dwp_layer_norm_backward_args *args, void *d_scratch,
                                    size_t *scratch_bytes, dwp_stream stream);
 
 /*
