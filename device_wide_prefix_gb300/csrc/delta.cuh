@@ -19,6 +19,7 @@
 #pragma once
 
 #include "sequence.cuh"
+#include "tensor.cuh"
 
 namespace dwp {
 
@@ -115,27 +116,56 @@ __device__ __forceinline__ void delta_sums(Sum2 *sums, F g) {
     sums[lane + 32] = sum2_add(half, b);
 }
 
-// store(i, j, sum over k < kk of a(i, k) b(k, j)) for i < m, j < n.
-template <class FA, class FB, class FS>
-__device__ __forceinline__ void delta_product(int m, int n, int kk, FA a, FB b, FS store) {
-    const int mt = (m + 3) / 4, nt = (n + 3) / 4;
-    for (int e = threadIdx.x; e < mt * nt; e += blockDim.x) {
-        const int i0 = e / nt * 4, j0 = e % nt * 4;
-        float s[4][4] = {};
-        for (int k = 0; k < kk; ++k) {
-            float x[4], y[4];
+// 16 bytes to shared memory without a register between; `bytes` of them are
+// read, the rest are zeros.
+__device__ __forceinline__ void copy16(uint32_t to, const void *from, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// Pieces of bf16 that hold a T: a bf16 itself, or the two that keep 16 bits of
+// an f32 and all 11 of an f16.
+template <class T>
+constexpr int kPieces = 2;
+template <>
+constexpr int kPieces<__nv_bfloat16> = 1;
+
+// Eight neighbouring elements of a row, zeros past its `left` elements.
+template <class T, bool kWide>
+__device__ __forceinline__ void load_eight(float (&f)[8], const T *p, int left) {
+    if (kWide && left >= 8) {
+        load_f32<8>(f, p);
+    } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) x[i] = a(min(i0 + i, m - 1), k), y[i] = b(k, min(j0 + i, n - 1));
+        for (int j = 0; j < 8; ++j) f[j] = j < left ? to_f32<T>(p[j]) : 0.0f;
+    }
+}
+__device__ __forceinline__ void store_pieces(char *hi, char *lo, uint32_t at, const float (&f)[8]) {
+    uint4 h, l;
+    split2(f[0], f[1], h.x, l.x), split2(f[2], f[3], h.y, l.y), split2(f[4], f[5], h.z, l.z), split2(f[6], f[7], h.w, l.w);
+    *reinterpret_cast<uint4 *>(hi + at) = h;
+    if (lo) *reinterpret_cast<uint4 *>(lo + at) = l;
+}
+
+// Rows of a head into tiles of kRows rows and kWidth columns, from row `first`
+// of the tile on: 64 rows, zeros past the chunk's `n` and past `dim` columns.
+// The second piece lies `lo` bytes behind the first.
+template <class T, bool kWide, int kRows, int kWidth, int kThreads>
+__device__ __forceinline__ void load_tile(char *tile, uint32_t lo, int first, const DeltaRows &r, int64_t batch, int64_t row,
+                                          int head, int n, int dim) {
+    const T *src = delta_at<T>(r, batch, row, head);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) s[i][j] = fmaf(x[i], y[j], s[i][j]);
+    for (int e = threadIdx.x; e < kChunk * kWidth / 8; e += kThreads) {
+        const int i = e / (kWidth / 8), c = e % (kWidth / 8), left = i < n ? dim - c * 8 : 0;
+        const uint32_t at = uint32_t(c / 8 * kRows) * kTileRow + tile_piece(uint32_t(first + i), uint32_t(c % 8));
+        const T *from = src + int64_t(left > 0 ? i : 0) * r.row + (left > 0 ? c * 8 : 0);
+        if constexpr (kPieces<T> == 1 && kWide) {
+            copy16(smem_addr(tile + at), from, left > 0 ? 16u : 0u);
+        } else {
+            float f[8];
+            load_eight<T, kWide>(f, from, left);
+            store_pieces(tile, kPieces<T> == 2 ? tile + lo : nullptr, at, f);
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (i0 + i < m && j0 + j < n) store(i0 + i, j0 + j, s[i][j]);
     }
 }
 

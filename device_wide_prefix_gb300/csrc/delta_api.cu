@@ -32,6 +32,13 @@ int64_t delta_slots(const dwp_delta_args &a) {
     return a.offsets ? a.rows / DWP_DELTA_CHUNK + a.num_segments : a.batch * delta_chunks(a);
 }
 
+// Words of a kept state: keys in whole 16-byte pieces of bf16.
+int64_t delta_state(const dwp_delta_args &a) { return (a.keys + 7) / 8 * 8 * a.values; }
+// Whether the rows that were checked so far are whole 16-byte pieces.
+bool delta_wide(const Check &c, const dwp_delta_args &a) {
+    return ((c.bits | uintptr_t((a.keys | a.values) * size_of(a.dtype))) & 15u) == 0;
+}
+
 int64_t check_delta(Check &c, const dwp_delta_args &a, bool backward) {
     c.require(delta_sizes_ok(a.dtype, a.beta_dtype, a.keys, a.values, a.key_heads, a.heads, a.scale));
     const int64_t seqs = sequences(c, 1, a.batch, a.rows, a.num_segments, a.offsets);
@@ -41,8 +48,8 @@ int64_t check_delta(Check &c, const dwp_delta_args &a, bool backward) {
         c.heads(a.q, a.dtype, a.batch, a.rows, a.key_heads, a.keys, false);
         c.heads(a.k, a.dtype, a.batch, a.rows, a.key_heads, a.keys, false);
         c.heads(a.v, a.dtype, a.batch, a.rows, a.heads, a.values, false);
-        if (!backward) c.heads(a.out, a.dtype, a.batch, a.rows, a.heads, a.values, true);
         const uintptr_t others = c.bits;
+        if (!backward) c.heads(a.out, a.dtype, a.batch, a.rows, a.heads, a.values, true);
         if (a.g.data) c.rows(a.g, DWP_F32, a.batch, a.rows, a.heads, false);
         c.rows(a.beta, a.beta_dtype, a.batch, a.rows, a.heads, false);
         c.bits = others;
@@ -50,7 +57,7 @@ int64_t check_delta(Check &c, const dwp_delta_args &a, bool backward) {
     c.dense(a.initial_state, DWP_F32, seqs * state, false, true);
     if (!backward) c.dense(a.final_state, DWP_F32, seqs * state, true, true);
     if (c.status != DWP_SUCCESS) return seqs;
-    const int64_t each = DWP_DELTA_CHUNK * a.values + a.keys * a.values + 2 * kTile;
+    const int64_t each = DWP_DELTA_CHUNK * a.values + delta_state(a) + 2 * kTile;
     c.dense(a.checkpoints, DWP_F32, delta_slots(a) * a.heads * each, !backward, !backward);
     if (!aligned(a.checkpoints, 16)) c.fail(DWP_ERR_MISALIGNED);
     return seqs;
@@ -82,7 +89,8 @@ dwp_status delta_forward(const dwp_delta_args &a, void *scratch, size_t *bytes, 
     const size_t need = a.checkpoints ? 0u : size_t(delta_slots(a) * a.heads * 2 * kTile) * 4u;
     if (!c.scratch(scratch, bytes, need, &st)) return st;
     if (seqs == 0) return DWP_SUCCESS;
-    const DeltaParams p = delta_params(a, seqs, scratch);
+    DeltaParams p = delta_params(a, seqs, scratch);
+    p.wide = delta_wide(c, a);
     const auto t = static_cast<dwp_dtype>(a.dtype);
     if (a.batch * a.rows > 0) {
         const cudaError_t err = launch_delta_local(t, p, s);
@@ -113,12 +121,13 @@ dwp_status delta_backward(const dwp_delta_backward_args &a, void *scratch, size_
     c.dense(a.grad_initial_state, DWP_F32, seqs * state, true, true);
     const int64_t places = delta_slots(f) * f.heads;
     const size_t dr = size_t(places * DWP_DELTA_CHUNK * f.values) * 4u;
-    const size_t ends = round16(size_t(places * f.keys * f.values) * 4u);
+    const size_t ends = round16(size_t(places * delta_state(f)) * 4u);
     const size_t share = f.heads == f.key_heads ? 0u : size_t(places * 2 * DWP_DELTA_CHUNK * f.keys) * 4u;
     if (!c.scratch(scratch, bytes, dr + ends + share, &st)) return st;
     if (seqs == 0) return DWP_SUCCESS;
     DeltaBackwardParams p = {};
     p.f = delta_params(f, seqs, nullptr);
+    p.f.wide = delta_wide(c, f);
     p.grad_out = delta_rows(a.grad_out);
     p.grad_q = delta_dense(a.grad_q, f.rows, f.key_heads, f.keys);
     p.grad_k = delta_dense(a.grad_k, f.rows, f.key_heads, f.keys);

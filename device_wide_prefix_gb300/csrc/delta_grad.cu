@@ -19,6 +19,31 @@ namespace {
 
 constexpr int kThreads = 256;
 
+// store(i, j, sum over k < kk of a(i, k) b(k, j)) for i < m, j < n.
+template <class FA, class FB, class FS>
+__device__ __forceinline__ void delta_product(int m, int n, int kk, FA a, FB b, FS store) {
+    const int mt = (m + 3) / 4, nt = (n + 3) / 4;
+    for (int e = threadIdx.x; e < mt * nt; e += blockDim.x) {
+        const int i0 = e / nt * 4, j0 = e % nt * 4;
+        float s[4][4] = {};
+        for (int k = 0; k < kk; ++k) {
+            float x[4], y[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = a(min(i0 + i, m - 1), k), y[i] = b(k, min(j0 + i, n - 1));
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) s[i][j] = fmaf(x[i], y[j], s[i][j]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (i0 + i < m && j0 + j < n) store(i0 + i, j0 + j, s[i][j]);
+    }
+}
+
+
 template <class T>
 __global__ void __launch_bounds__(kThreads) delta_grad_kernel(DeltaBackwardParams bp) {
     const DeltaParams &p = bp.f;
@@ -44,7 +69,11 @@ __global__ void __launch_bounds__(kThreads) delta_grad_kernel(DeltaBackwardParam
     }
     __syncthreads();
     const int64_t at = int64_t(blockIdx.x) * p.heads + head;
-    const float *S0 = p.states + at * keys * values, *S1 = bp.ends + at * keys * values;
+    const int kp = (keys + 7) / 8 * 8;
+    const __nv_bfloat16 *P0 = reinterpret_cast<const __nv_bfloat16 *>(p.states + at * kp * values);
+    const __nv_bfloat16 *P1 = reinterpret_cast<const __nv_bfloat16 *>(bp.ends + at * kp * values);
+    auto S0 = [&](int k, int v) { return __bfloat162float(P0[v * kp + k]) + __bfloat162float(P0[(values + v) * kp + k]); };
+    auto S1 = [&](int k, int v) { return __bfloat162float(P1[v * kp + k]) + __bfloat162float(P1[(values + v) * kp + k]); };
     const float *U = p.u + at * kChunk * values, *dR = bp.dr + at * kChunk * values;
     auto q = [&](int i, int k) { return i < n ? to_f32<T>(delta_at<T>(p.q, c.batch, c.row + i, kh)[k]) : 0.0f; };
     auto k_ = [&](int i, int k) { return i < n ? to_f32<T>(delta_at<T>(p.k, c.batch, c.row + i, kh)[k]) : 0.0f; };
@@ -72,7 +101,7 @@ __global__ void __launch_bounds__(kThreads) delta_grad_kernel(DeltaBackwardParam
         __syncthreads();
     };
     // dQ
-    delta_product(n, keys, values, go, [&](int v, int k) { return S0[int64_t(k) * values + v]; },
+    delta_product(n, keys, values, go, [&](int v, int k) { return S0(k, v); },
                   [&](int i, int k, float s) { acc[i * keys + k] = p.scale * first[i] * s; });
     __syncthreads();
     delta_product(n, keys, n, [&](int i, int j) { return dw[i * kChunk + j]; }, k_, [&](int i, int k, float s) {
@@ -82,7 +111,7 @@ __global__ void __launch_bounds__(kThreads) delta_grad_kernel(DeltaBackwardParam
     dot(0, [&](int i, int k) { return q(i, k) * acc[i * keys + k]; });
     // Z
     delta_product(n, keys, values, [&](int i, int v) { return dR[i * values + v]; },
-                  [&](int v, int k) { return S0[int64_t(k) * values + v]; },
+                  [&](int v, int k) { return S0(k, v); },
                   [&](int i, int k, float s) { z[i * keys + k] = -first[i] * s; });
     __syncthreads();
     delta_product(n, keys, n, [&](int i, int j) { return cross[i * kChunk + j]; }, k_,
@@ -90,7 +119,7 @@ __global__ void __launch_bounds__(kThreads) delta_grad_kernel(DeltaBackwardParam
     dot(1, [&](int i, int k) { return k_(i, k) * z[i * keys + k]; });
     // Y, and the part of <S1, dS1> that this chunk wrote
     delta_product(n, keys, values, [&](int i, int v) { return U[i * values + v]; },
-                  [&](int v, int k) { return S1[int64_t(k) * values + v]; },
+                  [&](int v, int k) { return S1(k, v); },
                   [&](int i, int k, float s) { acc[i * keys + k] = rest[i] * s; });
     __syncthreads();
     if (tid < 32) {
@@ -103,7 +132,7 @@ __global__ void __launch_bounds__(kThreads) delta_grad_kernel(DeltaBackwardParam
     __syncthreads();
     if (tid < 32) {
         float s = 0.0f;
-        for (int e = tid; e < keys * values; e += 32) s = fmaf(S0[e], S1[e], s);
+        for (int e = tid; e < keys * values; e += 32) s = fmaf(S0(e / values, e % values), S1(e / values, e % values), s);
         for (int o = 16; o > 0; o /= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
         if (tid == 0) whole_dot = fmaf(first[kChunk - 1], s, whole_dot);
     }

@@ -243,16 +243,19 @@ struct DeltaParams {
     const uint32_t *offsets;
     const float *initial;
     float *final;
-    // [slots][heads]: state before the chunk [keys][values], corrections u
-    // [64][values] (both NULL without a gradient), inverse and weights [64][64]
-    float *states, *u, *inverse, *weights;
+    bool wide;  // rows of q, k, v and grad_out are whole 16-byte pieces
+    // [slots][heads]: inverse and weights, each [64][64] in two planes of bf16
+    // (tensor.cuh, split2); and, without a gradient NULL, corrections u f32
+    // [64][values], and the state before the chunk, two planes of bf16
+    // [values][keys up to a multiple of 8]
+    float *inverse, *weights, *u, *states;
 };
 struct DeltaBackwardParams {
     DeltaParams f;
     DeltaRows grad_out, grad_q, grad_k, grad_v, grad_g, grad_beta;
     const float *grad_final;
     float *grad_initial;
-    float *ends, *dr;  // [slots][heads]: gradient of the state after the chunk, and of the corrections' right sides
+    float *dr, *ends;  // [slots][heads]: gradient of the corrections' right sides, and, as `states`, of the state after the chunk
     float *share;      // [slots][heads][2][64][keys]: shares of grad_q and grad_k where key heads are shared
 };
 struct DeltaStepParams {
@@ -268,6 +271,9 @@ struct DeltaStepParams {
 cudaError_t launch_delta_local(dwp_dtype t, const DeltaParams &p, cudaStream_t s);
 cudaError_t launch_delta_chain(dwp_dtype t, const DeltaParams &p, cudaStream_t s);
 cudaError_t launch_delta_chain_back(dwp_dtype t, const DeltaBackwardParams &p, cudaStream_t s);
+cudaError_t launch_delta_chain_f32(const DeltaBackwardParams &p, bool back, cudaStream_t s);
+cudaError_t launch_delta_chain_bf16(const DeltaBackwardParams &p, bool back, cudaStream_t s);
+cudaError_t launch_delta_chain_f16(const DeltaBackwardParams &p, bool back, cudaStream_t s);
 cudaError_t launch_delta_grad(dwp_dtype t, const DeltaBackwardParams &p, cudaStream_t s);
 cudaError_t launch_delta_step(dwp_dtype t, const DeltaStepParams &p, cudaStream_t s);
 

@@ -53,26 +53,47 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
         : "memory");
 }
 
-// An operand in shared memory: descriptor of its first 16 inner indices, and
-// what to add for each 16 more.
+// An operand in shared memory, in tiles of kRows rows.
+template <int kRows, bool kOuter>
 struct Operand {
-    uint32_t addr;   // of the tiles
-    uint32_t rows;   // rows of a tile
-    bool outer;
-    __device__ __forceinline__ uint64_t at(int k) const {  // k: inner index / 16
-        if (outer) return tile_descriptor(addr + uint32_t(k) * 16u * kTileRow, rows * kTileRow);
-        return tile_descriptor(addr + uint32_t(k / 4) * rows * kTileRow + uint32_t(k % 4) * 32u, 16u);
+    uint64_t first;
+    __device__ __forceinline__ explicit Operand(const void *tiles)
+        : first(tile_descriptor(smem_addr(tiles), kOuter ? kRows * kTileRow : 16u)) {}
+    // of sixteen inner indices: the address is the descriptor's low part
+    __device__ __forceinline__ uint64_t at(int k) const {
+        return first + (kOuter ? k * 16 * kTileRow : k / 4 * kRows * kTileRow + k % 4 * 32) / 16;
     }
 };
 
-// D (+)= A B over `k` sixteens of the inner index, N = n.
-__device__ __forceinline__ void product_ss(uint32_t d, const Operand &a, const Operand &b, int n, int k, bool add) {
-    const uint32_t kind = product_kind(n, a.outer, b.outer);
-    for (int i = 0; i < k; ++i) mma_ss(d, a.at(i), b.at(i), kind, add || i > 0);
+// D (+)= A B over K of the inner index.  By one thread; the loops unroll, so
+// that a product is a run of instructions whose descriptors differ by constants.
+template <int N, int K, int AR, bool AO, int BR, bool BO>
+__device__ __forceinline__ void product_ss(uint32_t d, const Operand<AR, AO> &a, const Operand<BR, BO> &b, bool add) {
+    const uint32_t kind = product_kind(N, AO, BO);
+#pragma unroll
+    for (int i = 0; i < K / 16; ++i) mma_ss(d, a.at(i), b.at(i), kind, add || i > 0);
 }
-__device__ __forceinline__ void product_ts(uint32_t d, uint32_t a, const Operand &b, int n, int k, bool add) {
-    const uint32_t kind = product_kind(n, false, b.outer);
-    for (int i = 0; i < k; ++i) mma_ts(d, a + uint32_t(i) * 8u, b.at(i), kind, add || i > 0);
+template <int N, int K, int BR, bool BO>
+__device__ __forceinline__ void product_ts(uint32_t d, uint32_t a, const Operand<BR, BO> &b, bool add) {
+    const uint32_t kind = product_kind(N, false, BO);
+#pragma unroll
+    for (int i = 0; i < K / 16; ++i) mma_ts(d, a + uint32_t(i) * 8u, b.at(i), kind, add || i > 0);
+}
+
+// One thread of a whole warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
+// Wait for the phase of the given parity, without sleeping between polls (a
+// product takes less than a sleep); false after a second or so.
+constexpr uint32_t kProductWaitLimit = 1u << 22;
+__device__ __forceinline__ bool mma_wait(uint64_t *bar, uint32_t parity) {
+    for (uint32_t i = 0; i < kProductWaitLimit; ++i)
+        if (mbar_try_wait(bar, parity)) return true;
+    return false;
 }
 
 // The products issued so far by this thread arrive on `bar` when done.
