@@ -13,9 +13,9 @@
 //   S1 = e^{G_C} S0 + K^T diag(e^{G_C - G}) U
 //
 // T and A depend on the chunk alone (delta_local.cu, all chunks at once); the
-// states go from chunk to chunk (delta_chain.cu).  The gradient walks the
-// chunks back for the states' gradients (delta_chain.cu) and then has all
-// chunks at once again (delta_grad.cu).
+// states go from chunk to chunk (delta_chain.cuh).  The gradient walks the
+// chunks back for the states' gradients (delta_chain.cuh) and then has all
+// chunks at once again (delta_grad.cuh).
 #pragma once
 
 #include "sequence.cuh"

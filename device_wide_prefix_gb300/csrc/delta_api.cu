@@ -108,8 +108,10 @@ dwp_status delta_backward(const dwp_delta_backward_args &a, void *scratch, size_
     dwp_status st = c.status;
     if (st != DWP_SUCCESS) return st;
     const int64_t n = f.batch * f.rows, state = f.heads * f.keys * f.values;
+    bool wide = false;
     if (n > 0) {
         c.heads(a.grad_out, f.dtype, f.batch, f.rows, f.heads, f.values, false);
+        wide = delta_wide(c, f);
         c.dense(a.grad_q, f.dtype, n * f.key_heads * f.keys, true, false);
         c.dense(a.grad_k, f.dtype, n * f.key_heads * f.keys, true, false);
         c.dense(a.grad_v, f.dtype, n * f.heads * f.values, true, false);
@@ -122,12 +124,11 @@ dwp_status delta_backward(const dwp_delta_backward_args &a, void *scratch, size_
     const int64_t places = delta_slots(f) * f.heads;
     const size_t dr = size_t(places * DWP_DELTA_CHUNK * f.values) * 4u;
     const size_t ends = round16(size_t(places * delta_state(f)) * 4u);
-    const size_t share = f.heads == f.key_heads ? 0u : size_t(places * 2 * DWP_DELTA_CHUNK * f.keys) * 4u;
-    if (!c.scratch(scratch, bytes, dr + ends + share, &st)) return st;
+    if (!c.scratch(scratch, bytes, dr + ends, &st)) return st;
     if (seqs == 0) return DWP_SUCCESS;
     DeltaBackwardParams p = {};
     p.f = delta_params(f, seqs, nullptr);
-    p.f.wide = delta_wide(c, f);
+    p.f.wide = wide;
     p.grad_out = delta_rows(a.grad_out);
     p.grad_q = delta_dense(a.grad_q, f.rows, f.key_heads, f.keys);
     p.grad_k = delta_dense(a.grad_k, f.rows, f.key_heads, f.keys);
@@ -138,7 +139,7 @@ dwp_status delta_backward(const dwp_delta_backward_args &a, void *scratch, size_
     char *at = static_cast<char *>(scratch);
     p.dr = reinterpret_cast<float *>(at);
     p.ends = reinterpret_cast<float *>(at + dr);
-    p.share = reinterpret_cast<float *>(at + dr + ends);
+    p.wide = aligned(a.grad_v, 16);
     const auto t = static_cast<dwp_dtype>(f.dtype);
     if (n > 0 || a.grad_initial_state) {
         const cudaError_t err = launch_delta_chain_back(t, p, s);

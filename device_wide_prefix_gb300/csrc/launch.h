@@ -228,8 +228,8 @@ cudaError_t launch_scan_walk_back_bf16(const ScanParams &p, cudaStream_t s);
 cudaError_t launch_scan_walk_back_f16(const ScanParams &p, cudaStream_t s);
 cudaError_t launch_selscan_step(dwp_dtype t, const ScanStepParams &p, cudaStream_t s);
 
-// Gated delta rule (delta_local.cu, delta_chain.cu, delta_grad.cu,
-// delta_step.cu).  Rows of [heads, keys] or [heads, values].
+// Gated delta rule (delta_local.cu, delta_chain.cuh, delta_grad.cuh,
+// delta_step.cu; delta_types.cu and a file for each type).  Rows of [heads, keys] or [heads, values].
 struct DeltaRows {
     char *data;
     int64_t batch, row, head;  // strides in elements
@@ -256,7 +256,7 @@ struct DeltaBackwardParams {
     const float *grad_final;
     float *grad_initial;
     float *dr, *ends;  // [slots][heads]: gradient of the corrections' right sides, and, as `states`, of the state after the chunk
-    float *share;      // [slots][heads][2][64][keys]: shares of grad_q and grad_k where key heads are shared
+    bool wide;  // rows of grad_v start on 16 bytes
 };
 struct DeltaStepParams {
     int keys, values, key_heads, heads;
@@ -275,6 +275,9 @@ cudaError_t launch_delta_chain_f32(const DeltaBackwardParams &p, bool back, cuda
 cudaError_t launch_delta_chain_bf16(const DeltaBackwardParams &p, bool back, cudaStream_t s);
 cudaError_t launch_delta_chain_f16(const DeltaBackwardParams &p, bool back, cudaStream_t s);
 cudaError_t launch_delta_grad(dwp_dtype t, const DeltaBackwardParams &p, cudaStream_t s);
+cudaError_t launch_delta_grad_f32(const DeltaBackwardParams &p, cudaStream_t s);
+cudaError_t launch_delta_grad_bf16(const DeltaBackwardParams &p, cudaStream_t s);
+cudaError_t launch_delta_grad_f16(const DeltaBackwardParams &p, cudaStream_t s);
 cudaError_t launch_delta_step(dwp_dtype t, const DeltaStepParams &p, cudaStream_t s);
 
 struct NormParams {

@@ -531,8 +531,7 @@ dwp_status dwp_gated_delta_rule(const dwp_delta_args *args, void *d_scratch, siz
  *                 grad_beta  the same, beta_dtype
  *   grad_initial_state  NULL, or as initial_state
  *   scratch       4 * (keys' + DWP_DELTA_CHUNK) * values bytes for each of the
- *                 chunks and head, and 8 * DWP_DELTA_CHUNK * keys more where
- *                 heads share keys
+ *                 chunks and head
  */
 typedef struct dwp_delta_backward_args {
     dwp_delta_args delta;
