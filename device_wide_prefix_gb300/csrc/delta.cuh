@@ -100,20 +100,19 @@ __device__ __forceinline__ Sum2 sum2_add(Sum2 a, Sum2 b) {
 }
 __device__ __forceinline__ float sum2_less(Sum2 a, Sum2 b) { return (a.hi - b.hi) + (a.lo - b.lo); }
 
-// Running sums of the chunk's log decays, by one warp: lane l has rows l and l + 32.
-template <class F>
-__device__ __forceinline__ void delta_sums(Sum2 *sums, F g) {
+// Running sums of a chunk's log decays, by one warp: lane l has rows l and l + 32.
+__device__ __forceinline__ void delta_sums(Sum2 (&sum)[2], const float (&g)[2]) {
     const int lane = threadIdx.x % 32;
-    Sum2 a = {g(lane), 0.0f}, b = {g(lane + 32), 0.0f};
+    sum[0] = {g[0], 0.0f}, sum[1] = {g[1], 0.0f};
 #pragma unroll
-    for (int o = 1; o < 32; o *= 2) {
-        const Sum2 pa = {__shfl_up_sync(0xffffffffu, a.hi, o), __shfl_up_sync(0xffffffffu, a.lo, o)};
-        const Sum2 pb = {__shfl_up_sync(0xffffffffu, b.hi, o), __shfl_up_sync(0xffffffffu, b.lo, o)};
-        if (lane >= o) a = sum2_add(pa, a), b = sum2_add(pb, b);
-    }
-    const Sum2 half = {__shfl_sync(0xffffffffu, a.hi, 31), __shfl_sync(0xffffffffu, a.lo, 31)};
-    sums[lane] = a;
-    sums[lane + 32] = sum2_add(half, b);
+    for (int o = 1; o < 32; o *= 2)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const Sum2 before = {__shfl_up_sync(0xffffffffu, sum[i].hi, o), __shfl_up_sync(0xffffffffu, sum[i].lo, o)};
+            if (lane >= o) sum[i] = sum2_add(before, sum[i]);
+        }
+    const Sum2 half = {__shfl_sync(0xffffffffu, sum[0].hi, 31), __shfl_sync(0xffffffffu, sum[0].lo, 31)};
+    sum[1] = sum2_add(half, sum[1]);
 }
 
 // 16 bytes to shared memory without a register between; `bytes` of them are
@@ -149,21 +148,23 @@ __device__ __forceinline__ void store_pieces(char *hi, char *lo, uint32_t at, co
 
 // Rows of a head into tiles of kRows rows and kWidth columns, from row `first`
 // of the tile on: 64 rows, zeros past the chunk's `n` and past `dim` columns.
-// The second piece lies `lo` bytes behind the first.
+// The second piece lies `lo` bytes behind the first.  By kThreads threads.
+// `wide`: the rows are whole 16-byte pieces (kWide: known to be).
 template <class T, bool kWide, int kRows, int kWidth, int kThreads>
-__device__ __forceinline__ void load_tile(char *tile, uint32_t lo, int first, const DeltaRows &r, int64_t batch, int64_t row,
-                                          int head, int n, int dim) {
+__device__ __forceinline__ void load_tile(int thread, char *tile, uint32_t lo, int first, const DeltaRows &r, int64_t batch,
+                                          int64_t row, int head, int n, int dim, bool wide = kWide) {
     const T *src = delta_at<T>(r, batch, row, head);
-#pragma unroll
-    for (int e = threadIdx.x; e < kChunk * kWidth / 8; e += kThreads) {
+#pragma unroll 4
+    for (int e = thread; e < kChunk * kWidth / 8; e += kThreads) {
         const int i = e / (kWidth / 8), c = e % (kWidth / 8), left = i < n ? dim - c * 8 : 0;
         const uint32_t at = uint32_t(c / 8 * kRows) * kTileRow + tile_piece(uint32_t(first + i), uint32_t(c % 8));
         const T *from = src + int64_t(left > 0 ? i : 0) * r.row + (left > 0 ? c * 8 : 0);
-        if constexpr (kPieces<T> == 1 && kWide) {
+        if (kPieces<T> == 1 && wide) {
             copy16(smem_addr(tile + at), from, left > 0 ? 16u : 0u);
         } else {
             float f[8];
-            load_eight<T, kWide>(f, from, left);
+            if (wide) load_eight<T, true>(f, from, left);
+            else load_eight<T, false>(f, from, left);
             store_pieces(tile, kPieces<T> == 2 ? tile + lo : nullptr, at, f);
         }
     }

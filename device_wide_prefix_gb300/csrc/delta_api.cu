@@ -32,14 +32,14 @@ int64_t delta_slots(const dwp_delta_args &a) {
     return a.offsets ? a.rows / DWP_DELTA_CHUNK + a.num_segments : a.batch * delta_chunks(a);
 }
 
-// Words of a kept state: keys in whole 16-byte pieces of bf16.
-int64_t delta_state(const dwp_delta_args &a) { return (a.keys + 7) / 8 * 8 * a.values; }
-// Whether the rows that were checked so far are whole 16-byte pieces.
-bool delta_wide(const Check &c, const dwp_delta_args &a) {
-    return ((c.bits | uintptr_t((a.keys | a.values) * size_of(a.dtype))) & 15u) == 0;
+// Words of a kept state: keys in whole tiles.
+int64_t delta_state(const dwp_delta_args &a) { return (a.keys + 63) / 64 * 64 * a.values; }
+// Whether rows with these address and stride bits are whole 16-byte pieces.
+bool delta_wide(uintptr_t bits, const dwp_delta_args &a) {
+    return ((bits | uintptr_t((a.keys | a.values) * size_of(a.dtype))) & 15u) == 0;
 }
 
-int64_t check_delta(Check &c, const dwp_delta_args &a, bool backward) {
+int64_t check_delta(Check &c, const dwp_delta_args &a, bool backward, uintptr_t &out_bits) {
     c.require(delta_sizes_ok(a.dtype, a.beta_dtype, a.keys, a.values, a.key_heads, a.heads, a.scale));
     const int64_t seqs = sequences(c, 1, a.batch, a.rows, a.num_segments, a.offsets);
     if (c.status != DWP_SUCCESS) return 0;
@@ -49,7 +49,9 @@ int64_t check_delta(Check &c, const dwp_delta_args &a, bool backward) {
         c.heads(a.k, a.dtype, a.batch, a.rows, a.key_heads, a.keys, false);
         c.heads(a.v, a.dtype, a.batch, a.rows, a.heads, a.values, false);
         const uintptr_t others = c.bits;
+        c.bits = 0;
         if (!backward) c.heads(a.out, a.dtype, a.batch, a.rows, a.heads, a.values, true);
+        out_bits = c.bits;
         if (a.g.data) c.rows(a.g, DWP_F32, a.batch, a.rows, a.heads, false);
         c.rows(a.beta, a.beta_dtype, a.batch, a.rows, a.heads, false);
         c.bits = others;
@@ -83,14 +85,15 @@ DeltaParams delta_params(const dwp_delta_args &a, int64_t seqs, void *scratch) {
 
 dwp_status delta_forward(const dwp_delta_args &a, void *scratch, size_t *bytes, cudaStream_t s) {
     Check c;
-    const int64_t seqs = check_delta(c, a, false);
+    uintptr_t out_bits = 0;
+    const int64_t seqs = check_delta(c, a, false, out_bits);
     dwp_status st = c.status;
     if (st != DWP_SUCCESS) return st;
     const size_t need = a.checkpoints ? 0u : size_t(delta_slots(a) * a.heads * 2 * kTile) * 4u;
     if (!c.scratch(scratch, bytes, need, &st)) return st;
     if (seqs == 0) return DWP_SUCCESS;
     DeltaParams p = delta_params(a, seqs, scratch);
-    p.wide = delta_wide(c, a);
+    p.wide = delta_wide(c.bits, a), p.out_wide = delta_wide(out_bits, a);
     const auto t = static_cast<dwp_dtype>(a.dtype);
     if (a.batch * a.rows > 0) {
         const cudaError_t err = launch_delta_local(t, p, s);
@@ -104,14 +107,15 @@ dwp_status delta_forward(const dwp_delta_args &a, void *scratch, size_t *bytes, 
 dwp_status delta_backward(const dwp_delta_backward_args &a, void *scratch, size_t *bytes, cudaStream_t s) {
     Check c;
     const dwp_delta_args &f = a.delta;
-    const int64_t seqs = check_delta(c, f, true);
+    uintptr_t out_bits = 0;
+    const int64_t seqs = check_delta(c, f, true, out_bits);
     dwp_status st = c.status;
     if (st != DWP_SUCCESS) return st;
     const int64_t n = f.batch * f.rows, state = f.heads * f.keys * f.values;
     bool wide = false;
     if (n > 0) {
         c.heads(a.grad_out, f.dtype, f.batch, f.rows, f.heads, f.values, false);
-        wide = delta_wide(c, f);
+        wide = delta_wide(c.bits, f);
         c.dense(a.grad_q, f.dtype, n * f.key_heads * f.keys, true, false);
         c.dense(a.grad_k, f.dtype, n * f.key_heads * f.keys, true, false);
         c.dense(a.grad_v, f.dtype, n * f.heads * f.values, true, false);

@@ -14,6 +14,14 @@
 // of the next products, as R and U do, and K, Q, T, A and dO are operands in
 // shared memory as they are stored.  What is not itself bf16 is two bf16
 // (split2), and of a product of two such the three larger parts are taken.
+// For bf16 outputs the weights, corrections and state of the last products
+// are one bf16 each: they cost at most 2^-8 of the output's terms.
+//
+// Eight warps do this, and only this.  Four more work ahead and behind: one
+// issues the products (a warp that issues is held back as long as the products
+// before it run), one loads, one has the decays and the copies of what is
+// kept, one stores the outputs.  With all of it done by the eight a chunk of
+// 128 x 128 took 11,200 cycles.
 #pragma once
 
 #include "delta.cuh"
@@ -22,12 +30,15 @@ namespace dwp {
 
 namespace {
 
-constexpr int kChainThreads = 256;
+constexpr int kChainThreads = 256, kHelpThreads = 128, kIssueWarp = kChainThreads / 32;
+// 168 registers a thread at launch, of which the helpers give some to the chain:
+// 256 x 224 + 128 x 56 = 384 x 168.
+constexpr int kChainRegisters = 224, kHelpRegisters = 56;
 constexpr int kMostValues = 128;
 
-// Shared memory of one chunk's inputs.
+// Shared memory: the chunks' inputs, the outputs on their way, and what is kept.
 template <class T, int KD, bool kBack>
-struct ChainStage {
+struct ChainSpace {
     static constexpr int kP = kPieces<T>;
     static constexpr uint32_t kTileBytes = kChunk * kTileRow;  // of 64 x 64
     static constexpr uint32_t kKeys = kChunk * KD * 2, kValues = kChunk * kMostValues * 2;
@@ -36,346 +47,521 @@ struct ChainStage {
     static constexpr uint32_t inverse = v + (kBack ? kP * kValues : kChunk * kMostValues * uint32_t(sizeof(T)));
     static constexpr uint32_t weights = inverse + 2 * kTileBytes, bytes = weights + kWeightPieces * kTileBytes;
     static constexpr int kStages = kP == 1 ? 2 : 1;
-    static constexpr size_t kAll = 1024 + size_t(kStages) * bytes;
+    static constexpr uint32_t out = kStages * bytes, kOut = kBack ? 0 : kChunk * kMostValues * uint32_t(sizeof(T));
+    static constexpr uint32_t keep = out + kOut, kKeep = 2 * kMostValues * KD * 2;
+    static_assert(kKeep >= kChunk * kMostValues * 4, "rows of f32 fit the kept state's place");
+    static constexpr size_t kAll = 1024 + keep + kKeep;
 };
 
-// Two planes of 64 x 64 as tiles.
-template <int kCount>
-__device__ __forceinline__ void load_planes(char *tile, const float *planes) {
-    const char *src = reinterpret_cast<const char *>(planes);
-#pragma unroll
-    for (int e = threadIdx.x; e < kCount * kChunk * 8; e += kChainThreads) {
-        const uint32_t plane = e / (kChunk * 8), r = e / 8 % kChunk, c = e % 8;
-        copy16(smem_addr(tile + plane * kChunk * kTileRow + tile_piece(r, c)), src + size_t(e) * 16, 16u);
-    }
-}
+// Decays and betas of a chunk's rows.
+struct ChainRows {
+    alignas(16) float beta[kChunk], first[kChunk], rest[kChunk];  // first: e^G, rest: e^{G_C - G}
+};
 
-template <class T, int KD, bool kBack, bool kWide>
-__global__ void __launch_bounds__(kChainThreads, 1) delta_chain_kernel(DeltaBackwardParams bp) {
-    using Stage = ChainStage<T, KD, kBack>;
-    constexpr int kP = Stage::kP, kH = KD / 2;  // kH: keys of a thread
+struct ChainMaps {
+    CUtensorMap k, q, v;  // v: or grad_out
+};
+
+// kMaps: bf16 rows of whole 16-byte pieces, which come by tensor maps.
+template <class T, int KD, bool kBack, bool kMaps>
+__global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
+    delta_chain_kernel(DeltaBackwardParams bp, const __grid_constant__ ChainMaps maps) {
+    using Space = ChainSpace<T, KD, kBack>;
+    constexpr int kP = Space::kP, kH = KD / 2, kStages = Space::kStages;  // kH: keys of a thread
+    constexpr int kLoadThreads = kMaps ? 32 : 96;
     extern __shared__ char raw[];
-    __shared__ float beta_[2][kChunk], first_[2][kChunk], rest_[2][kChunk];
-    __shared__ Sum2 sums[kChunk];
-    __shared__ uint64_t bars[5];
+    __shared__ ChainRows rows_of[2];
+    __shared__ uint64_t done[5], ready[3], full[2], empty[2], out_full, out_empty, kept_read, landed;
     __shared__ uint32_t tmem;
     const DeltaParams &p = bp.f;
     char *sm = reinterpret_cast<char *>((reinterpret_cast<uintptr_t>(raw) + 1023) / 1024 * 1024);
     pdl_trigger();
     pdl_wait();
     const int tid = threadIdx.x, lane = tid % 32, warp = __shfl_sync(0xffffffffu, tid / 32, 0);
-    const int half = warp / 4, dv = warp % 4 * 32 + lane, t0 = half * 32, k0 = half * kH;
     const int head = blockIdx.y, kh = head / (p.heads / p.key_heads), keys = p.keys, values = p.values;
     const int64_t seq = blockIdx.x;
     int64_t batch, row0, rows, slot0;
     delta_sequence(p, seq, batch, row0, rows, slot0);
     const int64_t chunks = (rows + kChunk - 1) / kChunk;
-    const int kp = (keys + 7) / 8 * 8;
+    auto chunk_of = [&](int64_t step) { return kBack ? chunks - 1 - step : step; };
+    auto rows_in = [&](int64_t c) { return int(min(rows - c * kChunk, int64_t(kChunk))); };
+    auto stage_of = [&](int64_t step) { return kStages == 2 ? int(step & 1) : 0; };
+    auto round_of = [&](int64_t step) { return uint32_t(step / kStages) & 1u; };
+    float *const kept = kBack ? bp.ends : p.states, *const kept_rows = kBack ? bp.dr : p.u;
 
     if (tid == 0) {
-        for (int i = 0; i < 5; ++i) mbar_init(&bars[i], 1);
+        for (int i = 0; i < 5; ++i) mbar_init(&done[i], 1);
+        for (int i = 0; i < 3; ++i) mbar_init(&ready[i], kChainThreads);
+        // the loaders, the bytes, the decays
+        for (int i = 0; i < 2; ++i) mbar_init(&full[i], kLoadThreads + 2), mbar_init(&empty[i], 1);
+        mbar_init(&out_full, kChainThreads);
+        mbar_init(&out_empty, 32);
+        mbar_init(&kept_read, 1);
+        mbar_init(&landed, 1);
         fence_mbar_init();
     }
     if (warp == 0) tmem_alloc(&tmem, 512);
+    tmem_fence_before();
     __syncthreads();
+    tmem_fence_after();
     // columns: sums of the first product; of the second; of the state's; then
     // operands: the state (hi, lo), R or U (hi, lo), U as it is or the queries' side (hi, lo)
-    const uint32_t tm = tmem, mine = tm + (uint32_t(warp % 4) << 21);
+    const uint32_t tm = tmem;
     constexpr uint32_t kD0 = 0, kD1 = 64, kDS = 128, kS = 256, kR = 384, kU = 448;
+    bool ok = true;
+    auto wait = [&](uint64_t &bar, uint32_t parity) {
+        if (ok) ok = mma_wait(&bar, parity & 1u);
+    };
 
-    float S[kH];
-    {
-        const float *from = (kBack ? bp.grad_final : p.initial);
-        const int64_t at = (seq * p.heads + head) * keys * values + dv;
-#pragma unroll
-        for (int k = 0; k < kH; ++k)
-            S[k] = from && dv < values && k0 + k < keys ? from[at + int64_t(k0 + k) * values] : 0.0f;
-    }
-    auto chunk_of = [&](int64_t step) { return kBack ? chunks - 1 - step : step; };
-    // a chunk's inputs to stage `st`; its decays and betas to registers of the last warp
-    float g2[2], b2[2];
-    auto load = [&](int64_t step, int st) {
-        const int64_t c = chunk_of(step), row = row0 + c * kChunk, at = (slot0 + c) * p.heads + head;
-        const int n = int(min(rows - c * kChunk, int64_t(kChunk)));
-        char *s = sm + st * Stage::bytes;
-        load_tile<T, kWide, kChunk, KD, kChainThreads>(s + Stage::k, Stage::kKeys, 0, p.k, batch, row, kh, n, keys);
-        load_tile<T, kWide, kChunk, KD, kChainThreads>(s + Stage::q, Stage::kKeys, 0, p.q, batch, row, kh, n, keys);
-        load_planes<2>(s + Stage::inverse, p.inverse + at * kChunk * kChunk);
-        load_planes<Stage::kWeightPieces>(s + Stage::weights, p.weights + at * kChunk * kChunk);
-        if constexpr (kBack) {
-            load_tile<T, kWide, kChunk, kMostValues, kChainThreads>(s + Stage::v, Stage::kValues, 0, bp.grad_out, batch, row,
-                                                                    head, n, values);
-        } else {
-            const T *src = delta_at<T>(p.v, batch, row, head);
-            constexpr int kEach = 16 / int(sizeof(T)), kRow = kMostValues / kEach;
-#pragma unroll
-            for (int e = tid; e < kChunk * kRow; e += kChainThreads) {
-                const int i = e / kRow, j = e % kRow * kEach, left = i < n ? values - j : 0;
-                T *to = reinterpret_cast<T *>(s + Stage::v) + i * kMostValues + j;
-                if constexpr (kWide) {
-                    copy16(smem_addr(to), left > 0 ? src + int64_t(i) * p.v.row + j : src, left > 0 ? 16u : 0u);
+    if (warp >= kIssueWarp) set_registers_down<kHelpRegisters>();
+    else set_registers_up<kChainRegisters>();
+    if (warp == kIssueWarp) {
+        const bool one = elect_one();
+        for (int64_t step = 0; step < chunks; ++step) {
+            const int st = stage_of(step);
+            char *s = sm + st * Space::bytes;
+            const Operand<kChunk, true> Ko(s + Space::k), Klo(s + Space::k + Space::kKeys);
+            wait(full[st], round_of(step));
+            wait(ready[0], uint32_t(step));
+            tmem_fence_after();
+            if (one) {
+                const Operand<kChunk, false> K(s + Space::k), Kl(s + Space::k + Space::kKeys);
+                product_ts<kChunk, KD>(tm + kD0, tm + kS, K, false);
+                product_ts<kChunk, KD>(tm + kD0, tm + kS + KD / 2, K, true);
+                if constexpr (kP == 2) product_ts<kChunk, KD>(tm + kD0, tm + kS, Kl, true);
+                mma_commit(&done[0]);
+                if constexpr (kBack) {
+                    const Operand<kChunk, true> dO(s + Space::v), dOl(s + Space::v + Space::kValues), A(s + Space::weights),
+                        Al(s + Space::weights + Space::kTileBytes);
+                    product_ss<kChunk, kChunk>(tm + kD1, dO, A, false);
+                    product_ss<kChunk, kChunk>(tm + kD1, dO, Al, true);
+                    if constexpr (kP == 2) product_ss<kChunk, kChunk>(tm + kD1, dOl, A, true);
                 } else {
+                    const Operand<kChunk, false> Q(s + Space::q), Ql(s + Space::q + Space::kKeys);
+                    product_ts<kChunk, KD>(tm + kDS, tm + kS, Q, false);
+                    if constexpr (kP == 2) {
+                        product_ts<kChunk, KD>(tm + kDS, tm + kS + KD / 2, Q, true);
+                        product_ts<kChunk, KD>(tm + kDS, tm + kS, Ql, true);
+                    }
+                }
+                mma_commit(&done[1]);
+            }
+            __syncwarp();
+            wait(ready[1], uint32_t(step));
+            tmem_fence_after();
+            if (one) {
+                const Operand<kChunk, kBack> inv(s + Space::inverse), invl(s + Space::inverse + Space::kTileBytes);
+                product_ts<kChunk, kChunk>(tm + kD0, tm + kR, inv, false);
+                product_ts<kChunk, kChunk>(tm + kD0, tm + kR + 32, inv, true);
+                product_ts<kChunk, kChunk>(tm + kD0, tm + kR, invl, true);
+                mma_commit(&done[2]);
+            }
+            __syncwarp();
+            wait(ready[2], uint32_t(step));
+            tmem_fence_after();
+            if (one) {
+                product_ts<KD, kChunk>(tm + kDS, tm + kR, Ko, false);
+                product_ts<KD, kChunk>(tm + kDS, tm + kR + 32, Ko, true);
+                if constexpr (kP == 2) product_ts<KD, kChunk>(tm + kDS, tm + kR, Klo, true);
+                if constexpr (kBack) {
+                    const Operand<kChunk, true> Q(s + Space::q), Ql(s + Space::q + Space::kKeys);
+                    product_ts<KD, kChunk>(tm + kDS, tm + kU, Q, true);
+                    product_ts<KD, kChunk>(tm + kDS, tm + kU + 32, Q, true);
+                    if constexpr (kP == 2) product_ts<KD, kChunk>(tm + kDS, tm + kU, Ql, true);
+                }
+                mma_commit(&done[3]);
+                if constexpr (!kBack) {
+                    const Operand<kChunk, false> A(s + Space::weights), Al(s + Space::weights + Space::kTileBytes);
+                    product_ts<kChunk, kChunk>(tm + kD1, tm + kU, A, false);
+                    if constexpr (kP == 2) {
+                        product_ts<kChunk, kChunk>(tm + kD1, tm + kU + 32, A, true);
+                        product_ts<kChunk, kChunk>(tm + kD1, tm + kU, Al, true);
+                    }
+                    mma_commit(&done[4]);
+                }
+                mma_commit(&empty[st]);
+            }
+            __syncwarp();
+        }
+    } else if (warp > kIssueWarp) {
+        const int t = tid - kChainThreads - 32;  // of the loaders
+        const bool loads = t < kLoadThreads, decays = warp == kIssueWarp + 2, stores = !kBack && warp == kIssueWarp + 3;
+        auto load = [&](int64_t step) {
+            const int st = stage_of(step);
+            const int64_t c = chunk_of(step), row = row0 + c * kChunk, at = (slot0 + c) * p.heads + head;
+            const int n = rows_in(c);
+            char *s = sm + st * Space::bytes;
+            if (step >= kStages) wait(empty[st], round_of(step) + 1u);
+            constexpr uint32_t planes = (2 + Space::kWeightPieces) * Space::kTileBytes;
+            constexpr uint32_t boxes = 2 * Space::kKeys + Space::kValues;
+            if (t == 0) {
+                mbar_arrive_expect_tx(&full[st], planes + (kMaps && n == kChunk ? boxes : 0u));
+                bulk_load(s + Space::inverse, p.inverse + at * kChunk * kChunk, 2 * Space::kTileBytes, &full[st]);
+                bulk_load(s + Space::weights, p.weights + at * kChunk * kChunk, Space::kWeightPieces * Space::kTileBytes,
+                          &full[st]);
+                if constexpr (kMaps) {
+                    // the rows after a short chunk's are another sequence's: they are made zeros before they count
+                    uint64_t *bar = n == kChunk ? &full[st] : &landed;
+                    if (n < kChunk) mbar_arrive_expect_tx(&landed, boxes);
+                    const int r = int(row), b = int(batch);
 #pragma unroll
-                    for (int l = 0; l < kEach; ++l) to[l] = l < left ? src[int64_t(i) * p.v.row + j + l] : from_f32<T>(0.0f);
+                    for (int x = 0; x < KD; x += 64) {
+                        map_load(s + Space::k + x * kTileRow, &maps.k, bar, x, kh, r, b);
+                        map_load(s + Space::q + x * kTileRow, &maps.q, bar, x, kh, r, b);
+                    }
+                    if constexpr (kBack) {
+                        map_load(s + Space::v, &maps.v, bar, 0, head, r, b);
+                        map_load(s + Space::v + 64 * kTileRow, &maps.v, bar, 64, head, r, b);
+                    } else {
+                        map_load(s + Space::v, &maps.v, bar, 0, head, r, b);
+                    }
                 }
             }
-        }
-        if (warp == 7)
+            if constexpr (kMaps) {
+                if (n < kChunk) {
+                    __syncwarp();
+                    wait(landed, 0);
+                    // rows of 128 bytes in tiles; of 256 in the values' forward
+                    auto clear = [&](char *tile, uint32_t pitch) {
+                        for (uint32_t e = uint32_t(n) * pitch / 16 + lane; e < kChunk * pitch / 16; e += 32)
+                            reinterpret_cast<uint4 *>(tile)[e] = make_uint4(0, 0, 0, 0);
+                    };
+                    for (int x = 0; x < KD; x += 64) clear(s + Space::k + x * kTileRow, 128), clear(s + Space::q + x * kTileRow, 128);
+                    if constexpr (kBack) clear(s + Space::v, 128), clear(s + Space::v + 64 * kTileRow, 128);
+                    else clear(s + Space::v, 256);
+                    fence_proxy_async_smem();
+                }
+            } else {
+                load_tile<T, false, kChunk, KD, kLoadThreads>(t, s + Space::k, Space::kKeys, 0, p.k, batch, row, kh, n, keys, p.wide);
+                load_tile<T, false, kChunk, KD, kLoadThreads>(t, s + Space::q, Space::kKeys, 0, p.q, batch, row, kh, n, keys, p.wide);
+                if constexpr (kBack) {
+                    load_tile<T, false, kChunk, kMostValues, kLoadThreads>(t, s + Space::v, Space::kValues, 0, bp.grad_out, batch,
+                                                                           row, head, n, values, p.wide);
+                } else {
+                    const T *src = delta_at<T>(p.v, batch, row, head);
+                    constexpr int kEach = 16 / int(sizeof(T)), kRow = kMostValues / kEach;
+#pragma unroll 4
+                    for (int e = t; e < kChunk * kRow; e += kLoadThreads) {
+                        const int i = e / kRow, j = e % kRow * kEach, left = i < n ? values - j : 0;
+                        T *to = reinterpret_cast<T *>(s + Space::v) + i * kMostValues + j;
+                        if (p.wide) {
+                            copy16(smem_addr(to), left > 0 ? src + i * p.v.row + j : src, left > 0 ? 16u : 0u);
+                        } else {
+#pragma unroll
+                            for (int l = 0; l < kEach; ++l) to[l] = l < left ? src[i * p.v.row + j + l] : from_f32<T>(0.0f);
+                        }
+                    }
+                }
+                copies_done();
+                fence_proxy_async_smem();
+            }
+            mbar_arrive(&full[st]);
+        };
+        float g[2], b[2];
+        auto read_decays = [&](int64_t step) {
+            if (step >= chunks) return;
+            const int64_t c = chunk_of(step), row = row0 + c * kChunk;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int r = lane + 32 * i;
-                g2[i] = r < n ? delta_g(p.g, batch, row + r, head) : 0.0f;
-                b2[i] = r < n ? delta_beta<T>(p, batch, row + r, head) : 0.0f;
+                g[i] = r < rows_in(c) ? delta_g(p.g, batch, row + r, head) : 0.0f;
+                b[i] = r < rows_in(c) ? delta_beta<T>(p, batch, row + r, head) : 0.0f;
             }
-    };
-    auto finish_load = [&](int st) {
-        if (warp != 7) return;
-        delta_sums(sums, [&](int i) { return i < 32 ? g2[0] : g2[1]; });
-        __syncwarp();
+        };
+        auto put_decays = [&](int64_t step) {
+            if (step >= chunks) return;
+            const int st = stage_of(step);
+            if (step >= kStages) wait(empty[st], round_of(step) + 1u);
+            ChainRows &r = rows_of[st];
+            Sum2 sum[2];
+            delta_sums(sum, g);
+            const Sum2 last = {__shfl_sync(0xffffffffu, sum[1].hi, 31), __shfl_sync(0xffffffffu, sum[1].lo, 31)};
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int r = lane + 32 * i;
-            const float e = __expf(sums[r].hi);
-            beta_[st][r] = b2[i];
-            first_[st][r] = fmaf(e, sums[r].lo, e);
-            rest_[st][r] = __expf(sum2_less(sums[kChunk - 1], sums[r]));
-        }
-    };
-    // the state as the next products' operand, and as kept for chunk `step`
-    auto put_state = [&](int64_t step) {
-        float *planes = kBack ? bp.ends : p.states;
-        const bool keep = planes && step < chunks && dv < values;
-        char *to = nullptr;
-        if (keep)
-            to = reinterpret_cast<char *>(planes + ((slot0 + chunk_of(step)) * p.heads + head) * kp * values) +
-                 int64_t(dv) * kp * 2;
-#pragma unroll
-        for (int k = 0; k < kH; k += 16) {
-            uint32_t hi[8], lo[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) split2(S[k + 2 * j], S[k + 2 * j + 1], hi[j], lo[j]);
-            tmem_store<8>(mine + kS + (k0 + k) / 2, hi);
-            tmem_store<8>(mine + kS + KD / 2 + (k0 + k) / 2, lo);
-            if (keep)
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    if (k0 + k + j * 8 < kp) {
-                        char *at = to + (k0 + k + j * 8) * 2;
-                        *reinterpret_cast<uint4 *>(at) = make_uint4(hi[4 * j], hi[4 * j + 1], hi[4 * j + 2], hi[4 * j + 3]);
-                        *reinterpret_cast<uint4 *>(at + int64_t(values) * kp * 2) =
-                            make_uint4(lo[4 * j], lo[4 * j + 1], lo[4 * j + 2], lo[4 * j + 3]);
-                    }
-        }
-        tmem_stored();
-    };
-    // 32 values of this thread's rows of the chunk, in two pieces, as an operand
-    auto put_rows = [&](uint32_t at, const float (&x)[32]) {
-        uint32_t hi[16], lo[16];
-#pragma unroll
-        for (int j = 0; j < 16; ++j) split2(x[2 * j], x[2 * j + 1], hi[j], lo[j]);
-        tmem_store<16>(mine + at + half * 16, hi);
-        tmem_store<16>(mine + at + 32 + half * 16, lo);
-    };
-    auto meet = [&] {  // what was stored is there for the products
-        tmem_stored();
-        tmem_fence_before();
-        __syncthreads();
-        tmem_fence_after();
-    };
-    bool ok = true;
-    auto wait = [&](int bar, int64_t step) {
-        if (ok) ok = mma_wait(&bars[bar], uint32_t(step & 1));
-        tmem_fence_after();
-    };
-    auto read = [&](float (&x)[32], uint32_t at) {
-        uint32_t v[32];
-        tmem_load<32>(v, mine + at);
-        tmem_ready();
-#pragma unroll
-        for (int j = 0; j < 32; ++j) x[j] = __uint_as_float(v[j]);
-    };
-
-    if (chunks > 0) {
-        load(0, 0);
-        put_state(0);
-        finish_load(0);
-    }
-    float o1[32];  // forward: what the state gives to the outputs
-    // forward: the outputs of chunk `step`
-    auto put_out = [&](int64_t step) {
-        const int64_t c = step, row = row0 + c * kChunk;
-        const int n = int(min(rows - c * kChunk, int64_t(kChunk)));
-        float o2[32];
-        read(o2, kD1 + t0);
-        if (dv >= values) return;
-        T *out = delta_at<T>(p.out, batch, row + t0, head) + dv;
-#pragma unroll
-        for (int j = 0; j < 32; ++j)
-            if (t0 + j < n) out[int64_t(j) * p.out.row] = from_f32<T>(ok ? fmaf(p.scale, o2[j], o1[j]) : __int_as_float(0x7fffffff));
-    };
-    for (int64_t step = 0; step < chunks; ++step) {
-        const int st = Stage::kStages == 2 ? int(step & 1) : 0, vs = int(step & 1);
-        const int64_t at = (slot0 + chunk_of(step)) * p.heads + head;
-        char *s = sm + st * Stage::bytes;
-        copies_done();
-        fence_proxy_async_smem();
-        meet();
-        const Operand<kChunk, false> K(s + Stage::k), Kl(s + Stage::k + Stage::kKeys);
-        const Operand<kChunk, true> Ko(s + Stage::k), Klo(s + Stage::k + Stage::kKeys);
-        if (warp == 0 && elect_one()) {
-            product_ts<kChunk, KD>(tm + kD0, tm + kS, K, false);
-            product_ts<kChunk, KD>(tm + kD0, tm + kS + KD / 2, K, true);
-            if constexpr (kP == 2) product_ts<kChunk, KD>(tm + kD0, tm + kS, Kl, true);
-            mma_commit(&bars[0]);
-            if constexpr (kBack) {
-                const Operand<kChunk, true> dO(s + Stage::v), dOl(s + Stage::v + Stage::kValues), A(s + Stage::weights),
-                    Al(s + Stage::weights + Stage::kTileBytes);
-                product_ss<kChunk, kChunk>(tm + kD1, dO, A, false);
-                product_ss<kChunk, kChunk>(tm + kD1, dO, Al, true);
-                if constexpr (kP == 2) product_ss<kChunk, kChunk>(tm + kD1, dOl, A, true);
+            for (int i = 0; i < 2; ++i) {
+                const float e = __expf(sum[i].hi);
+                r.beta[lane + 32 * i] = b[i], r.first[lane + 32 * i] = fmaf(e, sum[i].lo, e);
+                r.rest[lane + 32 * i] = __expf(sum2_less(last, sum[i]));
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&full[st]);
+        };
+        auto store = [&](int64_t step) {
+            wait(out_full, uint32_t(step));
+            const int64_t row = row0 + step * kChunk;
+            const int n = rows_in(step);
+            const T *from = reinterpret_cast<const T *>(sm + Space::out);
+            T *to = delta_at<T>(p.out, batch, row, head);
+            if (p.out_wide) {
+                for (int i = lane; i < n; i += 32) bulk_store(to + i * p.out.row, from + i * kMostValues, uint32_t(values * sizeof(T)));
+                bulk_commit();
+                bulk_wait_read<0>();
             } else {
-                const Operand<kChunk, false> Q(s + Stage::q), Ql(s + Stage::q + Stage::kKeys);
-                product_ts<kChunk, KD>(tm + kDS, tm + kS, Q, false);
-                if constexpr (kP == 2) {
-                    product_ts<kChunk, KD>(tm + kDS, tm + kS + KD / 2, Q, true);
-                    product_ts<kChunk, KD>(tm + kDS, tm + kS, Ql, true);
+                for (int i = 0; i < n; ++i)
+                    for (int j = lane; j < values; j += 32) to[i * p.out.row + j] = from[i * kMostValues + j];
+            }
+            mbar_arrive(&out_empty);
+        };
+        if (decays) {
+            read_decays(0);
+            put_decays(0);
+            if (kStages == 2) read_decays(1), put_decays(1);
+        }
+        if (loads && kStages == 2 && chunks > 0) load(0);
+        for (int64_t step = 0; step < chunks; ++step) {
+            if (decays) read_decays(step + kStages);
+            // a stage ahead: chunk step + 1 goes where step - 1 was
+            if (loads && (kStages == 1 || step + 1 < chunks)) load(kStages == 1 ? step : step + 1);
+            if (decays) {
+                if (kept) {
+                    wait(ready[0], uint32_t(step));
+                    if (lane == 0) {
+                        const int64_t at = (slot0 + chunk_of(step)) * p.heads + head;
+                        char *to = reinterpret_cast<char *>(kept + at * KD * values);
+                        const uint32_t tile = uint32_t(values) * kTileRow;
+#pragma unroll
+                        for (int i = 0; i < 2 * KD / 64; ++i)
+                            bulk_store(to + int64_t(i) * tile, sm + Space::keep + i * kMostValues * kTileRow, tile);
+                        bulk_commit();
+                        bulk_wait_read<0>();
+                        mbar_arrive(&kept_read);
+                    }
+                    __syncwarp();
+                    wait(ready[2], uint32_t(step));
+                    if (lane == 0) {
+                        const int64_t at = (slot0 + chunk_of(step)) * p.heads + head;
+                        bulk_store(kept_rows + at * kChunk * values, sm + Space::keep, uint32_t(kChunk * values) * 4u);
+                        bulk_commit();
+                        bulk_wait_read<0>();
+                        mbar_arrive(&kept_read);
+                    }
+                    __syncwarp();
                 }
+                put_decays(step + kStages);
             }
-            mma_commit(&bars[1]);
+            if (stores) store(step);
         }
-        // the last products that read the other stage have ended
-        if (!kBack && step > 0) wait(4, step - 1);
-        if (Stage::kStages == 2 && step + 1 < chunks) load(step + 1, st ^ 1);
-        const float *beta = beta_[vs], *first = first_[vs], *rest = rest_[vs];
-        const float whole = first[kChunk - 1];
-        float x[32], y[32];
-        if constexpr (!kBack) {
-            if (step > 0) put_out(step - 1);
-            wait(0, step);
-            read(x, kD0 + t0);
-            const T *v = reinterpret_cast<const T *>(s + Stage::v) + t0 * kMostValues + dv;
+        if (kept || stores) bulk_wait_all<0>();
+    } else {
+        const int half = warp / 4, dv = warp % 4 * 32 + lane, t0 = half * 32, k0 = half * kH;
+        const uint32_t mine = tm + (uint32_t(warp % 4) << 21);
+        float S[kH];
+        {
+            const float *from = kBack ? bp.grad_final : p.initial;
+            const int64_t at = (seq * p.heads + head) * keys * values + dv;
 #pragma unroll
-            for (int j = 0; j < 32; ++j) x[j] = beta[t0 + j] * fmaf(-first[t0 + j], x[j], to_f32<T>(v[j * kMostValues]));
-            put_rows(kR, x);
-            wait(1, step);
-            read(o1, kDS + t0);
-#pragma unroll
-            for (int j = 0; j < 32; ++j) o1[j] *= p.scale * first[t0 + j];
-        } else {
-            // the queries' side: scale e^G dO
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
-                const uint32_t e = tile_at(t0 + j, dv, kChunk);
-                float f = __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(s + Stage::v + e));
-                if constexpr (kP == 2)
-                    f += __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(s + Stage::v + Stage::kValues + e));
-                x[j] = p.scale * first[t0 + j] * f;
-            }
-            put_rows(kU, x);
-            wait(0, step);
-            read(x, kD0 + t0);
-            wait(1, step);
-            read(y, kD1 + t0);
-#pragma unroll
-            for (int j = 0; j < 32; ++j) x[j] = fmaf(rest[t0 + j], x[j], p.scale * y[j]);
-            put_rows(kR, x);
+            for (int k = 0; k < kH; ++k)
+                S[k] = from && dv < values && k0 + k < keys ? from[at + int64_t(k0 + k) * values] : 0.0f;
         }
-        meet();
-        if (warp == 0 && elect_one()) {
-            const Operand<kChunk, kBack> inv(s + Stage::inverse), invl(s + Stage::inverse + Stage::kTileBytes);
-            product_ts<kChunk, kChunk>(tm + kD0, tm + kR, inv, false);
-            product_ts<kChunk, kChunk>(tm + kD0, tm + kR + 32, inv, true);
-            product_ts<kChunk, kChunk>(tm + kD0, tm + kR, invl, true);
-            mma_commit(&bars[2]);
-        }
-        wait(2, step);
-        read(x, kD0 + t0);
-        if (float *keep = kBack ? bp.dr : p.u; keep && dv < values) {
-            keep += at * kChunk * values + int64_t(t0) * values + dv;
+        // what was stored is there for the products, and for bulk copies
+        auto arrive = [&](int which) {
+            tmem_stored();
+            if (kept) fence_proxy_async_smem();
+            tmem_fence_before();
+            mbar_arrive(&ready[which]);
+        };
+        auto wait_done = [&](int which, int64_t step) {
+            wait(done[which], uint32_t(step));
+            tmem_fence_after();
+        };
+        auto read = [&](float (&x)[32], uint32_t at) {
+            uint32_t v[32];
+            tmem_load<32>(v, mine + at);
+            tmem_ready();
 #pragma unroll
-            for (int j = 0; j < 32; ++j) keep[j * values] = x[j];
-        }
-        if constexpr (!kBack) {
+            for (int j = 0; j < 32; ++j) x[j] = __uint_as_float(v[j]);
+        };
+        // 32 numbers of this thread's rows of the chunk, in two pieces, as an operand
+        auto put_rows = [&](uint32_t at, const float (&x)[32]) {
             uint32_t hi[16], lo[16];
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                if constexpr (kP == 2) split2(x[2 * j], x[2 * j + 1], hi[j], lo[j]);
-                else hi[j] = round2(x[2 * j], x[2 * j + 1]);
-            }
-            tmem_store<16>(mine + kU + half * 16, hi);
-            if constexpr (kP == 2) tmem_store<16>(mine + kU + 32 + half * 16, lo);
-        }
+            for (int j = 0; j < 16; ++j) split2(x[2 * j], x[2 * j + 1], hi[j], lo[j]);
+            tmem_store<16>(mine + at + half * 16, hi);
+            tmem_store<16>(mine + at + 32 + half * 16, lo);
+        };
+        // what was kept last has been read
+        uint32_t kept_times = 0;
+        auto wait_kept = [&] {
+            if (kept && kept_times) wait(kept_read, kept_times - 1u);
+            ++kept_times;
+        };
+        // the state as the next products' operand, and as kept
+        auto put_state = [&] {
+            wait_kept();
 #pragma unroll
-        for (int j = 0; j < 32; ++j) x[j] *= kBack ? -beta[t0 + j] * first[t0 + j] : rest[t0 + j];
-        put_rows(kR, x);
-        meet();
-        if (warp == 0 && elect_one()) {
-            product_ts<KD, kChunk>(tm + kDS, tm + kR, Ko, false);
-            product_ts<KD, kChunk>(tm + kDS, tm + kR + 32, Ko, true);
-            if constexpr (kP == 2) product_ts<KD, kChunk>(tm + kDS, tm + kR, Klo, true);
-            if constexpr (kBack) {
-                const Operand<kChunk, true> Q(s + Stage::q), Ql(s + Stage::q + Stage::kKeys);
-                product_ts<KD, kChunk>(tm + kDS, tm + kU, Q, true);
-                product_ts<KD, kChunk>(tm + kDS, tm + kU + 32, Q, true);
-                if constexpr (kP == 2) product_ts<KD, kChunk>(tm + kDS, tm + kU, Ql, true);
+            for (int k = 0; k < kH; k += 16) {
+                uint32_t hi[8], lo[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) split2(S[k + 2 * j], S[k + 2 * j + 1], hi[j], lo[j]);
+                tmem_store<8>(mine + kS + (k0 + k) / 2, hi);
+                tmem_store<8>(mine + kS + KD / 2 + (k0 + k) / 2, lo);
+                if (kept)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const int key = k0 + k + j * 8;
+                        char *to = sm + Space::keep + uint32_t(key / 64) * kMostValues * kTileRow +
+                                   tile_piece(uint32_t(dv), uint32_t(key % 64 / 8));
+                        *reinterpret_cast<uint4 *>(to) = make_uint4(hi[4 * j], hi[4 * j + 1], hi[4 * j + 2], hi[4 * j + 3]);
+                        *reinterpret_cast<uint4 *>(to + Space::kKeep / 2) =
+                            make_uint4(lo[4 * j], lo[4 * j + 1], lo[4 * j + 2], lo[4 * j + 3]);
+                    }
             }
-            mma_commit(&bars[3]);
+            arrive(0);
+        };
+        float o1[32];  // forward: what the state gives to the outputs
+        // forward: the outputs of a chunk, to shared memory
+        auto put_out = [&](int64_t step) {
+            wait_done(4, step);
+            float o2[32];
+            read(o2, kD1 + t0);
+            if (step > 0) wait(out_empty, uint32_t(step - 1));
+            T *to = reinterpret_cast<T *>(sm + Space::out) + t0 * kMostValues + dv;
+            const float bad = ok ? 0.0f : __int_as_float(0x7fffffff);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) to[j * kMostValues] = from_f32<T>(fmaf(p.scale, o2[j], o1[j]) + bad);
+            fence_proxy_async_smem();
+            mbar_arrive(&out_full);
+        };
+        if (chunks > 0) put_state();
+        for (int64_t step = 0; step < chunks; ++step) {
+            const int st = stage_of(step);
+            char *s = sm + st * Space::bytes;
+            // before the next chunk's inputs: its loaders may be waiting for the outputs' place
+            if constexpr (!kBack)
+                if (step > 0) put_out(step - 1);
+            wait(full[st], round_of(step));
+            const ChainRows &r = rows_of[st];
+            const float whole = r.first[kChunk - 1];
+            const float4 *const first4 = reinterpret_cast<const float4 *>(r.first + t0);
+            const float4 *const beta4 = reinterpret_cast<const float4 *>(r.beta + t0);
+            const float4 *const rest4 = reinterpret_cast<const float4 *>(r.rest + t0);
+            float x[32];
             if constexpr (!kBack) {
-                const Operand<kChunk, false> A(s + Stage::weights), Al(s + Stage::weights + Stage::kTileBytes);
-                product_ts<kChunk, kChunk>(tm + kD1, tm + kU, A, false);
-                if constexpr (kP == 2) {
-                    product_ts<kChunk, kChunk>(tm + kD1, tm + kU + 32, A, true);
-                    product_ts<kChunk, kChunk>(tm + kD1, tm + kU, Al, true);
+                float y[32];
+                const T *v = reinterpret_cast<const T *>(s + Space::v) + t0 * kMostValues + dv;
+#pragma unroll
+                for (int j = 0; j < 32; ++j) y[j] = to_f32<T>(v[j * kMostValues]);
+                wait_done(0, step);
+                read(x, kD0 + t0);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float4 f = first4[j], b = beta4[j];
+                    x[4 * j] = b.x * fmaf(-f.x, x[4 * j], y[4 * j]);
+                    x[4 * j + 1] = b.y * fmaf(-f.y, x[4 * j + 1], y[4 * j + 1]);
+                    x[4 * j + 2] = b.z * fmaf(-f.z, x[4 * j + 2], y[4 * j + 2]);
+                    x[4 * j + 3] = b.w * fmaf(-f.w, x[4 * j + 3], y[4 * j + 3]);
                 }
-                mma_commit(&bars[4]);
+                put_rows(kR, x);
+            } else {
+                // the queries' side: scale e^G dO
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                    const uint32_t e = tile_at(t0 + j, dv, kChunk);
+                    float f = __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(s + Space::v + e));
+                    if constexpr (kP == 2)
+                        f += __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(s + Space::v + Space::kValues + e));
+                    x[j] = p.scale * r.first[t0 + j] * f;
+                }
+                put_rows(kU, x);
+                wait_done(0, step);
+                read(x, kD0 + t0);
+                wait_done(1, step);
+                float y[32];
+                read(y, kD1 + t0);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float4 f = rest4[j];
+                    x[4 * j] = fmaf(f.x, x[4 * j], p.scale * y[4 * j]);
+                    x[4 * j + 1] = fmaf(f.y, x[4 * j + 1], p.scale * y[4 * j + 1]);
+                    x[4 * j + 2] = fmaf(f.z, x[4 * j + 2], p.scale * y[4 * j + 2]);
+                    x[4 * j + 3] = fmaf(f.w, x[4 * j + 3], p.scale * y[4 * j + 3]);
+                }
+                put_rows(kR, x);
             }
-        }
-        wait(3, step);
+            arrive(1);
+            if constexpr (!kBack) {
+                wait_done(1, step);
+                read(o1, kDS + t0);
 #pragma unroll
-        for (int k = 0; k < kH; k += 32) {
-            read(x, kDS + k0 + k);
-#pragma unroll
-            for (int j = 0; j < 32; ++j) S[k + j] = fmaf(whole, S[k + j], x[j]);
-        }
-        if (step + 1 < chunks) {
-            if (Stage::kStages == 1) {
-                // the last products and reads of this stage end first
-                if constexpr (!kBack) wait(4, step);
-                __syncthreads();
-                load(step + 1, 0);
+                for (int j = 0; j < 8; ++j) {
+                    const float4 f = first4[j];
+                    o1[4 * j] *= p.scale * f.x, o1[4 * j + 1] *= p.scale * f.y;
+                    o1[4 * j + 2] *= p.scale * f.z, o1[4 * j + 3] *= p.scale * f.w;
+                }
             }
-            put_state(step + 1);
-            finish_load(vs ^ 1);
-        }
-    }
-    if constexpr (!kBack)
-        if (chunks > 0) {
-            wait(4, chunks - 1);
-            put_out(chunks - 1);
-        }
-    if (float *to = kBack ? bp.grad_initial : p.final; to && dv < values) {
-        to += (seq * p.heads + head) * keys * values + dv;
+            wait_kept();
+            wait_done(2, step);
+            read(x, kD0 + t0);
+            if (kept && dv < values) {
+                float *to = reinterpret_cast<float *>(sm + Space::keep) + t0 * values + dv;
 #pragma unroll
-        for (int k = 0; k < kH; ++k)
-            if (k0 + k < keys) to[int64_t(k0 + k) * values] = ok ? S[k] : __int_as_float(0x7fffffff);
+                for (int j = 0; j < 32; ++j) to[j * values] = x[j];
+            }
+            if constexpr (!kBack) {
+                uint32_t hi[16], lo[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    if constexpr (kP == 2) split2(x[2 * j], x[2 * j + 1], hi[j], lo[j]);
+                    else hi[j] = round2(x[2 * j], x[2 * j + 1]);
+                }
+                tmem_store<16>(mine + kU + half * 16, hi);
+                if constexpr (kP == 2) tmem_store<16>(mine + kU + 32 + half * 16, lo);
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                float4 f = kBack ? beta4[j] : rest4[j];
+                if constexpr (kBack) {
+                    const float4 e = first4[j];
+                    f = make_float4(-f.x * e.x, -f.y * e.y, -f.z * e.z, -f.w * e.w);
+                }
+                x[4 * j] *= f.x, x[4 * j + 1] *= f.y, x[4 * j + 2] *= f.z, x[4 * j + 3] *= f.w;
+            }
+            put_rows(kR, x);
+            arrive(2);
+            wait_done(3, step);
+#pragma unroll
+            for (int k = 0; k < kH; k += 32) {
+                read(x, kDS + k0 + k);
+#pragma unroll
+                for (int j = 0; j < 32; ++j) S[k + j] = fmaf(whole, S[k + j], x[j]);
+            }
+            if (step + 1 < chunks) put_state();
+        }
+        if constexpr (!kBack)
+            if (chunks > 0) put_out(chunks - 1);
+        if (float *to = kBack ? bp.grad_initial : p.final; to && dv < values) {
+            to += (seq * p.heads + head) * keys * values + dv;
+            const float bad = ok ? 0.0f : __int_as_float(0x7fffffff);
+#pragma unroll
+            for (int k = 0; k < kH; ++k)
+                if (k0 + k < keys) to[int64_t(k0 + k) * values] = S[k] + bad;
+        }
     }
     tmem_fence_before();
     __syncthreads();
     if (warp == 0) tmem_free(tm, 512);
 }
 
-template <class T, int KD, bool kBack, bool kWide>
-cudaError_t chain_k(const DeltaBackwardParams &p, cudaStream_t s) {
-    const auto kernel = delta_chain_kernel<T, KD, kBack, kWide>;
-    constexpr size_t bytes = ChainStage<T, KD, kBack>::kAll;
-    if (device_blocks(reinterpret_cast<const void *>(kernel), kChainThreads, bytes) == 0) return cudaErrorInvalidConfiguration;
-    return launch_pdl(kernel, dim3(uint32_t(p.f.sequences), uint32_t(p.f.heads)), dim3(kChainThreads), bytes, s, p);
+template <class T, int KD, bool kBack, bool kMaps>
+cudaError_t chain_k(const DeltaBackwardParams &p, const ChainMaps &maps, cudaStream_t s) {
+    const auto kernel = delta_chain_kernel<T, KD, kBack, kMaps>;
+    constexpr size_t bytes = ChainSpace<T, KD, kBack>::kAll;
+    constexpr int threads = kChainThreads + kHelpThreads;
+    if (device_blocks(reinterpret_cast<const void *>(kernel), threads, bytes) == 0) return cudaErrorInvalidConfiguration;
+    return launch_pdl(kernel, dim3(uint32_t(p.f.sequences), uint32_t(p.f.heads)), dim3(threads), bytes, s, p, maps);
 }
 
 template <class T, bool kBack>
 cudaError_t chain_t(const DeltaBackwardParams &p, cudaStream_t s) {
-    if (p.f.keys <= 64) return p.f.wide ? chain_k<T, 64, kBack, true>(p, s) : chain_k<T, 64, kBack, false>(p, s);
-    return p.f.wide ? chain_k<T, 128, kBack, true>(p, s) : chain_k<T, 128, kBack, false>(p, s);
+    const DeltaParams &f = p.f;
+    ChainMaps maps = {};
+    if constexpr (kPieces<T> == 1) {
+        if (f.wide && f.batch * f.rows > 0 &&
+            delta_map(&maps.k, f.k, f.batch, f.rows, f.key_heads, f.keys, 64, true) &&
+            delta_map(&maps.q, f.q, f.batch, f.rows, f.key_heads, f.keys, 64, true) &&
+            delta_map(&maps.v, kBack ? p.grad_out : f.v, f.batch, f.rows, f.heads, f.values, kBack ? 64 : kMostValues, kBack))
+            return f.keys <= 64 ? chain_k<T, 64, kBack, true>(p, maps, s) : chain_k<T, 128, kBack, true>(p, maps, s);
+    }
+    return f.keys <= 64 ? chain_k<T, 64, kBack, false>(p, maps, s) : chain_k<T, 128, kBack, false>(p, maps, s);
 }
 
 }  // namespace

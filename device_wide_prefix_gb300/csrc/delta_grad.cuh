@@ -82,14 +82,13 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(DeltaBackwa
     extern __shared__ char raw[];
     __shared__ Sum2 sums[kChunk];
     __shared__ float beta[kChunk], first[kChunk], rest[kChunk], value_dot[kChunk];
-    __shared__ uint64_t bars[3];
+    __shared__ uint64_t bars[4];
     __shared__ uint32_t tmem;
     const DeltaParams &p = bp.f;
     char *sm = reinterpret_cast<char *>((reinterpret_cast<uintptr_t>(raw) + 1023) / 1024 * 1024);
     // sums over the keys, in U's place when its products have ended
     struct Dots {
         float key[4][kChunk], all[4][kChunk], whole[kGradThreads / 32];
-        Sum2 rev[kChunk];
     };
     Dots &dots = *reinterpret_cast<Dots *>(sm + Space::u);
     pdl_trigger();
@@ -98,14 +97,18 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(DeltaBackwa
     if (c.rows == 0) return;
     const int tid = threadIdx.x, lane = tid % 32, warp = __shfl_sync(0xffffffffu, tid / 32, 0);
     const int half = warp / 4, dk = warp % 4 * 32 + lane, t0 = half * 32, n = c.rows;
-    const int kh = blockIdx.y, per = p.heads / p.key_heads, keys = p.keys, values = p.values, kp = (keys + 7) / 8 * 8;
+    const int kh = blockIdx.y, per = p.heads / p.key_heads, keys = p.keys, values = p.values, tiles = (keys + 63) / 64;
     if (tid == 0) {
-        for (int i = 0; i < 3; ++i) mbar_init(&bars[i], 1);
+        for (int i = 0; i < 4; ++i) mbar_init(&bars[i], 1);
         fence_mbar_init();
     }
     if (warp == 0) tmem_alloc(&tmem, 512);
-    load_tile<T, kWide, kChunk, kMost, kGradThreads>(sm + Space::k, kRows, 0, p.k, c.batch, c.row, kh, n, keys);
-    load_tile<T, kWide, kChunk, kMost, kGradThreads>(sm + Space::q, kRows, 0, p.q, c.batch, c.row, kh, n, keys);
+    load_tile<T, kWide, kChunk, kMost, kGradThreads>(tid, sm + Space::k, kRows, 0, p.k, c.batch, c.row, kh, n, keys);
+    load_tile<T, kWide, kChunk, kMost, kGradThreads>(tid, sm + Space::q, kRows, 0, p.q, c.batch, c.row, kh, n, keys);
+    // of the states' tiles what no state fills
+    for (int e = tid; e < 2 * kMost * kMost / 8; e += kGradThreads)
+        if (e / 8 % kMost >= values || e / (kMost * 8) % 2 >= tiles)
+            *reinterpret_cast<uint4 *>(sm + Space::state + uint32_t(e) * 16) = make_uint4(0, 0, 0, 0);
     __syncthreads();
     const uint32_t tm = tmem, mine = tm + (uint32_t(warp % 4) << 21);
     constexpr uint32_t kDX = 0, kDA = 128, kDW = 192, kDY = 320, kDU = 384;
@@ -140,17 +143,17 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(DeltaBackwa
             if (ok) ok = mma_wait(&bars[bar], parity);
             tmem_fence_after();
         };
-        // state before the chunk, [values][keys] in two planes
-        const char *S0 = reinterpret_cast<const char *>(p.states + at * kp * values);
-        const char *S1 = reinterpret_cast<const char *>(bp.ends + at * kp * values);
-        for (int e = tid; e < 2 * kMost * kMost / 8; e += kGradThreads) {
-            const int plane = e / (kMost * kMost / 8), r = e / (kMost / 8) % kMost, j = e % (kMost / 8);
-            const bool in = r < values && j * 8 < kp;
-            copy16(smem_addr(sm + Space::state + plane * kState + uint32_t(j / 8) * kMost * kTileRow +
-                             tile_piece(uint32_t(r), uint32_t(j % 8))),
-                   in ? S0 + (int64_t(plane * values + r) * kp + j * 8) * 2 : S0, in ? 16u : 0u);
+        // the state before the chunk, as it was kept
+        const char *S0 = reinterpret_cast<const char *>(p.states + at * tiles * 64 * values);
+        const char *S1 = reinterpret_cast<const char *>(bp.ends + at * tiles * 64 * values);
+        if (tid == 0) {
+            const uint32_t each = uint32_t(values) * kTileRow;
+            mbar_arrive_expect_tx(&bars[3], 2 * tiles * each);
+            for (int i = 0; i < 2 * tiles; ++i)
+                bulk_load(sm + Space::state + i / tiles * kState + i % tiles * kMost * kTileRow, S0 + int64_t(i) * each, each,
+                          &bars[3]);
         }
-        load_tile<T, kWide, 2 * kChunk, kMost, kGradThreads>(sm + Space::stack, 2 * kRows, 0, bp.grad_out, c.batch, c.row,
+        load_tile<T, kWide, 2 * kChunk, kMost, kGradThreads>(tid, sm + Space::stack, 2 * kRows, 0, bp.grad_out, c.batch, c.row,
                                                              head, n, values);
         if constexpr (kP == 1)  // its second piece
             for (int e = tid; e < kChunk * kMost / 8; e += kGradThreads) {
@@ -159,14 +162,22 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(DeltaBackwa
                                            tile_piece(i, j % 8)) = make_uint4(0, 0, 0, 0);
             }
         if (warp == 7) {
-            delta_sums(sums, [&](int i) { return i < n ? delta_g(p.g, c.batch, c.row + i, head) : 0.0f; });
-            __syncwarp();
+            float g[2];
+            Sum2 s[2];
 #pragma unroll
-            for (int i = lane; i < kChunk; i += 32) {
-                beta[i] = i < n ? delta_beta<T>(p, c.batch, c.row + i, head) : 0.0f;
-                const float e = __expf(sums[i].hi);
-                first[i] = fmaf(e, sums[i].lo, e);
-                rest[i] = __expf(sum2_less(sums[kChunk - 1], sums[i]));
+            for (int i = 0; i < 2; ++i) {
+                const int r = lane + 32 * i;
+                g[i] = r < n ? delta_g(p.g, c.batch, c.row + r, head) : 0.0f;
+                beta[r] = r < n ? delta_beta<T>(p, c.batch, c.row + r, head) : 0.0f;
+            }
+            delta_sums(s, g);
+            const Sum2 last = {__shfl_sync(0xffffffffu, s[1].hi, 31), __shfl_sync(0xffffffffu, s[1].lo, 31)};
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float e = __expf(s[i].hi);
+                sums[lane + 32 * i] = s[i];
+                first[lane + 32 * i] = fmaf(e, s[i].lo, e);
+                rest[lane + 32 * i] = __expf(sum2_less(last, s[i]));
             }
         }
         __syncthreads();
@@ -196,6 +207,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(DeltaBackwa
                       });
         load_f32_rows(sm + Space::u, sm + Space::u + kRows, kChunk, 0, p.u + at * kChunk * values, values, wide_values,
                       [](int, int, int, const float (&)[8]) {});
+        if (ok) ok = mma_wait(&bars[3], parity);
         meet();
         const Operand<kChunk, false> U(sm + Space::u), Ul(sm + Space::u + kRows);
         const Operand<kMost, true> S(sm + Space::state), Sl(sm + Space::state + kState);
@@ -250,15 +262,10 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(DeltaBackwa
         // the gradient of the state after the chunk takes the state's place, and meets it on the way
         float meeting = 0.0f;
 #pragma unroll 4
-        for (int e = tid; e < kMost * kMost / 8; e += kGradThreads) {
-            const int r = e / (kMost / 8), j = e % (kMost / 8);
-            uint4 hi = make_uint4(0, 0, 0, 0), lo = hi;
-            if (r < values && j * 8 < kp) {
-                hi = *reinterpret_cast<const uint4 *>(S1 + (int64_t(r) * kp + j * 8) * 2);
-                lo = *reinterpret_cast<const uint4 *>(S1 + (int64_t(values + r) * kp + j * 8) * 2);
-            }
-            uint4 *at_hi = reinterpret_cast<uint4 *>(sm + Space::state + uint32_t(j / 8) * kMost * kTileRow +
-                                                     tile_piece(uint32_t(r), uint32_t(j % 8)));
+        for (int e = tid; e < tiles * values * 8; e += kGradThreads) {
+            const uint4 hi = *reinterpret_cast<const uint4 *>(S1 + e * 16);
+            const uint4 lo = *reinterpret_cast<const uint4 *>(S1 + (tiles * values * 8 + e) * 16);
+            uint4 *at_hi = reinterpret_cast<uint4 *>(sm + Space::state + (e >= values * 8 ? kMost * 8 + e - values * 8 : e) * 16);
             uint4 *at_lo = reinterpret_cast<uint4 *>(reinterpret_cast<char *>(at_hi) + kState);
             const uint4 shi = *at_hi, slo = *at_lo;
             auto with = [&](uint32_t a, uint32_t b, uint32_t x, uint32_t y) {
@@ -335,14 +342,20 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(DeltaBackwa
             float whole = 0.0f;
             for (int w = 0; w < kGradThreads / 32; ++w) whole += dots.whole[w];
             const float bad = ok ? 0.0f : __int_as_float(0x7fffffff);
-            delta_sums(dots.rev, [&](int r) {
-                const int i = kChunk - 1 - r;
-                if (i >= n) return 0.0f;
-                return (dots.all[0][i] + dots.all[1][i]) + (dots.all[2][i] + dots.all[3][i]) + (i == n - 1 ? whole : 0.0f) + bad;
-            });
-            __syncwarp();
-            for (int i = lane; i < n; i += 32) {
-                if (bp.grad_g.data) *delta_at<float>(bp.grad_g, c.batch, c.row + i, head) = dots.rev[kChunk - 1 - i].hi;
+            float g[2];
+            Sum2 sum[2];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const int i = kChunk - 1 - (lane + 32 * r);
+                g[r] = i >= n ? 0.0f : (dots.all[0][i] + dots.all[1][i]) + (dots.all[2][i] + dots.all[3][i]) +
+                                           (i == n - 1 ? whole : 0.0f) + bad;
+            }
+            delta_sums(sum, g);
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const int i = kChunk - 1 - (lane + 32 * r);
+                if (i >= n) continue;
+                if (bp.grad_g.data) *delta_at<float>(bp.grad_g, c.batch, c.row + i, head) = sum[r].hi;
                 const float d = value_dot[i] + ((dots.key[0][i] + dots.key[1][i]) + (dots.key[2][i] + dots.key[3][i])) + bad;
                 if (p.beta_f32) *delta_at<float>(bp.grad_beta, c.batch, c.row + i, head) = d;
                 else *delta_at<T>(bp.grad_beta, c.batch, c.row + i, head) = from_f32<T>(d);

@@ -3,6 +3,8 @@
 
 #include <cuda_runtime.h>
 
+#include <cuda.h>
+
 #include "common.h"
 
 namespace dwp {
@@ -234,6 +236,11 @@ struct DeltaRows {
     char *data;
     int64_t batch, row, head;  // strides in elements
 };
+// A map of bf16 rows [batch][rows][heads][size] for boxes of 64 rows of one
+// head, `columns` wide, exchanged as tiles are (tensor.cuh) if `tiles`.  False
+// where the tensor's strides are past what a map holds.
+bool delta_map(CUtensorMap *map, const DeltaRows &r, int64_t batch, int64_t rows, int64_t heads, int64_t size, int columns,
+               bool tiles);
 struct DeltaParams {
     int keys, values, key_heads, heads;
     int64_t batch, rows, sequences, chunks, slots;  // chunks: of a batch entry; slots: chunk places in all
@@ -243,11 +250,11 @@ struct DeltaParams {
     const uint32_t *offsets;
     const float *initial;
     float *final;
-    bool wide;  // rows of q, k, v and grad_out are whole 16-byte pieces
-    // [slots][heads]: inverse and weights, each [64][64] in two planes of bf16
-    // (tensor.cuh, split2); and, without a gradient NULL, corrections u f32
-    // [64][values], and the state before the chunk, two planes of bf16
-    // [values][keys up to a multiple of 8]
+    bool wide, out_wide;  // rows of q, k, v and grad_out, of out, are whole 16-byte pieces
+    // [slots][heads]: inverse and weights, each two tiles of 64 x 64 (tensor.cuh,
+    // split2); and, without a gradient NULL, corrections u f32 [64][values], and
+    // the state before the chunk: two pieces of [keys / 64, rounded up] tiles of
+    // `values` rows
     float *inverse, *weights, *u, *states;
 };
 struct DeltaBackwardParams {

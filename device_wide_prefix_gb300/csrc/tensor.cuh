@@ -87,6 +87,13 @@ __device__ __forceinline__ bool elect_one() {
     return p != 0;
 }
 
+// A warpgroup's registers a thread, from the block's own share: all shares
+// together are at most the threads' at launch.
+template <int N>
+__device__ __forceinline__ void set_registers_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void set_registers_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
 // Wait for the phase of the given parity, without sleeping between polls (a
 // product takes less than a sleep); false after a second or so.
 constexpr uint32_t kProductWaitLimit = 1u << 22;
@@ -94,6 +101,16 @@ __device__ __forceinline__ bool mma_wait(uint64_t *bar, uint32_t parity) {
     for (uint32_t i = 0; i < kProductWaitLimit; ++i)
         if (mbar_try_wait(bar, parity)) return true;
     return false;
+}
+
+// A box of a tensor to shared memory, completing its bytes on `bar`; from
+// column `x`, whose byte offset is a multiple of 16, of head, row and batch.
+__device__ __forceinline__ void map_load(void *to, const void *map, uint64_t *bar, int x, int head, int row, int batch) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(
+            smem_addr(to)),
+        "l"(map), "r"(smem_addr(bar)), "r"(x), "r"(head), "r"(row), "r"(batch)
+        : "memory");
 }
 
 // The products issued so far by this thread arrive on `bar` when done.

@@ -495,7 +495,7 @@ dwp_status dwp_selective_scan_step(const dwp_selective_scan_step_args *args, dwp
  *   checkpoints    NULL, or what the gradient needs, to be handed on as it is:
  *                  f32 [chunks, heads, DWP_DELTA_CHUNK * (2 * DWP_DELTA_CHUNK
  *                  + values) + keys' * values], 16-byte aligned, keys' being
- *                  keys rounded up to a multiple of 8; chunks is batch *
+ *                  keys rounded up to a multiple of 64; chunks is batch *
  *                  ceil(rows / DWP_DELTA_CHUNK), or with offsets rows /
  *                  DWP_DELTA_CHUNK + num_segments
  *   scratch        without checkpoints 8 * DWP_DELTA_CHUNK^2 bytes for each
