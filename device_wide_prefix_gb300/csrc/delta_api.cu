@@ -32,8 +32,9 @@ int64_t delta_slots(const dwp_delta_args &a) {
     return a.offsets ? a.rows / DWP_DELTA_CHUNK + a.num_segments : a.batch * delta_chunks(a);
 }
 
-// Words of a kept state: keys in whole tiles.
-int64_t delta_state(const dwp_delta_args &a) { return (a.keys + 63) / 64 * 64 * a.values; }
+// Words of a kept state, keys in whole tiles, and of a chunk's kept rows, values in whole tiles.
+int64_t delta_state(const dwp_delta_args &a) { return ceil_div(a.keys, 64) * 64 * a.values; }
+int64_t delta_kept_rows(const dwp_delta_args &a) { return DWP_DELTA_CHUNK * ceil_div(a.values, 64) * 64; }
 // Whether rows with these address and stride bits are whole 16-byte pieces.
 bool delta_wide(uintptr_t bits, const dwp_delta_args &a) {
     return ((bits | uintptr_t((a.keys | a.values) * size_of(a.dtype))) & 15u) == 0;
@@ -59,7 +60,7 @@ int64_t check_delta(Check &c, const dwp_delta_args &a, bool backward, uintptr_t 
     c.dense(a.initial_state, DWP_F32, seqs * state, false, true);
     if (!backward) c.dense(a.final_state, DWP_F32, seqs * state, true, true);
     if (c.status != DWP_SUCCESS) return seqs;
-    const int64_t each = DWP_DELTA_CHUNK * a.values + delta_state(a) + 2 * kTile;
+    const int64_t each = delta_kept_rows(a) + delta_state(a) + 2 * kTile;
     c.dense(a.checkpoints, DWP_F32, delta_slots(a) * a.heads * each, !backward, !backward);
     if (!aligned(a.checkpoints, 16)) c.fail(DWP_ERR_MISALIGNED);
     return seqs;
@@ -78,7 +79,7 @@ DeltaParams delta_params(const dwp_delta_args &a, int64_t seqs, void *scratch) {
     p.weights = p.inverse + places * kTile;
     if (a.checkpoints) {
         p.u = p.weights + places * kTile;
-        p.states = p.u + places * DWP_DELTA_CHUNK * a.values;
+        p.states = p.u + places * delta_kept_rows(a);
     }
     return p;
 }
@@ -126,7 +127,7 @@ dwp_status delta_backward(const dwp_delta_backward_args &a, void *scratch, size_
     c.dense(a.grad_final_state, DWP_F32, seqs * state, false, true);
     c.dense(a.grad_initial_state, DWP_F32, seqs * state, true, true);
     const int64_t places = delta_slots(f) * f.heads;
-    const size_t dr = size_t(places * DWP_DELTA_CHUNK * f.values) * 4u;
+    const size_t dr = size_t(places * delta_kept_rows(f)) * 4u;
     const size_t ends = round16(size_t(places * delta_state(f)) * 4u);
     if (!c.scratch(scratch, bytes, dr + ends, &st)) return st;
     if (seqs == 0) return DWP_SUCCESS;

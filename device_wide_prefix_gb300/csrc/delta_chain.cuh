@@ -49,7 +49,7 @@ struct ChainSpace {
     static constexpr int kStages = kP == 1 ? 2 : 1;
     static constexpr uint32_t out = kStages * bytes, kOut = kBack ? 0 : kChunk * kMostValues * uint32_t(sizeof(T));
     static constexpr uint32_t keep = out + kOut, kKeep = 2 * kMostValues * KD * 2;
-    static_assert(kKeep >= kChunk * kMostValues * 4, "rows of f32 fit the kept state's place");
+    static_assert(kKeep >= 2 * kValues, "the corrections fit the kept state's place");
     static constexpr size_t kAll = 1024 + keep + kKeep;
 };
 
@@ -329,7 +329,11 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
                     wait(ready[2], uint32_t(step));
                     if (lane == 0) {
                         const int64_t at = (slot0 + chunk_of(step)) * p.heads + head;
-                        bulk_store(kept_rows + at * kChunk * values, sm + Space::keep, uint32_t(kChunk * values) * 4u);
+                        const int tiles = (values + 63) / 64;
+                        char *to = reinterpret_cast<char *>(kept_rows + at * kChunk * 64 * tiles);
+                        for (int i = 0; i < 2; ++i)
+                            bulk_store(to + i * tiles * Space::kTileBytes, sm + Space::keep + i * Space::kValues,
+                                       uint32_t(tiles) * Space::kTileBytes);
                         bulk_commit();
                         bulk_wait_read<0>();
                         mbar_arrive(&kept_read);
@@ -491,10 +495,17 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
             wait_kept();
             wait_done(2, step);
             read(x, kD0 + t0);
-            if (kept && dv < values) {
-                float *to = reinterpret_cast<float *>(sm + Space::keep) + t0 * values + dv;
+            if (kept) {
 #pragma unroll
-                for (int j = 0; j < 32; ++j) to[j * values] = x[j];
+                for (int j = 0; j < 16; ++j) {
+                    uint32_t hi, lo;
+                    split2(x[2 * j], x[2 * j + 1], hi, lo);
+                    char *a = sm + Space::keep + tile_at(uint32_t(t0 + 2 * j), uint32_t(dv), kChunk);
+                    char *b = sm + Space::keep + tile_at(uint32_t(t0 + 2 * j + 1), uint32_t(dv), kChunk);
+                    *reinterpret_cast<uint16_t *>(a) = uint16_t(hi), *reinterpret_cast<uint16_t *>(b) = uint16_t(hi >> 16);
+                    *reinterpret_cast<uint16_t *>(a + Space::kValues) = uint16_t(lo);
+                    *reinterpret_cast<uint16_t *>(b + Space::kValues) = uint16_t(lo >> 16);
+                }
             }
             if constexpr (!kBack) {
                 uint32_t hi[16], lo[16];

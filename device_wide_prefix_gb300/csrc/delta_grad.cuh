@@ -25,8 +25,9 @@ namespace dwp {
 
 namespace {
 
-constexpr int kGradThreads = 256;
+constexpr int kGradThreads = 512;
 constexpr int kMost = 128;  // keys and values, zeros past their own count
+constexpr int kCols = 16;   // of the chunk's rows, a thread's share
 
 template <class T>
 struct GradSpace {
@@ -54,35 +55,26 @@ __device__ __forceinline__ float sums_of_32(float (&x)[32], int lane) {
     return x[0];
 }
 
-// 64 rows of f32, `dim` columns, to a tile in two pieces from row `first` on.
-template <class F>
-__device__ __forceinline__ void load_f32_rows(char *hi, char *lo, uint32_t tile_rows, int first, const float *src, int dim,
-                                              bool wide, F each) {
-    for (int e = threadIdx.x; e < kChunk * kMost / 8; e += kGradThreads) {
-        const int i = e / (kMost / 8), c = e % (kMost / 8), left = dim - c * 8;
-        const uint32_t at = uint32_t(c / 8) * tile_rows * kTileRow + tile_piece(uint32_t(first + i), uint32_t(c % 8));
-        float f[8];
-        if (wide) load_eight<float, true>(f, src + int64_t(i) * dim + c * 8, left);
-        else load_eight<float, false>(f, src + int64_t(i) * dim + c * 8, left);
-        store_pieces(hi, lo, at, f);
-        each(i, c * 8, left, f);
-    }
-}
-
 __device__ __forceinline__ float2 pair_of(uint32_t hi, uint32_t lo) {
     return make_float2(__uint_as_float(hi << 16) + __uint_as_float(lo << 16),
                        __uint_as_float(hi & 0xffff0000u) + __uint_as_float(lo & 0xffff0000u));
 }
 
-template <class T, bool kWide>
-__global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(DeltaBackwardParams bp) {
+struct GradMaps {
+    CUtensorMap k, q, grad_out;
+};
+
+// kMaps: bf16 rows of whole 16-byte pieces, which come by tensor maps.
+template <class T, bool kMaps>
+__global__ void __launch_bounds__(kGradThreads, 1)
+    delta_grad_kernel(DeltaBackwardParams bp, const __grid_constant__ GradMaps maps) {
     using Space = GradSpace<T>;
     constexpr int kP = Space::kP;
-    constexpr uint32_t kRows = Space::kRows, kState = Space::kState;
+    constexpr uint32_t kRows = Space::kRows, kState = Space::kState, kTileBytes = kChunk * kTileRow;
     extern __shared__ char raw[];
     __shared__ Sum2 sums[kChunk];
     __shared__ float beta[kChunk], first[kChunk], rest[kChunk], value_dot[kChunk];
-    __shared__ uint64_t bars[4];
+    __shared__ uint64_t bars[5];
     __shared__ uint32_t tmem;
     const DeltaParams &p = bp.f;
     char *sm = reinterpret_cast<char *>((reinterpret_cast<uintptr_t>(raw) + 1023) / 1024 * 1024);
@@ -96,29 +88,36 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(DeltaBackwa
     const DeltaChunk c = delta_chunk(p, blockIdx.x);
     if (c.rows == 0) return;
     const int tid = threadIdx.x, lane = tid % 32, warp = __shfl_sync(0xffffffffu, tid / 32, 0);
-    const int half = warp / 4, dk = warp % 4 * 32 + lane, t0 = half * 32, n = c.rows;
-    const int kh = blockIdx.y, per = p.heads / p.key_heads, keys = p.keys, values = p.values, tiles = (keys + 63) / 64;
+    const int part = warp / 4, dk = warp % 4 * 32 + lane, t0 = part * kCols, n = c.rows;
+    const int kh = blockIdx.y, per = p.heads / p.key_heads, keys = p.keys, values = p.values;
+    const int tiles = (keys + 63) / 64, value_tiles = (values + 63) / 64;
     if (tid == 0) {
-        for (int i = 0; i < 4; ++i) mbar_init(&bars[i], 1);
+        for (int i = 0; i < 5; ++i) mbar_init(&bars[i], 1);
         fence_mbar_init();
     }
     if (warp == 0) tmem_alloc(&tmem, 512);
-    load_tile<T, kWide, kChunk, kMost, kGradThreads>(tid, sm + Space::k, kRows, 0, p.k, c.batch, c.row, kh, n, keys);
-    load_tile<T, kWide, kChunk, kMost, kGradThreads>(tid, sm + Space::q, kRows, 0, p.q, c.batch, c.row, kh, n, keys);
-    // of the states' tiles what no state fills
+    // what no input fills: of the states' tiles, of the stack's, U's and the
+    // second pieces of bf16 gradients
     for (int e = tid; e < 2 * kMost * kMost / 8; e += kGradThreads)
         if (e / 8 % kMost >= values || e / (kMost * 8) % 2 >= tiles)
             *reinterpret_cast<uint4 *>(sm + Space::state + uint32_t(e) * 16) = make_uint4(0, 0, 0, 0);
+    if (value_tiles == 1)
+        for (int e = tid; e < kChunk * 8; e += kGradThreads)
+#pragma unroll
+            for (int piece = 0; piece < 2; ++piece) {
+                *reinterpret_cast<uint4 *>(sm + Space::u + piece * kRows + kTileBytes + e * 16) = make_uint4(0, 0, 0, 0);
+            }
+    fence_proxy_async_smem();
     __syncthreads();
     const uint32_t tm = tmem, mine = tm + (uint32_t(warp % 4) << 21);
     constexpr uint32_t kDX = 0, kDA = 128, kDW = 192, kDY = 320, kDU = 384;
     bool ok = true;
-    auto read = [&](float (&x)[32], uint32_t at) {
-        uint32_t v[32];
-        tmem_load<32>(v, mine + at);
+    auto read = [&](float (&x)[kCols], uint32_t at) {
+        uint32_t v[kCols];
+        tmem_load<kCols>(v, mine + at);
         tmem_ready();
 #pragma unroll
-        for (int j = 0; j < 32; ++j) x[j] = __uint_as_float(v[j]);
+        for (int j = 0; j < kCols; ++j) x[j] = __uint_as_float(v[j]);
     };
     auto meet = [&] {
         copies_done();
@@ -134,7 +133,14 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(DeltaBackwa
         if constexpr (kP == 2) f += __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(at + kRows));
         return f;
     };
-    float dq[32], dkey[32];
+    // rows of zeros where the chunk is short (a map's box goes on into the next sequence)
+    auto clear = [&](uint32_t tile, uint32_t tile_bytes, int first_row) {
+        for (int e = tid; e < 2 * (kChunk - n) * 8; e += kGradThreads) {
+            const int x = e / ((kChunk - n) * 8), l = e % ((kChunk - n) * 8);
+            *reinterpret_cast<uint4 *>(sm + tile + x * tile_bytes + (first_row + n) * kTileRow + l * 16) = make_uint4(0, 0, 0, 0);
+        }
+    };
+    float dq[kCols], dkey[kCols];
     for (int h = 0; h < per; ++h) {
         const int head = kh * per + h;
         const int64_t at = int64_t(blockIdx.x) * p.heads + head;
@@ -143,25 +149,68 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(DeltaBackwa
             if (ok) ok = mma_wait(&bars[bar], parity);
             tmem_fence_after();
         };
-        // the state before the chunk, as it was kept
         const char *S0 = reinterpret_cast<const char *>(p.states + at * tiles * 64 * values);
         const char *S1 = reinterpret_cast<const char *>(bp.ends + at * tiles * 64 * values);
+        const char *kept_u = reinterpret_cast<const char *>(p.u + at * value_tiles * 64 * kChunk);
+        const char *kept_dr = reinterpret_cast<const char *>(bp.dr + at * value_tiles * 64 * kChunk);
+        // where the last head's [dA; E] were, zeros again
+        if constexpr (kP == 1)
+            for (int e = tid; e < 2 * kChunk * 8; e += kGradThreads)
+                *reinterpret_cast<uint4 *>(sm + Space::stack + 2 * kRows + e / (kChunk * 8) * 2 * kTileBytes +
+                                           e % (kChunk * 8) * 16) = make_uint4(0, 0, 0, 0);
+        if (value_tiles == 1)
+            for (int e = tid; e < kChunk * 8; e += kGradThreads)
+#pragma unroll
+                for (int piece = 0; piece < 2; ++piece)
+                    *reinterpret_cast<uint4 *>(sm + Space::stack + piece * 2 * kRows + 3 * kTileBytes + e * 16) =
+                        make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();
+        __syncthreads();
         if (tid == 0) {
             const uint32_t each = uint32_t(values) * kTileRow;
-            mbar_arrive_expect_tx(&bars[3], 2 * tiles * each);
-            for (int i = 0; i < 2 * tiles; ++i)
-                bulk_load(sm + Space::state + i / tiles * kState + i % tiles * kMost * kTileRow, S0 + int64_t(i) * each, each,
-                          &bars[3]);
-        }
-        load_tile<T, kWide, 2 * kChunk, kMost, kGradThreads>(tid, sm + Space::stack, 2 * kRows, 0, bp.grad_out, c.batch, c.row,
-                                                             head, n, values);
-        if constexpr (kP == 1)  // its second piece
-            for (int e = tid; e < kChunk * kMost / 8; e += kGradThreads) {
-                const uint32_t i = e / (kMost / 8), j = e % (kMost / 8);
-                *reinterpret_cast<uint4 *>(sm + Space::stack + 2 * kRows + j / 8 * 2 * kChunk * kTileRow +
-                                           tile_piece(i, j % 8)) = make_uint4(0, 0, 0, 0);
+            mbar_arrive_expect_tx(&bars[3], 2 * tiles * each + 4 * value_tiles * kTileBytes +
+                                                (kMaps ? 2 * kTileBytes + (h == 0 ? 4 * kTileBytes : 0) : 0));
+            if constexpr (kMaps) {
+                const int r = int(c.row), b = int(c.batch);
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    map_load(sm + Space::stack + x * 2 * kTileBytes, &maps.grad_out, &bars[3], x * 64, head, r, b);
+                    if (h == 0) {
+                        map_load(sm + Space::k + x * kTileBytes, &maps.k, &bars[3], x * 64, kh, r, b);
+                        map_load(sm + Space::q + x * kTileBytes, &maps.q, &bars[3], x * 64, kh, r, b);
+                    }
+                }
             }
-        if (warp == 7) {
+            for (int piece = 0; piece < 2; ++piece) {
+                for (int i = 0; i < value_tiles; ++i)
+                    bulk_load(sm + Space::stack + piece * 2 * kRows + i * 2 * kTileBytes + kTileBytes,
+                              kept_dr + (piece * value_tiles + i) * kTileBytes, kTileBytes, &bars[3]);
+                bulk_load(sm + Space::u + piece * kRows, kept_u + piece * value_tiles * kTileBytes, value_tiles * kTileBytes,
+                          &bars[3]);
+                for (int i = 0; i < tiles; ++i)
+                    bulk_load(sm + Space::state + piece * kState + i * kMost * kTileRow, S0 + int64_t(piece * tiles + i) * each,
+                              each, &bars[3]);
+            }
+        }
+        if constexpr (!kMaps) {
+            if (h == 0) {
+                load_tile<T, false, kChunk, kMost, kGradThreads>(tid, sm + Space::k, kRows, 0, p.k, c.batch, c.row, kh, n, keys, p.wide);
+                load_tile<T, false, kChunk, kMost, kGradThreads>(tid, sm + Space::q, kRows, 0, p.q, c.batch, c.row, kh, n, keys, p.wide);
+            }
+            load_tile<T, false, 2 * kChunk, kMost, kGradThreads>(tid, sm + Space::stack, 2 * kRows, 0, bp.grad_out, c.batch, c.row,
+                                                                 head, n, values, p.wide);
+        }
+        // this thread's values of V: two pieces of eight
+        float v[2][8];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int i = e * (kGradThreads / 16) + tid / 16, j0 = tid % 16 * 8;
+            const int left = i < n ? values - j0 : 0;
+            const T *from = delta_at<T>(p.v, c.batch, c.row + (i < n ? i : 0), head) + (left > 0 ? j0 : 0);
+            if (p.wide) load_eight<T, true>(v[e], from, left);
+            else load_eight<T, false>(v[e], from, left);
+        }
+        if (warp == 15) {
             float g[2];
             Sum2 s[2];
 #pragma unroll
@@ -180,34 +229,11 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(DeltaBackwa
                 rest[lane + 32 * i] = __expf(sum2_less(last, s[i]));
             }
         }
-        __syncthreads();
-        const bool wide_values = values % 4 == 0;
-        load_f32_rows(sm + Space::stack, sm + Space::stack + 2 * kRows, 2 * kChunk, kChunk, bp.dr + at * kChunk * values, values,
-                      wide_values, [&](int i, int j0, int left, const float (&f)[8]) {
-                          // the row's share of dR.V, and dV
-                          float s = 0.0f;
-                          if (i < n && left > 0) {
-                              float v[8], d[8];
-                              load_eight<T, kWide>(v, delta_at<T>(p.v, c.batch, c.row + i, head) + j0, left);
-                              T *to = delta_at<T>(bp.grad_v, c.batch, c.row + i, head) + j0;
-#pragma unroll
-                              for (int j = 0; j < 8; ++j) s = fmaf(f[j], v[j], s), d[j] = beta[i] * f[j];
-                              // dense rows of whole 16-byte pieces start on 16 bytes if the first does
-                              if (kWide && bp.wide && left >= 8) {
-                                  store_f32<8>(to, d);
-                              } else {
-#pragma unroll
-                                  for (int j = 0; j < 8; ++j)
-                                      if (j < left) to[j] = from_f32<T>(d[j]);
-                              }
-                          }
-#pragma unroll
-                          for (int o = 8; o > 0; o /= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
-                          if (lane % 16 == 0) value_dot[i] = s;
-                      });
-        load_f32_rows(sm + Space::u, sm + Space::u + kRows, kChunk, 0, p.u + at * kChunk * values, values, wide_values,
-                      [](int, int, int, const float (&)[8]) {});
-        if (ok) ok = mma_wait(&bars[3], parity);
+        wait(3);
+        if (kMaps && n < kChunk) {
+            clear(Space::stack, 2 * kTileBytes, 0);
+            if (h == 0) clear(Space::k, kTileBytes, 0), clear(Space::q, kTileBytes, 0);
+        }
         meet();
         const Operand<kChunk, false> U(sm + Space::u), Ul(sm + Space::u + kRows);
         const Operand<kMost, true> S(sm + Space::state), Sl(sm + Space::state + kState);
@@ -222,13 +248,52 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(DeltaBackwa
             if constexpr (kP == 2) {
                 product_ss<2 * kChunk, kMost>(tm + kDX, S, bothl, true);
             } else {
-                const Operand<2 * kChunk, false> drl(sm + Space::stack + 2 * kRows + kChunk * kTileRow);
+                const Operand<2 * kChunk, false> drl(sm + Space::stack + 2 * kRows + kTileBytes);
                 product_ss<kChunk, kMost>(tm + kDX + kChunk, S, drl, true);
             }
             mma_commit(&bars[1]);
         }
-        // dA and E, this thread's row and half of the columns
-        float w[32];
+        // the gradient of the state after the chunk, on its way into registers
+        uint4 ends[4][2];
+#pragma unroll
+        for (int l = 0; l < 4; ++l) {
+            const int e = tid + l * kGradThreads;
+            ends[l][0] = ends[l][1] = make_uint4(0, 0, 0, 0);
+            if (e < tiles * values * 8) {
+                ends[l][0] = *reinterpret_cast<const uint4 *>(S1 + e * 16);
+                ends[l][1] = *reinterpret_cast<const uint4 *>(S1 + (tiles * values * 8 + e) * 16);
+            }
+        }
+        // dV, and dR.V
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int i = e * (kGradThreads / 16) + tid / 16, j0 = tid % 16 * 8, left = values - j0;
+            const char *from = sm + Space::stack + j0 / 64 * 2 * kTileBytes + tile_piece(uint32_t(kChunk + i), uint32_t(j0 % 64 / 8));
+            const uint4 hi = *reinterpret_cast<const uint4 *>(from), lo = *reinterpret_cast<const uint4 *>(from + 2 * kRows);
+            const float2 f[4] = {pair_of(hi.x, lo.x), pair_of(hi.y, lo.y), pair_of(hi.z, lo.z), pair_of(hi.w, lo.w)};
+            float s = 0.0f, d[8];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                s = fmaf(f[j].x, v[e][2 * j], fmaf(f[j].y, v[e][2 * j + 1], s));
+                d[2 * j] = beta[i] * f[j].x, d[2 * j + 1] = beta[i] * f[j].y;
+            }
+            if (i < n && left > 0) {
+                T *to = delta_at<T>(bp.grad_v, c.batch, c.row + i, head) + j0;
+                // dense rows of whole 16-byte pieces start on 16 bytes if the first does
+                if (p.wide && bp.wide && left >= 8) {
+                    store_f32<8>(to, d);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (j < left) to[j] = from_f32<T>(d[j]);
+                }
+            }
+#pragma unroll
+            for (int o = 8; o > 0; o /= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
+            if (lane % 16 == 0) value_dot[i] = s;
+        }
+        // dA and E: this thread's row, and a quarter of the columns
+        float w[kCols];
         wait(0);
         read(w, kDA + t0);
         const int row = dk % kChunk;
@@ -236,35 +301,33 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(DeltaBackwa
         {
             const Sum2 own = sums[row];
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
+            for (int j = 0; j < kCols; ++j) {
                 const int col = t0 + j;
                 const bool in = cross ? col < row : col <= row;
                 w[j] = in ? (cross ? -1.0f : p.scale) * __expf(sum2_less(own, sums[col])) * w[j] : 0.0f;
             }
         }
         wait(1);
-        __syncthreads();  // every thread's products from the stack have ended, and their reads of it
-        {
+        __syncthreads();  // the stack and the state have been read, by products and threads
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                float f[8];
+        for (int j = 0; j < kCols / 8; ++j) {
+            float f[8];
 #pragma unroll
-                for (int l = 0; l < 8; ++l) f[l] = w[j * 8 + l];
-                store_pieces(sm + Space::cross, sm + Space::cross + kRows, tile_piece(uint32_t(dk), uint32_t(half * 4 + j)), f);
-                if (cross) {
+            for (int l = 0; l < 8; ++l) f[l] = w[j * 8 + l];
+            const uint32_t piece = uint32_t(t0 / 8 + j);
+            store_pieces(sm + Space::cross, sm + Space::cross + kRows, tile_piece(uint32_t(dk), piece), f);
+            if (cross) {
 #pragma unroll
-                    for (int l = 0; l < 8; ++l) f[l] *= beta[row];
-                    store_pieces(sm + Space::scaled, sm + Space::scaled + kChunk * kTileRow,
-                                 tile_piece(uint32_t(row), uint32_t(half * 4 + j)), f);
-                }
+                for (int l = 0; l < 8; ++l) f[l] *= beta[row];
+                store_pieces(sm + Space::scaled, sm + Space::scaled + kTileBytes, tile_piece(uint32_t(row), piece), f);
             }
         }
         // the gradient of the state after the chunk takes the state's place, and meets it on the way
         float meeting = 0.0f;
-#pragma unroll 4
-        for (int e = tid; e < tiles * values * 8; e += kGradThreads) {
-            const uint4 hi = *reinterpret_cast<const uint4 *>(S1 + e * 16);
-            const uint4 lo = *reinterpret_cast<const uint4 *>(S1 + (tiles * values * 8 + e) * 16);
+#pragma unroll
+        for (int l = 0; l < 4; ++l) {
+            const int e = tid + l * kGradThreads;
+            if (e >= tiles * values * 8) continue;
             uint4 *at_hi = reinterpret_cast<uint4 *>(sm + Space::state + (e >= values * 8 ? kMost * 8 + e - values * 8 : e) * 16);
             uint4 *at_lo = reinterpret_cast<uint4 *>(reinterpret_cast<char *>(at_hi) + kState);
             const uint4 shi = *at_hi, slo = *at_lo;
@@ -272,9 +335,9 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(DeltaBackwa
                 const float2 f = pair_of(a, b), g = pair_of(x, y);
                 meeting = fmaf(f.x, g.x, fmaf(f.y, g.y, meeting));
             };
-            with(hi.x, lo.x, shi.x, slo.x), with(hi.y, lo.y, shi.y, slo.y);
-            with(hi.z, lo.z, shi.z, slo.z), with(hi.w, lo.w, shi.w, slo.w);
-            *at_hi = hi, *at_lo = lo;
+            with(ends[l][0].x, ends[l][1].x, shi.x, slo.x), with(ends[l][0].y, ends[l][1].y, shi.y, slo.y);
+            with(ends[l][0].z, ends[l][1].z, shi.z, slo.z), with(ends[l][0].w, ends[l][1].w, shi.w, slo.w);
+            *at_hi = ends[l][0], *at_lo = ends[l][1];
         }
         meeting *= first[kChunk - 1];
         meet();
@@ -282,7 +345,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(DeltaBackwa
             const Operand<kChunk, true> K(sm + Space::k), Q(sm + Space::q);
             const Operand<2 * kChunk, false> W(sm + Space::cross), Wl(sm + Space::cross + kRows);
             const Operand<2 * kChunk, true> A(sm + Space::cross), Al(sm + Space::cross + kRows);
-            const Operand<kChunk, true> E(sm + Space::scaled), El(sm + Space::scaled + kChunk * kTileRow);
+            const Operand<kChunk, true> E(sm + Space::scaled), El(sm + Space::scaled + kTileBytes);
             product_ss<2 * kChunk, kChunk>(tm + kDW, K, W, false);
             product_ss<2 * kChunk, kChunk>(tm + kDW, K, Wl, true);
             product_ss<kChunk, kChunk>(tm + kDY, Q, A, false);
@@ -295,50 +358,53 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(DeltaBackwa
                 product_ss<kChunk, kChunk>(tm + kDY, Ql, A, true);
                 product_ss<kChunk, kChunk>(tm + kDY, Kl, E, true);
             }
+            mma_commit(&bars[2]);
             product_ss<kChunk, kMost>(tm + kDU, S, U, false);
             product_ss<kChunk, kMost>(tm + kDU, S, Ul, true);
             product_ss<kChunk, kMost>(tm + kDU, Sl, U, true);
-            mma_commit(&bars[2]);
+            mma_commit(&bars[4]);
         }
+        float x[kCols], both_sums[2 * kCols];  // of q.dQ + beta k.Z - k.Y, and of k.Z
         wait(2);
-        float x[32], key_sum[32], all_sum[32];
         // dQ
         read(w, kDX + t0);
         read(x, kDW + t0);
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
+        for (int j = 0; j < kCols; ++j) {
             const float d = fmaf(p.scale * first[t0 + j], w[j], x[j]);
             dq[j] = h ? dq[j] + d : d;
-            all_sum[j] = d * entry(Space::q, t0 + j);
+            both_sums[j] = d * entry(Space::q, t0 + j);
         }
         // Z
         read(w, kDX + kChunk + t0);
         read(x, kDW + kChunk + t0);
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
+        for (int j = 0; j < kCols; ++j) {
             const float z = fmaf(-first[t0 + j], w[j], x[j]), b = beta[t0 + j] * z, k = entry(Space::k, t0 + j);
             dkey[j] = h ? dkey[j] + b : b;
-            key_sum[j] = k * z;
-            all_sum[j] = fmaf(k, b, all_sum[j]);
+            both_sums[kCols + j] = k * z;
+            both_sums[j] = fmaf(k, b, both_sums[j]);
         }
         // Y
-        read(w, kDU + t0);
         read(x, kDY + t0);
+        wait(4);
+        read(w, kDU + t0);
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
+        for (int j = 0; j < kCols; ++j) {
             const float r = rest[t0 + j] * w[j], y = r + x[j], k = entry(Space::k, t0 + j);
             meeting = fmaf(k, r, meeting);
             dkey[j] += y;
-            all_sum[j] = fmaf(-k, y, all_sum[j]);
+            both_sums[j] = fmaf(-k, y, both_sums[j]);
         }
-        const float a = sums_of_32(all_sum, lane), b = sums_of_32(key_sum, lane);
-        dots.all[warp % 4][t0 + lane] = a, dots.key[warp % 4][t0 + lane] = b;
+        const float sum = sums_of_32(both_sums, lane);
+        if (lane < kCols) dots.all[warp % 4][t0 + lane] = sum;
+        else dots.key[warp % 4][t0 + lane - kCols] = sum;
 #pragma unroll
         for (int o = 16; o > 0; o /= 2) meeting += __shfl_xor_sync(0xffffffffu, meeting, o);
         if (lane == 0) dots.whole[warp] = meeting;
         tmem_fence_before();
         __syncthreads();
-        if (warp == 7) {
+        if (warp == 15) {
             float whole = 0.0f;
             for (int w = 0; w < kGradThreads / 32; ++w) whole += dots.whole[w];
             const float bad = ok ? 0.0f : __int_as_float(0x7fffffff);
@@ -366,7 +432,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(DeltaBackwa
         T *to_q = delta_at<T>(bp.grad_q, c.batch, c.row + t0, kh) + dk, *to_k = delta_at<T>(bp.grad_k, c.batch, c.row + t0, kh) + dk;
         const float bad = ok ? 0.0f : __int_as_float(0x7fffffff);
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
+        for (int j = 0; j < kCols; ++j)
             if (t0 + j < n) {
                 to_q[j * bp.grad_q.row] = from_f32<T>(dq[j] + bad);
                 to_k[j * bp.grad_k.row] = from_f32<T>(dkey[j] + bad);
@@ -376,17 +442,25 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(DeltaBackwa
     if (warp == 0) tmem_free(tm, 512);
 }
 
-template <class T, bool kWide>
-cudaError_t grad_k(const DeltaBackwardParams &p, cudaStream_t s) {
-    const auto kernel = delta_grad_kernel<T, kWide>;
+template <class T, bool kMaps>
+cudaError_t grad_k(const DeltaBackwardParams &p, const GradMaps &maps, cudaStream_t s) {
+    const auto kernel = delta_grad_kernel<T, kMaps>;
     constexpr size_t bytes = GradSpace<T>::kAll;
     if (device_blocks(reinterpret_cast<const void *>(kernel), kGradThreads, bytes) == 0) return cudaErrorInvalidConfiguration;
-    return launch_pdl(kernel, dim3(uint32_t(p.f.slots), uint32_t(p.f.key_heads)), dim3(kGradThreads), bytes, s, p);
+    return launch_pdl(kernel, dim3(uint32_t(p.f.slots), uint32_t(p.f.key_heads)), dim3(kGradThreads), bytes, s, p, maps);
 }
 
 template <class T>
 cudaError_t grad_t(const DeltaBackwardParams &p, cudaStream_t s) {
-    return p.f.wide ? grad_k<T, true>(p, s) : grad_k<T, false>(p, s);
+    const DeltaParams &f = p.f;
+    GradMaps maps = {};
+    if constexpr (kPieces<T> == 1) {
+        if (f.wide && delta_map(&maps.k, f.k, f.batch, f.rows, f.key_heads, f.keys, 64, true) &&
+            delta_map(&maps.q, f.q, f.batch, f.rows, f.key_heads, f.keys, 64, true) &&
+            delta_map(&maps.grad_out, p.grad_out, f.batch, f.rows, f.heads, f.values, 64, true))
+            return grad_k<T, true>(p, maps, s);
+    }
+    return grad_k<T, false>(p, maps, s);
 }
 
 }  // namespace

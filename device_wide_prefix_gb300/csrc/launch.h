@@ -252,9 +252,9 @@ struct DeltaParams {
     float *final;
     bool wide, out_wide;  // rows of q, k, v and grad_out, of out, are whole 16-byte pieces
     // [slots][heads]: inverse and weights, each two tiles of 64 x 64 (tensor.cuh,
-    // split2); and, without a gradient NULL, corrections u f32 [64][values], and
-    // the state before the chunk: two pieces of [keys / 64, rounded up] tiles of
-    // `values` rows
+    // split2); and, without a gradient NULL, corrections u, two pieces of
+    // [values / 64, rounded up] tiles of 64 rows, and the state before the chunk,
+    // two pieces of [keys / 64, rounded up] tiles of `values` rows
     float *inverse, *weights, *u, *states;
 };
 struct DeltaBackwardParams {

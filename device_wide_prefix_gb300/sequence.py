@@ -512,7 +512,7 @@ def _delta_sequences(v, offsets):
 
 def _delta_points(batch, rows, nseg, offsets, heads, keys, values):
     chunks = rows // DELTA_CHUNK + nseg if offsets is not None else batch * -(-rows // DELTA_CHUNK)
-    return chunks, heads, DELTA_CHUNK * (2 * DELTA_CHUNK + values) + (keys + 63) // 64 * 64 * values
+    return chunks, heads, DELTA_CHUNK * (2 * DELTA_CHUNK + (values + 63) // 64 * 64) + (keys + 63) // 64 * 64 * values
 
 
 def _delta_fields(q, k, v, g, beta, scale, out, offsets, initial, final, checkpoints):

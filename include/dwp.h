@@ -494,9 +494,9 @@ dwp_status dwp_selective_scan_step(const dwp_selective_scan_step_args *args, dwp
  *                  overlap initial_state)
  *   checkpoints    NULL, or what the gradient needs, to be handed on as it is:
  *                  f32 [chunks, heads, DWP_DELTA_CHUNK * (2 * DWP_DELTA_CHUNK
- *                  + values) + keys' * values], 16-byte aligned, keys' being
- *                  keys rounded up to a multiple of 64; chunks is batch *
- *                  ceil(rows / DWP_DELTA_CHUNK), or with offsets rows /
+ *                  + values') + keys' * values], 16-byte aligned, keys' and
+ *                  values' being rounded up to a multiple of 64; chunks is
+ *                  batch * ceil(rows / DWP_DELTA_CHUNK), or with offsets rows /
  *                  DWP_DELTA_CHUNK + num_segments
  *   scratch        without checkpoints 8 * DWP_DELTA_CHUNK^2 bytes for each
  *                  of those chunks and head
@@ -530,8 +530,8 @@ dwp_status dwp_gated_delta_rule(const dwp_delta_args *args, void *d_scratch, siz
  *   grad_g        f32 [batch, rows, heads], dense, or NULL (always without g);
  *                 grad_beta  the same, beta_dtype
  *   grad_initial_state  NULL, or as initial_state
- *   scratch       4 * (keys' + DWP_DELTA_CHUNK) * values bytes for each of the
- *                 chunks and head
+ *   scratch       4 * (keys' * values + DWP_DELTA_CHUNK * values') bytes for
+ *                 each of the chunks and head
  */
 typedef struct dwp_delta_backward_args {
     dwp_delta_args delta;
