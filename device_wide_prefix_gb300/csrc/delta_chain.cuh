@@ -91,11 +91,12 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
 
     if (tid == 0) {
         for (int i = 0; i < 5; ++i) mbar_init(&done[i], 1);
-        for (int i = 0; i < 3; ++i) mbar_init(&ready[i], kChainThreads);
+        // one arrival a warp: 256 on one word take a thousand cycles
+        for (int i = 0; i < 3; ++i) mbar_init(&ready[i], kChainThreads / 32);
         // the loaders, the bytes, the decays
-        for (int i = 0; i < 2; ++i) mbar_init(&full[i], kLoadThreads + 2), mbar_init(&empty[i], 1);
-        mbar_init(&out_full, kChainThreads);
-        mbar_init(&out_empty, 32);
+        for (int i = 0; i < 2; ++i) mbar_init(&full[i], kLoadThreads / 32 + 2), mbar_init(&empty[i], 1);
+        mbar_init(&out_full, kChainThreads / 32);
+        mbar_init(&out_empty, 1);
         mbar_init(&kept_read, 1);
         mbar_init(&landed, 1);
         fence_mbar_init();
@@ -255,7 +256,8 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
                 copies_done();
                 fence_proxy_async_smem();
             }
-            mbar_arrive(&full[st]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&full[st]);
         };
         float g[2], b[2];
         auto read_decays = [&](int64_t step) {
@@ -299,7 +301,8 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
                 for (int i = 0; i < n; ++i)
                     for (int j = lane; j < values; j += 32) to[i * p.out.row + j] = from[i * kMostValues + j];
             }
-            mbar_arrive(&out_empty);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&out_empty);
         };
         if (decays) {
             read_decays(0);
@@ -361,7 +364,8 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
             tmem_stored();
             if (kept) fence_proxy_async_smem();
             tmem_fence_before();
-            mbar_arrive(&ready[which]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ready[which]);
         };
         auto wait_done = [&](int which, int64_t step) {
             wait(done[which], uint32_t(step));
@@ -423,7 +427,8 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
 #pragma unroll
             for (int j = 0; j < 32; ++j) to[j * kMostValues] = from_f32<T>(fmaf(p.scale, o2[j], o1[j]) + bad);
             fence_proxy_async_smem();
-            mbar_arrive(&out_full);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&out_full);
         };
         if (chunks > 0) put_state();
         for (int64_t step = 0; step < chunks; ++step) {
