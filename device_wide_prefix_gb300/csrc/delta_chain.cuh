@@ -19,9 +19,8 @@
 //
 // Eight warps do this, and only this.  Four more work ahead and behind: one
 // issues the products (a warp that issues is held back as long as the products
-// before it run), one loads, one has the decays and the copies of what is
-// kept, one stores the outputs.  With all of it done by the eight a chunk of
-// 128 x 128 took 11,200 cycles.
+// before it run), one loads, one has the decays, and the last two copy the outputs and what is kept to memory.  With
+// all of it done by the eight a chunk of 128 x 128 took 11,200 cycles.
 #pragma once
 
 #include "delta.cuh"
@@ -35,6 +34,7 @@ constexpr int kChainThreads = 256, kHelpThreads = 128, kIssueWarp = kChainThread
 // 256 x 224 + 128 x 56 = 384 x 168.
 constexpr int kChainRegisters = 224, kHelpRegisters = 56;
 constexpr int kMostValues = 128;
+constexpr int kCopyThreads = 64;  // the last two warps: outputs and what is kept, from shared to global memory
 
 // Shared memory: the chunks' inputs, the outputs on their way, and what is kept.
 template <class T, int KD, bool kBack>
@@ -96,8 +96,8 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
         // the loaders, the bytes, the decays
         for (int i = 0; i < 2; ++i) mbar_init(&full[i], kLoadThreads / 32 + 2), mbar_init(&empty[i], 1);
         mbar_init(&out_full, kChainThreads / 32);
-        mbar_init(&out_empty, 1);
-        mbar_init(&kept_read, 1);
+        mbar_init(&out_empty, kCopyThreads / 32);
+        mbar_init(&kept_read, kCopyThreads / 32);
         mbar_init(&landed, 1);
         fence_mbar_init();
     }
@@ -186,7 +186,8 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
         }
     } else if (warp > kIssueWarp) {
         const int t = tid - kChainThreads - 32;  // of the loaders
-        const bool loads = t < kLoadThreads, decays = warp == kIssueWarp + 2, stores = !kBack && warp == kIssueWarp + 3;
+        const bool loads = t < kLoadThreads, decays = warp == kIssueWarp + 2;
+        const bool copies = warp >= kIssueWarp + 2;
         auto load = [&](int64_t step) {
             const int st = stage_of(step);
             const int64_t c = chunk_of(step), row = row0 + c * kChunk, at = (slot0 + c) * p.heads + head;
@@ -287,6 +288,25 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&full[st]);
         };
+        // Copies by loads and stores: bulk copies to global memory run at a fifth
+        // of their rate here (256 bytes in 83 cycles, 64 KB in 5000).
+        const int copier = t - kHelpThreads + 32 + kCopyThreads;
+        auto copy = [&](char *to, const char *from, int bytes) {
+            int e = copier * 16;
+            for (; e + 3 * kCopyThreads * 16 < bytes; e += 4 * kCopyThreads * 16) {
+                uint4 v[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<const uint4 *>(from + e + i * kCopyThreads * 16);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4 *>(to + e + i * kCopyThreads * 16) = v[i];
+            }
+            for (; e < bytes; e += kCopyThreads * 16)
+                *reinterpret_cast<uint4 *>(to + e) = *reinterpret_cast<const uint4 *>(from + e);
+        };
+        auto copied = [&](uint64_t &bar) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar);
+        };
         auto store = [&](int64_t step) {
             wait(out_full, uint32_t(step));
             const int64_t row = row0 + step * kChunk;
@@ -294,15 +314,23 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
             const T *from = reinterpret_cast<const T *>(sm + Space::out);
             T *to = delta_at<T>(p.out, batch, row, head);
             if (p.out_wide) {
-                for (int i = lane; i < n; i += 32) bulk_store(to + i * p.out.row, from + i * kMostValues, uint32_t(values * sizeof(T)));
-                bulk_commit();
-                bulk_wait_read<0>();
+                constexpr int kEach = 16 / int(sizeof(T)), kRow = kMostValues / kEach, kRows = kCopyThreads / kRow;
+                const int j = copier % kRow * kEach;
+                if (j < values)
+                    for (int i0 = copier / kRow; i0 < n; i0 += 4 * kRows) {
+                        uint4 v[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (i0 + i * kRows < n) v[i] = *reinterpret_cast<const uint4 *>(from + (i0 + i * kRows) * kMostValues + j);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (i0 + i * kRows < n) *reinterpret_cast<uint4 *>(to + (i0 + i * kRows) * p.out.row + j) = v[i];
+                    }
             } else {
                 for (int i = 0; i < n; ++i)
-                    for (int j = lane; j < values; j += 32) to[i * p.out.row + j] = from[i * kMostValues + j];
+                    for (int j = copier; j < values; j += kCopyThreads) to[i * p.out.row + j] = from[i * kMostValues + j];
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&out_empty);
+            copied(out_empty);
         };
         if (decays) {
             read_decays(0);
@@ -314,40 +342,24 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
             if (decays) read_decays(step + kStages);
             // a stage ahead: chunk step + 1 goes where step - 1 was
             if (loads && (kStages == 1 || step + 1 < chunks)) load(kStages == 1 ? step : step + 1);
-            if (decays) {
-                if (kept) {
-                    wait(ready[0], uint32_t(step));
-                    if (lane == 0) {
-                        const int64_t at = (slot0 + chunk_of(step)) * p.heads + head;
-                        char *to = reinterpret_cast<char *>(kept + at * KD * values);
-                        const uint32_t tile = uint32_t(values) * kTileRow;
-#pragma unroll
-                        for (int i = 0; i < 2 * KD / 64; ++i)
-                            bulk_store(to + int64_t(i) * tile, sm + Space::keep + i * kMostValues * kTileRow, tile);
-                        bulk_commit();
-                        bulk_wait_read<0>();
-                        mbar_arrive(&kept_read);
-                    }
-                    __syncwarp();
-                    wait(ready[2], uint32_t(step));
-                    if (lane == 0) {
-                        const int64_t at = (slot0 + chunk_of(step)) * p.heads + head;
-                        const int tiles = (values + 63) / 64;
-                        char *to = reinterpret_cast<char *>(kept_rows + at * kChunk * 64 * tiles);
-                        for (int i = 0; i < 2; ++i)
-                            bulk_store(to + i * tiles * Space::kTileBytes, sm + Space::keep + i * Space::kValues,
-                                       uint32_t(tiles) * Space::kTileBytes);
-                        bulk_commit();
-                        bulk_wait_read<0>();
-                        mbar_arrive(&kept_read);
-                    }
-                    __syncwarp();
-                }
-                put_decays(step + kStages);
+            if (copies && kept) {
+                const int64_t at = (slot0 + chunk_of(step)) * p.heads + head;
+                wait(ready[0], uint32_t(step));
+                for (int i = 0; i < 2 * KD / 64; ++i)
+                    copy(reinterpret_cast<char *>(kept + at * KD * values) + int64_t(i) * values * kTileRow,
+                         sm + Space::keep + i * kMostValues * kTileRow, values * int(kTileRow));
+                copied(kept_read);
+                wait(ready[2], uint32_t(step));
+                const int tiles = (values + 63) / 64;
+                for (int i = 0; i < 2; ++i)
+                    copy(reinterpret_cast<char *>(kept_rows + at * kChunk * 64 * tiles) + i * tiles * int(Space::kTileBytes),
+                         sm + Space::keep + i * Space::kValues, tiles * int(Space::kTileBytes));
+                copied(kept_read);
             }
-            if (stores) store(step);
+            if (decays) put_decays(step + kStages);
+            if (copies && !kBack && step > 0) store(step - 1);
         }
-        if (kept || stores) bulk_wait_all<0>();
+        if (copies && !kBack && chunks > 0) store(chunks - 1);
     } else {
         const int half = warp / 4, dv = warp % 4 * 32 + lane, t0 = half * 32, k0 = half * kH;
         const uint32_t mine = tm + (uint32_t(warp % 4) << 21);
@@ -359,10 +371,9 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
             for (int k = 0; k < kH; ++k)
                 S[k] = from && dv < values && k0 + k < keys ? from[at + int64_t(k0 + k) * values] : 0.0f;
         }
-        // what was stored is there for the products, and for bulk copies
+        // what was stored is there for the products, and the copies
         auto arrive = [&](int which) {
             tmem_stored();
-            if (kept) fence_proxy_async_smem();
             tmem_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&ready[which]);
@@ -416,27 +427,54 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
             arrive(0);
         };
         float o1[32];  // forward: what the state gives to the outputs
-        // forward: the outputs of a chunk, to shared memory
-        auto put_out = [&](int64_t step) {
+        T o[32];       // forward: the outputs of the chunk before
+        auto finish_out = [&](int64_t step) {
             wait_done(4, step);
             float o2[32];
             read(o2, kD1 + t0);
-            if (step > 0) wait(out_empty, uint32_t(step - 1));
-            T *to = reinterpret_cast<T *>(sm + Space::out) + t0 * kMostValues + dv;
             const float bad = ok ? 0.0f : __int_as_float(0x7fffffff);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) to[j * kMostValues] = from_f32<T>(fmaf(p.scale, o2[j], o1[j]) + bad);
-            fence_proxy_async_smem();
+            for (int j = 0; j < 32; ++j) o[j] = from_f32<T>(fmaf(p.scale, o2[j], o1[j]) + bad);
+        };
+        auto put_out = [&](int64_t step) {
+            if (step > 0) wait(out_empty, uint32_t(step - 1));
+            T *to = reinterpret_cast<T *>(sm + Space::out) + t0 * kMostValues + dv;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) to[j * kMostValues] = o[j];
             __syncwarp();
             if (lane == 0) mbar_arrive(&out_full);
         };
-        if (chunks > 0) put_state();
+        // back: the queries' side, scale e^G dO, in two pieces
+        uint32_t side_hi[kBack ? 16 : 1], side_lo[kBack ? 16 : 1];
+        auto prepare_side = [&](int64_t step) {
+            const int st = stage_of(step);
+            const char *dO = sm + st * Space::bytes + Space::v;
+            wait(full[st], round_of(step));
+            const float4 *const first4 = reinterpret_cast<const float4 *>(rows_of[st].first + t0);
+#pragma unroll
+            for (int j = 0; j < 32; j += 4) {
+                const float4 f = first4[j / 4];
+                float x[4] = {p.scale * f.x, p.scale * f.y, p.scale * f.z, p.scale * f.w};
+#pragma unroll
+                for (int l = 0; l < 4; ++l) {
+                    const char *e = dO + tile_at(uint32_t(t0 + j + l), uint32_t(dv), kChunk);
+                    float d = __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(e));
+                    if constexpr (kP == 2) d += __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(e + Space::kValues));
+                    x[l] *= d;
+                }
+                split2(x[0], x[1], side_hi[kBack ? j / 2 : 0], side_lo[kBack ? j / 2 : 0]);
+                split2(x[2], x[3], side_hi[kBack ? j / 2 + 1 : 0], side_lo[kBack ? j / 2 + 1 : 0]);
+            }
+        };
+        if (chunks > 0) {
+            put_state();
+            if constexpr (kBack) prepare_side(0);
+        }
         for (int64_t step = 0; step < chunks; ++step) {
             const int st = stage_of(step);
             char *s = sm + st * Space::bytes;
-            // before the next chunk's inputs: its loaders may be waiting for the outputs' place
             if constexpr (!kBack)
-                if (step > 0) put_out(step - 1);
+                if (step > 0) finish_out(step - 1);
             wait(full[st], round_of(step));
             const ChainRows &r = rows_of[st];
             const float whole = r.first[kChunk - 1];
@@ -461,16 +499,10 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
                 }
                 put_rows(kR, x);
             } else {
-                // the queries' side: scale e^G dO
-#pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    const uint32_t e = tile_at(t0 + j, dv, kChunk);
-                    float f = __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(s + Space::v + e));
-                    if constexpr (kP == 2)
-                        f += __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(s + Space::v + Space::kValues + e));
-                    x[j] = p.scale * r.first[t0 + j] * f;
+                if constexpr (kBack) {
+                    tmem_store<16>(mine + kU + half * 16, side_hi);
+                    tmem_store<16>(mine + kU + 32 + half * 16, side_lo);
                 }
-                put_rows(kU, x);
                 wait_done(0, step);
                 read(x, kD0 + t0);
                 wait_done(1, step);
@@ -533,6 +565,12 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
             }
             put_rows(kR, x);
             arrive(2);
+            // while the state's product runs
+            if constexpr (!kBack) {
+                if (step > 0) put_out(step - 1);
+            } else if (kStages == 2 && step + 1 < chunks) {
+                prepare_side(step + 1);
+            }
             wait_done(3, step);
 #pragma unroll
             for (int k = 0; k < kH; k += 32) {
@@ -540,10 +578,16 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
 #pragma unroll
                 for (int j = 0; j < 32; ++j) S[k + j] = fmaf(whole, S[k + j], x[j]);
             }
-            if (step + 1 < chunks) put_state();
+            if (step + 1 < chunks) {
+                put_state();
+                if (kBack && kStages == 1) prepare_side(step + 1);
+            }
         }
         if constexpr (!kBack)
-            if (chunks > 0) put_out(chunks - 1);
+            if (chunks > 0) {
+                finish_out(chunks - 1);
+                put_out(chunks - 1);
+            }
         if (float *to = kBack ? bp.grad_initial : p.final; to && dv < values) {
             to += (seq * p.heads + head) * keys * values + dv;
             const float bad = ok ? 0.0f : __int_as_float(0x7fffffff);
