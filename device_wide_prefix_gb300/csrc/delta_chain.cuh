@@ -17,10 +17,13 @@
 // For bf16 outputs the weights, corrections and state of the last products
 // are one bf16 each: they cost at most 2^-8 of the output's terms.
 //
-// Eight warps do this, and only this.  Four more work ahead and behind: one
-// issues the products (a warp that issues is held back as long as the products
-// before it run), one loads, one has the decays, and the last two copy the outputs and what is kept to memory.  With
-// all of it done by the eight a chunk of 128 x 128 took 11,200 cycles.
+// Eight warps do this; of four more one issues the products (a warp that issues
+// is held back as long as the products before it run), one loads, and one has
+// the decays: they work ahead.  Outputs, and what is kept for the gradient, go
+// through shared memory, and the eight copy them on while they wait for
+// products: one of the four warps is slower at that (instructions that come in
+// between the chain's are fetched anew each time; 9,000 cycles a chunk), bulk
+// copies are slower still (256 bytes in 83 cycles, 64 KB in 5,000).
 #pragma once
 
 #include "delta.cuh"
@@ -34,7 +37,6 @@ constexpr int kChainThreads = 256, kHelpThreads = 128, kIssueWarp = kChainThread
 // 256 x 224 + 128 x 56 = 384 x 168.
 constexpr int kChainRegisters = 224, kHelpRegisters = 56;
 constexpr int kMostValues = 128;
-constexpr int kCopyThreads = 64;  // the last two warps: outputs and what is kept, from shared to global memory
 
 // Shared memory: the chunks' inputs, the outputs on their way, and what is kept.
 template <class T, int KD, bool kBack>
@@ -71,7 +73,7 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
     constexpr int kLoadThreads = kMaps ? 32 : 96;
     extern __shared__ char raw[];
     __shared__ ChainRows rows_of[2];
-    __shared__ uint64_t done[5], ready[3], full[2], empty[2], out_full, out_empty, kept_read, landed;
+    __shared__ uint64_t done[5], ready[3], full[2], empty[2], landed;
     __shared__ uint32_t tmem;
     const DeltaParams &p = bp.f;
     char *sm = reinterpret_cast<char *>((reinterpret_cast<uintptr_t>(raw) + 1023) / 1024 * 1024);
@@ -95,9 +97,6 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
         for (int i = 0; i < 3; ++i) mbar_init(&ready[i], kChainThreads / 32);
         // the loaders, the bytes, the decays
         for (int i = 0; i < 2; ++i) mbar_init(&full[i], kLoadThreads / 32 + 2), mbar_init(&empty[i], 1);
-        mbar_init(&out_full, kChainThreads / 32);
-        mbar_init(&out_empty, kCopyThreads / 32);
-        mbar_init(&kept_read, kCopyThreads / 32);
         mbar_init(&landed, 1);
         fence_mbar_init();
     }
@@ -187,7 +186,6 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
     } else if (warp > kIssueWarp) {
         const int t = tid - kChainThreads - 32;  // of the loaders
         const bool loads = t < kLoadThreads, decays = warp == kIssueWarp + 2;
-        const bool copies = warp >= kIssueWarp + 2;
         auto load = [&](int64_t step) {
             const int st = stage_of(step);
             const int64_t c = chunk_of(step), row = row0 + c * kChunk, at = (slot0 + c) * p.heads + head;
@@ -288,50 +286,6 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&full[st]);
         };
-        // Copies by loads and stores: bulk copies to global memory run at a fifth
-        // of their rate here (256 bytes in 83 cycles, 64 KB in 5000).
-        const int copier = t - kHelpThreads + 32 + kCopyThreads;
-        auto copy = [&](char *to, const char *from, int bytes) {
-            int e = copier * 16;
-            for (; e + 3 * kCopyThreads * 16 < bytes; e += 4 * kCopyThreads * 16) {
-                uint4 v[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<const uint4 *>(from + e + i * kCopyThreads * 16);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4 *>(to + e + i * kCopyThreads * 16) = v[i];
-            }
-            for (; e < bytes; e += kCopyThreads * 16)
-                *reinterpret_cast<uint4 *>(to + e) = *reinterpret_cast<const uint4 *>(from + e);
-        };
-        auto copied = [&](uint64_t &bar) {
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bar);
-        };
-        auto store = [&](int64_t step) {
-            wait(out_full, uint32_t(step));
-            const int64_t row = row0 + step * kChunk;
-            const int n = rows_in(step);
-            const T *from = reinterpret_cast<const T *>(sm + Space::out);
-            T *to = delta_at<T>(p.out, batch, row, head);
-            if (p.out_wide) {
-                constexpr int kEach = 16 / int(sizeof(T)), kRow = kMostValues / kEach, kRows = kCopyThreads / kRow;
-                const int j = copier % kRow * kEach;
-                if (j < values)
-                    for (int i0 = copier / kRow; i0 < n; i0 += 4 * kRows) {
-                        uint4 v[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (i0 + i * kRows < n) v[i] = *reinterpret_cast<const uint4 *>(from + (i0 + i * kRows) * kMostValues + j);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (i0 + i * kRows < n) *reinterpret_cast<uint4 *>(to + (i0 + i * kRows) * p.out.row + j) = v[i];
-                    }
-            } else {
-                for (int i = 0; i < n; ++i)
-                    for (int j = copier; j < values; j += kCopyThreads) to[i * p.out.row + j] = from[i * kMostValues + j];
-            }
-            copied(out_empty);
-        };
         if (decays) {
             read_decays(0);
             put_decays(0);
@@ -342,24 +296,8 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
             if (decays) read_decays(step + kStages);
             // a stage ahead: chunk step + 1 goes where step - 1 was
             if (loads && (kStages == 1 || step + 1 < chunks)) load(kStages == 1 ? step : step + 1);
-            if (copies && kept) {
-                const int64_t at = (slot0 + chunk_of(step)) * p.heads + head;
-                wait(ready[0], uint32_t(step));
-                for (int i = 0; i < 2 * KD / 64; ++i)
-                    copy(reinterpret_cast<char *>(kept + at * KD * values) + int64_t(i) * values * kTileRow,
-                         sm + Space::keep + i * kMostValues * kTileRow, values * int(kTileRow));
-                copied(kept_read);
-                wait(ready[2], uint32_t(step));
-                const int tiles = (values + 63) / 64;
-                for (int i = 0; i < 2; ++i)
-                    copy(reinterpret_cast<char *>(kept_rows + at * kChunk * 64 * tiles) + i * tiles * int(Space::kTileBytes),
-                         sm + Space::keep + i * Space::kValues, tiles * int(Space::kTileBytes));
-                copied(kept_read);
-            }
             if (decays) put_decays(step + kStages);
-            if (copies && !kBack && step > 0) store(step - 1);
         }
-        if (copies && !kBack && chunks > 0) store(chunks - 1);
     } else {
         const int half = warp / 4, dv = warp % 4 * 32 + lane, t0 = half * 32, k0 = half * kH;
         const uint32_t mine = tm + (uint32_t(warp % 4) << 21);
@@ -397,15 +335,45 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
             tmem_store<16>(mine + at + half * 16, hi);
             tmem_store<16>(mine + at + 32 + half * 16, lo);
         };
-        // what was kept last has been read
-        uint32_t kept_times = 0;
-        auto wait_kept = [&] {
-            if (kept && kept_times) wait(kept_read, kept_times - 1u);
-            ++kept_times;
+        auto meet = [] { asm volatile("bar.sync 1, %0;" ::"n"(kChainThreads) : "memory"); };
+        // from shared to global memory, whole 16-byte pieces
+        auto copy = [&](char *to, const char *from, int bytes) {
+#pragma unroll 4
+            for (int e = tid * 16; e < bytes; e += kChainThreads * 16)
+                *reinterpret_cast<uint4 *>(to + e) = *reinterpret_cast<const uint4 *>(from + e);
+        };
+        auto copy_state = [&](int64_t at) {
+            for (int i = 0; i < 2 * KD / 64; ++i)
+                copy(reinterpret_cast<char *>(kept + at * KD * values) + int64_t(i) * values * kTileRow,
+                     sm + Space::keep + i * kMostValues * kTileRow, values * int(kTileRow));
+        };
+        auto copy_rows = [&](int64_t at) {
+            const int tiles = (values + 63) / 64;
+            for (int i = 0; i < 2; ++i)
+                copy(reinterpret_cast<char *>(kept_rows + at * kChunk * 64 * tiles) + i * tiles * int(Space::kTileBytes),
+                     sm + Space::keep + i * Space::kValues, tiles * int(Space::kTileBytes));
+        };
+        auto copy_out = [&](int64_t step) {
+            const int n = rows_in(step);
+            const T *from = reinterpret_cast<const T *>(sm + Space::out);
+            T *to = delta_at<T>(p.out, batch, row0 + step * kChunk, head);
+            if (p.out_wide) {
+                constexpr int kEach = 16 / int(sizeof(T)), kRow = kMostValues / kEach;
+                const int j = tid % kRow * kEach;
+                if (j < values)
+#pragma unroll 4
+                    for (int i = tid / kRow; i < n; i += kChainThreads / kRow)
+                        *reinterpret_cast<uint4 *>(to + i * p.out.row + j) =
+                            *reinterpret_cast<const uint4 *>(from + i * kMostValues + j);
+            } else {
+                const int j = tid % kMostValues;
+                if (j < values)
+                    for (int i = tid / kMostValues; i < n; i += kChainThreads / kMostValues)
+                        to[i * p.out.row + j] = from[i * kMostValues + j];
+            }
         };
         // the state as the next products' operand, and as kept
         auto put_state = [&] {
-            wait_kept();
 #pragma unroll
             for (int k = 0; k < kH; k += 16) {
                 uint32_t hi[8], lo[8];
@@ -436,13 +404,10 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
 #pragma unroll
             for (int j = 0; j < 32; ++j) o[j] = from_f32<T>(fmaf(p.scale, o2[j], o1[j]) + bad);
         };
-        auto put_out = [&](int64_t step) {
-            if (step > 0) wait(out_empty, uint32_t(step - 1));
+        auto put_out = [&] {
             T *to = reinterpret_cast<T *>(sm + Space::out) + t0 * kMostValues + dv;
 #pragma unroll
             for (int j = 0; j < 32; ++j) to[j * kMostValues] = o[j];
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&out_full);
         };
         // back: the queries' side, scale e^G dO, in two pieces
         uint32_t side_hi[kBack ? 16 : 1], side_lo[kBack ? 16 : 1];
@@ -473,8 +438,15 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
         for (int64_t step = 0; step < chunks; ++step) {
             const int st = stage_of(step);
             char *s = sm + st * Space::bytes;
+            const int64_t at = (slot0 + chunk_of(step)) * p.heads + head;
             if constexpr (!kBack)
                 if (step > 0) finish_out(step - 1);
+            // what was put in shared memory last is copied on while the product runs
+            if (!kBack || kept) {
+                meet();
+                if (kept) copy_state(at);
+                if (!kBack && step > 1) copy_out(step - 2);
+            }
             wait(full[st], round_of(step));
             const ChainRows &r = rows_of[st];
             const float whole = r.first[kChunk - 1];
@@ -519,6 +491,7 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
                 put_rows(kR, x);
             }
             arrive(1);
+            if (!kBack || kept) meet();  // every copy has read its place
             if constexpr (!kBack) {
                 wait_done(1, step);
                 read(o1, kDS + t0);
@@ -529,7 +502,6 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
                     o1[4 * j + 2] *= p.scale * f.z, o1[4 * j + 3] *= p.scale * f.w;
                 }
             }
-            wait_kept();
             wait_done(2, step);
             read(x, kD0 + t0);
             if (kept) {
@@ -566,8 +538,12 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
             put_rows(kR, x);
             arrive(2);
             // while the state's product runs
+            if (kept) {
+                meet();
+                copy_rows(at);
+            }
             if constexpr (!kBack) {
-                if (step > 0) put_out(step - 1);
+                if (step > 0) put_out();
             } else if (kStages == 2 && step + 1 < chunks) {
                 prepare_side(step + 1);
             }
@@ -579,6 +555,7 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
                 for (int j = 0; j < 32; ++j) S[k + j] = fmaf(whole, S[k + j], x[j]);
             }
             if (step + 1 < chunks) {
+                if (kept) meet();
                 put_state();
                 if (kBack && kStages == 1) prepare_side(step + 1);
             }
@@ -586,7 +563,12 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
         if constexpr (!kBack)
             if (chunks > 0) {
                 finish_out(chunks - 1);
-                put_out(chunks - 1);
+                meet();
+                if (chunks > 1) copy_out(chunks - 2);
+                meet();
+                put_out();
+                meet();
+                copy_out(chunks - 1);
             }
         if (float *to = kBack ? bp.grad_initial : p.final; to && dv < values) {
             to += (seq * p.heads + head) * keys * values + dv;
