@@ -10,17 +10,18 @@
 //
 // All products are taken transposed, so that their 128 rows are the values
 // and never a chunk's 64 rows: the state, f32 in registers (a thread has one
-// value's row and half of the keys), goes to tensor memory as the first operand
+// value's row and a quarter of the keys), goes to tensor memory as the first operand
 // of the next products, as R and U do, and K, Q, T, A and dO are operands in
 // shared memory as they are stored.  What is not itself bf16 is two bf16
 // (split2), and of a product of two such the three larger parts are taken.
 // For bf16 outputs the weights, corrections and state of the last products
 // are one bf16 each: they cost at most 2^-8 of the output's terms.
 //
-// Eight warps do this; of four more one issues the products (a warp that issues
+// Sixteen warps do this (with eight, twice the registers and rows each, a chunk
+// took 1.2 times as long); of four more one issues the products (a warp that issues
 // is held back as long as the products before it run), one loads, and one has
 // the decays: they work ahead.  Outputs, and what is kept for the gradient, go
-// through shared memory, and the eight copy them on while they wait for
+// through shared memory, and the sixteen copy them on while they wait for
 // products: one of the four warps is slower at that (instructions that come in
 // between the chain's are fetched anew each time; 9,000 cycles a chunk), bulk
 // copies are slower still (256 bytes in 83 cycles, 64 KB in 5,000).
@@ -32,10 +33,11 @@ namespace dwp {
 
 namespace {
 
-constexpr int kChainThreads = 256, kHelpThreads = 128, kIssueWarp = kChainThreads / 32;
-// 168 registers a thread at launch, of which the helpers give some to the chain:
-// 256 x 224 + 128 x 56 = 384 x 168.
-constexpr int kChainRegisters = 224, kHelpRegisters = 56;
+constexpr int kChainThreads = 512, kHelpThreads = 128, kIssueWarp = kChainThreads / 32;
+constexpr int kParts = kChainThreads / 128, kT = kChunk / kParts;  // kT: a thread's rows of the chunk
+// 96 registers a thread at launch, of which the helpers give some to the chain:
+// 512 x 104 + 128 x 64 = 640 x 96.
+constexpr int kChainRegisters = 104, kHelpRegisters = 64;
 constexpr int kMostValues = 128;
 
 // Shared memory: the chunks' inputs, the outputs on their way, and what is kept.
@@ -69,7 +71,7 @@ template <class T, int KD, bool kBack, bool kMaps>
 __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
     delta_chain_kernel(DeltaBackwardParams bp, const __grid_constant__ ChainMaps maps) {
     using Space = ChainSpace<T, KD, kBack>;
-    constexpr int kP = Space::kP, kH = KD / 2, kStages = Space::kStages;  // kH: keys of a thread
+    constexpr int kP = Space::kP, kH = KD / kParts, kStages = Space::kStages;  // kH: keys of a thread
     constexpr int kLoadThreads = kMaps ? 32 : 96;
     extern __shared__ char raw[];
     __shared__ ChainRows rows_of[2];
@@ -299,7 +301,7 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
             if (decays) put_decays(step + kStages);
         }
     } else {
-        const int half = warp / 4, dv = warp % 4 * 32 + lane, t0 = half * 32, k0 = half * kH;
+        const int part = warp / 4, dv = warp % 4 * 32 + lane, t0 = part * kT, k0 = part * kH;
         const uint32_t mine = tm + (uint32_t(warp % 4) << 21);
         float S[kH];
         {
@@ -320,20 +322,20 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
             wait(done[which], uint32_t(step));
             tmem_fence_after();
         };
-        auto read = [&](float (&x)[32], uint32_t at) {
-            uint32_t v[32];
-            tmem_load<32>(v, mine + at);
+        auto read = [&](float (&x)[kT], uint32_t at) {
+            uint32_t v[kT];
+            tmem_load<kT>(v, mine + at);
             tmem_ready();
 #pragma unroll
-            for (int j = 0; j < 32; ++j) x[j] = __uint_as_float(v[j]);
+            for (int j = 0; j < kT; ++j) x[j] = __uint_as_float(v[j]);
         };
-        // 32 numbers of this thread's rows of the chunk, in two pieces, as an operand
-        auto put_rows = [&](uint32_t at, const float (&x)[32]) {
-            uint32_t hi[16], lo[16];
+        // numbers of this thread's rows of the chunk, in two pieces, as an operand
+        auto put_rows = [&](uint32_t at, const float (&x)[kT]) {
+            uint32_t hi[kT / 2], lo[kT / 2];
 #pragma unroll
-            for (int j = 0; j < 16; ++j) split2(x[2 * j], x[2 * j + 1], hi[j], lo[j]);
-            tmem_store<16>(mine + at + half * 16, hi);
-            tmem_store<16>(mine + at + 32 + half * 16, lo);
+            for (int j = 0; j < kT / 2; ++j) split2(x[2 * j], x[2 * j + 1], hi[j], lo[j]);
+            tmem_store<kT / 2>(mine + at + part * (kT / 2), hi);
+            tmem_store<kT / 2>(mine + at + 32 + part * (kT / 2), lo);
         };
         auto meet = [] { asm volatile("bar.sync 1, %0;" ::"n"(kChainThreads) : "memory"); };
         // from shared to global memory, whole 16-byte pieces
@@ -394,30 +396,30 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
             }
             arrive(0);
         };
-        float o1[32];  // forward: what the state gives to the outputs
-        T o[32];       // forward: the outputs of the chunk before
+        float o1[kT];  // forward: what the state gives to the outputs
+        T o[kT];       // forward: the outputs of the chunk before
         auto finish_out = [&](int64_t step) {
             wait_done(4, step);
-            float o2[32];
+            float o2[kT];
             read(o2, kD1 + t0);
             const float bad = ok ? 0.0f : __int_as_float(0x7fffffff);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) o[j] = from_f32<T>(fmaf(p.scale, o2[j], o1[j]) + bad);
+            for (int j = 0; j < kT; ++j) o[j] = from_f32<T>(fmaf(p.scale, o2[j], o1[j]) + bad);
         };
         auto put_out = [&] {
             T *to = reinterpret_cast<T *>(sm + Space::out) + t0 * kMostValues + dv;
 #pragma unroll
-            for (int j = 0; j < 32; ++j) to[j * kMostValues] = o[j];
+            for (int j = 0; j < kT; ++j) to[j * kMostValues] = o[j];
         };
         // back: the queries' side, scale e^G dO, in two pieces
-        uint32_t side_hi[kBack ? 16 : 1], side_lo[kBack ? 16 : 1];
+        uint32_t side_hi[kBack ? kT / 2 : 1], side_lo[kBack ? kT / 2 : 1];
         auto prepare_side = [&](int64_t step) {
             const int st = stage_of(step);
             const char *dO = sm + st * Space::bytes + Space::v;
             wait(full[st], round_of(step));
             const float4 *const first4 = reinterpret_cast<const float4 *>(rows_of[st].first + t0);
 #pragma unroll
-            for (int j = 0; j < 32; j += 4) {
+            for (int j = 0; j < kT; j += 4) {
                 const float4 f = first4[j / 4];
                 float x[4] = {p.scale * f.x, p.scale * f.y, p.scale * f.z, p.scale * f.w};
 #pragma unroll
@@ -453,16 +455,16 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
             const float4 *const first4 = reinterpret_cast<const float4 *>(r.first + t0);
             const float4 *const beta4 = reinterpret_cast<const float4 *>(r.beta + t0);
             const float4 *const rest4 = reinterpret_cast<const float4 *>(r.rest + t0);
-            float x[32];
+            float x[kT];
             if constexpr (!kBack) {
-                float y[32];
+                float y[kT];
                 const T *v = reinterpret_cast<const T *>(s + Space::v) + t0 * kMostValues + dv;
 #pragma unroll
-                for (int j = 0; j < 32; ++j) y[j] = to_f32<T>(v[j * kMostValues]);
+                for (int j = 0; j < kT; ++j) y[j] = to_f32<T>(v[j * kMostValues]);
                 wait_done(0, step);
                 read(x, kD0 + t0);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
+                for (int j = 0; j < kT / 4; ++j) {
                     const float4 f = first4[j], b = beta4[j];
                     x[4 * j] = b.x * fmaf(-f.x, x[4 * j], y[4 * j]);
                     x[4 * j + 1] = b.y * fmaf(-f.y, x[4 * j + 1], y[4 * j + 1]);
@@ -472,16 +474,16 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
                 put_rows(kR, x);
             } else {
                 if constexpr (kBack) {
-                    tmem_store<16>(mine + kU + half * 16, side_hi);
-                    tmem_store<16>(mine + kU + 32 + half * 16, side_lo);
+                    tmem_store<kT / 2>(mine + kU + part * (kT / 2), side_hi);
+                    tmem_store<kT / 2>(mine + kU + 32 + part * (kT / 2), side_lo);
                 }
                 wait_done(0, step);
                 read(x, kD0 + t0);
                 wait_done(1, step);
-                float y[32];
+                float y[kT];
                 read(y, kD1 + t0);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
+                for (int j = 0; j < kT / 4; ++j) {
                     const float4 f = rest4[j];
                     x[4 * j] = fmaf(f.x, x[4 * j], p.scale * y[4 * j]);
                     x[4 * j + 1] = fmaf(f.y, x[4 * j + 1], p.scale * y[4 * j + 1]);
@@ -496,7 +498,7 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
                 wait_done(1, step);
                 read(o1, kDS + t0);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
+                for (int j = 0; j < kT / 4; ++j) {
                     const float4 f = first4[j];
                     o1[4 * j] *= p.scale * f.x, o1[4 * j + 1] *= p.scale * f.y;
                     o1[4 * j + 2] *= p.scale * f.z, o1[4 * j + 3] *= p.scale * f.w;
@@ -506,7 +508,7 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
             read(x, kD0 + t0);
             if (kept) {
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
+                for (int j = 0; j < kT / 2; ++j) {
                     uint32_t hi, lo;
                     split2(x[2 * j], x[2 * j + 1], hi, lo);
                     char *a = sm + Space::keep + tile_at(uint32_t(t0 + 2 * j), uint32_t(dv), kChunk);
@@ -517,17 +519,17 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
                 }
             }
             if constexpr (!kBack) {
-                uint32_t hi[16], lo[16];
+                uint32_t hi[kT / 2], lo[kT / 2];
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
+                for (int j = 0; j < kT / 2; ++j) {
                     if constexpr (kP == 2) split2(x[2 * j], x[2 * j + 1], hi[j], lo[j]);
                     else hi[j] = round2(x[2 * j], x[2 * j + 1]);
                 }
-                tmem_store<16>(mine + kU + half * 16, hi);
-                if constexpr (kP == 2) tmem_store<16>(mine + kU + 32 + half * 16, lo);
+                tmem_store<kT / 2>(mine + kU + part * (kT / 2), hi);
+                if constexpr (kP == 2) tmem_store<kT / 2>(mine + kU + 32 + part * (kT / 2), lo);
             }
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
+            for (int j = 0; j < kT / 4; ++j) {
                 float4 f = kBack ? beta4[j] : rest4[j];
                 if constexpr (kBack) {
                     const float4 e = first4[j];
@@ -549,10 +551,10 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
             }
             wait_done(3, step);
 #pragma unroll
-            for (int k = 0; k < kH; k += 32) {
+            for (int k = 0; k < kH; k += kT) {
                 read(x, kDS + k0 + k);
 #pragma unroll
-                for (int j = 0; j < 32; ++j) S[k + j] = fmaf(whole, S[k + j], x[j]);
+                for (int j = 0; j < kT; ++j) S[k + j] = fmaf(whole, S[k + j], x[j]);
             }
             if (step + 1 < chunks) {
                 if (kept) meet();
