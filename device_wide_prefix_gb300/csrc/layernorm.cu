@@ -5,70 +5,99 @@
 //   h = (v - mean) r,  r = 1 / sqrt(mean((v - mean)^2) + eps),  y = h weight + bias
 //
 // A team of threads holds one row's group in registers, so each input is read
-// once: up to a warp's threads where the group fits them, a block above.  Mean
-// and squares come from one reduction: each thread has the mean and the sum of
-// squares about it of its own values, and two such pairs join as
-//   d = mean_b - mean_a,  M2 = M2_a + M2_b + d^2 n_a n_b / n,
-// which loses nothing where the mean is far from zero.
+// once: up to a warp's threads where the group fits them, a block above.  Sums
+// are taken about means: a warp finds its mean, then its squares about it, and
+// warps join by
+//   M2 = sum M2_w + n_w (mean_w - mean)^2,
+// so a mean far from zero costs nothing, and a block meets once a row.
 #include "sequence.cuh"
 
 namespace dwp {
 
 namespace {
 
-// Count, mean, squares about the mean; and for the gradient the mean of a
-// second value and the products of both about their means.
+// Mean and squares about it; and for the gradient the mean of a second value
+// and the products of both about their means.
 template <bool kTwo>
 struct Moments {
-    float n, mean, m2, mean_g, c;
+    float mean, m2, mean_g, c;
 };
 
-template <bool kTwo>
-__device__ __forceinline__ Moments<kTwo> join(const Moments<kTwo> &a, const Moments<kTwo> &b) {
-    Moments<kTwo> r;
-    r.n = a.n + b.n;
-    const float share = r.n > 0.0f ? __fdividef(b.n, r.n) : 0.0f, d = b.mean - a.mean, w = a.n * share;
-    r.mean = fmaf(d, share, a.mean);
-    r.m2 = fmaf(d * d, w, a.m2 + b.m2);
-    if constexpr (kTwo) {
-        const float e = b.mean_g - a.mean_g;
-        r.mean_g = fmaf(e, share, a.mean_g);
-        r.c = fmaf(d * e, w, a.c + b.c);
-    }
-    return r;
-}
-
-template <bool kTwo>
-__device__ __forceinline__ Moments<kTwo> shuffled(const Moments<kTwo> &a, int o) {
-    Moments<kTwo> r;
-    r.n = __shfl_xor_sync(0xffffffffu, a.n, o);
-    r.mean = __shfl_xor_sync(0xffffffffu, a.mean, o);
-    r.m2 = __shfl_xor_sync(0xffffffffu, a.m2, o);
-    if constexpr (kTwo) {
-        r.mean_g = __shfl_xor_sync(0xffffffffu, a.mean_g, o);
-        r.c = __shfl_xor_sync(0xffffffffu, a.c, o);
-    }
-    return r;
-}
-
-// The team's moments, in every thread of it.  sh: two sets of 32, used in turn.
-template <bool kTwo, bool kBlock>
-__device__ __forceinline__ Moments<kTwo> team_moments(Moments<kTwo> m, int team, Moments<kTwo> *sh, int turn) {
-    if constexpr (!kBlock) {
-        for (int o = team / 2; o > 0; o /= 2) m = join(m, shuffled(m, o));
-        return m;
-    } else {
+template <int N>
+__device__ __forceinline__ void team_sums(float (&v)[N], int team) {
+    for (int o = team / 2; o > 0; o /= 2)
 #pragma unroll
-        for (int o = 16; o > 0; o /= 2) m = join(m, shuffled(m, o));
+        for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+}
+
+// Elements of a group of n that a warp of a block has, K accesses of V a thread.
+template <int V, int K>
+__device__ __forceinline__ float warp_count(int64_t n, int warp) {
+    int64_t s = 0;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int64_t left = n - (int64_t(k) * blockDim.x + warp * 32) * V;
+        s += left < 0 ? 0 : left > 32 * V ? 32 * V : left;
+    }
+    return float(int(s));
+}
+
+// The team's moments of K accesses of V values, `in` telling which count, in
+// every thread.  n: the group's elements, mine: this warp's.  sh: two sets of
+// 32, used in turn.
+template <int V, int K, bool kTwo, bool kBlock>
+__device__ __forceinline__ Moments<kTwo> team_moments(const float (&v)[K][V], const float (*g)[V], const bool (&in)[K], int team,
+                                                      float n, float mine, Moments<kTwo> *sh, int turn) {
+    constexpr int N = kTwo ? 2 : 1;
+    float s[N] = {};
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+        if (in[k])
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                s[0] += v[k][j];
+                if constexpr (kTwo) s[1] += g[k][j];
+            }
+    team_sums(s, kBlock ? 32 : team);
+    const float inv = mine > 0.0f ? __fdividef(1.0f, mine) : 0.0f;
+    Moments<kTwo> m = {};
+    m.mean = s[0] * inv;
+    if constexpr (kTwo) m.mean_g = s[1] * inv;
+    float q[N] = {};
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+        if (in[k])
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const float d = v[k][j] - m.mean;
+                q[0] = fmaf(d, d, q[0]);
+                if constexpr (kTwo) q[1] = fmaf(d, g[k][j] - m.mean_g, q[1]);
+            }
+    team_sums(q, kBlock ? 32 : team);
+    m.m2 = q[0];
+    if constexpr (kTwo) m.c = q[1];
+    if constexpr (kBlock) {
         const int warps = blockDim.x / 32, lane = threadIdx.x % 32;
+        if (warps == 1) return m;
         Moments<kTwo> *set = sh + turn % 2 * 32;  // the other set may still be read
         if (lane == 0) set[threadIdx.x / 32] = m;
         __syncthreads();
-        m = lane < warps ? set[lane] : Moments<kTwo>{};
-#pragma unroll
-        for (int o = 16; o > 0; o /= 2) m = join(m, shuffled(m, o));
-        return m;
+        const Moments<kTwo> w = lane < warps ? set[lane] : Moments<kTwo>{};
+        const float count = lane < warps ? warp_count<V, K>(int64_t(n), lane) : 0.0f;
+        const float all = __fdividef(1.0f, n);
+        s[0] = w.mean * count;
+        if constexpr (kTwo) s[1] = w.mean_g * count;
+        team_sums(s, 32);
+        m.mean = s[0] * all;
+        if constexpr (kTwo) m.mean_g = s[1] * all;
+        const float d = (w.mean - m.mean) * count;
+        q[0] = fmaf(d, w.mean - m.mean, w.m2);
+        if constexpr (kTwo) q[1] = fmaf(d, w.mean_g - m.mean_g, w.c);
+        team_sums(q, 32);
+        m.m2 = q[0];
+        if constexpr (kTwo) m.c = q[1];
     }
+    return m;
 }
 
 template <class T, int V>
@@ -82,38 +111,8 @@ __device__ __forceinline__ void store_either(void *p, int64_t i, const float (&f
     else store_f32<V>(static_cast<T *>(p) + i, f);
 }
 
-// A thread's own moments of K accesses of V values, `in` telling which count.
-template <int V, int K, bool kTwo>
-__device__ __forceinline__ Moments<kTwo> own_moments(const float (&v)[K][V], const float (*g)[V], const bool (&in)[K]) {
-    Moments<kTwo> m = {};
-#pragma unroll
-    for (int k = 0; k < K; ++k)
-        if (in[k]) {
-            m.n += float(V);
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                m.mean += v[k][j];
-                if constexpr (kTwo) m.mean_g += g[k][j];
-            }
-        }
-    const float inv = m.n > 0.0f ? __fdividef(1.0f, m.n) : 0.0f;
-    m.mean *= inv;
-    if constexpr (kTwo) m.mean_g *= inv;
-#pragma unroll
-    for (int k = 0; k < K; ++k)
-        if (in[k]) {
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const float d = v[k][j] - m.mean;
-                m.m2 = fmaf(d, d, m.m2);
-                if constexpr (kTwo) m.c = fmaf(d, g[k][j] - m.mean_g, m.c);
-            }
-        }
-    return m;
-}
-
 template <class T, int V, int K, bool kBlock>
-__global__ void __launch_bounds__(kBlock ? 1024 : 256) layer_norm_kernel(LayerNormParams p) {
+__global__ void __launch_bounds__(kBlock ? 1024 : 256, kBlock ? 1 : 4) layer_norm_kernel(LayerNormParams p) {
     __shared__ Moments<false> sh[kBlock ? 64 : 1];
     pdl_trigger();
     pdl_wait();
@@ -142,8 +141,9 @@ __global__ void __launch_bounds__(kBlock ? 1024 : 256) layer_norm_kernel(LayerNo
                 for (int j = 0; j < V; ++j) v[k][j] += more[k][j];
                 store_either<T, V>(p.sum, row * p.sum_row + g0 + (int64_t(k) * team + t) * V, v[k], p.residual_f32);
             }
-    const Moments<false> m = team_moments<false, kBlock>(own_moments<V, K, false>(v, nullptr, in), team, sh, 0);
-    const float r = rsqrtf(m.m2 / float(p.group) + p.eps);
+    const float n = float(int(p.group)), mine = kBlock ? warp_count<V, K>(p.group, threadIdx.x / 32) : n;
+    const Moments<false> m = team_moments<V, K, false, kBlock>(v, nullptr, in, team, n, mine, sh, 0);
+    const float r = rsqrtf(m.m2 / n + p.eps);
 #pragma unroll
     for (int k = 0; k < K; ++k)
         if (in[k]) {
@@ -164,22 +164,31 @@ __global__ void __launch_bounds__(kBlock ? 1024 : 256) layer_norm_kernel(LayerNo
 // Gradient, with gw = dy weight:
 //   dv = r (gw - mean(gw) - h mean(gw h)),  dweight = sum_rows dy h,  dbias = sum_rows dy
 // The products of gw and v about their means come with the same reduction.  A
-// block keeps one group's columns and its teams walk the rows, so the column
-// sums stay with the thread; the teams of a block add theirs in order, each
-// block writes its share, and a second kernel adds the shares in order.
-template <class T, int V, int K, bool kBlock, bool kWideV>
-__global__ void __launch_bounds__(kBlock ? 512 : 256) layer_norm_backward_kernel(LayerNormBackwardParams q) {
+// block keeps one group's columns and its teams walk the rows, the next row's
+// values on their way while this one's sums are found, so the column sums stay
+// with the thread (of 4 accesses a thread and more: in shared memory, and
+// nothing is read ahead); the teams of a block add theirs in order, each block
+// writes its share, and a second kernel adds the shares in order.
+template <class T, class TV, int V, int K>
+struct LayerNormRow {
+    Pack<TV, V> v[K];
+    Pack<T, V> dy[K];
+};
+
+template <class T, int V, int K, int kMost, bool kBlock, bool kWideV>
+__global__ void __launch_bounds__(kMost, 512 / kMost) layer_norm_backward_kernel(LayerNormBackwardParams q) {
     __shared__ Moments<true> sh[kBlock ? 64 : 1];
-    extern __shared__ float sums[];  // K > 1: [2][K * V][threads]; else the teams' sums at the end
+    extern __shared__ float sums[];  // kShared: [2][K * V][threads]; else the teams' sums at the end
     pdl_trigger();
     pdl_wait();
     const LayerNormParams &p = q.n;
-    constexpr bool kShared = K > 1;  // column sums in shared memory, each word one thread's own
+    constexpr bool kShared = K > 2;  // column sums in shared memory, each word one thread's own
     using TV = typename std::conditional<kWideV, float, T>::type;
     const int threads = blockDim.x, tid = threadIdx.x, team = kBlock ? threads : p.team, t = tid % team;
     const int teams = threads / team;
     const int64_t g0 = int64_t(blockIdx.y) * p.group;
-    float dw[kShared ? 1 : V], db[kShared ? 1 : V];
+    const float n = float(int(p.group)), mine = kBlock ? warp_count<V, K>(p.group, tid / 32) : n;
+    float dw[kShared ? 1 : K][V], db[kShared ? 1 : K][V];
     auto slot = [&](int which, int k, int j) -> float & { return sums[((which * K + k) * V + j) * threads + tid]; };
     int at[K];
     bool own[K];
@@ -190,47 +199,67 @@ __global__ void __launch_bounds__(kBlock ? 512 : 256) layer_norm_backward_kernel
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             if constexpr (kShared) slot(0, k, j) = slot(1, k, j) = 0.0f;
-            else dw[j] = db[j] = 0.0f;
+            else dw[k][j] = db[k][j] = 0.0f;
         }
     }
+    auto load = [&](LayerNormRow<T, TV, V, K> &r, int64_t row) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            r.v[k] = *reinterpret_cast<const Pack<TV, V> *>(static_cast<const TV *>(q.v) + row * q.v_row + at[k]);
+            r.dy[k] = *reinterpret_cast<const Pack<T, V> *>(static_cast<const T *>(q.grad_out) + row * q.grad_row + at[k]);
+        }
+    };
     const int64_t stride = int64_t(gridDim.x) * teams;
     int turn = 0;
+    LayerNormRow<T, TV, V, K> now, next;
+    const int64_t mine0 = int64_t(blockIdx.x) * teams + tid / team;
+    if (!kShared) load(next, min(mine0, p.rows - 1));
     // whole blocks go round together: the moments' shuffles take every lane
     for (int64_t r0 = int64_t(blockIdx.x) * teams; r0 < p.rows; r0 += stride, ++turn) {
         const int64_t row = r0 + tid / team;
         const bool live = row < p.rows;
-        float v[K][V], dy[K][V], gw[K][V];
+        if constexpr (kShared) {
+            load(now, min(row, p.rows - 1));
+        } else {
+            now = next;
+            load(next, min(row + stride, p.rows - 1));
+        }
+        Pack<TV, V> add[K];
+        if (q.grad_sum)
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+                add[k] = *reinterpret_cast<const Pack<TV, V> *>(static_cast<const TV *>(q.grad_sum) +
+                                                                min(row, p.rows - 1) * q.gsum_row + at[k]);
+        float v[K][V], gw[K][V];
         bool in[K];
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             in[k] = own[k] && live;
-            if (in[k]) {
-                load_f32<V>(v[k], static_cast<const TV *>(q.v) + row * q.v_row + at[k]);
-                load_f32<V>(dy[k], static_cast<const T *>(q.grad_out) + row * q.grad_row + at[k]);
-                if (p.weight) load_params<T, V>(gw[k], p.weight, at[k], p.weight_f32);
+            float w[V];
+            if (p.weight) load_params<T, V>(w, p.weight, at[k], p.weight_f32);
 #pragma unroll
-                for (int j = 0; j < V; ++j) gw[k][j] = p.weight ? gw[k][j] * dy[k][j] : dy[k][j];
+            for (int j = 0; j < V; ++j) {
+                v[k][j] = to_f32<TV>(now.v[k].e[j]);
+                gw[k][j] = p.weight ? w[j] * to_f32<T>(now.dy[k].e[j]) : to_f32<T>(now.dy[k].e[j]);
             }
         }
-        const Moments<true> m = team_moments<true, kBlock>(own_moments<V, K, true>(v, gw, in), team, sh, turn);
-        const float inv = 1.0f / float(p.group), r = rsqrtf(m.m2 * inv + p.eps), c = m.c * inv * r * r;
+        const Moments<true> m = team_moments<V, K, true, kBlock>(v, gw, in, team, n, mine, sh, turn);
+        const float inv = __fdividef(1.0f, n), r = rsqrtf(m.m2 * inv + p.eps), c = m.c * inv * r * r;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             if (!in[k]) continue;
-            float add[V];
-            if (q.grad_sum) load_f32<V>(add, static_cast<const TV *>(q.grad_sum) + row * q.gsum_row + at[k]);
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                const float d = v[k][j] - m.mean;
+                const float d = v[k][j] - m.mean, dy = to_f32<T>(now.dy[k].e[j]);
                 if constexpr (kShared) {
-                    slot(0, k, j) = fmaf(dy[k][j] * d, r, slot(0, k, j));
-                    slot(1, k, j) += dy[k][j];
+                    slot(0, k, j) = fmaf(dy * d, r, slot(0, k, j));
+                    slot(1, k, j) += dy;
                 } else {
-                    dw[j] = fmaf(dy[k][j] * d, r, dw[j]);
-                    db[j] += dy[k][j];
+                    dw[k][j] = fmaf(dy * d, r, dw[k][j]);
+                    db[k][j] += dy;
                 }
                 gw[k][j] = r * (gw[k][j] - m.mean_g - d * c);
-                if (q.grad_sum) gw[k][j] += add[j];
+                if (q.grad_sum) gw[k][j] += to_f32<TV>(add[k].e[j]);
             }
             if (q.grad_residual)
                 store_f32<V>(static_cast<TV *>(q.grad_residual) + row * q.gres_row + at[k], gw[k]);
@@ -241,7 +270,9 @@ __global__ void __launch_bounds__(kBlock ? 512 : 256) layer_norm_backward_kernel
     if constexpr (!kShared) {
         __syncthreads();
 #pragma unroll
-        for (int j = 0; j < V; ++j) slot(0, 0, j) = dw[j], slot(1, 0, j) = db[j];
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int j = 0; j < V; ++j) slot(0, k, j) = dw[k][j], slot(1, k, j) = db[k][j];
     }
     __syncthreads();
     if (tid >= team) return;
@@ -262,24 +293,33 @@ __global__ void __launch_bounds__(kBlock ? 512 : 256) layer_norm_backward_kernel
     }
 }
 
-// How a group is spread: accesses a thread, and threads of a team.
+// How a group is spread: accesses a thread, and threads of a team (a block, or
+// up to a warp of it).
 struct Spread {
     int k, team;
     bool block;
 };
-Spread spread(int64_t group, int v, int most_threads) {
+Spread few(int64_t pieces) {
+    int team = 1;
+    while (team < pieces && team < 32) team *= 2;
+    return {pieces <= 32 ? 1 : 2, team, false};
+}
+Spread spread(int64_t group, int v) {
     const int64_t pieces = (group + v - 1) / v;
-    if (pieces <= 32) {
-        int team = 1;
-        while (team < pieces) team *= 2;
-        return {1, team, false};
-    }
-    if (pieces <= 64) return {2, 32, false};
-    for (int k : {1, 2, 4, 8, 16}) {
+    if (pieces <= 64) return few(pieces);
+    for (int k : {1, 2, 4, 16}) {
         const int64_t threads = (pieces + k - 1) / k;
-        if (threads <= most_threads) return {k, int((threads + 31) / 32 * 32), true};
+        if (threads <= 1024) return {k, int((threads + 31) / 32 * 32), true};
     }
-    return {32, most_threads, true};
+    return {16, 1024, true};
+}
+// The gradient has more to hold: 256 threads up to 4 accesses each, so that two
+// blocks share an SM, and 512 above.
+Spread spread_backward(int64_t group, int v) {
+    const int64_t pieces = (group + v - 1) / v;
+    if (pieces <= 64) return few(pieces);
+    int k = pieces <= 256 ? 1 : pieces <= 512 ? 2 : pieces <= 2048 ? 4 : pieces <= 4096 ? 8 : 32;
+    return {k, int(((pieces + k - 1) / k + 31) / 32 * 32), true};
 }
 
 constexpr int kTeamThreads = 256;
@@ -296,7 +336,7 @@ cudaError_t forward_k(const LayerNormParams &p, cudaStream_t s) {
 
 template <class T, int V>
 cudaError_t forward_v(LayerNormParams p, cudaStream_t s) {
-    const Spread a = spread(p.group, V, 1024);
+    const Spread a = spread(p.group, V);
     p.team = a.team;
     if (!a.block) return a.k == 1 ? forward_k<T, V, 1, false>(p, s) : forward_k<T, V, 2, false>(p, s);
     switch (a.k) {
@@ -307,28 +347,29 @@ cudaError_t forward_v(LayerNormParams p, cudaStream_t s) {
     }
 }
 
-template <class T, int V, int K, bool kBlock, bool kWideV>
+template <class T, int V, int K, int kMost, bool kBlock, bool kWideV>
 cudaError_t backward_k(const LayerNormBackwardParams &q, cudaStream_t s) {
-    const auto kernel = layer_norm_backward_kernel<T, V, K, kBlock, kWideV>;
+    const auto kernel = layer_norm_backward_kernel<T, V, K, kMost, kBlock, kWideV>;
     const int threads = kBlock ? q.n.team : kTeamThreads;
     const size_t smem = size_t(2) * K * V * threads * sizeof(float);
-    if (smem > 48u * 1024 && device_blocks(reinterpret_cast<const void *>(kernel), 512, kSumBytes) == 0)
+    if (smem > 48u * 1024 && device_blocks(reinterpret_cast<const void *>(kernel), kMost, kSumBytes) == 0)
         return cudaErrorInvalidConfiguration;
     return launch_pdl(kernel, dim3(uint32_t(q.blocks), uint32_t(q.n.groups)), dim3(threads), smem, s, q);
 }
 
 template <class T, int V, bool kWideV>
 cudaError_t backward_v(LayerNormBackwardParams q, cudaStream_t s) {
-    const Spread a = spread(q.n.group, V, 512);
+    const Spread a = spread_backward(q.n.group, V);
     q.n.team = a.team;
-    if (!a.block) return a.k == 1 ? backward_k<T, V, 1, false, kWideV>(q, s) : backward_k<T, V, 2, false, kWideV>(q, s);
-    switch (a.k) {
-        case 1: return backward_k<T, V, 1, true, kWideV>(q, s);
-        case 2: return backward_k<T, V, 2, true, kWideV>(q, s);
-        case 4: return backward_k<T, V, 4, true, kWideV>(q, s);
-        case 8: return backward_k<T, V, 8, true, kWideV>(q, s);
-        default: return backward_k<T, V, 32, true, kWideV>(q, s);
-    }
+    if (!a.block) return a.k == 1 ? backward_k<T, V, 1, 256, false, kWideV>(q, s) : backward_k<T, V, 2, 256, false, kWideV>(q, s);
+    if (a.k == 1) return backward_k<T, V, 1, 256, true, kWideV>(q, s);
+    if (a.k == 2) return backward_k<T, V, 2, 256, true, kWideV>(q, s);
+    if (a.k == 4) return a.team <= 256 ? backward_k<T, V, 4, 256, true, kWideV>(q, s) : backward_k<T, V, 4, 512, true, kWideV>(q, s);
+    // groups of at most 16384: 16-bit types, 8 an access, end here
+    if constexpr (V <= 4)
+        if (a.k == 8) return backward_k<T, V, 8, 512, true, kWideV>(q, s);
+    if constexpr (V == 1) return backward_k<T, V, 32, 512, true, kWideV>(q, s);
+    return cudaErrorInvalidConfiguration;
 }
 
 template <class T, int V>
@@ -341,7 +382,7 @@ cudaError_t backward_t(const LayerNormBackwardParams &q, cudaStream_t s) {
 }  // namespace
 
 int64_t layer_norm_teams(dwp_dtype t, int64_t group, bool vec) {
-    const Spread a = spread(group, !vec ? 1 : t == DWP_F32 ? 4 : 8, 512);
+    const Spread a = spread_backward(group, !vec ? 1 : t == DWP_F32 ? 4 : 8);
     return a.block ? 1 : kTeamThreads / a.team;
 }
 
