@@ -41,7 +41,7 @@ constexpr int kChainRegisters = 104, kHelpRegisters = 64;
 constexpr int kMostValues = 128;
 
 // Shared memory: the chunks' inputs, the outputs on their way, and what is kept.
-template <class T, int KD, bool kBack>
+template <class T, int KD, bool kBack, bool kMaps>
 struct ChainSpace {
     static constexpr int kP = kPieces<T>;
     static constexpr uint32_t kTileBytes = kChunk * kTileRow;  // of 64 x 64
@@ -50,7 +50,7 @@ struct ChainSpace {
     static constexpr uint32_t k = 0, q = k + kP * kKeys, v = q + kP * kKeys;
     static constexpr uint32_t inverse = v + (kBack ? kP * kValues : kChunk * kMostValues * uint32_t(sizeof(T)));
     static constexpr uint32_t weights = inverse + 2 * kTileBytes, bytes = weights + kWeightPieces * kTileBytes;
-    static constexpr int kStages = kP == 1 ? 2 : 1;
+    static constexpr int kStages = kMaps ? 2 : 1;
     static constexpr uint32_t out = kStages * bytes, kOut = kBack ? 0 : kChunk * kMostValues * uint32_t(sizeof(T));
     static constexpr uint32_t keep = out + kOut, kKeep = 2 * kMostValues * KD * 2;
     static_assert(kKeep >= 2 * kValues, "the corrections fit the kept state's place");
@@ -70,9 +70,8 @@ struct ChainMaps {
 template <class T, int KD, bool kBack, bool kMaps>
 __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
     delta_chain_kernel(DeltaBackwardParams bp, const __grid_constant__ ChainMaps maps) {
-    using Space = ChainSpace<T, KD, kBack>;
+    using Space = ChainSpace<T, KD, kBack, kMaps>;
     constexpr int kP = Space::kP, kH = KD / kParts, kStages = Space::kStages;  // kH: keys of a thread
-    constexpr int kLoadThreads = kMaps ? 32 : 96;
     extern __shared__ char raw[];
     __shared__ ChainRows rows_of[2];
     __shared__ uint64_t done[5], ready[3], full[2], empty[2], landed;
@@ -97,8 +96,9 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
         for (int i = 0; i < 5; ++i) mbar_init(&done[i], 1);
         // one arrival a warp: 256 on one word take a thousand cycles
         for (int i = 0; i < 3; ++i) mbar_init(&ready[i], kChainThreads / 32);
-        // the loaders, the bytes, the decays
-        for (int i = 0; i < 2; ++i) mbar_init(&full[i], kLoadThreads / 32 + 2), mbar_init(&empty[i], 1);
+        // the planes and boxes, the decays, and, without maps, the chain's own loads
+        for (int i = 0; i < 2; ++i)
+            mbar_init(&full[i], kMaps ? 3 : 2 + kChainThreads / 32), mbar_init(&empty[i], 1);
         mbar_init(&landed, 1);
         fence_mbar_init();
     }
@@ -186,8 +186,7 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
             __syncwarp();
         }
     } else if (warp > kIssueWarp) {
-        const int t = tid - kChainThreads - 32;  // of the loaders
-        const bool loads = t < kLoadThreads, decays = warp == kIssueWarp + 2;
+        const bool loads = warp == kIssueWarp + 1, decays = warp == kIssueWarp + 2;
         auto load = [&](int64_t step) {
             const int st = stage_of(step);
             const int64_t c = chunk_of(step), row = row0 + c * kChunk, at = (slot0 + c) * p.heads + head;
@@ -196,7 +195,7 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
             if (step >= kStages) wait(empty[st], round_of(step) + 1u);
             constexpr uint32_t planes = (2 + Space::kWeightPieces) * Space::kTileBytes;
             constexpr uint32_t boxes = 2 * Space::kKeys + Space::kValues;
-            if (t == 0) {
+            if (lane == 0) {
                 mbar_arrive_expect_tx(&full[st], planes + (kMaps && n == kChunk ? boxes : 0u));
                 bulk_load(s + Space::inverse, p.inverse + at * kChunk * kChunk, 2 * Space::kTileBytes, &full[st]);
                 bulk_load(s + Space::weights, p.weights + at * kChunk * kChunk, Space::kWeightPieces * Space::kTileBytes,
@@ -233,32 +232,9 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
                     else clear(s + Space::v, 256);
                     fence_proxy_async_smem();
                 }
-            } else {
-                load_tile<T, false, kChunk, KD, kLoadThreads>(t, s + Space::k, Space::kKeys, 0, p.k, batch, row, kh, n, keys, p.wide);
-                load_tile<T, false, kChunk, KD, kLoadThreads>(t, s + Space::q, Space::kKeys, 0, p.q, batch, row, kh, n, keys, p.wide);
-                if constexpr (kBack) {
-                    load_tile<T, false, kChunk, kMostValues, kLoadThreads>(t, s + Space::v, Space::kValues, 0, bp.grad_out, batch,
-                                                                           row, head, n, values, p.wide);
-                } else {
-                    const T *src = delta_at<T>(p.v, batch, row, head);
-                    constexpr int kEach = 16 / int(sizeof(T)), kRow = kMostValues / kEach;
-#pragma unroll 4
-                    for (int e = t; e < kChunk * kRow; e += kLoadThreads) {
-                        const int i = e / kRow, j = e % kRow * kEach, left = i < n ? values - j : 0;
-                        T *to = reinterpret_cast<T *>(s + Space::v) + i * kMostValues + j;
-                        if (p.wide) {
-                            copy16(smem_addr(to), left > 0 ? src + i * p.v.row + j : src, left > 0 ? 16u : 0u);
-                        } else {
-#pragma unroll
-                            for (int l = 0; l < kEach; ++l) to[l] = l < left ? src[i * p.v.row + j + l] : from_f32<T>(0.0f);
-                        }
-                    }
-                }
-                copies_done();
-                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&full[st]);
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&full[st]);
         };
         float g[2], b[2];
         auto read_decays = [&](int64_t step) {
@@ -374,6 +350,36 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
                         to[i * p.out.row + j] = from[i * kMostValues + j];
             }
         };
+        // Rows that no map brings (in two pieces of bf16, or off 16 bytes): by all
+        // threads, between chunks, into the one stage.
+        auto load_rows = [&](int64_t step) {
+            const int64_t c = chunk_of(step), row = row0 + c * kChunk;
+            const int n = rows_in(c);
+            load_tile<T, false, kChunk, KD, kChainThreads>(tid, sm + Space::k, Space::kKeys, 0, p.k, batch, row, kh, n, keys, p.wide);
+            load_tile<T, false, kChunk, KD, kChainThreads>(tid, sm + Space::q, Space::kKeys, 0, p.q, batch, row, kh, n, keys, p.wide);
+            if constexpr (kBack) {
+                load_tile<T, false, kChunk, kMostValues, kChainThreads>(tid, sm + Space::v, Space::kValues, 0, bp.grad_out, batch,
+                                                                        row, head, n, values, p.wide);
+            } else {
+                const T *src = delta_at<T>(p.v, batch, row, head);
+                constexpr int kEach = 16 / int(sizeof(T)), kRow = kMostValues / kEach;
+#pragma unroll 4
+                for (int e = tid; e < kChunk * kRow; e += kChainThreads) {
+                    const int i = e / kRow, j = e % kRow * kEach, left = i < n ? values - j : 0;
+                    T *to = reinterpret_cast<T *>(sm + Space::v) + i * kMostValues + j;
+                    if (p.wide) {
+                        copy16(smem_addr(to), left > 0 ? src + i * p.v.row + j : src, left > 0 ? 16u : 0u);
+                    } else {
+#pragma unroll
+                        for (int l = 0; l < kEach; ++l) to[l] = l < left ? src[i * p.v.row + j + l] : from_f32<T>(0.0f);
+                    }
+                }
+            }
+            copies_done();
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&full[0]);
+        };
         // the state as the next products' operand, and as kept
         auto put_state = [&] {
 #pragma unroll
@@ -435,6 +441,7 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
         };
         if (chunks > 0) {
             put_state();
+            if constexpr (!kMaps) load_rows(0);
             if constexpr (kBack) prepare_side(0);
         }
         for (int64_t step = 0; step < chunks; ++step) {
@@ -559,7 +566,11 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
             if (step + 1 < chunks) {
                 if (kept) meet();
                 put_state();
-                if (kBack && kStages == 1) prepare_side(step + 1);
+                if constexpr (!kMaps) {
+                    wait(empty[0], uint32_t(step));
+                    load_rows(step + 1);
+                    if constexpr (kBack) prepare_side(step + 1);
+                }
             }
         }
         if constexpr (!kBack)
@@ -588,7 +599,7 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
 template <class T, int KD, bool kBack, bool kMaps>
 cudaError_t chain_k(const DeltaBackwardParams &p, const ChainMaps &maps, cudaStream_t s) {
     const auto kernel = delta_chain_kernel<T, KD, kBack, kMaps>;
-    constexpr size_t bytes = ChainSpace<T, KD, kBack>::kAll;
+    constexpr size_t bytes = ChainSpace<T, KD, kBack, kMaps>::kAll;
     constexpr int threads = kChainThreads + kHelpThreads;
     if (device_blocks(reinterpret_cast<const void *>(kernel), threads, bytes) == 0) return cudaErrorInvalidConfiguration;
     return launch_pdl(kernel, dim3(uint32_t(p.f.sequences), uint32_t(p.f.heads)), dim3(threads), bytes, s, p, maps);
