@@ -321,7 +321,9 @@ dwp_status dwp_linear_recurrence_f32(const float *d_a, const float *d_b, float *
  * DWP_ERR_INVALID_VALUE for a NULL required pointer, a size, stride or type out
  * of range, or a stride below the row it spans.
  *
- * No wait on the device: these calls keep no status word.  Results are
+ * These calls keep no status word: no kernel of theirs waits for another, and
+ * only the gated delta rule's wait for copies and products of their own, each
+ * wait bounded; should one run out, what the block writes is NaN.  Results are
  * deterministic, bit for bit from run to run.  Scratch follows the two-call
  * pattern above, 16-byte aligned and never less than 16 bytes; its contents on
  * entry do not matter.
@@ -500,6 +502,12 @@ dwp_status dwp_selective_scan_step(const dwp_selective_scan_step_args *args, dwp
  *                  DWP_DELTA_CHUNK + num_segments
  *   scratch        without checkpoints 8 * DWP_DELTA_CHUNK^2 bytes for each
  *                  of those chunks and head
+ * A sequence is taken in chunks of DWP_DELTA_CHUNK rows from its first.  A
+ * value that is not finite reaches its own sequence and head only, there also
+ * the rows before it in its chunk.  Products of two f32 numbers (states,
+ * corrections, f32 rows) take each in two pieces of bf16, 16 bits together;
+ * the last products of a bf16 output take weights, corrections and states in
+ * one.
  */
 #define DWP_DELTA_CHUNK 64
 typedef struct dwp_heads {
