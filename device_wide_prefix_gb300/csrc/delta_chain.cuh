@@ -13,9 +13,10 @@
 // value's row and a quarter of the keys), goes to tensor memory as the first operand
 // of the next products, as R and U do, and K, Q, T, A and dO are operands in
 // shared memory as they are stored.  What is not itself bf16 is two bf16
-// (split2), and of a product of two such the three larger parts are taken.
-// For bf16 outputs the weights, corrections and state of the last products
-// are one bf16 each: they cost at most 2^-8 of the output's terms.
+// (split2): 16 bits, 2^-18 of a number at most is lost; of two such all four
+// products are taken, but for bf16 rows the smallest.  The weights of a bf16
+// output are one bf16 each (two more tiles would not fit): they cost at most
+// 2^-9 of the output's terms.
 //
 // Sixteen warps do this (with eight, twice the registers and rows each, a chunk
 // took 1.2 times as long); of four more one issues the products (a warp that issues
@@ -130,20 +131,27 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
                 const Operand<kChunk, false> K(s + Space::k), Kl(s + Space::k + Space::kKeys);
                 product_ts<kChunk, KD>(tm + kD0, tm + kS, K, false);
                 product_ts<kChunk, KD>(tm + kD0, tm + kS + KD / 2, K, true);
-                if constexpr (kP == 2) product_ts<kChunk, KD>(tm + kD0, tm + kS, Kl, true);
+                if constexpr (kP == 2) {
+                    product_ts<kChunk, KD>(tm + kD0, tm + kS, Kl, true);
+                    product_ts<kChunk, KD>(tm + kD0, tm + kS + KD / 2, Kl, true);
+                }
                 mma_commit(&done[0]);
                 if constexpr (kBack) {
                     const Operand<kChunk, true> dO(s + Space::v), dOl(s + Space::v + Space::kValues), A(s + Space::weights),
                         Al(s + Space::weights + Space::kTileBytes);
                     product_ss<kChunk, kChunk>(tm + kD1, dO, A, false);
                     product_ss<kChunk, kChunk>(tm + kD1, dO, Al, true);
-                    if constexpr (kP == 2) product_ss<kChunk, kChunk>(tm + kD1, dOl, A, true);
+                    if constexpr (kP == 2) {
+                        product_ss<kChunk, kChunk>(tm + kD1, dOl, A, true);
+                        product_ss<kChunk, kChunk>(tm + kD1, dOl, Al, true);
+                    }
                 } else {
                     const Operand<kChunk, false> Q(s + Space::q), Ql(s + Space::q + Space::kKeys);
                     product_ts<kChunk, KD>(tm + kDS, tm + kS, Q, false);
+                    product_ts<kChunk, KD>(tm + kDS, tm + kS + KD / 2, Q, true);
                     if constexpr (kP == 2) {
-                        product_ts<kChunk, KD>(tm + kDS, tm + kS + KD / 2, Q, true);
                         product_ts<kChunk, KD>(tm + kDS, tm + kS, Ql, true);
+                        product_ts<kChunk, KD>(tm + kDS, tm + kS + KD / 2, Ql, true);
                     }
                 }
                 mma_commit(&done[1]);
@@ -156,6 +164,7 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
                 product_ts<kChunk, kChunk>(tm + kD0, tm + kR, inv, false);
                 product_ts<kChunk, kChunk>(tm + kD0, tm + kR + 32, inv, true);
                 product_ts<kChunk, kChunk>(tm + kD0, tm + kR, invl, true);
+                if constexpr (kP == 2) product_ts<kChunk, kChunk>(tm + kD0, tm + kR + 32, invl, true);
                 mma_commit(&done[2]);
             }
             __syncwarp();
@@ -164,20 +173,27 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
             if (one) {
                 product_ts<KD, kChunk>(tm + kDS, tm + kR, Ko, false);
                 product_ts<KD, kChunk>(tm + kDS, tm + kR + 32, Ko, true);
-                if constexpr (kP == 2) product_ts<KD, kChunk>(tm + kDS, tm + kR, Klo, true);
+                if constexpr (kP == 2) {
+                    product_ts<KD, kChunk>(tm + kDS, tm + kR, Klo, true);
+                    product_ts<KD, kChunk>(tm + kDS, tm + kR + 32, Klo, true);
+                }
                 if constexpr (kBack) {
                     const Operand<kChunk, true> Q(s + Space::q), Ql(s + Space::q + Space::kKeys);
                     product_ts<KD, kChunk>(tm + kDS, tm + kU, Q, true);
                     product_ts<KD, kChunk>(tm + kDS, tm + kU + 32, Q, true);
-                    if constexpr (kP == 2) product_ts<KD, kChunk>(tm + kDS, tm + kU, Ql, true);
+                    if constexpr (kP == 2) {
+                        product_ts<KD, kChunk>(tm + kDS, tm + kU, Ql, true);
+                        product_ts<KD, kChunk>(tm + kDS, tm + kU + 32, Ql, true);
+                    }
                 }
                 mma_commit(&done[3]);
                 if constexpr (!kBack) {
                     const Operand<kChunk, false> A(s + Space::weights), Al(s + Space::weights + Space::kTileBytes);
                     product_ts<kChunk, kChunk>(tm + kD1, tm + kU, A, false);
+                    product_ts<kChunk, kChunk>(tm + kD1, tm + kU + 32, A, true);
                     if constexpr (kP == 2) {
-                        product_ts<kChunk, kChunk>(tm + kD1, tm + kU + 32, A, true);
                         product_ts<kChunk, kChunk>(tm + kD1, tm + kU, Al, true);
+                        product_ts<kChunk, kChunk>(tm + kD1, tm + kU + 32, Al, true);
                     }
                     mma_commit(&done[4]);
                 }
@@ -525,16 +541,7 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
                     *reinterpret_cast<uint16_t *>(b + Space::kValues) = uint16_t(lo >> 16);
                 }
             }
-            if constexpr (!kBack) {
-                uint32_t hi[kT / 2], lo[kT / 2];
-#pragma unroll
-                for (int j = 0; j < kT / 2; ++j) {
-                    if constexpr (kP == 2) split2(x[2 * j], x[2 * j + 1], hi[j], lo[j]);
-                    else hi[j] = round2(x[2 * j], x[2 * j + 1]);
-                }
-                tmem_store<kT / 2>(mine + kU + part * (kT / 2), hi);
-                if constexpr (kP == 2) tmem_store<kT / 2>(mine + kU + 32 + part * (kT / 2), lo);
-            }
+            if constexpr (!kBack) put_rows(kU, x);
 #pragma unroll
             for (int j = 0; j < kT / 4; ++j) {
                 float4 f = kBack ? beta4[j] : rest4[j];

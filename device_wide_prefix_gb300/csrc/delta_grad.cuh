@@ -242,11 +242,13 @@ __global__ void __launch_bounds__(kGradThreads, 1)
             product_ss<kChunk, kMost>(tm + kDA, both, U, false);
             product_ss<kChunk, kMost>(tm + kDA, both, Ul, true);
             product_ss<kChunk, kMost>(tm + kDA, bothl, U, true);
+            if constexpr (kP == 2) product_ss<kChunk, kMost>(tm + kDA, bothl, Ul, true);
             mma_commit(&bars[0]);
             product_ss<2 * kChunk, kMost>(tm + kDX, S, both, false);
             product_ss<2 * kChunk, kMost>(tm + kDX, Sl, both, true);
             if constexpr (kP == 2) {
                 product_ss<2 * kChunk, kMost>(tm + kDX, S, bothl, true);
+                product_ss<2 * kChunk, kMost>(tm + kDX, Sl, bothl, true);
             } else {
                 const Operand<2 * kChunk, false> drl(sm + Space::stack + 2 * kRows + kTileBytes);
                 product_ss<kChunk, kMost>(tm + kDX + kChunk, S, drl, true);
@@ -355,13 +357,17 @@ __global__ void __launch_bounds__(kGradThreads, 1)
             if constexpr (kP == 2) {
                 const Operand<kChunk, true> Kl(sm + Space::k + kRows), Ql(sm + Space::q + kRows);
                 product_ss<2 * kChunk, kChunk>(tm + kDW, Kl, W, true);
+                product_ss<2 * kChunk, kChunk>(tm + kDW, Kl, Wl, true);
                 product_ss<kChunk, kChunk>(tm + kDY, Ql, A, true);
+                product_ss<kChunk, kChunk>(tm + kDY, Ql, Al, true);
                 product_ss<kChunk, kChunk>(tm + kDY, Kl, E, true);
+                product_ss<kChunk, kChunk>(tm + kDY, Kl, El, true);
             }
             mma_commit(&bars[2]);
             product_ss<kChunk, kMost>(tm + kDU, S, U, false);
             product_ss<kChunk, kMost>(tm + kDU, S, Ul, true);
             product_ss<kChunk, kMost>(tm + kDU, Sl, U, true);
+            if constexpr (kP == 2) product_ss<kChunk, kMost>(tm + kDU, Sl, Ul, true);
             mma_commit(&bars[4]);
         }
         float x[kCols], both_sums[2 * kCols];  // of q.dQ + beta k.Z - k.Y, and of k.Z

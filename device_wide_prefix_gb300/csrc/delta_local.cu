@@ -95,6 +95,7 @@ __global__ void __launch_bounds__(kTeam * kTeams, 4 / kTeams)
             if constexpr (kPieces<T> == 2) {
                 product_ss<kChunk, KD>(d, hi, lo, true);
                 product_ss<kChunk, KD>(d, lo, hi, true);
+                product_ss<kChunk, KD>(d, lo, lo, true);
             }
             mma_commit(&bar);
         }

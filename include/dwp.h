@@ -506,8 +506,7 @@ dwp_status dwp_selective_scan_step(const dwp_selective_scan_step_args *args, dwp
  * value that is not finite reaches its own sequence and head only, there also
  * the rows before it in its chunk.  Products of two f32 numbers (states,
  * corrections, f32 rows) take each in two pieces of bf16, 16 bits together;
- * the last products of a bf16 output take weights, corrections and states in
- * one.
+ * a bf16 output's own weights q.k are rounded to one.
  */
 #define DWP_DELTA_CHUNK 64
 typedef struct dwp_heads {

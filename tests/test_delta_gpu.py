@@ -7,11 +7,9 @@ and from an input to an output there are at most four such products one after
 another (the chunk's inverse, the corrections, the state, the read).  r(T) is
 half a unit of T and as much again for its neighbourhood.
 
-A bf16 output's last products take the weights, the corrections and the state
-rounded to one bf16: half a unit, 2^-9, of each.  The terms are q.S0 decayed
-(the state's rounding) and, for each row j of the chunk, weight_j u_j (both
-others'), and the size bounds |q||S0| + sum_j |q||k_j||u_j|, decayed.  So these
-roundings cost at most 2 * 2^-9 of the size.
+A bf16 output's weights are rounded to one bf16: half a unit, 2^-9, of each.
+The terms are weight_j u_j for each row j of the chunk, and the size bounds
+sum_j |q||k_j||u_j|, decayed.  So this rounding costs at most 2^-9 of the size.
 """
 import math
 
@@ -33,7 +31,7 @@ from test_sequence_gpu import SHAPES, IDS, SENTINEL, TYPES, covered, offs, spans
 HALF = {torch.float32: 2.0 ** -24, torch.bfloat16: 2.0 ** -9, torch.float16: 2.0 ** -12}
 TINY = {torch.float32: 1e-35, torch.bfloat16: 1e-35, torch.float16: 2.0 ** -24}
 E = 2.0 ** -14
-E_OUT = {torch.float32: E, torch.float16: E, torch.bfloat16: E + 2.0 ** -8}
+E_OUT = {torch.float32: E, torch.float16: E, torch.bfloat16: E + 2.0 ** -9}
 
 
 @pytest.fixture(scope="module", autouse=True)
