@@ -35,9 +35,31 @@ int64_t delta_slots(const dwp_delta_args &a) {
 // Words of a kept state, keys in whole tiles, and of a chunk's kept rows, values in whole tiles.
 int64_t delta_state(const dwp_delta_args &a) { return ceil_div(a.keys, 64) * 64 * a.values; }
 int64_t delta_kept_rows(const dwp_delta_args &a) { return DWP_DELTA_CHUNK * ceil_div(a.values, 64) * 64; }
-// Whether rows with these address and stride bits are whole 16-byte pieces.
+// Whether rows with these address and stride bits are whole 16-byte pieces, and
+// whether a tensor map holds their strides (under 2^40 bytes).
 bool delta_wide(uintptr_t bits, const dwp_delta_args &a) {
     return ((bits | uintptr_t((a.keys | a.values) * size_of(a.dtype))) & 15u) == 0;
+}
+bool delta_near(const dwp_heads &x) {
+    return x.batch_stride < (int64_t(1) << 39) && x.row_stride < (int64_t(1) << 39) && x.head_stride < (int64_t(1) << 39);
+}
+
+// Parts that a call's sequences are cut in, and the words that takes (of bf16;
+// wherever its rows lie, so that a size does not go by addresses).
+int64_t delta_parts_of(const dwp_delta_args &a, int64_t seqs) {
+    return a.offsets || a.dtype != DWP_BF16 ? 1 : delta_parts(seqs * a.heads, delta_chunks(a));
+}
+size_t delta_part_bytes(const dwp_delta_args &a, int64_t seqs) {
+    const int64_t parts = delta_parts_of(a, seqs);
+    return parts == 1 ? 0u : round16(size_t(seqs * parts * a.heads * (2 * a.keys * a.values + a.keys * a.keys)) * 4u);
+}
+void set_parts(DeltaParams &p, const dwp_delta_args &a, int64_t seqs, void *at) {
+    // only rows that come by maps are cut
+    p.parts = p.wide ? delta_parts_of(a, seqs) : 1, p.part_chunks = ceil_div(p.chunks, p.parts);
+    const int64_t places = seqs * p.parts * a.heads;
+    p.part_starts = static_cast<float *>(at);
+    p.part_ends = p.part_starts + places * a.keys * a.values;
+    p.part_maps = p.part_ends + places * a.keys * a.values;
 }
 
 int64_t check_delta(Check &c, const dwp_delta_args &a, bool backward, uintptr_t &out_bits) {
@@ -91,10 +113,12 @@ dwp_status delta_forward(const dwp_delta_args &a, void *scratch, size_t *bytes, 
     dwp_status st = c.status;
     if (st != DWP_SUCCESS) return st;
     const size_t need = a.checkpoints ? 0u : size_t(delta_slots(a) * a.heads * 2 * kTile) * 4u;
-    if (!c.scratch(scratch, bytes, need, &st)) return st;
+    if (!c.scratch(scratch, bytes, need + delta_part_bytes(a, seqs), &st)) return st;
     if (seqs == 0) return DWP_SUCCESS;
     DeltaParams p = delta_params(a, seqs, scratch);
-    p.wide = delta_wide(c.bits, a), p.out_wide = delta_wide(out_bits, a);
+    p.wide = delta_wide(c.bits, a) && delta_near(a.q) && delta_near(a.k) && delta_near(a.v);
+    p.out_wide = delta_wide(out_bits, a);
+    set_parts(p, a, seqs, static_cast<char *>(scratch) + need);
     const auto t = static_cast<dwp_dtype>(a.dtype);
     if (a.batch * a.rows > 0) {
         const cudaError_t err = launch_delta_local(t, p, s);
@@ -116,7 +140,7 @@ dwp_status delta_backward(const dwp_delta_backward_args &a, void *scratch, size_
     bool wide = false;
     if (n > 0) {
         c.heads(a.grad_out, f.dtype, f.batch, f.rows, f.heads, f.values, false);
-        wide = delta_wide(c.bits, f);
+        wide = delta_wide(c.bits, f) && delta_near(f.q) && delta_near(f.k) && delta_near(f.v) && delta_near(a.grad_out);
         c.dense(a.grad_q, f.dtype, n * f.key_heads * f.keys, true, false);
         c.dense(a.grad_k, f.dtype, n * f.key_heads * f.keys, true, false);
         c.dense(a.grad_v, f.dtype, n * f.heads * f.values, true, false);
@@ -129,7 +153,7 @@ dwp_status delta_backward(const dwp_delta_backward_args &a, void *scratch, size_
     const int64_t places = delta_slots(f) * f.heads;
     const size_t dr = size_t(places * delta_kept_rows(f)) * 4u;
     const size_t ends = round16(size_t(places * delta_state(f)) * 4u);
-    if (!c.scratch(scratch, bytes, dr + ends, &st)) return st;
+    if (!c.scratch(scratch, bytes, dr + ends + delta_part_bytes(f, seqs), &st)) return st;
     if (seqs == 0) return DWP_SUCCESS;
     DeltaBackwardParams p = {};
     p.f = delta_params(f, seqs, nullptr);
@@ -144,6 +168,7 @@ dwp_status delta_backward(const dwp_delta_backward_args &a, void *scratch, size_
     char *at = static_cast<char *>(scratch);
     p.dr = reinterpret_cast<float *>(at);
     p.ends = reinterpret_cast<float *>(at + dr);
+    set_parts(p.f, f, seqs, at + dr + ends);
     p.wide = aligned(a.grad_v, 16);
     const auto t = static_cast<dwp_dtype>(f.dtype);
     if (n > 0 || a.grad_initial_state) {

@@ -26,6 +26,13 @@
 // products: one of the four warps is slower at that (instructions that come in
 // between the chain's are fetched anew each time; 9,000 cycles a chunk), bulk
 // copies are slower still (256 bytes in 83 cycles, 64 KB in 5,000).
+//
+// Few sequences and heads leave most of the GPU idle while each walks its
+// chunks.  A state goes through a part of a sequence linearly, S -> M S + E, so
+// such sequences are cut in parts: pass 1 walks the first part and finds E (from
+// zeros) and M (from the unit matrix, without values) of those between at the
+// same time; their states are joined (delta_join_kernel); pass 2 walks the
+// others.  That is two parts' time for the whole sequence's.
 #pragma once
 
 #include "delta.cuh"
@@ -67,8 +74,10 @@ struct ChainMaps {
     CUtensorMap k, q, v;  // v: or grad_out
 };
 
-// kMaps: bf16 rows of whole 16-byte pieces, which come by tensor maps.
-template <class T, int KD, bool kBack, bool kMaps>
+// kMaps: bf16 rows of whole 16-byte pieces, which come by tensor maps.  kPass: 0,
+// or 1 and 2 over parts of sequences (what a block finds in pass 1, asked in
+// every chunk, makes a chunk 1.25 times as long).
+template <class T, int KD, bool kBack, bool kMaps, int kPass>
 __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
     delta_chain_kernel(DeltaBackwardParams bp, const __grid_constant__ ChainMaps maps) {
     using Space = ChainSpace<T, KD, kBack, kMaps>;
@@ -82,16 +91,24 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
     pdl_trigger();
     pdl_wait();
     const int tid = threadIdx.x, lane = tid % 32, warp = __shfl_sync(0xffffffffu, tid / 32, 0);
-    const int head = blockIdx.y, kh = head / (p.heads / p.key_heads), keys = p.keys, values = p.values;
+    const int head = blockIdx.y, kh = head / (p.heads / p.key_heads), keys = p.keys;
     const int64_t seq = blockIdx.x;
     int64_t batch, row0, rows, slot0;
     delta_sequence(p, seq, batch, row0, rows, slot0);
-    const int64_t chunks = (rows + kChunk - 1) / kChunk;
-    auto chunk_of = [&](int64_t step) { return kBack ? chunks - 1 - step : step; };
+    // this block's part of the walk, and what it finds: the whole (pass 0, or the
+    // part's own outputs), E or M
+    const int64_t all_chunks = (rows + kChunk - 1) / kChunk;
+    constexpr bool kCut = kPass != 0;
+    const int64_t part = kPass == 0 ? 0 : kPass == 1 ? (blockIdx.z + 1) / 2 : blockIdx.z + 1;
+    const bool unit = kPass == 1 && part > 0 && blockIdx.z % 2 == 0, whole_part = kPass != 1 || part == 0;
+    const int64_t first_step = kCut ? part * p.part_chunks : 0;
+    const int64_t chunks = !kCut ? all_chunks : max(min(p.part_chunks, all_chunks - first_step), int64_t(0));
+    const int values = unit ? keys : p.values;
+    auto chunk_of = [&](int64_t step) { return kBack ? all_chunks - 1 - first_step - step : first_step + step; };
     auto rows_in = [&](int64_t c) { return int(min(rows - c * kChunk, int64_t(kChunk))); };
     auto stage_of = [&](int64_t step) { return kStages == 2 ? int(step & 1) : 0; };
     auto round_of = [&](int64_t step) { return uint32_t(step / kStages) & 1u; };
-    float *const kept = kBack ? bp.ends : p.states, *const kept_rows = kBack ? bp.dr : p.u;
+    float *const kept = whole_part ? kBack ? bp.ends : p.states : nullptr, *const kept_rows = kBack ? bp.dr : p.u;
 
     if (tid == 0) {
         for (int i = 0; i < 5; ++i) mbar_init(&done[i], 1);
@@ -139,13 +156,15 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
                 if constexpr (kBack) {
                     const Operand<kChunk, true> dO(s + Space::v), dOl(s + Space::v + Space::kValues), A(s + Space::weights),
                         Al(s + Space::weights + Space::kTileBytes);
-                    product_ss<kChunk, kChunk>(tm + kD1, dO, A, false);
-                    product_ss<kChunk, kChunk>(tm + kD1, dO, Al, true);
+                    if (!unit) product_ss<kChunk, kChunk>(tm + kD1, dO, A, false);
+                    if (!unit) product_ss<kChunk, kChunk>(tm + kD1, dO, Al, true);
                     if constexpr (kP == 2) {
-                        product_ss<kChunk, kChunk>(tm + kD1, dOl, A, true);
-                        product_ss<kChunk, kChunk>(tm + kD1, dOl, Al, true);
+                        if (!unit) {
+                            product_ss<kChunk, kChunk>(tm + kD1, dOl, A, true);
+                            product_ss<kChunk, kChunk>(tm + kD1, dOl, Al, true);
+                        }
                     }
-                } else {
+                } else if (whole_part) {
                     const Operand<kChunk, false> Q(s + Space::q), Ql(s + Space::q + Space::kKeys);
                     product_ts<kChunk, KD>(tm + kDS, tm + kS, Q, false);
                     product_ts<kChunk, KD>(tm + kDS, tm + kS + KD / 2, Q, true);
@@ -177,7 +196,7 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
                     product_ts<KD, kChunk>(tm + kDS, tm + kR, Klo, true);
                     product_ts<KD, kChunk>(tm + kDS, tm + kR + 32, Klo, true);
                 }
-                if constexpr (kBack) {
+                if (kBack && !unit) {
                     const Operand<kChunk, true> Q(s + Space::q), Ql(s + Space::q + Space::kKeys);
                     product_ts<KD, kChunk>(tm + kDS, tm + kU, Q, true);
                     product_ts<KD, kChunk>(tm + kDS, tm + kU + 32, Q, true);
@@ -187,7 +206,7 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
                     }
                 }
                 mma_commit(&done[3]);
-                if constexpr (!kBack) {
+                if (!kBack && whole_part) {
                     const Operand<kChunk, false> A(s + Space::weights), Al(s + Space::weights + Space::kTileBytes);
                     product_ts<kChunk, kChunk>(tm + kD1, tm + kU, A, false);
                     product_ts<kChunk, kChunk>(tm + kD1, tm + kU + 32, A, true);
@@ -293,15 +312,17 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
             if (decays) put_decays(step + kStages);
         }
     } else {
-        const int part = warp / 4, dv = warp % 4 * 32 + lane, t0 = part * kT, k0 = part * kH;
+        const int quarter = warp / 4, dv = warp % 4 * 32 + lane, t0 = quarter * kT, k0 = quarter * kH;
         const uint32_t mine = tm + (uint32_t(warp % 4) << 21);
         float S[kH];
         {
-            const float *from = kBack ? bp.grad_final : p.initial;
-            const int64_t at = (seq * p.heads + head) * keys * values + dv;
+            const float *from = !kCut || part == 0 ? kBack ? bp.grad_final : p.initial : whole_part ? p.part_starts : nullptr;
+            const int64_t at = (!kCut || part == 0 ? seq * p.heads + head : (seq * p.parts + part) * p.heads + head) * keys * values + dv;
 #pragma unroll
-            for (int k = 0; k < kH; ++k)
+            for (int k = 0; k < kH; ++k) {
                 S[k] = from && dv < values && k0 + k < keys ? from[at + int64_t(k0 + k) * values] : 0.0f;
+                if (unit && k0 + k == dv && dv < keys) S[k] = 1.0f;
+            }
         }
         // what was stored is there for the products, and the copies
         auto arrive = [&](int which) {
@@ -326,8 +347,8 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
             uint32_t hi[kT / 2], lo[kT / 2];
 #pragma unroll
             for (int j = 0; j < kT / 2; ++j) split2(x[2 * j], x[2 * j + 1], hi[j], lo[j]);
-            tmem_store<kT / 2>(mine + at + part * (kT / 2), hi);
-            tmem_store<kT / 2>(mine + at + 32 + part * (kT / 2), lo);
+            tmem_store<kT / 2>(mine + at + quarter * (kT / 2), hi);
+            tmem_store<kT / 2>(mine + at + 32 + quarter * (kT / 2), lo);
         };
         auto meet = [] { asm volatile("bar.sync 1, %0;" ::"n"(kChainThreads) : "memory"); };
         // from shared to global memory, whole 16-byte pieces
@@ -348,9 +369,10 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
                      sm + Space::keep + i * Space::kValues, tiles * int(Space::kTileBytes));
         };
         auto copy_out = [&](int64_t step) {
-            const int n = rows_in(step);
+            const int64_t c = chunk_of(step);
+            const int n = rows_in(c);
             const T *from = reinterpret_cast<const T *>(sm + Space::out);
-            T *to = delta_at<T>(p.out, batch, row0 + step * kChunk, head);
+            T *to = delta_at<T>(p.out, batch, row0 + c * kChunk, head);
             if (p.out_wide) {
                 constexpr int kEach = 16 / int(sizeof(T)), kRow = kMostValues / kEach;
                 const int j = tid % kRow * kEach;
@@ -375,13 +397,13 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
             load_tile<T, false, kChunk, KD, kChainThreads>(tid, sm + Space::q, Space::kKeys, 0, p.q, batch, row, kh, n, keys, p.wide);
             if constexpr (kBack) {
                 load_tile<T, false, kChunk, kMostValues, kChainThreads>(tid, sm + Space::v, Space::kValues, 0, bp.grad_out, batch,
-                                                                        row, head, n, values, p.wide);
+                                                                        row, head, n, p.values, p.wide);
             } else {
                 const T *src = delta_at<T>(p.v, batch, row, head);
                 constexpr int kEach = 16 / int(sizeof(T)), kRow = kMostValues / kEach;
 #pragma unroll 4
                 for (int e = tid; e < kChunk * kRow; e += kChainThreads) {
-                    const int i = e / kRow, j = e % kRow * kEach, left = i < n ? values - j : 0;
+                    const int i = e / kRow, j = e % kRow * kEach, left = i < n ? p.values - j : 0;
                     T *to = reinterpret_cast<T *>(sm + Space::v) + i * kMostValues + j;
                     if (p.wide) {
                         copy16(smem_addr(to), left > 0 ? src + i * p.v.row + j : src, left > 0 ? 16u : 0u);
@@ -465,9 +487,9 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
             char *s = sm + st * Space::bytes;
             const int64_t at = (slot0 + chunk_of(step)) * p.heads + head;
             if constexpr (!kBack)
-                if (step > 0) finish_out(step - 1);
+                if (whole_part && step > 0) finish_out(step - 1);
             // what was put in shared memory last is copied on while the product runs
-            if (!kBack || kept) {
+            if ((!kBack && whole_part) || kept) {
                 meet();
                 if (kept) copy_state(at);
                 if (!kBack && step > 1) copy_out(step - 2);
@@ -483,7 +505,7 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
                 float y[kT];
                 const T *v = reinterpret_cast<const T *>(s + Space::v) + t0 * kMostValues + dv;
 #pragma unroll
-                for (int j = 0; j < kT; ++j) y[j] = to_f32<T>(v[j * kMostValues]);
+                for (int j = 0; j < kT; ++j) y[j] = unit ? 0.0f : to_f32<T>(v[j * kMostValues]);
                 wait_done(0, step);
                 read(x, kD0 + t0);
 #pragma unroll
@@ -497,14 +519,14 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
                 put_rows(kR, x);
             } else {
                 if constexpr (kBack) {
-                    tmem_store<kT / 2>(mine + kU + part * (kT / 2), side_hi);
-                    tmem_store<kT / 2>(mine + kU + 32 + part * (kT / 2), side_lo);
+                    tmem_store<kT / 2>(mine + kU + quarter * (kT / 2), side_hi);
+                    tmem_store<kT / 2>(mine + kU + 32 + quarter * (kT / 2), side_lo);
                 }
                 wait_done(0, step);
                 read(x, kD0 + t0);
                 wait_done(1, step);
-                float y[kT];
-                read(y, kD1 + t0);
+                float y[kT] = {};
+                if (!unit) read(y, kD1 + t0);
 #pragma unroll
                 for (int j = 0; j < kT / 4; ++j) {
                     const float4 f = rest4[j];
@@ -516,8 +538,8 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
                 put_rows(kR, x);
             }
             arrive(1);
-            if (!kBack || kept) meet();  // every copy has read its place
-            if constexpr (!kBack) {
+            if ((!kBack && whole_part) || kept) meet();  // every copy has read its place
+            if (!kBack && whole_part) {
                 wait_done(1, step);
                 read(o1, kDS + t0);
 #pragma unroll
@@ -559,7 +581,7 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
                 copy_rows(at);
             }
             if constexpr (!kBack) {
-                if (step > 0) put_out();
+                if (whole_part && step > 0) put_out();
             } else if (kStages == 2 && step + 1 < chunks) {
                 prepare_side(step + 1);
             }
@@ -581,7 +603,7 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
             }
         }
         if constexpr (!kBack)
-            if (chunks > 0) {
+            if (whole_part && chunks > 0) {
                 finish_out(chunks - 1);
                 meet();
                 if (chunks > 1) copy_out(chunks - 2);
@@ -590,8 +612,13 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
                 meet();
                 copy_out(chunks - 1);
             }
-        if (float *to = kBack ? bp.grad_initial : p.final; to && dv < values) {
-            to += (seq * p.heads + head) * keys * values + dv;
+        // the last part's is the sequence's; another's own is the next one's start
+        const bool last = !kCut || (kPass == 2 && part + 1 == p.parts);
+        float *to = last ? kBack ? bp.grad_initial : p.final : unit ? p.part_maps : kPass == 1 ? p.part_ends : nullptr;
+        int64_t place = last ? seq * p.heads + head : (seq * p.parts + part) * p.heads + head;
+        if (kPass == 1 && part == 0) to = p.part_starts, place += p.heads;
+        if (to && dv < values) {
+            to += place * keys * values + dv;
             const float bad = ok ? 0.0f : __int_as_float(0x7fffffff);
 #pragma unroll
             for (int k = 0; k < kH; ++k)
@@ -603,17 +630,24 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
     if (warp == 0) tmem_free(tm, 512);
 }
 
-template <class T, int KD, bool kBack, bool kMaps>
-cudaError_t chain_k(const DeltaBackwardParams &p, const ChainMaps &maps, cudaStream_t s) {
-    const auto kernel = delta_chain_kernel<T, KD, kBack, kMaps>;
+template <class T, int KD, bool kBack, bool kMaps, int kPass>
+cudaError_t chain_n(const DeltaBackwardParams &p, const ChainMaps &maps, cudaStream_t s) {
+    const auto kernel = delta_chain_kernel<T, KD, kBack, kMaps, kPass>;
     constexpr size_t bytes = ChainSpace<T, KD, kBack, kMaps>::kAll;
     constexpr int threads = kChainThreads + kHelpThreads;
     if (device_blocks(reinterpret_cast<const void *>(kernel), threads, bytes) == 0) return cudaErrorInvalidConfiguration;
-    return launch_pdl(kernel, dim3(uint32_t(p.f.sequences), uint32_t(p.f.heads)), dim3(threads), bytes, s, p, maps);
+    const uint32_t jobs = kPass == 0 ? 1u : uint32_t(kPass == 1 ? 2 * p.f.parts - 3 : p.f.parts - 1);
+    return launch_pdl(kernel, dim3(uint32_t(p.f.sequences), uint32_t(p.f.heads), jobs), dim3(threads), bytes, s, p, maps);
+}
+
+template <class T, int KD, bool kBack>
+cudaError_t chain_maps(const DeltaBackwardParams &p, const ChainMaps &maps, int pass, cudaStream_t s) {
+    if (pass == 0) return chain_n<T, KD, kBack, true, 0>(p, maps, s);
+    return pass == 1 ? chain_n<T, KD, kBack, true, 1>(p, maps, s) : chain_n<T, KD, kBack, true, 2>(p, maps, s);
 }
 
 template <class T, bool kBack>
-cudaError_t chain_t(const DeltaBackwardParams &p, cudaStream_t s) {
+cudaError_t chain_t(const DeltaBackwardParams &p, int pass, cudaStream_t s) {
     const DeltaParams &f = p.f;
     ChainMaps maps = {};
     if constexpr (kPieces<T> == 1) {
@@ -621,9 +655,10 @@ cudaError_t chain_t(const DeltaBackwardParams &p, cudaStream_t s) {
             delta_map(&maps.k, f.k, f.batch, f.rows, f.key_heads, f.keys, 64, true) &&
             delta_map(&maps.q, f.q, f.batch, f.rows, f.key_heads, f.keys, 64, true) &&
             delta_map(&maps.v, kBack ? p.grad_out : f.v, f.batch, f.rows, f.heads, f.values, kBack ? 64 : kMostValues, kBack))
-            return f.keys <= 64 ? chain_k<T, 64, kBack, true>(p, maps, s) : chain_k<T, 128, kBack, true>(p, maps, s);
+            return f.keys <= 64 ? chain_maps<T, 64, kBack>(p, maps, pass, s) : chain_maps<T, 128, kBack>(p, maps, pass, s);
     }
-    return f.keys <= 64 ? chain_k<T, 64, kBack, false>(p, maps, s) : chain_k<T, 128, kBack, false>(p, maps, s);
+    if (pass != 0) return cudaErrorNotSupported;  // only rows that come by maps are cut
+    return f.keys <= 64 ? chain_n<T, 64, kBack, false, 0>(p, maps, s) : chain_n<T, 128, kBack, false, 0>(p, maps, s);
 }
 
 }  // namespace

@@ -1,0 +1,9 @@
+#include "delta_chain.cuh"
+
+namespace dwp {
+
+cudaError_t launch_delta_chain_back_bf16(const DeltaBackwardParams &p, int pass, cudaStream_t s) {
+    return chain_t<__nv_bfloat16, true>(p, pass, s);
+}
+
+}  // namespace dwp

@@ -1,0 +1,9 @@
+#include "delta_chain.cuh"
+
+namespace dwp {
+
+cudaError_t launch_delta_chain_back_f32(const DeltaBackwardParams &p, int pass, cudaStream_t s) {
+    return chain_t<float, true>(p, pass, s);
+}
+
+}  // namespace dwp

@@ -2,8 +2,8 @@
 
 namespace dwp {
 
-cudaError_t launch_delta_chain_bf16(const DeltaBackwardParams &p, bool back, cudaStream_t s) {
-    return back ? chain_t<__nv_bfloat16, true>(p, s) : chain_t<__nv_bfloat16, false>(p, s);
+cudaError_t launch_delta_chain_bf16(const DeltaBackwardParams &p, int pass, cudaStream_t s) {
+    return chain_t<__nv_bfloat16, false>(p, pass, s);
 }
 
 }  // namespace dwp

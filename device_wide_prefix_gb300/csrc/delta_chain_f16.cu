@@ -2,8 +2,8 @@
 
 namespace dwp {
 
-cudaError_t launch_delta_chain_f16(const DeltaBackwardParams &p, bool back, cudaStream_t s) {
-    return back ? chain_t<__half, true>(p, s) : chain_t<__half, false>(p, s);
+cudaError_t launch_delta_chain_f16(const DeltaBackwardParams &p, int pass, cudaStream_t s) {
+    return chain_t<__half, false>(p, pass, s);
 }
 
 }  // namespace dwp

@@ -2,8 +2,8 @@
 
 namespace dwp {
 
-cudaError_t launch_delta_chain_f32(const DeltaBackwardParams &p, bool back, cudaStream_t s) {
-    return back ? chain_t<float, true>(p, s) : chain_t<float, false>(p, s);
+cudaError_t launch_delta_chain_f32(const DeltaBackwardParams &p, int pass, cudaStream_t s) {
+    return chain_t<float, false>(p, pass, s);
 }
 
 }  // namespace dwp

@@ -1,7 +1,9 @@
 // Gated delta rule: the chain's and the gradient's kernels by type (a
-// translation unit each), and the maps of their inputs.
+// translation unit each), the maps of their inputs, and the chain over
+// sequences cut in parts.
 #include <atomic>
 
+#include "device.cuh"
 #include "launch.h"
 
 namespace dwp {
@@ -48,12 +50,79 @@ bool delta_map(CUtensorMap *map, const DeltaRows &r, int64_t batch, int64_t rows
 
 namespace {
 
+cudaError_t chain_pass(dwp_dtype t, const DeltaBackwardParams &p, bool back, int pass, cudaStream_t s) {
+    if (back) {
+        if (t == DWP_F32) return launch_delta_chain_back_f32(p, pass, s);
+        return t == DWP_BF16 ? launch_delta_chain_back_bf16(p, pass, s) : launch_delta_chain_back_f16(p, pass, s);
+    }
+    if (t == DWP_F32) return launch_delta_chain_f32(p, pass, s);
+    return t == DWP_BF16 ? launch_delta_chain_bf16(p, pass, s) : launch_delta_chain_f16(p, pass, s);
+}
+
 cudaError_t chain(dwp_dtype t, const DeltaBackwardParams &p, bool back, cudaStream_t s) {
-    if (t == DWP_F32) return launch_delta_chain_f32(p, back, s);
-    return t == DWP_BF16 ? launch_delta_chain_bf16(p, back, s) : launch_delta_chain_f16(p, back, s);
+    if (p.f.parts == 1) return chain_pass(t, p, back, 0, s);
+    cudaError_t err = chain_pass(t, p, back, 1, s);
+    if (err == cudaSuccess && p.f.parts > 2) err = launch_delta_join(p.f, s);
+    return err == cudaSuccess ? chain_pass(t, p, back, 2, s) : err;
+}
+
+constexpr int kJoinThreads = 256, kJoinCols = 16, kJoinKeys = 128, kJoinPitch = kJoinKeys + 1;
+constexpr size_t kJoinBytes = sizeof(float) * (kJoinKeys * kJoinPitch + kJoinKeys * kJoinCols);
+
+// start[part + 1] = map[part] start[part] + end[part], 16 columns a block.
+__global__ void __launch_bounds__(kJoinThreads) delta_join_kernel(DeltaParams p) {
+    extern __shared__ float sh[];
+    float *map = sh, *S = sh + kJoinKeys * kJoinPitch;
+    pdl_trigger();
+    pdl_wait();
+    const int tid = threadIdx.x, keys = p.keys, values = p.values, c0 = blockIdx.x * kJoinCols;
+    const int k = tid / 2, c = tid % 2 * (kJoinCols / 2);
+    for (int64_t part = 1; part + 1 < p.parts; ++part) {
+        const int64_t at = (int64_t(blockIdx.z) * p.parts + part) * p.heads + blockIdx.y;
+        const float *from = p.part_maps + at * keys * keys, *start = p.part_starts + at * keys * values;
+        __syncthreads();
+        for (int e = tid; e < keys * keys; e += kJoinThreads) map[e / keys * kJoinPitch + e % keys] = from[e];
+        for (int e = tid; e < keys * kJoinCols; e += kJoinThreads) {
+            const int col = c0 + e % kJoinCols;
+            // the first start is pass 1's; the later ones this block wrote itself
+            S[e] = col < values ? start[int64_t(e / kJoinCols) * values + col] : 0.0f;
+        }
+        __syncthreads();
+        float s[kJoinCols / 2] = {};
+        if (k < keys)
+            for (int m = 0; m < keys; ++m) {
+                const float x = map[k * kJoinPitch + m];
+#pragma unroll
+                for (int j = 0; j < kJoinCols / 2; ++j) s[j] = fmaf(x, S[m * kJoinCols + c + j], s[j]);
+            }
+        float *to = p.part_starts + (at + p.heads) * keys * values;
+        const float *end = p.part_ends + at * keys * values;
+#pragma unroll
+        for (int j = 0; j < kJoinCols / 2; ++j)
+            if (k < keys && c0 + c + j < values) {
+                const int64_t e = int64_t(k) * values + c0 + c + j;
+                to[e] = s[j] + end[e];
+            }
+        __threadfence_block();
+    }
 }
 
 }  // namespace
+
+int64_t delta_parts(int64_t walks, int64_t chunks) {
+    if (walks < 1) return 1;
+    int64_t parts = (kSMs / walks + 3) / 2;  // walks (2 parts - 3) blocks in pass 1
+    if (parts > chunks / 8) parts = chunks / 8;
+    return parts < 3 ? 1 : parts;
+}
+
+cudaError_t launch_delta_join(const DeltaParams &p, cudaStream_t s) {
+    if (device_blocks(reinterpret_cast<const void *>(delta_join_kernel), kJoinThreads, kJoinBytes) == 0)
+        return cudaErrorInvalidConfiguration;
+    return launch_pdl(delta_join_kernel,
+                      dim3(uint32_t((p.values + kJoinCols - 1) / kJoinCols), uint32_t(p.heads), uint32_t(p.sequences)),
+                      dim3(kJoinThreads), kJoinBytes, s, p);
+}
 
 cudaError_t launch_delta_chain(dwp_dtype t, const DeltaParams &p, cudaStream_t s) {
     DeltaBackwardParams b = {};

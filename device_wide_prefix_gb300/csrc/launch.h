@@ -231,7 +231,8 @@ cudaError_t launch_scan_walk_back_f16(const ScanParams &p, cudaStream_t s);
 cudaError_t launch_selscan_step(dwp_dtype t, const ScanStepParams &p, cudaStream_t s);
 
 // Gated delta rule (delta_local.cu, delta_chain.cuh, delta_grad.cuh,
-// delta_step.cu; delta_types.cu and a file for each type).  Rows of [heads, keys] or [heads, values].
+// delta_step.cu; delta_types.cu and a file for each type and direction).
+// pass: 0, or 1 and 2 over parts.  Rows of [heads, keys] or [heads, values].
 struct DeltaRows {
     char *data;
     int64_t batch, row, head;  // strides in elements
@@ -256,6 +257,11 @@ struct DeltaParams {
     // [values / 64, rounded up] tiles of 64 rows, and the state before the chunk,
     // two pieces of [keys / 64, rounded up] tiles of `values` rows
     float *inverse, *weights, *u, *states;
+    // Sequences cut in `parts` that are walked at once (delta_chain.cuh):
+    // [sequences][parts][heads]: states at the parts' first chunks, what a part
+    // makes of zeros, and [keys][keys] what it makes of any state
+    int64_t parts, part_chunks;
+    float *part_starts, *part_ends, *part_maps;
 };
 struct DeltaBackwardParams {
     DeltaParams f;
@@ -276,11 +282,19 @@ struct DeltaStepParams {
     const int32_t *slots;
 };
 cudaError_t launch_delta_local(dwp_dtype t, const DeltaParams &p, cudaStream_t s);
+// The cut: parts that fill the GPU's blocks of one chain each, eight chunks or
+// more to a part; 1 for none.
+int64_t delta_parts(int64_t walks, int64_t chunks);
+// States at the parts' first chunks, from the first's and each part's map.
+cudaError_t launch_delta_join(const DeltaParams &p, cudaStream_t s);
 cudaError_t launch_delta_chain(dwp_dtype t, const DeltaParams &p, cudaStream_t s);
 cudaError_t launch_delta_chain_back(dwp_dtype t, const DeltaBackwardParams &p, cudaStream_t s);
-cudaError_t launch_delta_chain_f32(const DeltaBackwardParams &p, bool back, cudaStream_t s);
-cudaError_t launch_delta_chain_bf16(const DeltaBackwardParams &p, bool back, cudaStream_t s);
-cudaError_t launch_delta_chain_f16(const DeltaBackwardParams &p, bool back, cudaStream_t s);
+cudaError_t launch_delta_chain_f32(const DeltaBackwardParams &p, int pass, cudaStream_t s);
+cudaError_t launch_delta_chain_back_f32(const DeltaBackwardParams &p, int pass, cudaStream_t s);
+cudaError_t launch_delta_chain_bf16(const DeltaBackwardParams &p, int pass, cudaStream_t s);
+cudaError_t launch_delta_chain_back_bf16(const DeltaBackwardParams &p, int pass, cudaStream_t s);
+cudaError_t launch_delta_chain_f16(const DeltaBackwardParams &p, int pass, cudaStream_t s);
+cudaError_t launch_delta_chain_back_f16(const DeltaBackwardParams &p, int pass, cudaStream_t s);
 cudaError_t launch_delta_grad(dwp_dtype t, const DeltaBackwardParams &p, cudaStream_t s);
 cudaError_t launch_delta_grad_f32(const DeltaBackwardParams &p, cudaStream_t s);
 cudaError_t launch_delta_grad_bf16(const DeltaBackwardParams &p, cudaStream_t s);

@@ -501,7 +501,9 @@ dwp_status dwp_selective_scan_step(const dwp_selective_scan_step_args *args, dwp
  *                  batch * ceil(rows / DWP_DELTA_CHUNK), or with offsets rows /
  *                  DWP_DELTA_CHUNK + num_segments
  *   scratch        without checkpoints 8 * DWP_DELTA_CHUNK^2 bytes for each
- *                  of those chunks and head
+ *                  of those chunks and head; beside it up to 30 MB where long
+ *                  bf16 batch entries (24 chunks and more) have few heads (under
+ *                  51 in all) and are cut in parts
  * A sequence is taken in chunks of DWP_DELTA_CHUNK rows from its first.  A
  * value that is not finite reaches its own sequence and head only, there also
  * the rows before it in its chunk.  Products of two f32 numbers (states,
@@ -538,7 +540,7 @@ dwp_status dwp_gated_delta_rule(const dwp_delta_args *args, void *d_scratch, siz
  *                 grad_beta  the same, beta_dtype
  *   grad_initial_state  NULL, or as initial_state
  *   scratch       4 * (keys' * values + DWP_DELTA_CHUNK * values') bytes for
- *                 each of the chunks and head
+ *                 each of the chunks and head; beside it as the forward's
  */
 typedef struct dwp_delta_backward_args {
     dwp_delta_args delta;

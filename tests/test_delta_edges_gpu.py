@@ -121,6 +121,17 @@ def test_many_chunks(dtype, rows):
     check(c, out, final, backward(c, points))
 
 
+@pytest.mark.parametrize("dtype,batch,rows,heads,keys,values,pad", [
+    ("bf16", 1, 1600, 1, 128, 128, 0), ("bf16", 2, 2049, 1, 64, 128, 0), ("f32", 1, 1537, 2, 40, 72, 0),
+    ("f16", 1, 1599, 1, 128, 64, 0), ("bf16", 1, 1600, 1, 72, 24, 1), ("f32", 1, 5184, 1, 16, 16, 0),
+    ("bf16", 1, 5185, 1, 16, 16, 0)])
+def test_sequences_cut_in_parts(dtype, batch, rows, heads, keys, values, pad):
+    """Few heads and many chunks: three parts and more, the last one short, one row long or empty."""
+    c = Case(24, (batch, rows), None, dtype, 1, heads, keys, values, pad, decay=0.01)
+    out, final, points = forward(c)
+    check(c, out, final, backward(c, points))
+
+
 def test_keys_all_alike():
     """One key over and over, strength 1, no decay: the worst inverse, whose entries stay bounded."""
     c = Case(11, (1, 192), None, "f32", 1, 1, 64, 64, decay=0.0)
