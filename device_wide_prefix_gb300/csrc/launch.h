@@ -343,8 +343,8 @@ struct LayerNormBackwardParams {
     float *partial;  // NULL, or [blocks][weight, bias][channels]
 };
 cudaError_t launch_layer_norm(dwp_dtype t, const LayerNormParams &p, bool vec, cudaStream_t s);
-// Rows that a block of the gradient takes at once.
-int64_t layer_norm_teams(dwp_dtype t, int64_t group, bool vec);
+// Rows that a block of the gradient takes at once, and blocks that an SM holds.
+int64_t layer_norm_teams(dwp_dtype t, int64_t group, bool vec, int64_t &per_sm);
 cudaError_t launch_layer_norm_backward(dwp_dtype t, const LayerNormBackwardParams &p, bool vec, cudaStream_t s);
 
 }  // namespace dwp

@@ -519,11 +519,12 @@ dwp_status layer_norm_forward(const dwp_layer_norm_args &a, cudaStream_t s) {
                                       c.wide(a.channels / a.groups, a.dtype), s));
 }
 
-// Blocks that share a group's rows in the gradient: those that run at once (two
-// of 256 threads an SM), each team with four rows or more.
+// Blocks that share a group's rows in the gradient: those that run at once, each
+// team with four rows or more.
 int64_t layer_norm_blocks(const dwp_layer_norm_args &a, bool wide) {
-    const int64_t teams = layer_norm_teams(static_cast<dwp_dtype>(a.dtype), a.channels / a.groups, wide);
-    int64_t blocks = kSMs * 2 / a.groups;
+    int64_t per_sm;
+    const int64_t teams = layer_norm_teams(static_cast<dwp_dtype>(a.dtype), a.channels / a.groups, wide, per_sm);
+    int64_t blocks = kSMs * per_sm / a.groups;
     if (4 * blocks * teams > a.rows) blocks = ceil_div(a.rows, 4 * teams);
     return blocks < 1 && a.rows > 0 ? 1 : blocks;
 }
