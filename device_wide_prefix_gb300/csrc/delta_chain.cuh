@@ -14,9 +14,10 @@
 // of the next products, as R and U do, and K, Q, T, A and dO are operands in
 // shared memory as they are stored.  What is not itself bf16 is two bf16
 // (split2): 16 bits, 2^-18 of a number at most is lost; of two such all four
-// products are taken, but for bf16 rows the smallest.  The weights of a bf16
-// output are one bf16 each (two more tiles would not fit): they cost at most
-// 2^-9 of the output's terms.
+// products are taken (without the smallest, 202 us in place of 204, the
+// gradient of g was up to a fifth further off).  The weights of a bf16 output
+// are one bf16 each (two more tiles would not fit): they cost at most 2^-9 of
+// the output's terms.
 //
 // Sixteen warps do this (with eight, twice the registers and rows each, a chunk
 // took 1.2 times as long); of four more one issues the products (a warp that issues
@@ -26,6 +27,16 @@
 // products: one of the four warps is slower at that (instructions that come in
 // between the chain's are fetched anew each time; 9,000 cycles a chunk), bulk
 // copies are slower still (256 bytes in 83 cycles, 64 KB in 5,000).
+//
+// What bounds it is that each product needs the one before it: a chunk of 128 x
+// 128 forward takes about 5,500 cycles (32768 rows x 32 heads, a block an SM at
+// most; 6,900 with 128 blocks), of which the products that wait for one another
+// are 1,500; carrying numbers between tensor memory, registers and pieces is the
+// rest.  4 x 2048 rows x 32 heads take 117 us; x 16 heads, with what the gradient
+// needs kept, 190, and back 168.  Keys up to 64 take half the state (KD 64): 177
+// us a call of 4 x 2048 x 32 in place of 197.  bf16 rows of whole 16-byte pieces
+// come by tensor maps, a chunk ahead (197); others are read and split by the
+// sixteen warps between chunks (off 16 bytes 491, f16 416, f32 437).
 //
 // Few sequences and heads leave most of the GPU idle while each walks its
 // chunks.  A state goes through a part of a sequence linearly, S -> M S + E, so
@@ -183,7 +194,7 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
                 product_ts<kChunk, kChunk>(tm + kD0, tm + kR, inv, false);
                 product_ts<kChunk, kChunk>(tm + kD0, tm + kR + 32, inv, true);
                 product_ts<kChunk, kChunk>(tm + kD0, tm + kR, invl, true);
-                if constexpr (kP == 2) product_ts<kChunk, kChunk>(tm + kD0, tm + kR + 32, invl, true);
+                product_ts<kChunk, kChunk>(tm + kD0, tm + kR + 32, invl, true);
                 mma_commit(&done[2]);
             }
             __syncwarp();

@@ -16,7 +16,15 @@
 // adding their dQ and dK in registers.  The products with the states and the
 // second ones have the keys as rows and the chunk's rows as columns; dA and E
 // come from one product of [dO; dR] with U.  Numbers that are not bf16 are in
-// two pieces, as in the chain.
+// two pieces, and all four products of two such are taken; dA and E are in three,
+// since the gradient of g is a sum of their products in which much cancels.
+//
+// 4 x 2048 rows x 16 heads of 128 x 128 take 240 us, of which moving the data
+// is 93 (543 MB read, 88 written): 2,048 blocks of one chunk each wait for their
+// states and rows (long scoreboard 3.3 cycles an instruction, barriers 2.0; one
+// block fits an SM), tensor cores are 12% busy.  Tried and slower: asking for the
+// next block's rows ahead of it (275), loads earlier in the block (273), blocks
+// of one chunk's heads together (287), S1 through shared memory (246).
 #pragma once
 
 #include "delta.cuh"
@@ -36,8 +44,10 @@ struct GradSpace {
     // keys and queries; [dO; dR] (hi, lo), later [dA; E] and beta E; U (hi, lo);
     // the state before the chunk, later the gradient of the one after it (hi, lo)
     static constexpr uint32_t k = 0, q = k + kP * kRows, stack = q + kP * kRows, u = stack + 4 * kRows;
-    static constexpr uint32_t state = u + 2 * kRows, bytes = state + 2 * kState;
-    static constexpr uint32_t cross = stack, scaled = stack + 2 * kRows;
+    static constexpr uint32_t state = u + 2 * kRows, cross = stack, scaled = stack + 2 * kRows;
+    // third pieces: of [dA; E], and for bf16 rows of beta E
+    static constexpr uint32_t cross_third = scaled + kRows, scaled_third = state + 2 * kState;
+    static constexpr uint32_t bytes = scaled_third + (kP == 1 ? kRows / 2 : 0);
     static constexpr size_t kAll = 1024 + bytes;
 };
 
@@ -63,6 +73,21 @@ __device__ __forceinline__ float2 pair_of(uint32_t hi, uint32_t lo) {
 struct GradMaps {
     CUtensorMap k, q, grad_out;
 };
+
+// Eight numbers in three pieces of bf16.
+__device__ __forceinline__ void store_thirds(char *hi, char *lo, char *third, uint32_t at, const float (&f)[8]) {
+    uint32_t h[4], l[4], t[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        split2(f[2 * j], f[2 * j + 1], h[j], l[j]);
+        const float2 two = pair_of(h[j], l[j]);
+        const __nv_bfloat162 rest = __floats2bfloat162_rn(f[2 * j] - two.x, f[2 * j + 1] - two.y);
+        t[j] = *reinterpret_cast<const uint32_t *>(&rest);
+    }
+    *reinterpret_cast<uint4 *>(hi + at) = make_uint4(h[0], h[1], h[2], h[3]);
+    *reinterpret_cast<uint4 *>(lo + at) = make_uint4(l[0], l[1], l[2], l[3]);
+    if (third) *reinterpret_cast<uint4 *>(third + at) = make_uint4(t[0], t[1], t[2], t[3]);
+}
 
 // kMaps: bf16 rows of whole 16-byte pieces, which come by tensor maps.
 template <class T, bool kMaps>
@@ -242,7 +267,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
             product_ss<kChunk, kMost>(tm + kDA, both, U, false);
             product_ss<kChunk, kMost>(tm + kDA, both, Ul, true);
             product_ss<kChunk, kMost>(tm + kDA, bothl, U, true);
-            if constexpr (kP == 2) product_ss<kChunk, kMost>(tm + kDA, bothl, Ul, true);
+            product_ss<kChunk, kMost>(tm + kDA, bothl, Ul, true);
             mma_commit(&bars[0]);
             product_ss<2 * kChunk, kMost>(tm + kDX, S, both, false);
             product_ss<2 * kChunk, kMost>(tm + kDX, Sl, both, true);
@@ -252,6 +277,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
             } else {
                 const Operand<2 * kChunk, false> drl(sm + Space::stack + 2 * kRows + kTileBytes);
                 product_ss<kChunk, kMost>(tm + kDX + kChunk, S, drl, true);
+                product_ss<kChunk, kMost>(tm + kDX + kChunk, Sl, drl, true);
             }
             mma_commit(&bars[1]);
         }
@@ -317,11 +343,12 @@ __global__ void __launch_bounds__(kGradThreads, 1)
 #pragma unroll
             for (int l = 0; l < 8; ++l) f[l] = w[j * 8 + l];
             const uint32_t piece = uint32_t(t0 / 8 + j);
-            store_pieces(sm + Space::cross, sm + Space::cross + kRows, tile_piece(uint32_t(dk), piece), f);
+            store_thirds(sm + Space::cross, sm + Space::cross + kRows, sm + Space::cross_third, tile_piece(uint32_t(dk), piece), f);
             if (cross) {
 #pragma unroll
                 for (int l = 0; l < 8; ++l) f[l] *= beta[row];
-                store_pieces(sm + Space::scaled, sm + Space::scaled + kTileBytes, tile_piece(uint32_t(row), piece), f);
+                store_thirds(sm + Space::scaled, sm + Space::scaled + kTileBytes, kP == 1 ? sm + Space::scaled_third : nullptr,
+                             tile_piece(uint32_t(row), piece), f);
             }
         }
         // the gradient of the state after the chunk takes the state's place, and meets it on the way
@@ -354,7 +381,11 @@ __global__ void __launch_bounds__(kGradThreads, 1)
             product_ss<kChunk, kChunk>(tm + kDY, Q, Al, true);
             product_ss<kChunk, kChunk>(tm + kDY, K, E, true);
             product_ss<kChunk, kChunk>(tm + kDY, K, El, true);
-            if constexpr (kP == 2) {
+            product_ss<2 * kChunk, kChunk>(tm + kDW, K, Operand<2 * kChunk, false>(sm + Space::cross_third), true);
+            product_ss<kChunk, kChunk>(tm + kDY, Q, Operand<2 * kChunk, true>(sm + Space::cross_third), true);
+            if constexpr (kP == 1) {
+                product_ss<kChunk, kChunk>(tm + kDY, K, Operand<kChunk, true>(sm + Space::scaled_third), true);
+            } else {
                 const Operand<kChunk, true> Kl(sm + Space::k + kRows), Ql(sm + Space::q + kRows);
                 product_ss<2 * kChunk, kChunk>(tm + kDW, Kl, W, true);
                 product_ss<2 * kChunk, kChunk>(tm + kDW, Kl, Wl, true);
@@ -367,7 +398,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
             product_ss<kChunk, kMost>(tm + kDU, S, U, false);
             product_ss<kChunk, kMost>(tm + kDU, S, Ul, true);
             product_ss<kChunk, kMost>(tm + kDU, Sl, U, true);
-            if constexpr (kP == 2) product_ss<kChunk, kMost>(tm + kDU, Sl, Ul, true);
+            product_ss<kChunk, kMost>(tm + kDU, Sl, Ul, true);
             mma_commit(&bars[4]);
         }
         float x[kCols], both_sums[2 * kCols];  // of q.dQ + beta k.Z - k.Y, and of k.Z

@@ -10,6 +10,11 @@
 // -T22 L21 T11 below each pair: the substitution's steps wait for one another.
 // The loops are short on purpose: unrolled, three of ten cycles of a warp went
 // to fetching instructions.
+//
+// 4 x 2048 rows, 16 key heads and 32 heads of 128 keys take 83 us, of which moving
+// the data would be 20; 16 heads 46.  The
+// substitutions' steps bound it: barriers are the longest wait (2.6 cycles an
+// instruction), the scheduler issues 0.43 a cycle, tensor cores are 2% busy.
 #include "delta.cuh"
 
 namespace dwp {

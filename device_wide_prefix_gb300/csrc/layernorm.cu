@@ -10,6 +10,12 @@
 // warps join by
 //   M2 = sum M2_w + n_w (mean_w - mean)^2,
 // so a mean far from zero costs nothing, and a block meets once a row.
+//
+// Memory bounds the forward: 8192 x 4096 bf16 onto an f32 residual (403 MB) takes
+// 76 us, 0.78 of the copy rate; 8 rows 2 us, the rest of a call is the host's.
+// The gradient of the same (537 MB) 124 us, 0.64: it holds a row's values, its
+// gradients and the columns' sums, and waits for each row's moments.  4099 x 32
+// groups of 128 in f16 36 us, 0.41: few warps a row's loads are spread over.
 #include "sequence.cuh"
 
 namespace dwp {
