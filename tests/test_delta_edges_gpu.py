@@ -132,6 +132,48 @@ def test_sequences_cut_in_parts(dtype, batch, rows, heads, keys, values, pad):
     check(c, out, final, backward(c, points))
 
 
+def test_cut_sequences_scratch_capture_and_neighbours():
+    """Sequences cut in parts: any scratch gives the same, captured calls too; a value that is not finite reaches
+    neither its neighbours nor, forward, the chunks before it."""
+    cases = [Case(s, (2, 2000), None, "bf16", 1, 2, 128, 64, decay=0.01) for s in (25, 26)]
+    live = Case(25, (2, 2000), None, "bf16", 1, 2, 128, 64, decay=0.01)
+    wants = [forward(c) for c in cases]
+    backs = [backward(c, w[2]) for c, w in zip(cases, wants)]
+    for byte in (0, 0xFF):
+        scratch = torch.full((1 << 25,), byte, dtype=torch.uint8, device="cuda")
+        got = forward(cases[0], scratch=scratch)
+        assert all(torch.equal(a, b) for a, b in zip(wants[0][:2], got[:2]))
+        scratch.fill_(byte)
+        again = backward(cases[0], got[2], scratch=scratch)
+        assert all(torch.equal(backs[0][k], again[k]) for k in again)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        backward(live, forward(live)[2])
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        res = forward(live)
+        grads = backward(live, res[2])
+    for c, want, back in list(zip(cases, wants, backs))[::-1]:
+        for n in ("q", "k", "v", "g", "beta", "grad", "state", "grad_state"):
+            getattr(live, n).copy_(getattr(c, n))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(res[0], want[0]) and torch.equal(res[1], want[1])
+        assert all(torch.equal(grads[k], back[k]) for k in back)
+    for value in (NAN, math.inf):
+        live.v.copy_(cases[0].v)
+        live.v[0, 1000, 1, 5] = value
+        out, final, points = forward(live)
+        assert torch.equal(out[1], wants[0][0][1]) and torch.equal(final[1], wants[0][1][1])
+        assert torch.equal(out[0, :, 0], wants[0][0][0, :, 0]) and torch.equal(out[0, :960], wants[0][0][0, :960])
+        more = backward(live, points)
+        for n in ("v", "g", "beta"):
+            assert torch.equal(more[n][1], backs[0][n][1]) and torch.equal(more[n][0, :, 0], backs[0][n][0, :, 0]), n
+        assert torch.equal(more["initial_state"][1], backs[0]["initial_state"][1])
+
+
 def test_keys_all_alike():
     """One key over and over, strength 1, no decay: the worst inverse, whose entries stay bounded."""
     c = Case(11, (1, 192), None, "f32", 1, 1, 64, 64, decay=0.0)
