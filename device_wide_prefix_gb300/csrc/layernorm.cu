@@ -339,12 +339,13 @@ cudaError_t forward_v(LayerNormParams p, cudaStream_t s) {
     const Spread a = spread(p.group, V);
     p.team = a.team;
     if (!a.block) return a.k == 1 ? forward_k<T, V, 1, false>(p, s) : forward_k<T, V, 2, false>(p, s);
-    switch (a.k) {
-        case 1: return forward_k<T, V, 1, true>(p, s);
-        case 2: return forward_k<T, V, 2, true>(p, s);
-        case 4: return forward_k<T, V, 4, true>(p, s);
-        default: return forward_k<T, V, 16, true>(p, s);
-    }
+    if (a.k == 1) return forward_k<T, V, 1, true>(p, s);
+    if (a.k == 2) return forward_k<T, V, 2, true>(p, s);
+    // groups of at most 16384: 8 an access end here, 4 an access below
+    if constexpr (V <= 4)
+        if (a.k == 4) return forward_k<T, V, 4, true>(p, s);
+    if constexpr (V == 1) return forward_k<T, V, 16, true>(p, s);
+    return cudaErrorInvalidConfiguration;
 }
 
 template <class T, int V, int K, int kMost, bool kBlock, bool kWideV>
