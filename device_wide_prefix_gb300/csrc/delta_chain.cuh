@@ -14,8 +14,8 @@
 // of the next products, as R and U do, and K, Q, T, A and dO are operands in
 // shared memory as they are stored.  What is not itself bf16 is two bf16
 // (split2): 16 bits, 2^-18 of a number at most is lost; of two such all four
-// products are taken (without the smallest, 202 us in place of 204, the
-// gradient of g was up to a fifth further off).  The weights of a bf16 output
+// products are taken (without the smallest a call took 1% less, and
+// the gradient of g was up to a fifth further off).  The weights of a bf16 output
 // are one bf16 each (two more tiles would not fit): they cost at most 2^-9 of
 // the output's terms.
 //
@@ -33,10 +33,10 @@
 // most; 6,900 with 128 blocks), of which the products that wait for one another
 // are 1,500; carrying numbers between tensor memory, registers and pieces is the
 // rest.  4 x 2048 rows x 32 heads take 117 us; x 16 heads, with what the gradient
-// needs kept, 190, and back 168.  Keys up to 64 take half the state (KD 64): 177
-// us a call of 4 x 2048 x 32 in place of 197.  bf16 rows of whole 16-byte pieces
-// come by tensor maps, a chunk ahead (197); others are read and split by the
-// sixteen warps between chunks (off 16 bytes 491, f16 416, f32 437).
+// needs kept, 190, and back 168.  Keys up to 64 take half the state (KD 64): 171
+// us a call of 4 x 2048 x 32 in place of 195.  bf16 rows of whole 16-byte pieces
+// come by tensor maps, a chunk ahead (195); others are read and split by the
+// sixteen warps between chunks (off 16 bytes 497, f16 419, f32 443).
 //
 // Few sequences and heads leave most of the GPU idle while each walks its
 // chunks.  A state goes through a part of a sequence linearly, S -> M S + E, so

@@ -11,7 +11,7 @@
 // The loops are short on purpose: unrolled, three of ten cycles of a warp went
 // to fetching instructions.
 //
-// 4 x 2048 rows, 16 key heads and 32 heads of 128 keys take 83 us, of which moving
+// 4 x 2048 rows, 16 key heads and 32 heads of 128 keys take 77 us, of which moving
 // the data would be 20; 16 heads 46.  The
 // substitutions' steps bound it: barriers are the longest wait (2.6 cycles an
 // instruction), the scheduler issues 0.43 a cycle, tensor cores are 2% busy.
@@ -257,9 +257,16 @@ cudaError_t local_n(const DeltaParams &p, const LocalMaps &maps, cudaStream_t s)
     return launch_pdl(kernel, dim3(uint32_t(p.slots), uint32_t(p.key_heads)), dim3(kTeam * kTeams), bytes, s, p, maps);
 }
 
+// Two teams share a block's keys where heads do, unless there are blocks enough
+// without, of rows that maps bring (others take more threads to load and split).
+// A call with one team against two, 128 x 128, bf16: 4 x 2048 rows x 16 key heads
+// 195 us against 202, 4 key heads 198 against 202, 1 key head (128 blocks) of 16
+// heads 196 against 171, 512 rows x 2 key heads of 16 heads 74 against 61; off 16
+// bytes, 4 x 2048 rows x 16 key heads, 581 against 497, in f32 504 against 440.
 template <class T, int KD, bool kMaps>
 cudaError_t local_k(const DeltaParams &p, const LocalMaps &maps, cudaStream_t s) {
-    return p.heads == p.key_heads ? local_n<T, KD, kMaps, 1>(p, maps, s) : local_n<T, KD, kMaps, 2>(p, maps, s);
+    const bool many = kMaps && p.slots * p.key_heads > 3 * kSMs;
+    return p.heads == p.key_heads || many ? local_n<T, KD, kMaps, 1>(p, maps, s) : local_n<T, KD, kMaps, 2>(p, maps, s);
 }
 
 template <class T>

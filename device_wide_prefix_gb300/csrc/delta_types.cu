@@ -62,7 +62,7 @@ cudaError_t chain_pass(dwp_dtype t, const DeltaBackwardParams &p, bool back, int
 cudaError_t chain(dwp_dtype t, const DeltaBackwardParams &p, bool back, cudaStream_t s) {
     if (p.f.parts == 1) return chain_pass(t, p, back, 0, s);
     cudaError_t err = chain_pass(t, p, back, 1, s);
-    if (err == cudaSuccess && p.f.parts > 2) err = launch_delta_join(p.f, s);
+    if (err == cudaSuccess) err = launch_delta_join(p.f, s);
     return err == cudaSuccess ? chain_pass(t, p, back, 2, s) : err;
 }
 
@@ -112,8 +112,8 @@ __global__ void __launch_bounds__(kJoinThreads) delta_join_kernel(DeltaParams p)
 // Parts that a walk along a sequence is cut into: as many as fill the GPU's
 // blocks in pass 1, eight chunks each at least, and three or none (of two parts
 // the second would wait for the first as before).  Cut against uncut, bf16 heads
-// of 128 x 128: 1 sequence x 8192 rows x 32 heads 471 us against 502, 32768 rows
-// 1687 against 1961, the training step of 8192 rows x 16 heads 1029 against 1720.
+// of 128 x 128: 1 sequence x 8192 rows x 32 heads 468 us against 502, 32768 rows
+// 1668 against 1961, the training step of 8192 rows x 16 heads 1053 against 1720.
 // With more than 50 walks the two passes would be longer than the one; with
 // offsets the parts would depend on what the host has not read.
 int64_t delta_parts(int64_t walks, int64_t chunks) {
