@@ -15,9 +15,7 @@
 // shared memory as they are stored.  What is not itself bf16 is two bf16
 // (split2): 16 bits, 2^-18 of a number at most is lost; of two such all four
 // products are taken (without the smallest a call took 1% less, and
-// the gradient of g was up to a fifth further off).  The weights of a bf16 output
-// are one bf16 each (two more tiles would not fit): they cost at most 2^-9 of
-// the output's terms.
+// the gradient of g was up to a fifth further off).
 //
 // Sixteen warps do this (with eight, twice the registers and rows each, a chunk
 // took 1.2 times as long); of four more one issues the products (a warp that issues
@@ -65,12 +63,15 @@ struct ChainSpace {
     static constexpr int kP = kPieces<T>;
     static constexpr uint32_t kTileBytes = kChunk * kTileRow;  // of 64 x 64
     static constexpr uint32_t kKeys = kChunk * KD * 2, kValues = kChunk * kMostValues * 2;
-    static constexpr int kWeightPieces = kBack || kP == 2 ? 2 : 1;
     static constexpr uint32_t k = 0, q = k + kP * kKeys, v = q + kP * kKeys;
     static constexpr uint32_t inverse = v + (kBack ? kP * kValues : kChunk * kMostValues * uint32_t(sizeof(T)));
-    static constexpr uint32_t weights = inverse + 2 * kTileBytes, bytes = weights + kWeightPieces * kTileBytes;
+    static constexpr uint32_t weights = inverse + 2 * kTileBytes, bytes = weights + 2 * kTileBytes;
     static constexpr int kStages = kMaps ? 2 : 1;
-    static constexpr uint32_t out = kStages * bytes, kOut = kBack ? 0 : kChunk * kMostValues * uint32_t(sizeof(T));
+    // With two stages there is no room for outputs on their way beside the two
+    // pieces of the weights and what is kept: they wait where a state would be
+    // kept, or, if one is, in the place of a chunk's V, which nothing reads by then.
+    static constexpr bool kOutInV = kMaps && !kBack;
+    static constexpr uint32_t out = kStages * bytes, kOut = kBack || kOutInV ? 0 : kChunk * kMostValues * uint32_t(sizeof(T));
     static constexpr uint32_t keep = out + kOut, kKeep = 2 * kMostValues * KD * 2;
     static_assert(kKeep >= 2 * kValues, "the corrections fit the kept state's place");
     static constexpr size_t kAll = 1024 + keep + kKeep;
@@ -127,7 +128,8 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
         for (int i = 0; i < 3; ++i) mbar_init(&ready[i], kChainThreads / 32);
         // the planes and boxes, the decays, and, without maps, the chain's own loads
         for (int i = 0; i < 2; ++i)
-            mbar_init(&full[i], kMaps ? 3 : 2 + kChainThreads / 32), mbar_init(&empty[i], 1);
+            mbar_init(&full[i], kMaps ? 3 : 2 + kChainThreads / 32),
+                mbar_init(&empty[i], Space::kOutInV ? 1 + kChainThreads / 32 : 1);  // the products; and outputs that waited there
         mbar_init(&landed, 1);
         fence_mbar_init();
     }
@@ -221,10 +223,9 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
                     const Operand<kChunk, false> A(s + Space::weights), Al(s + Space::weights + Space::kTileBytes);
                     product_ts<kChunk, kChunk>(tm + kD1, tm + kU, A, false);
                     product_ts<kChunk, kChunk>(tm + kD1, tm + kU + 32, A, true);
-                    if constexpr (kP == 2) {
-                        product_ts<kChunk, kChunk>(tm + kD1, tm + kU, Al, true);
-                        product_ts<kChunk, kChunk>(tm + kD1, tm + kU + 32, Al, true);
-                    }
+                    product_ts<kChunk, kChunk>(tm + kD1, tm + kU, Al, true);
+                    // (the smallest product is 2^-18 of a term: nothing to a bf16 output)
+                    if constexpr (kP == 2) product_ts<kChunk, kChunk>(tm + kD1, tm + kU + 32, Al, true);
                     mma_commit(&done[4]);
                 }
                 mma_commit(&empty[st]);
@@ -239,13 +240,12 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
             const int n = rows_in(c);
             char *s = sm + st * Space::bytes;
             if (step >= kStages) wait(empty[st], round_of(step) + 1u);
-            constexpr uint32_t planes = (2 + Space::kWeightPieces) * Space::kTileBytes;
+            constexpr uint32_t planes = 4 * Space::kTileBytes;
             constexpr uint32_t boxes = 2 * Space::kKeys + Space::kValues;
             if (lane == 0) {
                 mbar_arrive_expect_tx(&full[st], planes + (kMaps && n == kChunk ? boxes : 0u));
                 bulk_load(s + Space::inverse, p.inverse + at * kChunk * kChunk, 2 * Space::kTileBytes, &full[st]);
-                bulk_load(s + Space::weights, p.weights + at * kChunk * kChunk, Space::kWeightPieces * Space::kTileBytes,
-                          &full[st]);
+                bulk_load(s + Space::weights, p.weights + at * kChunk * kChunk, 2 * Space::kTileBytes, &full[st]);
                 if constexpr (kMaps) {
                     // the rows after a short chunk's are another sequence's: they are made zeros before they count
                     uint64_t *bar = n == kChunk ? &full[st] : &landed;
@@ -379,10 +379,14 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
                 copy(reinterpret_cast<char *>(kept_rows + at * kChunk * 64 * tiles) + i * tiles * int(Space::kTileBytes),
                      sm + Space::keep + i * Space::kValues, tiles * int(Space::kTileBytes));
         };
+        // where the outputs of chunk `step` wait while the next chunk is taken
+        auto out_place = [&](int64_t step) {
+            return reinterpret_cast<T *>(sm + (Space::kOutInV && kept ? stage_of(step + 1) * Space::bytes + Space::v : Space::out));
+        };
         auto copy_out = [&](int64_t step) {
             const int64_t c = chunk_of(step);
             const int n = rows_in(c);
-            const T *from = reinterpret_cast<const T *>(sm + Space::out);
+            const T *from = out_place(step);
             T *to = delta_at<T>(p.out, batch, row0 + c * kChunk, head);
             if (p.out_wide) {
                 constexpr int kEach = 16 / int(sizeof(T)), kRow = kMostValues / kEach;
@@ -461,8 +465,8 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
 #pragma unroll
             for (int j = 0; j < kT; ++j) o[j] = from_f32<T>(fmaf(p.scale, o2[j], o1[j]) + bad);
         };
-        auto put_out = [&] {
-            T *to = reinterpret_cast<T *>(sm + Space::out) + t0 * kMostValues + dv;
+        auto put_out = [&](int64_t step) {
+            T *to = out_place(step) + t0 * kMostValues + dv;
 #pragma unroll
             for (int j = 0; j < kT; ++j) to[j * kMostValues] = o[j];
         };
@@ -504,6 +508,12 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
                 meet();
                 if (kept) copy_state(at);
                 if (!kBack && step > 1) copy_out(step - 2);
+            }
+            // V's place in the stage of the chunk before: the outputs there are on their way
+            if (Space::kOutInV && kept && step > 0) {
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&empty[stage_of(step - 1)]);
             }
             wait(full[st], round_of(step));
             const ChainRows &r = rows_of[st];
@@ -549,6 +559,7 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
                 put_rows(kR, x);
             }
             arrive(1);
+            if (Space::kOutInV && !kept && lane == 0) mbar_arrive(&empty[st]);  // V has been read
             if ((!kBack && whole_part) || kept) meet();  // every copy has read its place
             if (!kBack && whole_part) {
                 wait_done(1, step);
@@ -592,7 +603,7 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
                 copy_rows(at);
             }
             if constexpr (!kBack) {
-                if (whole_part && step > 0) put_out();
+                if (whole_part && step > 0) put_out(step - 1);
             } else if (kStages == 2 && step + 1 < chunks) {
                 prepare_side(step + 1);
             }
@@ -619,7 +630,7 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
                 meet();
                 if (chunks > 1) copy_out(chunks - 2);
                 meet();
-                put_out();
+                put_out(chunks - 1);
                 meet();
                 copy_out(chunks - 1);
             }

@@ -128,7 +128,6 @@ __global__ void __launch_bounds__(kTeam * kTeams, 4 / kTeams)
         const float scale = ok ? tid < kChunk ? beta[row] : 1.0f : __int_as_float(0x7fffffff);
         // columns that this row reads: those before it, and a query's own
         const int cols = row < c.rows ? row + (tid >= kChunk) : 0;
-        char *lo_out = p.u || kPieces<T> == 2 ? A_out + kChunk * kTileRow : nullptr;
 #pragma unroll 1
         for (int j0 = 0; j0 < kChunk; j0 += 16) {
             float f[16] = {};
@@ -152,7 +151,7 @@ __global__ void __launch_bounds__(kTeam * kTeams, 4 / kTeams)
                     float e[8];
 #pragma unroll
                     for (int l = 0; l < 8; ++l) e[l] = f[8 * j + l];
-                    store_pieces(A_out, lo_out, tile_piece(uint32_t(row), uint32_t(j0 / 8 + j)), e);
+                    store_pieces(A_out, A_out + kChunk * kTileRow, tile_piece(uint32_t(row), uint32_t(j0 / 8 + j)), e);
                 }
             }
         }

@@ -507,9 +507,9 @@ dwp_status dwp_selective_scan_step(const dwp_selective_scan_step_args *args, dwp
  * A sequence is taken in chunks of DWP_DELTA_CHUNK rows from its first.  A
  * value that is not finite reaches its own sequence and head only, there also
  * the rows before it in its chunk.  Products of two f32 numbers (states,
- * corrections, f32 rows) take each in two pieces of bf16, 16 bits together (f32
- * outputs are 3e-6 to 8e-6 off in the 2-norm, dg of a few rows up to 1.2e-5);
- * a bf16 output's own weights q.k are rounded to one.
+ * corrections, weights q.k, f32 rows) take each in two pieces of bf16, 16 bits
+ * together (f32 outputs are 3e-6 to 8e-6 off in the 2-norm, dg of a few rows up
+ * to 1.2e-5; a bf16 output by its own rounding, 1.7e-3).
  */
 #define DWP_DELTA_CHUNK 64
 typedef struct dwp_heads {
