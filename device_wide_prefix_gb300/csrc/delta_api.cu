@@ -35,13 +35,9 @@ int64_t delta_slots(const dwp_delta_args &a) {
 // Words of a kept state, keys in whole tiles, and of a chunk's kept rows, values in whole tiles.
 int64_t delta_state(const dwp_delta_args &a) { return ceil_div(a.keys, 64) * 64 * a.values; }
 int64_t delta_kept_rows(const dwp_delta_args &a) { return DWP_DELTA_CHUNK * ceil_div(a.values, 64) * 64; }
-// Whether rows with these address and stride bits are whole 16-byte pieces, and
-// whether a tensor map holds their strides (under 2^40 bytes).
+// Whether rows with these address and stride bits are whole 16-byte pieces.
 bool delta_wide(uintptr_t bits, const dwp_delta_args &a) {
     return ((bits | uintptr_t((a.keys | a.values) * size_of(a.dtype))) & 15u) == 0;
-}
-bool delta_near(const dwp_heads &x) {
-    return x.batch_stride < (int64_t(1) << 39) && x.row_stride < (int64_t(1) << 39) && x.head_stride < (int64_t(1) << 39);
 }
 
 // Parts that a call's sequences are cut in, and the words that takes (of bf16;
@@ -53,9 +49,9 @@ size_t delta_part_bytes(const dwp_delta_args &a, int64_t seqs) {
     const int64_t parts = delta_parts_of(a, seqs);
     return parts == 1 ? 0u : round16(size_t(seqs * parts * a.heads * (2 * a.keys * a.values + a.keys * a.keys)) * 4u);
 }
-void set_parts(DeltaParams &p, const dwp_delta_args &a, int64_t seqs, void *at) {
+void set_parts(DeltaParams &p, const dwp_delta_args &a, int64_t seqs, bool maps, void *at) {
     // only rows that come by maps are cut
-    p.parts = p.wide ? delta_parts_of(a, seqs) : 1, p.part_chunks = ceil_div(p.chunks, p.parts);
+    p.parts = maps ? delta_parts_of(a, seqs) : 1, p.part_chunks = ceil_div(p.chunks, p.parts);
     const int64_t places = seqs * p.parts * a.heads;
     p.part_starts = static_cast<float *>(at);
     p.part_ends = p.part_starts + places * a.keys * a.values;
@@ -116,17 +112,18 @@ dwp_status delta_forward(const dwp_delta_args &a, void *scratch, size_t *bytes, 
     if (!c.scratch(scratch, bytes, need + delta_part_bytes(a, seqs), &st)) return st;
     if (seqs == 0) return DWP_SUCCESS;
     DeltaParams p = delta_params(a, seqs, scratch);
-    p.wide = delta_wide(c.bits, a) && delta_near(a.q) && delta_near(a.k) && delta_near(a.v);
+    p.wide = delta_wide(c.bits, a);
     p.out_wide = delta_wide(out_bits, a);
-    set_parts(p, a, seqs, static_cast<char *>(scratch) + need);
     const auto t = static_cast<dwp_dtype>(a.dtype);
+    const DeltaMaps maps = delta_maps(t, p, nullptr);
+    set_parts(p, a, seqs, maps.made, static_cast<char *>(scratch) + need);
     if (a.batch * a.rows > 0) {
-        const cudaError_t err = launch_delta_local(t, p, s);
+        const cudaError_t err = launch_delta_local(t, p, maps, s);
         if (err != cudaSuccess) return launched(err);
     } else if (!a.final_state) {
         return DWP_SUCCESS;
     }
-    return launched(launch_delta_chain(t, p, s));
+    return launched(launch_delta_chain(t, p, maps, s));
 }
 
 dwp_status delta_backward(const dwp_delta_backward_args &a, void *scratch, size_t *bytes, cudaStream_t s) {
@@ -140,7 +137,7 @@ dwp_status delta_backward(const dwp_delta_backward_args &a, void *scratch, size_
     bool wide = false;
     if (n > 0) {
         c.heads(a.grad_out, f.dtype, f.batch, f.rows, f.heads, f.values, false);
-        wide = delta_wide(c.bits, f) && delta_near(f.q) && delta_near(f.k) && delta_near(f.v) && delta_near(a.grad_out);
+        wide = delta_wide(c.bits, f);
         c.dense(a.grad_q, f.dtype, n * f.key_heads * f.keys, true, false);
         c.dense(a.grad_k, f.dtype, n * f.key_heads * f.keys, true, false);
         c.dense(a.grad_v, f.dtype, n * f.heads * f.values, true, false);
@@ -168,14 +165,15 @@ dwp_status delta_backward(const dwp_delta_backward_args &a, void *scratch, size_
     char *at = static_cast<char *>(scratch);
     p.dr = reinterpret_cast<float *>(at);
     p.ends = reinterpret_cast<float *>(at + dr);
-    set_parts(p.f, f, seqs, at + dr + ends);
     p.wide = aligned(a.grad_v, 16);
     const auto t = static_cast<dwp_dtype>(f.dtype);
+    const DeltaMaps maps = delta_maps(t, p.f, &p.grad_out);
+    set_parts(p.f, f, seqs, maps.made, at + dr + ends);
     if (n > 0 || a.grad_initial_state) {
-        const cudaError_t err = launch_delta_chain_back(t, p, s);
+        const cudaError_t err = launch_delta_chain_back(t, p, maps, s);
         if (err != cudaSuccess) return launched(err);
     }
-    return n > 0 ? launched(launch_delta_grad(t, p, s)) : DWP_SUCCESS;
+    return n > 0 ? launched(launch_delta_grad(t, p, maps, s)) : DWP_SUCCESS;
 }
 
 dwp_status delta_step(const dwp_delta_step_args &a, cudaStream_t s) {

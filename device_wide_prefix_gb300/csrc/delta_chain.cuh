@@ -82,16 +82,12 @@ struct ChainRows {
     alignas(16) float beta[kChunk], first[kChunk], rest[kChunk];  // first: e^G, rest: e^{G_C - G}
 };
 
-struct ChainMaps {
-    CUtensorMap k, q, v;  // v: or grad_out
-};
-
 // kMaps: bf16 rows of whole 16-byte pieces, which come by tensor maps.  kPass: 0,
 // or 1 and 2 over parts of sequences (what a block finds in pass 1, asked in
 // every chunk, makes a chunk 1.25 times as long).
 template <class T, int KD, bool kBack, bool kMaps, int kPass>
 __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
-    delta_chain_kernel(DeltaBackwardParams bp, const __grid_constant__ ChainMaps maps) {
+    delta_chain_kernel(DeltaBackwardParams bp, const __grid_constant__ DeltaMaps maps) {
     using Space = ChainSpace<T, KD, kBack, kMaps>;
     constexpr int kP = Space::kP, kH = KD / kParts, kStages = Space::kStages;  // kH: keys of a thread
     extern __shared__ char raw[];
@@ -653,7 +649,7 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
 }
 
 template <class T, int KD, bool kBack, bool kMaps, int kPass>
-cudaError_t chain_n(const DeltaBackwardParams &p, const ChainMaps &maps, cudaStream_t s) {
+cudaError_t chain_n(const DeltaBackwardParams &p, const DeltaMaps &maps, cudaStream_t s) {
     const auto kernel = delta_chain_kernel<T, KD, kBack, kMaps, kPass>;
     constexpr size_t bytes = ChainSpace<T, KD, kBack, kMaps>::kAll;
     constexpr int threads = kChainThreads + kHelpThreads;
@@ -663,23 +659,18 @@ cudaError_t chain_n(const DeltaBackwardParams &p, const ChainMaps &maps, cudaStr
 }
 
 template <class T, int KD, bool kBack>
-cudaError_t chain_maps(const DeltaBackwardParams &p, const ChainMaps &maps, int pass, cudaStream_t s) {
+cudaError_t chain_maps(const DeltaBackwardParams &p, const DeltaMaps &maps, int pass, cudaStream_t s) {
     if (pass == 0) return chain_n<T, KD, kBack, true, 0>(p, maps, s);
     return pass == 1 ? chain_n<T, KD, kBack, true, 1>(p, maps, s) : chain_n<T, KD, kBack, true, 2>(p, maps, s);
 }
 
 template <class T, bool kBack>
-cudaError_t chain_t(const DeltaBackwardParams &p, int pass, cudaStream_t s) {
+cudaError_t chain_t(const DeltaBackwardParams &p, const DeltaMaps &maps, int pass, cudaStream_t s) {
     const DeltaParams &f = p.f;
-    ChainMaps maps = {};
-    if constexpr (kPieces<T> == 1) {
-        if (f.wide && f.batch * f.rows > 0 &&
-            delta_map(&maps.k, f.k, f.batch, f.rows, f.key_heads, f.keys, 64, true) &&
-            delta_map(&maps.q, f.q, f.batch, f.rows, f.key_heads, f.keys, 64, true) &&
-            delta_map(&maps.v, kBack ? p.grad_out : f.v, f.batch, f.rows, f.heads, f.values, kBack ? 64 : kMostValues, kBack))
+    if constexpr (kPieces<T> == 1)
+        if (maps.made)
             return f.keys <= 64 ? chain_maps<T, 64, kBack>(p, maps, pass, s) : chain_maps<T, 128, kBack>(p, maps, pass, s);
-    }
-    if (pass != 0) return cudaErrorNotSupported;  // only rows that come by maps are cut
+    // others are not cut in parts: there is no pass but the one
     return f.keys <= 64 ? chain_n<T, 64, kBack, false, 0>(p, maps, s) : chain_n<T, 128, kBack, false, 0>(p, maps, s);
 }
 

@@ -2,8 +2,8 @@
 
 namespace dwp {
 
-cudaError_t launch_delta_chain_back_f32(const DeltaBackwardParams &p, int pass, cudaStream_t s) {
-    return chain_t<float, true>(p, pass, s);
+cudaError_t launch_delta_chain_back_f32(const DeltaBackwardParams &p, const DeltaMaps &m, int pass, cudaStream_t s) {
+    return chain_t<float, true>(p, m, pass, s);
 }
 
 }  // namespace dwp

@@ -2,8 +2,8 @@
 
 namespace dwp {
 
-cudaError_t launch_delta_chain_bf16(const DeltaBackwardParams &p, int pass, cudaStream_t s) {
-    return chain_t<__nv_bfloat16, false>(p, pass, s);
+cudaError_t launch_delta_chain_bf16(const DeltaBackwardParams &p, const DeltaMaps &m, int pass, cudaStream_t s) {
+    return chain_t<__nv_bfloat16, false>(p, m, pass, s);
 }
 
 }  // namespace dwp

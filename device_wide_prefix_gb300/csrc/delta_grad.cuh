@@ -71,10 +71,6 @@ __device__ __forceinline__ float2 pair_of(uint32_t hi, uint32_t lo) {
                        __uint_as_float(hi & 0xffff0000u) + __uint_as_float(lo & 0xffff0000u));
 }
 
-struct GradMaps {
-    CUtensorMap k, q, grad_out;
-};
-
 // Eight numbers in three pieces of bf16.
 __device__ __forceinline__ void store_thirds(char *hi, char *lo, char *third, uint32_t at, const float (&f)[8]) {
     uint32_t h[4], l[4], t[4];
@@ -93,7 +89,7 @@ __device__ __forceinline__ void store_thirds(char *hi, char *lo, char *third, ui
 // kMaps: bf16 rows of whole 16-byte pieces, which come by tensor maps.
 template <class T, bool kMaps>
 __global__ void __launch_bounds__(kGradThreads, 1)
-    delta_grad_kernel(DeltaBackwardParams bp, const __grid_constant__ GradMaps maps) {
+    delta_grad_kernel(DeltaBackwardParams bp, const __grid_constant__ DeltaMaps maps) {
     using Space = GradSpace<T>;
     constexpr int kP = Space::kP;
     constexpr uint32_t kRows = Space::kRows, kState = Space::kState, kTileBytes = kChunk * kTileRow;
@@ -200,7 +196,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
                 const int r = int(c.row), b = int(c.batch);
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    map_load(sm + Space::stack + x * 2 * kTileBytes, &maps.grad_out, &bars[3], x * 64, head, r, b);
+                    map_load(sm + Space::stack + x * 2 * kTileBytes, &maps.v, &bars[3], x * 64, head, r, b);
                     if (h == 0) {
                         map_load(sm + Space::k + x * kTileBytes, &maps.k, &bars[3], x * 64, kh, r, b);
                         map_load(sm + Space::q + x * kTileBytes, &maps.q, &bars[3], x * 64, kh, r, b);
@@ -481,7 +477,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
 }
 
 template <class T, bool kMaps>
-cudaError_t grad_k(const DeltaBackwardParams &p, const GradMaps &maps, cudaStream_t s) {
+cudaError_t grad_k(const DeltaBackwardParams &p, const DeltaMaps &maps, cudaStream_t s) {
     const auto kernel = delta_grad_kernel<T, kMaps>;
     constexpr size_t bytes = GradSpace<T>::kAll;
     if (device_blocks(reinterpret_cast<const void *>(kernel), kGradThreads, bytes) == 0) return cudaErrorInvalidConfiguration;
@@ -489,15 +485,9 @@ cudaError_t grad_k(const DeltaBackwardParams &p, const GradMaps &maps, cudaStrea
 }
 
 template <class T>
-cudaError_t grad_t(const DeltaBackwardParams &p, cudaStream_t s) {
-    const DeltaParams &f = p.f;
-    GradMaps maps = {};
-    if constexpr (kPieces<T> == 1) {
-        if (f.wide && delta_map(&maps.k, f.k, f.batch, f.rows, f.key_heads, f.keys, 64, true) &&
-            delta_map(&maps.q, f.q, f.batch, f.rows, f.key_heads, f.keys, 64, true) &&
-            delta_map(&maps.grad_out, p.grad_out, f.batch, f.rows, f.heads, f.values, 64, true))
-            return grad_k<T, true>(p, maps, s);
-    }
+cudaError_t grad_t(const DeltaBackwardParams &p, const DeltaMaps &maps, cudaStream_t s) {
+    if constexpr (kPieces<T> == 1)
+        if (maps.made) return grad_k<T, true>(p, maps, s);
     return grad_k<T, false>(p, maps, s);
 }
 

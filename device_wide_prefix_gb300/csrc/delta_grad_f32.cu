@@ -2,6 +2,8 @@
 
 namespace dwp {
 
-cudaError_t launch_delta_grad_f32(const DeltaBackwardParams &p, cudaStream_t s) { return grad_t<float>(p, s); }
+cudaError_t launch_delta_grad_f32(const DeltaBackwardParams &p, const DeltaMaps &m, cudaStream_t s) {
+    return grad_t<float>(p, m, s);
+}
 
 }  // namespace dwp

@@ -27,15 +27,11 @@ constexpr int kPitch = kChunk + 4;  // words a row of L and T: rows start on 16 
 template <class T, int KD, int kTeams>
 constexpr size_t local_bytes = 1024 + size_t(kPieces<T>) * 2 * kChunk * KD * 2 + size_t(kTeams) * kChunk * kPitch * 4;
 
-struct LocalMaps {
-    CUtensorMap k, q;
-};
-
 // kMaps: bf16 rows of whole 16-byte pieces, which come by tensor maps.  (Rows
 // past a short chunk's are another sequence's: nothing that is kept reads them.)
 template <class T, int KD, bool kMaps, int kTeams>
 __global__ void __launch_bounds__(kTeam * kTeams, 4 / kTeams)
-    delta_local_kernel(DeltaParams p, const __grid_constant__ LocalMaps maps) {
+    delta_local_kernel(DeltaParams p, const __grid_constant__ DeltaMaps maps) {
     extern __shared__ char raw[];
     __shared__ Sum2 sums_[kTeams][kChunk];
     __shared__ float beta_[kTeams][kChunk];
@@ -249,7 +245,7 @@ __global__ void __launch_bounds__(kTeam * kTeams, 4 / kTeams)
 }
 
 template <class T, int KD, bool kMaps, int kTeams>
-cudaError_t local_n(const DeltaParams &p, const LocalMaps &maps, cudaStream_t s) {
+cudaError_t local_n(const DeltaParams &p, const DeltaMaps &maps, cudaStream_t s) {
     const auto kernel = delta_local_kernel<T, KD, kMaps, kTeams>;
     constexpr size_t bytes = local_bytes<T, KD, kTeams>;
     if (device_blocks(reinterpret_cast<const void *>(kernel), kTeam * kTeams, bytes) == 0) return cudaErrorInvalidConfiguration;
@@ -263,27 +259,23 @@ cudaError_t local_n(const DeltaParams &p, const LocalMaps &maps, cudaStream_t s)
 // heads 196 against 171, 512 rows x 2 key heads of 16 heads 74 against 61; off 16
 // bytes, 4 x 2048 rows x 16 key heads, 581 against 497, in f32 504 against 440.
 template <class T, int KD, bool kMaps>
-cudaError_t local_k(const DeltaParams &p, const LocalMaps &maps, cudaStream_t s) {
+cudaError_t local_k(const DeltaParams &p, const DeltaMaps &maps, cudaStream_t s) {
     const bool many = kMaps && p.slots * p.key_heads > 3 * kSMs;
     return p.heads == p.key_heads || many ? local_n<T, KD, kMaps, 1>(p, maps, s) : local_n<T, KD, kMaps, 2>(p, maps, s);
 }
 
 template <class T>
-cudaError_t local_t(const DeltaParams &p, cudaStream_t s) {
-    LocalMaps maps = {};
-    if constexpr (kPieces<T> == 1) {
-        if (p.wide && delta_map(&maps.k, p.k, p.batch, p.rows, p.key_heads, p.keys, 64, true) &&
-            delta_map(&maps.q, p.q, p.batch, p.rows, p.key_heads, p.keys, 64, true))
-            return p.keys <= 64 ? local_k<T, 64, true>(p, maps, s) : local_k<T, 128, true>(p, maps, s);
-    }
+cudaError_t local_t(const DeltaParams &p, const DeltaMaps &maps, cudaStream_t s) {
+    if constexpr (kPieces<T> == 1)
+        if (maps.made) return p.keys <= 64 ? local_k<T, 64, true>(p, maps, s) : local_k<T, 128, true>(p, maps, s);
     return p.keys <= 64 ? local_k<T, 64, false>(p, maps, s) : local_k<T, 128, false>(p, maps, s);
 }
 
 }  // namespace
 
-cudaError_t launch_delta_local(dwp_dtype t, const DeltaParams &p, cudaStream_t s) {
-    if (t == DWP_F32) return local_t<float>(p, s);
-    return t == DWP_BF16 ? local_t<__nv_bfloat16>(p, s) : local_t<__half>(p, s);
+cudaError_t launch_delta_local(dwp_dtype t, const DeltaParams &p, const DeltaMaps &m, cudaStream_t s) {
+    if (t == DWP_F32) return local_t<float>(p, m, s);
+    return t == DWP_BF16 ? local_t<__nv_bfloat16>(p, m, s) : local_t<__half>(p, m, s);
 }
 
 }  // namespace dwp

@@ -8,6 +8,12 @@
 
 namespace dwp {
 
+#if DWP_DELTA_TEST
+// Build for tests (-DDWP_DELTA_TEST=1): calls as where no tensor map can be made.
+static std::atomic<int> delta_test_no_maps{0};
+extern "C" void dwp_delta_test_no_maps(int on) { delta_test_no_maps = on; }
+#endif
+
 namespace {
 
 using EncodeMap = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
@@ -16,6 +22,9 @@ using EncodeMap = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, v
 
 // The driver's encoder, by way of the runtime, so that nothing links the driver.
 EncodeMap encode_map() {
+#if DWP_DELTA_TEST
+    if (delta_test_no_maps) return nullptr;
+#endif
     static std::atomic<void *> known{nullptr};
     void *f = known.load();
     if (!f) {
@@ -30,8 +39,8 @@ EncodeMap encode_map() {
     return reinterpret_cast<EncodeMap>(f);
 }
 
-}  // namespace
-
+// A map of rows [batch][rows][heads][size] for boxes `columns` wide, exchanged as
+// tiles are if `tiles`.
 bool delta_map(CUtensorMap *map, const DeltaRows &r, int64_t batch, int64_t rows, int64_t heads, int64_t size, int columns,
                bool tiles) {
     const EncodeMap encode = encode_map();
@@ -48,22 +57,20 @@ bool delta_map(CUtensorMap *map, const DeltaRows &r, int64_t batch, int64_t rows
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-namespace {
-
-cudaError_t chain_pass(dwp_dtype t, const DeltaBackwardParams &p, bool back, int pass, cudaStream_t s) {
+cudaError_t chain_pass(dwp_dtype t, const DeltaBackwardParams &p, const DeltaMaps &m, bool back, int pass, cudaStream_t s) {
     if (back) {
-        if (t == DWP_F32) return launch_delta_chain_back_f32(p, pass, s);
-        return t == DWP_BF16 ? launch_delta_chain_back_bf16(p, pass, s) : launch_delta_chain_back_f16(p, pass, s);
+        if (t == DWP_F32) return launch_delta_chain_back_f32(p, m, pass, s);
+        return t == DWP_BF16 ? launch_delta_chain_back_bf16(p, m, pass, s) : launch_delta_chain_back_f16(p, m, pass, s);
     }
-    if (t == DWP_F32) return launch_delta_chain_f32(p, pass, s);
-    return t == DWP_BF16 ? launch_delta_chain_bf16(p, pass, s) : launch_delta_chain_f16(p, pass, s);
+    if (t == DWP_F32) return launch_delta_chain_f32(p, m, pass, s);
+    return t == DWP_BF16 ? launch_delta_chain_bf16(p, m, pass, s) : launch_delta_chain_f16(p, m, pass, s);
 }
 
-cudaError_t chain(dwp_dtype t, const DeltaBackwardParams &p, bool back, cudaStream_t s) {
-    if (p.f.parts == 1) return chain_pass(t, p, back, 0, s);
-    cudaError_t err = chain_pass(t, p, back, 1, s);
+cudaError_t chain(dwp_dtype t, const DeltaBackwardParams &p, const DeltaMaps &m, bool back, cudaStream_t s) {
+    if (p.f.parts == 1) return chain_pass(t, p, m, back, 0, s);
+    cudaError_t err = chain_pass(t, p, m, back, 1, s);
     if (err == cudaSuccess) err = launch_delta_join(p.f, s);
-    return err == cudaSuccess ? chain_pass(t, p, back, 2, s) : err;
+    return err == cudaSuccess ? chain_pass(t, p, m, back, 2, s) : err;
 }
 
 constexpr int kJoinThreads = 256, kJoinCols = 16, kJoinKeys = 128, kJoinPitch = kJoinKeys + 1;
@@ -109,6 +116,16 @@ __global__ void __launch_bounds__(kJoinThreads) delta_join_kernel(DeltaParams p)
 
 }  // namespace
 
+DeltaMaps delta_maps(dwp_dtype t, const DeltaParams &p, const DeltaRows *grad_out) {
+    DeltaMaps m = {};
+    m.made = t == DWP_BF16 && p.wide && p.batch * p.rows > 0 &&
+             delta_map(&m.k, p.k, p.batch, p.rows, p.key_heads, p.keys, 64, true) &&
+             delta_map(&m.q, p.q, p.batch, p.rows, p.key_heads, p.keys, 64, true) &&
+             delta_map(&m.v, grad_out ? *grad_out : p.v, p.batch, p.rows, p.heads, p.values, grad_out ? 64 : 128,
+                       grad_out != nullptr);
+    return m;
+}
+
 // Parts that a walk along a sequence is cut into: as many as fill the GPU's
 // blocks in pass 1, eight chunks each at least, and three or none (of two parts
 // the second would wait for the first as before).  Cut against uncut, bf16 heads
@@ -131,18 +148,18 @@ cudaError_t launch_delta_join(const DeltaParams &p, cudaStream_t s) {
                       dim3(kJoinThreads), kJoinBytes, s, p);
 }
 
-cudaError_t launch_delta_chain(dwp_dtype t, const DeltaParams &p, cudaStream_t s) {
+cudaError_t launch_delta_chain(dwp_dtype t, const DeltaParams &p, const DeltaMaps &m, cudaStream_t s) {
     DeltaBackwardParams b = {};
     b.f = p;
-    return chain(t, b, false, s);
+    return chain(t, b, m, false, s);
 }
-cudaError_t launch_delta_chain_back(dwp_dtype t, const DeltaBackwardParams &p, cudaStream_t s) {
-    return chain(t, p, true, s);
+cudaError_t launch_delta_chain_back(dwp_dtype t, const DeltaBackwardParams &p, const DeltaMaps &m, cudaStream_t s) {
+    return chain(t, p, m, true, s);
 }
 
-cudaError_t launch_delta_grad(dwp_dtype t, const DeltaBackwardParams &p, cudaStream_t s) {
-    if (t == DWP_F32) return launch_delta_grad_f32(p, s);
-    return t == DWP_BF16 ? launch_delta_grad_bf16(p, s) : launch_delta_grad_f16(p, s);
+cudaError_t launch_delta_grad(dwp_dtype t, const DeltaBackwardParams &p, const DeltaMaps &m, cudaStream_t s) {
+    if (t == DWP_F32) return launch_delta_grad_f32(p, m, s);
+    return t == DWP_BF16 ? launch_delta_grad_bf16(p, m, s) : launch_delta_grad_f16(p, m, s);
 }
 
 }  // namespace dwp

@@ -237,11 +237,6 @@ struct DeltaRows {
     char *data;
     int64_t batch, row, head;  // strides in elements
 };
-// A map of bf16 rows [batch][rows][heads][size] for boxes of 64 rows of one
-// head, `columns` wide, exchanged as tiles are (tensor.cuh) if `tiles`.  False
-// where the tensor's strides are past what a map holds.
-bool delta_map(CUtensorMap *map, const DeltaRows &r, int64_t batch, int64_t rows, int64_t heads, int64_t size, int columns,
-               bool tiles);
 struct DeltaParams {
     int keys, values, key_heads, heads;
     int64_t batch, rows, sequences, chunks, slots;  // chunks: of a batch entry; slots: chunk places in all
@@ -263,6 +258,14 @@ struct DeltaParams {
     int64_t parts, part_chunks;
     float *part_starts, *part_ends, *part_maps;
 };
+// Tensor maps of a call's bf16 rows, for all its kernels: boxes of 64 rows of one
+// head.  Not made for other rows, nor where a stride is past what a map holds or
+// the driver has no encoder: then the kernels load the rows themselves.
+struct DeltaMaps {
+    bool made;
+    CUtensorMap k, q;  // tiles of 64 columns (tensor.cuh)
+    CUtensorMap v;     // forward: v, rows as they are; back: grad_out, tiles
+};
 struct DeltaBackwardParams {
     DeltaParams f;
     DeltaRows grad_out, grad_q, grad_k, grad_v, grad_g, grad_beta;
@@ -281,24 +284,25 @@ struct DeltaStepParams {
     int64_t state_slot;
     const int32_t *slots;
 };
-cudaError_t launch_delta_local(dwp_dtype t, const DeltaParams &p, cudaStream_t s);
+DeltaMaps delta_maps(dwp_dtype t, const DeltaParams &p, const DeltaRows *grad_out);
+cudaError_t launch_delta_local(dwp_dtype t, const DeltaParams &p, const DeltaMaps &m, cudaStream_t s);
 // The cut: parts that fill the GPU's blocks of one chain each, eight chunks or
 // more to a part; 1 for none.
 int64_t delta_parts(int64_t walks, int64_t chunks);
 // States at the parts' first chunks, from the first's and each part's map.
 cudaError_t launch_delta_join(const DeltaParams &p, cudaStream_t s);
-cudaError_t launch_delta_chain(dwp_dtype t, const DeltaParams &p, cudaStream_t s);
-cudaError_t launch_delta_chain_back(dwp_dtype t, const DeltaBackwardParams &p, cudaStream_t s);
-cudaError_t launch_delta_chain_f32(const DeltaBackwardParams &p, int pass, cudaStream_t s);
-cudaError_t launch_delta_chain_back_f32(const DeltaBackwardParams &p, int pass, cudaStream_t s);
-cudaError_t launch_delta_chain_bf16(const DeltaBackwardParams &p, int pass, cudaStream_t s);
-cudaError_t launch_delta_chain_back_bf16(const DeltaBackwardParams &p, int pass, cudaStream_t s);
-cudaError_t launch_delta_chain_f16(const DeltaBackwardParams &p, int pass, cudaStream_t s);
-cudaError_t launch_delta_chain_back_f16(const DeltaBackwardParams &p, int pass, cudaStream_t s);
-cudaError_t launch_delta_grad(dwp_dtype t, const DeltaBackwardParams &p, cudaStream_t s);
-cudaError_t launch_delta_grad_f32(const DeltaBackwardParams &p, cudaStream_t s);
-cudaError_t launch_delta_grad_bf16(const DeltaBackwardParams &p, cudaStream_t s);
-cudaError_t launch_delta_grad_f16(const DeltaBackwardParams &p, cudaStream_t s);
+cudaError_t launch_delta_chain(dwp_dtype t, const DeltaParams &p, const DeltaMaps &m, cudaStream_t s);
+cudaError_t launch_delta_chain_back(dwp_dtype t, const DeltaBackwardParams &p, const DeltaMaps &m, cudaStream_t s);
+cudaError_t launch_delta_chain_f32(const DeltaBackwardParams &p, const DeltaMaps &m, int pass, cudaStream_t s);
+cudaError_t launch_delta_chain_back_f32(const DeltaBackwardParams &p, const DeltaMaps &m, int pass, cudaStream_t s);
+cudaError_t launch_delta_chain_bf16(const DeltaBackwardParams &p, const DeltaMaps &m, int pass, cudaStream_t s);
+cudaError_t launch_delta_chain_back_bf16(const DeltaBackwardParams &p, const DeltaMaps &m, int pass, cudaStream_t s);
+cudaError_t launch_delta_chain_f16(const DeltaBackwardParams &p, const DeltaMaps &m, int pass, cudaStream_t s);
+cudaError_t launch_delta_chain_back_f16(const DeltaBackwardParams &p, const DeltaMaps &m, int pass, cudaStream_t s);
+cudaError_t launch_delta_grad(dwp_dtype t, const DeltaBackwardParams &p, const DeltaMaps &m, cudaStream_t s);
+cudaError_t launch_delta_grad_f32(const DeltaBackwardParams &p, const DeltaMaps &m, cudaStream_t s);
+cudaError_t launch_delta_grad_bf16(const DeltaBackwardParams &p, const DeltaMaps &m, cudaStream_t s);
+cudaError_t launch_delta_grad_f16(const DeltaBackwardParams &p, const DeltaMaps &m, cudaStream_t s);
 cudaError_t launch_delta_step(dwp_dtype t, const DeltaStepParams &p, cudaStream_t s);
 
 struct NormParams {
