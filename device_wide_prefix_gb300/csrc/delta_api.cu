@@ -92,6 +92,9 @@ DeltaParams delta_params(const dwp_delta_args &a, int64_t seqs, void *scratch) {
     p.q = delta_rows(a.q), p.k = delta_rows(a.k), p.v = delta_rows(a.v), p.out = delta_rows(a.out);
     p.g = delta_rows(a.g), p.beta = delta_rows(a.beta);
     p.offsets = a.offsets, p.initial = a.initial_state, p.final = a.final_state;
+#ifdef DWP_DELTA_TEST
+    delta_stall(p);
+#endif
     const int64_t places = p.slots * a.heads;
     p.inverse = a.checkpoints ? a.checkpoints : static_cast<float *>(scratch);
     p.weights = p.inverse + places * kTile;

@@ -82,18 +82,76 @@ struct ChainRows {
     alignas(16) float beta[kChunk], first[kChunk], rest[kChunk];  // first: e^G, rest: e^{G_C - G}
 };
 
+// A block's part of the walk along its sequence, and what it finds: the whole
+// (pass 0, or a part's own outputs), E or M.
+template <bool kBack, int kPass>
+struct ChainWalk {
+    int64_t batch, slot0, part;
+    int row0, rows, chunks, last;  // chunks from slot0 on, and the one that a walk back begins at (rows are under 2^31)
+    bool unit, whole_part;         // finds M; has outputs of its own
+    int values;
+    __device__ __forceinline__ explicit ChainWalk(const DeltaParams &p) {
+        int64_t row, all;
+        delta_sequence(p, blockIdx.x, batch, row, all, slot0);
+        part = kPass == 0 ? 0 : kPass == 1 ? (blockIdx.z + 1) / 2 : blockIdx.z + 1;
+        unit = kPass == 1 && part > 0 && blockIdx.z % 2 == 0, whole_part = kPass != 1 || part == 0;
+        const int64_t all_chunks = (all + kChunk - 1) / kChunk, before = kPass != 0 ? min(part * p.part_chunks, all_chunks) : 0;
+        last = int(all_chunks - 1 - before);
+        chunks = int(kPass != 0 ? min(p.part_chunks, all_chunks - before) : all_chunks);
+        const int64_t skip = kBack ? 0 : before;
+        row0 = int(row + skip * kChunk), rows = int(all - skip * kChunk), slot0 += skip;
+        values = unit ? p.keys : p.values;
+    }
+    __device__ __forceinline__ int chunk_of(int step) const { return kBack ? last - step : step; }
+    __device__ __forceinline__ int rows_in(int c) const { return min(rows - c * kChunk, kChunk); }
+    // Where the state at its end goes: the last part's is the sequence's, another's own is the next one's start.
+    __device__ __forceinline__ float *end_state(const DeltaBackwardParams &bp) const {
+        const DeltaParams &p = bp.f;
+        const bool last = kPass == 0 || (kPass == 2 && part + 1 == p.parts);
+        float *to = last ? kBack ? bp.grad_initial : p.final : unit ? p.part_maps : kPass == 1 ? p.part_ends : nullptr;
+        int64_t place = last ? int64_t(blockIdx.x) * p.heads + blockIdx.y : (blockIdx.x * p.parts + part) * p.heads + blockIdx.y;
+        if (kPass == 1 && part == 0) to = p.part_starts, place += p.heads;
+        return to ? to + place * p.keys * values : nullptr;
+    }
+};
+
+// Of a walk in which a wait was in vain: NaN in all that it writes.  By the whole block.
+template <class T, int KD, bool kBack, int kPass>
+__device__ __noinline__ void chain_give_up(const DeltaBackwardParams &bp) {
+    constexpr int kThreads = kChainThreads + kHelpThreads;
+    const DeltaParams &p = bp.f;
+    const ChainWalk<kBack, kPass> walk(p);
+    const int tid = threadIdx.x, head = blockIdx.y, values = walk.values, tiles = (values + 63) / 64;
+    auto fill = [&](float *to, int words) {
+        for (int e = tid; e < words; e += kThreads) to[e] = __uint_as_float(0xffffffffu);  // in pairs of bf16 too
+    };
+    float *kept = kBack ? bp.ends : p.states, *kept_rows = kBack ? bp.dr : p.u;
+    for (int step = 0; walk.whole_part && kept && step < walk.chunks; ++step) {
+        const int64_t at = (walk.slot0 + walk.chunk_of(step)) * p.heads + head;
+        fill(kept + at * KD * values, KD * values);
+        fill(kept_rows + at * kChunk * 64 * tiles, kChunk * 64 * tiles);
+    }
+    for (int step = 0; !kBack && walk.whole_part && step < walk.chunks; ++step) {
+        const int c = walk.chunk_of(step);
+        T *to = delta_at<T>(p.out, walk.batch, walk.row0 + c * kChunk, head);
+        for (int e = tid; e < walk.rows_in(c) * values; e += kThreads)
+            to[e / values * p.out.row + e % values] = from_f32<T>(not_a_number());
+    }
+    if (float *to = walk.end_state(bp)) fill(to, p.keys * values);
+}
+
 // kMaps: bf16 rows of whole 16-byte pieces, which come by tensor maps.  kPass: 0,
 // or 1 and 2 over parts of sequences (what a block finds in pass 1, asked in
 // every chunk, makes a chunk 1.25 times as long).
 template <class T, int KD, bool kBack, bool kMaps, int kPass>
 __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
-    delta_chain_kernel(DeltaBackwardParams bp, const __grid_constant__ DeltaMaps maps) {
+    delta_chain_kernel(const __grid_constant__ DeltaBackwardParams bp, const __grid_constant__ DeltaMaps maps) {
     using Space = ChainSpace<T, KD, kBack, kMaps>;
     constexpr int kP = Space::kP, kH = KD / kParts, kStages = Space::kStages;  // kH: keys of a thread
     extern __shared__ char raw[];
     __shared__ ChainRows rows_of[2];
-    __shared__ uint64_t done[5], ready[3], full[2], empty[2], landed;
-    __shared__ uint32_t tmem;
+    __shared__ uint64_t done[5], ready[3], full[2], empty[2], landed[2], drained;
+    __shared__ uint32_t tmem, in_vain;
     const DeltaParams &p = bp.f;
     char *sm = reinterpret_cast<char *>((reinterpret_cast<uintptr_t>(raw) + 1023) / 1024 * 1024);
     pdl_trigger();
@@ -101,32 +159,33 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
     const int tid = threadIdx.x, lane = tid % 32, warp = __shfl_sync(0xffffffffu, tid / 32, 0);
     const int head = blockIdx.y, kh = head / (p.heads / p.key_heads), keys = p.keys;
     const int64_t seq = blockIdx.x;
-    int64_t batch, row0, rows, slot0;
-    delta_sequence(p, seq, batch, row0, rows, slot0);
-    // this block's part of the walk, and what it finds: the whole (pass 0, or the
-    // part's own outputs), E or M
-    const int64_t all_chunks = (rows + kChunk - 1) / kChunk;
+    const ChainWalk<kBack, kPass> walk(p);
     constexpr bool kCut = kPass != 0;
-    const int64_t part = kPass == 0 ? 0 : kPass == 1 ? (blockIdx.z + 1) / 2 : blockIdx.z + 1;
-    const bool unit = kPass == 1 && part > 0 && blockIdx.z % 2 == 0, whole_part = kPass != 1 || part == 0;
-    const int64_t first_step = kCut ? part * p.part_chunks : 0;
-    const int64_t chunks = !kCut ? all_chunks : max(min(p.part_chunks, all_chunks - first_step), int64_t(0));
-    const int values = unit ? keys : p.values;
-    auto chunk_of = [&](int64_t step) { return kBack ? all_chunks - 1 - first_step - step : first_step + step; };
-    auto rows_in = [&](int64_t c) { return int(min(rows - c * kChunk, int64_t(kChunk))); };
-    auto stage_of = [&](int64_t step) { return kStages == 2 ? int(step & 1) : 0; };
-    auto round_of = [&](int64_t step) { return uint32_t(step / kStages) & 1u; };
+    const int64_t batch = walk.batch, slot0 = walk.slot0, part = walk.part;
+    const int row0 = walk.row0, chunks = walk.chunks;
+    const bool unit = walk.unit, whole_part = walk.whole_part;
+    const int values = walk.values;
+    auto chunk_of = [&](int step) { return walk.chunk_of(step); };
+    auto rows_in = [&](int c) { return walk.rows_in(c); };
+    auto stage_of = [&](int step) { return kStages == 2 ? step & 1 : 0; };
+    auto round_of = [&](int step) { return uint32_t(step) / kStages & 1u; };
     float *const kept = whole_part ? kBack ? bp.ends : p.states : nullptr, *const kept_rows = kBack ? bp.dr : p.u;
 
+#ifdef DWP_DELTA_TEST
+    __shared__ uint64_t never;
+    if (tid == 0) mbar_init(&never, 1);
+    Stall stall{&never, p.stall_site, p.stall_skip};
+#endif
     if (tid == 0) {
+        in_vain = 0;
         for (int i = 0; i < 5; ++i) mbar_init(&done[i], 1);
         // one arrival a warp: 256 on one word take a thousand cycles
         for (int i = 0; i < 3; ++i) mbar_init(&ready[i], kChainThreads / 32);
         // the planes and boxes, the decays, and, without maps, the chain's own loads
         for (int i = 0; i < 2; ++i)
-            mbar_init(&full[i], kMaps ? 3 : 2 + kChainThreads / 32),
+            mbar_init(&landed[i], 1), mbar_init(&full[i], kMaps ? 2 : 2 + kChainThreads / 32),
                 mbar_init(&empty[i], Space::kOutInV ? 1 + kChainThreads / 32 : 1);  // the products; and outputs that waited there
-        mbar_init(&landed, 1);
+        mbar_init(&drained, 1);
         fence_mbar_init();
     }
     if (warp == 0) tmem_alloc(&tmem, 512);
@@ -137,8 +196,14 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
     // operands: the state (hi, lo), R or U (hi, lo), U as it is or the queries' side (hi, lo)
     const uint32_t tm = tmem;
     constexpr uint32_t kD0 = 0, kD1 = 64, kDS = 128, kS = 256, kR = 384, kU = 448;
+    // No wait of this thread was in vain.  Where one was, a helper arrives nowhere and
+    // issues nothing more; the chain's threads go on to the walk's end, where they
+    // ask one another (asked each chunk, a walk took 1 to 6% longer).
     bool ok = true;
-    auto wait = [&](uint64_t &bar, uint32_t parity) {
+    auto wait = [&](uint64_t &bar, uint32_t parity, [[maybe_unused]] WaitSite site) {
+#ifdef DWP_DELTA_TEST
+        if (ok && stall.at(site)) ok = false;
+#endif
         if (ok) ok = mma_wait(&bar, parity & 1u);
     };
 
@@ -146,14 +211,14 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
     else set_registers_up<kChainRegisters>();
     if (warp == kIssueWarp) {
         const bool one = elect_one();
-        for (int64_t step = 0; step < chunks; ++step) {
+        for (int step = 0; step < chunks; ++step) {
             const int st = stage_of(step);
             char *s = sm + st * Space::bytes;
             const Operand<kChunk, true> Ko(s + Space::k), Klo(s + Space::k + Space::kKeys);
-            wait(full[st], round_of(step));
-            wait(ready[0], uint32_t(step));
+            wait(full[st], round_of(step), kIssueRows);
+            wait(ready[0], uint32_t(step), kIssueState);
             tmem_fence_after();
-            if (one) {
+            if (one && ok) {
                 const Operand<kChunk, false> K(s + Space::k), Kl(s + Space::k + Space::kKeys);
                 product_ts<kChunk, KD>(tm + kD0, tm + kS, K, false);
                 product_ts<kChunk, KD>(tm + kD0, tm + kS + KD / 2, K, true);
@@ -185,9 +250,9 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
                 mma_commit(&done[1]);
             }
             __syncwarp();
-            wait(ready[1], uint32_t(step));
+            wait(ready[1], uint32_t(step), kIssueSides);
             tmem_fence_after();
-            if (one) {
+            if (one && ok) {
                 const Operand<kChunk, kBack> inv(s + Space::inverse), invl(s + Space::inverse + Space::kTileBytes);
                 product_ts<kChunk, kChunk>(tm + kD0, tm + kR, inv, false);
                 product_ts<kChunk, kChunk>(tm + kD0, tm + kR + 32, inv, true);
@@ -196,9 +261,9 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
                 mma_commit(&done[2]);
             }
             __syncwarp();
-            wait(ready[2], uint32_t(step));
+            wait(ready[2], uint32_t(step), kIssueCorrections);
             tmem_fence_after();
-            if (one) {
+            if (one && ok) {
                 product_ts<KD, kChunk>(tm + kDS, tm + kR, Ko, false);
                 product_ts<KD, kChunk>(tm + kDS, tm + kR + 32, Ko, true);
                 if constexpr (kP == 2) {
@@ -228,25 +293,29 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
             }
             __syncwarp();
         }
+        // however the walk ended, no product is on its way after this
+        if (one) mma_commit(&drained);
+        mma_wait(&drained, 0);
+        __syncwarp();
     } else if (warp > kIssueWarp) {
         const bool loads = warp == kIssueWarp + 1, decays = warp == kIssueWarp + 2;
-        auto load = [&](int64_t step) {
+        // A chunk's copies, and, when they have landed, word of it.  `asked`: they were issued.
+        auto load = [&](int step) {
             const int st = stage_of(step);
-            const int64_t c = chunk_of(step), row = row0 + c * kChunk, at = (slot0 + c) * p.heads + head;
-            const int n = rows_in(c);
+            const int c = chunk_of(step), row = row0 + c * kChunk;
+            const int64_t at = (slot0 + c) * p.heads + head;
             char *s = sm + st * Space::bytes;
-            if (step >= kStages) wait(empty[st], round_of(step) + 1u);
+            if (step >= kStages) wait(empty[st], round_of(step) + 1u, kLoadRoom);
             constexpr uint32_t planes = 4 * Space::kTileBytes;
-            constexpr uint32_t boxes = 2 * Space::kKeys + Space::kValues;
-            if (lane == 0) {
-                mbar_arrive_expect_tx(&full[st], planes + (kMaps && n == kChunk ? boxes : 0u));
-                bulk_load(s + Space::inverse, p.inverse + at * kChunk * kChunk, 2 * Space::kTileBytes, &full[st]);
-                bulk_load(s + Space::weights, p.weights + at * kChunk * kChunk, 2 * Space::kTileBytes, &full[st]);
+            constexpr uint32_t boxes = kMaps ? 2 * Space::kKeys + Space::kValues : 0;
+            const bool asked = __shfl_sync(0xffffffffu, ok, 0);
+            if (lane == 0 && asked) {
+                uint64_t *bar = &landed[st];
+                mbar_arrive_expect_tx(bar, planes + boxes);
+                bulk_load(s + Space::inverse, p.inverse + at * kChunk * kChunk, 2 * Space::kTileBytes, bar);
+                bulk_load(s + Space::weights, p.weights + at * kChunk * kChunk, 2 * Space::kTileBytes, bar);
                 if constexpr (kMaps) {
-                    // the rows after a short chunk's are another sequence's: they are made zeros before they count
-                    uint64_t *bar = n == kChunk ? &full[st] : &landed;
-                    if (n < kChunk) mbar_arrive_expect_tx(&landed, boxes);
-                    const int r = int(row), b = int(batch);
+                    const int r = row, b = int(batch);
 #pragma unroll
                     for (int x = 0; x < KD; x += 64) {
                         map_load(s + Space::k + x * kTileRow, &maps.k, bar, x, kh, r, b);
@@ -260,10 +329,23 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
                     }
                 }
             }
+            return asked;
+        };
+        auto landing = [&](int step, bool asked) {
+            const int st = stage_of(step), n = rows_in(chunk_of(step));
+            // what was asked for is waited for, whatever else was in vain
+            bool here = asked && mma_wait(&landed[st], round_of(step));
+#ifdef DWP_DELTA_TEST
+            if (stall.at(kLoadLanded)) here = false;
+#endif
+            if (!__all_sync(0xffffffffu, here)) {
+                ok = false;
+                return;
+            }
             if constexpr (kMaps) {
+                // the rows after a short chunk's are another sequence's: they are made zeros before they count
                 if (n < kChunk) {
-                    __syncwarp();
-                    wait(landed, 0);
+                    char *s = sm + st * Space::bytes;
                     // rows of 128 bytes in tiles; of 256 in the values' forward
                     auto clear = [&](char *tile, uint32_t pitch) {
                         for (uint32_t e = uint32_t(n) * pitch / 16 + lane; e < kChunk * pitch / 16; e += 32)
@@ -272,16 +354,15 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
                     for (int x = 0; x < KD; x += 64) clear(s + Space::k + x * kTileRow, 128), clear(s + Space::q + x * kTileRow, 128);
                     if constexpr (kBack) clear(s + Space::v, 128), clear(s + Space::v + 64 * kTileRow, 128);
                     else clear(s + Space::v, 256);
-                    fence_proxy_async_smem();
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&full[st]);
             }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&full[st]);
         };
         float g[2], b[2];
-        auto read_decays = [&](int64_t step) {
-            if (step >= chunks) return;
-            const int64_t c = chunk_of(step), row = row0 + c * kChunk;
+        auto read_decays = [&](int step) {
+            const int c = chunk_of(step), row = row0 + c * kChunk;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int r = lane + 32 * i;
@@ -289,10 +370,13 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
                 b[i] = r < rows_in(c) ? delta_beta<T>(p, batch, row + r, head) : 0.0f;
             }
         };
-        auto put_decays = [&](int64_t step) {
-            if (step >= chunks) return;
+        auto put_decays = [&](int step) {
             const int st = stage_of(step);
-            if (step >= kStages) wait(empty[st], round_of(step) + 1u);
+            if (step >= kStages) wait(empty[st], round_of(step) + 1u, kDecayRoom);
+            if (!__all_sync(0xffffffffu, ok)) {
+                ok = false;
+                return;
+            }
             ChainRows &r = rows_of[st];
             Sum2 sum[2];
             delta_sums(sum, g);
@@ -306,18 +390,16 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&full[st]);
         };
-        if (decays) {
-            read_decays(0);
-            put_decays(0);
-            if (kStages == 2) read_decays(1), put_decays(1);
+        // the first stages at once, then each as it is free
+        const int first = min(chunks, kStages);
+        if (loads) {
+            bool asked[2] = {};
+            for (int step = 0; step < first; ++step) asked[step] = load(step);
+            for (int step = 0; step < first; ++step) landing(step, asked[step]);
+            for (int step = first; step < chunks; ++step) landing(step, load(step));
         }
-        if (loads && kStages == 2 && chunks > 0) load(0);
-        for (int64_t step = 0; step < chunks; ++step) {
-            if (decays) read_decays(step + kStages);
-            // a stage ahead: chunk step + 1 goes where step - 1 was
-            if (loads && (kStages == 1 || step + 1 < chunks)) load(kStages == 1 ? step : step + 1);
-            if (decays) put_decays(step + kStages);
-        }
+        if (decays)
+            for (int step = 0; step < chunks; ++step) read_decays(step), put_decays(step);
     } else {
         const int quarter = warp / 4, dv = warp % 4 * 32 + lane, t0 = quarter * kT, k0 = quarter * kH;
         const uint32_t mine = tm + (uint32_t(warp % 4) << 21);
@@ -338,8 +420,8 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&ready[which]);
         };
-        auto wait_done = [&](int which, int64_t step) {
-            wait(done[which], uint32_t(step));
+        auto wait_done = [&](int which, int step) {
+            wait(done[which], uint32_t(step), WaitSite(kChainKeys + which));
             tmem_fence_after();
         };
         auto read = [&](float (&x)[kT], uint32_t at) {
@@ -358,6 +440,15 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
             tmem_store<kT / 2>(mine + at + 32 + quarter * (kT / 2), lo);
         };
         auto meet = [] { asm volatile("bar.sync 1, %0;" ::"n"(kChainThreads) : "memory"); };
+        // the same, and whether no wait of any of the threads was in vain
+        auto all_well = [&] {
+            uint32_t all;
+            asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.and.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                         : "=r"(all)
+                         : "r"(uint32_t(ok)), "n"(kChainThreads)
+                         : "memory");
+            return all != 0;
+        };
         // from shared to global memory, whole 16-byte pieces
         auto copy = [&](char *to, const char *from, int bytes) {
 #pragma unroll 4
@@ -376,11 +467,11 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
                      sm + Space::keep + i * Space::kValues, tiles * int(Space::kTileBytes));
         };
         // where the outputs of chunk `step` wait while the next chunk is taken
-        auto out_place = [&](int64_t step) {
+        auto out_place = [&](int step) {
             return reinterpret_cast<T *>(sm + (Space::kOutInV && kept ? stage_of(step + 1) * Space::bytes + Space::v : Space::out));
         };
-        auto copy_out = [&](int64_t step) {
-            const int64_t c = chunk_of(step);
+        auto copy_out = [&](int step) {
+            const int c = chunk_of(step);
             const int n = rows_in(c);
             const T *from = out_place(step);
             T *to = delta_at<T>(p.out, batch, row0 + c * kChunk, head);
@@ -401,8 +492,8 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
         };
         // Rows that no map brings (in two pieces of bf16, or off 16 bytes): by all
         // threads, between chunks, into the one stage.
-        auto load_rows = [&](int64_t step) {
-            const int64_t c = chunk_of(step), row = row0 + c * kChunk;
+        auto load_rows = [&](int step) {
+            const int c = chunk_of(step), row = row0 + c * kChunk;
             const int n = rows_in(c);
             load_tile<T, false, kChunk, KD, kChainThreads>(tid, sm + Space::k, Space::kKeys, 0, p.k, batch, row, kh, n, keys, p.wide);
             load_tile<T, false, kChunk, KD, kChainThreads>(tid, sm + Space::q, Space::kKeys, 0, p.q, batch, row, kh, n, keys, p.wide);
@@ -453,25 +544,24 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
         };
         float o1[kT];  // forward: what the state gives to the outputs
         T o[kT];       // forward: the outputs of the chunk before
-        auto finish_out = [&](int64_t step) {
+        auto finish_out = [&](int step) {
             wait_done(4, step);
             float o2[kT];
             read(o2, kD1 + t0);
-            const float bad = ok ? 0.0f : __int_as_float(0x7fffffff);
 #pragma unroll
-            for (int j = 0; j < kT; ++j) o[j] = from_f32<T>(fmaf(p.scale, o2[j], o1[j]) + bad);
+            for (int j = 0; j < kT; ++j) o[j] = from_f32<T>(fmaf(p.scale, o2[j], o1[j]));
         };
-        auto put_out = [&](int64_t step) {
+        auto put_out = [&](int step) {
             T *to = out_place(step) + t0 * kMostValues + dv;
 #pragma unroll
             for (int j = 0; j < kT; ++j) to[j * kMostValues] = o[j];
         };
         // back: the queries' side, scale e^G dO, in two pieces
         uint32_t side_hi[kBack ? kT / 2 : 1], side_lo[kBack ? kT / 2 : 1];
-        auto prepare_side = [&](int64_t step) {
+        auto prepare_side = [&](int step) {
             const int st = stage_of(step);
             const char *dO = sm + st * Space::bytes + Space::v;
-            wait(full[st], round_of(step));
+            wait(full[st], round_of(step), kChainSide);
             const float4 *const first4 = reinterpret_cast<const float4 *>(rows_of[st].first + t0);
 #pragma unroll
             for (int j = 0; j < kT; j += 4) {
@@ -493,7 +583,7 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
             if constexpr (!kMaps) load_rows(0);
             if constexpr (kBack) prepare_side(0);
         }
-        for (int64_t step = 0; step < chunks; ++step) {
+        for (int step = 0; step < chunks; ++step) {
             const int st = stage_of(step);
             char *s = sm + st * Space::bytes;
             const int64_t at = (slot0 + chunk_of(step)) * p.heads + head;
@@ -511,7 +601,7 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&empty[stage_of(step - 1)]);
             }
-            wait(full[st], round_of(step));
+            wait(full[st], round_of(step), kChainRows);
             const ChainRows &r = rows_of[st];
             const float whole = r.first[kChunk - 1];
             const float4 *const first4 = reinterpret_cast<const float4 *>(r.first + t0);
@@ -614,38 +704,37 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
                 if (kept) meet();
                 put_state();
                 if constexpr (!kMaps) {
-                    wait(empty[0], uint32_t(step));
+                    wait(empty[0], uint32_t(step), kChainRoom);
                     load_rows(step + 1);
                     if constexpr (kBack) prepare_side(step + 1);
                 }
             }
         }
         if constexpr (!kBack)
-            if (whole_part && chunks > 0) {
-                finish_out(chunks - 1);
-                meet();
+            if (whole_part && chunks > 0) finish_out(chunks - 1);
+        if (!all_well()) {
+            in_vain = 1;
+        } else {
+            if (!kBack && whole_part && chunks > 0) {
                 if (chunks > 1) copy_out(chunks - 2);
                 meet();
                 put_out(chunks - 1);
                 meet();
                 copy_out(chunks - 1);
             }
-        // the last part's is the sequence's; another's own is the next one's start
-        const bool last = !kCut || (kPass == 2 && part + 1 == p.parts);
-        float *to = last ? kBack ? bp.grad_initial : p.final : unit ? p.part_maps : kPass == 1 ? p.part_ends : nullptr;
-        int64_t place = last ? seq * p.heads + head : (seq * p.parts + part) * p.heads + head;
-        if (kPass == 1 && part == 0) to = p.part_starts, place += p.heads;
-        if (to && dv < values) {
-            to += place * keys * values + dv;
-            const float bad = ok ? 0.0f : __int_as_float(0x7fffffff);
+            float *to = walk.end_state(bp);
+            if (to && dv < values) {
+                to += dv;
 #pragma unroll
-            for (int k = 0; k < kH; ++k)
-                if (k0 + k < keys) to[int64_t(k0 + k) * values] = S[k] + bad;
+                for (int k = 0; k < kH; ++k)
+                    if (k0 + k < keys) to[int64_t(k0 + k) * values] = S[k];
+            }
         }
     }
     tmem_fence_before();
     __syncthreads();
     if (warp == 0) tmem_free(tm, 512);
+    if (in_vain) chain_give_up<T, KD, kBack, kPass>(bp);
 }
 
 template <class T, int KD, bool kBack, bool kMaps, int kPass>

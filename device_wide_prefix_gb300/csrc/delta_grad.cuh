@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     extern __shared__ char raw[];
     __shared__ Sum2 sums[kChunk];
     __shared__ float beta[kChunk], first[kChunk], rest[kChunk], value_dot[kChunk];
-    __shared__ uint64_t bars[5];
+    __shared__ uint64_t bars[5], drained;
     __shared__ uint32_t tmem;
     const DeltaParams &p = bp.f;
     char *sm = reinterpret_cast<char *>((reinterpret_cast<uintptr_t>(raw) + 1023) / 1024 * 1024);
@@ -113,8 +113,14 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     const int part = warp / 4, dk = warp % 4 * 32 + lane, t0 = part * kCols, n = c.rows;
     const int kh = blockIdx.y, per = p.heads / p.key_heads, keys = p.keys, values = p.values;
     const int tiles = (keys + 63) / 64, value_tiles = (values + 63) / 64;
+#ifdef DWP_DELTA_TEST
+    __shared__ uint64_t never;
+    if (tid == 0) mbar_init(&never, 1);
+    Stall stall{&never, p.stall_site, p.stall_skip};
+#endif
     if (tid == 0) {
         for (int i = 0; i < 5; ++i) mbar_init(&bars[i], 1);
+        mbar_init(&drained, 1);
         fence_mbar_init();
     }
     if (warp == 0) tmem_alloc(&tmem, 512);
@@ -133,7 +139,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     __syncthreads();
     const uint32_t tm = tmem, mine = tm + (uint32_t(warp % 4) << 21);
     constexpr uint32_t kDX = 0, kDA = 128, kDW = 192, kDY = 320, kDU = 384;
-    bool ok = true;
+    bool ok = true;  // no wait was in vain: of this thread, and, where they meet, of any
     auto read = [&](float (&x)[kCols], uint32_t at) {
         uint32_t v[kCols];
         tmem_load<kCols>(v, mine + at);
@@ -145,7 +151,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
         copies_done();
         fence_proxy_async_smem();
         tmem_fence_before();
-        __syncthreads();
+        ok = __syncthreads_and(ok);
         tmem_fence_after();
     };
     // a key's or query's entry `dk` of row i
@@ -163,11 +169,15 @@ __global__ void __launch_bounds__(kGradThreads, 1)
         }
     };
     float dq[kCols], dkey[kCols];
+    int asked = 0;  // heads whose copies were issued, by thread 0
     for (int h = 0; h < per; ++h) {
         const int head = kh * per + h;
         const int64_t at = int64_t(blockIdx.x) * p.heads + head;
         const uint32_t parity = uint32_t(h & 1);
         auto wait = [&](int bar) {
+#ifdef DWP_DELTA_TEST
+            if (ok && stall.at(kGradFirst + bar)) ok = false;
+#endif
             if (ok) ok = mma_wait(&bars[bar], parity);
             tmem_fence_after();
         };
@@ -188,7 +198,8 @@ __global__ void __launch_bounds__(kGradThreads, 1)
                         make_uint4(0, 0, 0, 0);
         fence_proxy_async_smem();
         __syncthreads();
-        if (tid == 0) {
+        if (tid == 0 && ok) {
+            ++asked;
             const uint32_t each = uint32_t(values) * kTileRow;
             mbar_arrive_expect_tx(&bars[3], 2 * tiles * each + 4 * value_tiles * kTileBytes +
                                                 (kMaps ? 2 * kTileBytes + (h == 0 ? 4 * kTileBytes : 0) : 0));
@@ -259,7 +270,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
         meet();
         const Operand<kChunk, false> U(sm + Space::u), Ul(sm + Space::u + kRows);
         const Operand<kMost, true> S(sm + Space::state), Sl(sm + Space::state + kState);
-        if (warp == 0 && elect_one()) {
+        if (warp == 0 && elect_one() && ok) {
             const Operand<2 * kChunk, false> both(sm + Space::stack), bothl(sm + Space::stack + 2 * kRows);
             product_ss<kChunk, kMost>(tm + kDA, both, U, false);
             product_ss<kChunk, kMost>(tm + kDA, both, Ul, true);
@@ -290,6 +301,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
             }
         }
         // dV, and dR.V
+        const float in_vain = ok ? 0.0f : not_a_number();
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int i = e * (kGradThreads / 16) + tid / 16, j0 = tid % 16 * 8, left = values - j0;
@@ -300,7 +312,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 s = fmaf(f[j].x, v[e][2 * j], fmaf(f[j].y, v[e][2 * j + 1], s));
-                d[2 * j] = beta[i] * f[j].x, d[2 * j + 1] = beta[i] * f[j].y;
+                d[2 * j] = fmaf(beta[i], f[j].x, in_vain), d[2 * j + 1] = fmaf(beta[i], f[j].y, in_vain);
             }
             if (i < n && left > 0) {
                 T *to = delta_at<T>(bp.grad_v, c.batch, c.row + i, head) + j0;
@@ -367,7 +379,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
         }
         meeting *= first[kChunk - 1];
         meet();
-        if (warp == 0 && elect_one()) {
+        if (warp == 0 && elect_one() && ok) {
             const Operand<kChunk, true> K(sm + Space::k), Q(sm + Space::q);
             const Operand<2 * kChunk, false> W(sm + Space::cross), Wl(sm + Space::cross + kRows);
             const Operand<2 * kChunk, true> A(sm + Space::cross), Al(sm + Space::cross + kRows);
@@ -437,11 +449,11 @@ __global__ void __launch_bounds__(kGradThreads, 1)
         for (int o = 16; o > 0; o /= 2) meeting += __shfl_xor_sync(0xffffffffu, meeting, o);
         if (lane == 0) dots.whole[warp] = meeting;
         tmem_fence_before();
-        __syncthreads();
+        ok = __syncthreads_and(ok);
         if (warp == 15) {
             float whole = 0.0f;
             for (int w = 0; w < kGradThreads / 32; ++w) whole += dots.whole[w];
-            const float bad = ok ? 0.0f : __int_as_float(0x7fffffff);
+            const float bad = ok ? 0.0f : not_a_number();
             float g[2];
             Sum2 sum[2];
 #pragma unroll
@@ -464,7 +476,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     }
     if (dk < keys) {
         T *to_q = delta_at<T>(bp.grad_q, c.batch, c.row + t0, kh) + dk, *to_k = delta_at<T>(bp.grad_k, c.batch, c.row + t0, kh) + dk;
-        const float bad = ok ? 0.0f : __int_as_float(0x7fffffff);
+        const float bad = ok ? 0.0f : not_a_number();
 #pragma unroll
         for (int j = 0; j < kCols; ++j)
             if (t0 + j < n) {
@@ -473,7 +485,16 @@ __global__ void __launch_bounds__(kGradThreads, 1)
             }
     }
     __syncthreads();
-    if (warp == 0) tmem_free(tm, 512);
+    if (warp == 0) {
+        if (!ok) {
+            if (asked > 0) mma_wait(&bars[3], uint32_t(asked - 1) & 1u);
+            __syncwarp();
+            if (elect_one()) mma_commit(&drained);
+            mma_wait(&drained, 0);
+        }
+        __syncwarp();
+        tmem_free(tm, 512);
+    }
 }
 
 template <class T, bool kMaps>

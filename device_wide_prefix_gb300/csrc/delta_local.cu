@@ -50,6 +50,17 @@ __global__ void __launch_bounds__(kTeam * kTeams, 4 / kTeams)
     Sum2 *sums = sums_[team];
     float *beta = beta_[team];
     auto sync = [&] { asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "n"(kTeam) : "memory"); };
+#ifdef DWP_DELTA_TEST
+    __shared__ uint64_t never;
+    if (threadIdx.x == 0) mbar_init(&never, 1);
+    Stall stall{&never, p.stall_site, p.stall_skip};
+#endif
+    auto wait = [&](uint64_t &b, [[maybe_unused]] WaitSite site) {
+#ifdef DWP_DELTA_TEST
+        if (stall.at(site)) return false;
+#endif
+        return mma_wait(&b, 0);
+    };
     if (threadIdx.x == 0) {
         mbar_init(&bar, 1);
         mbar_init(&landed, 1);
@@ -87,10 +98,11 @@ __global__ void __launch_bounds__(kTeam * kTeams, 4 / kTeams)
     __syncthreads();
     tmem_fence_after();
     const uint32_t d = tmem;
-    bool ok = true;
+    bool issued = false;
     if (warp == 0) {
-        if (kMaps) ok = mma_wait(&landed, 0);
-        if (elect_one()) {
+        const bool rows_here = !kMaps || wait(landed, kLocalRows);
+        __syncwarp();
+        if (elect_one() && rows_here) {
             const Operand<2 * kChunk, false> hi(tile), lo(tile + kLo);
             product_ss<kChunk, KD>(d, hi, hi, false);
             if constexpr (kPieces<T> == 2) {
@@ -99,9 +111,11 @@ __global__ void __launch_bounds__(kTeam * kTeams, 4 / kTeams)
                 product_ss<kChunk, KD>(d, lo, lo, true);
             }
             mma_commit(&bar);
+            issued = true;
         }
         __syncwarp();
     }
+    bool ok = true;
     const int row = tid % kChunk;  // of the chunk, as key or as query
     for (int h = team; h < per; h += kTeams) {
         const int64_t at = int64_t(blockIdx.x) * p.heads + kh * per + h;
@@ -117,11 +131,12 @@ __global__ void __launch_bounds__(kTeam * kTeams, 4 / kTeams)
         load_rows(h + kTeams);
         sync();
         if (h == team) {
-            ok = mma_wait(&bar, 0) && ok;
+            ok = wait(bar, kLocalProduct);
+            __syncwarp();
             tmem_fence_after();
         }
         const Sum2 mine = sums[row];
-        const float scale = ok ? tid < kChunk ? beta[row] : 1.0f : __int_as_float(0x7fffffff);
+        const float scale = !ok ? not_a_number() : tid < kChunk ? beta[row] : 1.0f;
         // columns that this row reads: those before it, and a query's own
         const int cols = row < c.rows ? row + (tid >= kChunk) : 0;
 #pragma unroll 1
@@ -241,7 +256,14 @@ __global__ void __launch_bounds__(kTeam * kTeams, 4 / kTeams)
     }
     tmem_fence_before();
     __syncthreads();
-    if (warp == 0) tmem_free(d, kChunk);
+    if (warp == 0) {
+        if (!ok) {
+            if (kMaps) mma_wait(&landed, 0);
+            if (issued) mma_wait(&bar, 0);
+        }
+        __syncwarp();
+        tmem_free(d, kChunk);
+    }
 }
 
 template <class T, int KD, bool kMaps, int kTeams>

@@ -8,10 +8,14 @@
 
 namespace dwp {
 
-#if DWP_DELTA_TEST
+#ifdef DWP_DELTA_TEST
 // Build for tests (-DDWP_DELTA_TEST=1): calls as where no tensor map can be made.
 static std::atomic<int> delta_test_no_maps{0};
 extern "C" void dwp_delta_test_no_maps(int on) { delta_test_no_maps = on; }
+// And whose waits at one site run out (tensor.cuh, WaitSite; 0 for none).
+static std::atomic<int> delta_test_site{0}, delta_test_skip{0};
+extern "C" void dwp_delta_test_stall(int site, int skip) { delta_test_site = site, delta_test_skip = skip; }
+void delta_stall(DeltaParams &p) { p.stall_site = delta_test_site, p.stall_skip = delta_test_skip; }
 #endif
 
 namespace {
@@ -22,7 +26,7 @@ using EncodeMap = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, v
 
 // The driver's encoder, by way of the runtime, so that nothing links the driver.
 EncodeMap encode_map() {
-#if DWP_DELTA_TEST
+#ifdef DWP_DELTA_TEST
     if (delta_test_no_maps) return nullptr;
 #endif
     static std::atomic<void *> known{nullptr};

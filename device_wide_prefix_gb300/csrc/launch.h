@@ -257,6 +257,9 @@ struct DeltaParams {
     // makes of zeros, and [keys][keys] what it makes of any state
     int64_t parts, part_chunks;
     float *part_starts, *part_ends, *part_maps;
+#ifdef DWP_DELTA_TEST
+    int stall_site, stall_skip;  // tensor.cuh, Stall
+#endif
 };
 // Tensor maps of a call's bf16 rows, for all its kernels: boxes of 64 rows of one
 // head.  Not made for other rows, nor where a stride is past what a map holds or
@@ -284,6 +287,9 @@ struct DeltaStepParams {
     int64_t state_slot;
     const int32_t *slots;
 };
+#ifdef DWP_DELTA_TEST
+void delta_stall(DeltaParams &p);
+#endif
 DeltaMaps delta_maps(dwp_dtype t, const DeltaParams &p, const DeltaRows *grad_out);
 cudaError_t launch_delta_local(dwp_dtype t, const DeltaParams &p, const DeltaMaps &m, cudaStream_t s);
 // The cut: parts that fill the GPU's blocks of one chain each, eight chunks or

@@ -95,13 +95,41 @@ template <int N>
 __device__ __forceinline__ void set_registers_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
 // Wait for the phase of the given parity, without sleeping between polls (a
-// product takes less than a sleep); false after a second or so.
-constexpr uint32_t kProductWaitLimit = 1u << 22;
+// product takes less than a sleep); false after a second or so (a poll that finds
+// nothing takes 3.7 us).
+//
+// A block whose wait runs out gives up: whoever loads or issues and waited in vain
+// arrives nowhere and issues nothing from then on, so that who needs it waits in
+// vain too; what the block could not compute is NaN; and the copies and products
+// that are still on their way are waited for before it ends.
+#ifdef DWP_DELTA_TEST
+constexpr uint32_t kProductWaitLimit = 1u << 13;
+#else
+constexpr uint32_t kProductWaitLimit = 1u << 18;
+#endif
 __device__ __forceinline__ bool mma_wait(uint64_t *bar, uint32_t parity) {
     for (uint32_t i = 0; i < kProductWaitLimit; ++i)
         if (mbar_try_wait(bar, parity)) return true;
     return false;
 }
+__device__ __forceinline__ float not_a_number() { return __int_as_float(0x7fffffff); }
+
+// Places of a kernel that wait, for the build with test hooks.
+enum WaitSite {
+    kNoSite, kLocalRows, kLocalProduct,
+    kIssueRows, kIssueState, kIssueSides, kIssueCorrections, kLoadRoom, kLoadLanded, kDecayRoom,
+    kChainRows, kChainKeys, kChainOther, kChainInverse, kChainState, kChainOutputs, kChainRoom, kChainSide,
+    kGradFirst, kGradStates, kGradSecond, kGradRows, kGradEnds
+};
+#ifdef DWP_DELTA_TEST
+// A wait at the stalled site, but for the first `skip` of a thread, is for a barrier
+// at which nothing arrives.
+struct Stall {
+    uint64_t *never;
+    int site, skip;
+    __device__ __forceinline__ bool at(int here) { return here == site && skip-- <= 0 && !mma_wait(never, 0); }
+};
+#endif
 
 // A box of a tensor to shared memory, completing its bytes on `bar`; from
 // column `x`, whose byte offset is a multiple of 16, of head, row and batch.

@@ -323,7 +323,8 @@ dwp_status dwp_linear_recurrence_f32(const float *d_a, const float *d_b, float *
  *
  * These calls keep no status word: no kernel of theirs waits for another, and
  * only the gated delta rule's wait for copies and products of their own, each
- * wait bounded; should one run out, what the block writes is NaN.  Results are
+ * wait bounded; should one run out, what the block had still to compute is NaN
+ * (of a walk along a sequence and head all that it writes).  Results are
  * deterministic, bit for bit from run to run.  Scratch follows the two-call
  * pattern above, 16-byte aligned and never less than 16 bytes; its contents on
  * entry do not matter.
