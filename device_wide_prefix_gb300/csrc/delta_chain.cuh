@@ -13,7 +13,7 @@
 // value's row and a quarter of the keys), goes to tensor memory as the first operand
 // of the next products, as R and U do, and K, Q, T, A and dO are operands in
 // shared memory as they are stored.  What is not itself bf16 is two bf16
-// (split2): 16 bits, 2^-18 of a number at most is lost; of two such all four
+// (split2): 17 bits, 2^-17 of a number at most is lost; of two such all four
 // products are taken (without the smallest a call took 1% less, and
 // the gradient of g was up to a fifth further off).
 //
@@ -285,7 +285,7 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
                     product_ts<kChunk, kChunk>(tm + kD1, tm + kU, A, false);
                     product_ts<kChunk, kChunk>(tm + kD1, tm + kU + 32, A, true);
                     product_ts<kChunk, kChunk>(tm + kD1, tm + kU, Al, true);
-                    // (the smallest product is 2^-18 of a term: nothing to a bf16 output)
+                    // (the smallest product is at most 2^-16 of a term: nothing to a bf16 output)
                     if constexpr (kP == 2) product_ts<kChunk, kChunk>(tm + kD1, tm + kU + 32, Al, true);
                     mma_commit(&done[4]);
                 }

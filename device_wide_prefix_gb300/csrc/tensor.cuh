@@ -204,7 +204,7 @@ __device__ __forceinline__ void tmem_store(uint32_t at, const uint32_t (&v)[N]) 
 __device__ __forceinline__ void tmem_stored() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // A pair of f32 in two pieces of bf16 each: hi rounded, lo the rounded rest.
-// Together they hold 16 bits: |x - hi - lo| <= 2^-18 |x|.
+// Together they hold 17 bits, lo's sign among them: |x - hi - lo| <= 2^-17 |x|.
 __device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t &lo) {
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(y), "f"(x));
     const float xh = __uint_as_float(hi << 16), yh = __uint_as_float(hi & 0xffff0000u);

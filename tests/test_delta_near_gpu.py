@@ -1,9 +1,11 @@
 """How near the gated delta rule's results are to its 64-bit definition, head by
-head in the relative 2-norm: bounds of the size of what is stated for them, not
-of the largest that could be (test_delta_gpu)."""
+head in the relative 2-norm: bounds of the size of what is stated for them
+(delta_near, whose bounds are themselves tested in test_delta_near), not of the
+largest that could be (test_delta_gpu)."""
 import numpy as np
 import pytest
 
+import delta_near as near
 import delta_ref as ref
 
 pytestmark = pytest.mark.gpu
@@ -14,14 +16,8 @@ if not torch.cuda.is_available():
 
 import device_wide_prefix_gb300 as dwp  # noqa: E402
 from device_wide_prefix_gb300 import build as dwp_build  # noqa: E402
+from test_delta_edges_gpu import backward, forward  # noqa: E402
 from test_delta_gpu import Case  # noqa: E402
-
-# A rounding to a bf16 leaves at most 2^-9 of each value.  Beside it there are
-# products of numbers in two bf16 pieces, which keep 16 bits each: 2^-17 of a
-# term, in four products one after another and their sums, whose terms cancel by
-# some factors of two.  2^-14 counts eight such terms in line.
-PIECES = 2.0 ** -14
-BF16 = 2.0 ** -9
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -30,9 +26,11 @@ def lib():
     return dwp.load()
 
 
-def far(got, want):
-    got = got.detach().double().cpu().numpy().reshape(want.shape)
-    return np.sqrt(((got - want) ** 2).sum() / (want ** 2).sum())
+def check(name, got, want, by_rows=True):
+    rounded = torch.from_numpy(want).to(got.dtype).double().numpy()
+    if got.dtype == torch.float32:
+        rounded = want
+    near.check(name, got.detach().double().cpu().numpy().reshape(want.shape), want, rounded, by_rows)
 
 
 @pytest.mark.parametrize("keep", [False, True])
@@ -47,4 +45,33 @@ def test_bf16_outputs_are_off_by_their_own_rounding(batch, rows, key_heads, head
     for b in range(batch):
         for h in range(heads):
             want = ref.delta(*c.head(slice(b * rows, (b + 1) * rows), h), c.scale, c.values["state"][b, h])[0]
-            assert far(out[b, :, h], want) <= BF16 + PIECES
+            check("out", out[b, :, h], want)
+
+
+@pytest.mark.parametrize("dtype,batch,rows,key_heads,heads,keys,values,pad,decay", [
+    ("bf16", 1, 1027, 1, 1, 128, 128, 0, 0.02), ("f32", 1, 640, 1, 2, 128, 128, 0, 0.02), ("f16", 2, 500, 1, 2, 64, 24, 0, 0.05),
+    ("f32", 1, 300, 2, 4, 16, 16, 0, 0.1), ("bf16", 1, 300, 1, 3, 40, 72, 1, 0.1), ("f16", 1, 260, 1, 1, 128, 128, 3, 1.0),
+    # cut in parts, forward and back
+    ("bf16", 1, 1600, 1, 1, 128, 128, 0, 0.01), ("bf16", 2, 2049, 1, 2, 64, 128, 0, 0.01), ("bf16", 1, 1984, 2, 2, 16, 16, 0, 0.01)])
+def test_every_result_of_many_chunks(dtype, batch, rows, key_heads, heads, keys, values, pad, decay):
+    """Outputs, states and gradients of each head, as a whole and chunk by chunk."""
+    c = Case(32, (batch, rows), None, dtype, key_heads, heads, keys, values, pad, decay=decay)
+    out, final, points = forward(c)
+    grads = backward(c, points)
+    for b in range(batch):
+        span = slice(b * rows, (b + 1) * rows)
+        shared = {n: np.zeros((rows, key_heads, keys)) for n in ("q", "k")}
+        for h in range(heads):
+            x, s0 = c.head(span, h), c.values["state"][b, h]
+            want, last, *_ = ref.delta(*x, c.scale, s0)
+            check("out", out[b, :, h], want)
+            check("final", final[b, h], last, False)
+            G, _ = ref.delta_grad(c.grad_of(span, h), *x, c.scale, s0, c.values["grad_state"][b, h])
+            for n in ("v", "g", "beta"):
+                check(n, grads[n][b, :, h], G[n])
+            check("initial_state", grads["initial_state"][b, h], G["initial_state"], False)
+            for n in ("q", "k"):
+                shared[n][:, h // c.per] += G[n]
+        for n in ("q", "k"):
+            for kh in range(key_heads):
+                check(n, grads[n][b, :, kh], shared[n][:, kh])
