@@ -328,10 +328,10 @@ constexpr size_t kSumBytes = size_t(2) * 16384 * sizeof(float);
 template <class T, int V, int K, bool kBlock>
 cudaError_t forward_k(const LayerNormParams &p, cudaStream_t s) {
     const int64_t work = p.rows * p.groups;
-    if (kBlock) return launch_pdl(layer_norm_kernel<T, V, K, true>, dim3(uint32_t(work)), dim3(p.team), 0, s, p);
+    const auto kernel = layer_norm_kernel<T, V, K, kBlock>;
+    if constexpr (kBlock) return launch_pdl(kernel, dim3(uint32_t(work)), dim3(p.team), 0, s, p);
     const int64_t teams = kTeamThreads / p.team;
-    return launch_pdl(layer_norm_kernel<T, V, K, false>, dim3(uint32_t((work + teams - 1) / teams)), dim3(kTeamThreads), 0,
-                      s, p);
+    return launch_pdl(kernel, dim3(uint32_t((work + teams - 1) / teams)), dim3(kTeamThreads), 0, s, p);
 }
 
 template <class T, int V>
