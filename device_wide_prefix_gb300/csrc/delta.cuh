@@ -122,7 +122,7 @@ __device__ __forceinline__ void copy16(uint32_t to, const void *from, uint32_t b
 }
 __device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
-// Pieces of bf16 that hold a T: a bf16 itself, or the two that keep 16 bits of
+// Pieces of bf16 that hold a T: a bf16 itself, or the two that keep 17 bits of
 // an f32 and all 11 of an f16.
 template <class T>
 constexpr int kPieces = 2;
@@ -149,10 +149,10 @@ __device__ __forceinline__ void store_pieces(char *hi, char *lo, uint32_t at, co
 // Rows of a head into tiles of kRows rows and kWidth columns, from row `first`
 // of the tile on: 64 rows, zeros past the chunk's `n` and past `dim` columns.
 // The second piece lies `lo` bytes behind the first.  By kThreads threads.
-// `wide`: the rows are whole 16-byte pieces (kWide: known to be).
-template <class T, bool kWide, int kRows, int kWidth, int kThreads>
+// `wide`: the rows are whole 16-byte pieces.
+template <class T, int kRows, int kWidth, int kThreads>
 __device__ __forceinline__ void load_tile(int thread, char *tile, uint32_t lo, int first, const DeltaRows &r, int64_t batch,
-                                          int64_t row, int head, int n, int dim, bool wide = kWide) {
+                                          int64_t row, int head, int n, int dim, bool wide) {
     const T *src = delta_at<T>(r, batch, row, head);
 #pragma unroll 4
     for (int e = thread; e < kChunk * kWidth / 8; e += kThreads) {

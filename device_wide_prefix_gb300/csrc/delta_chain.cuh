@@ -426,7 +426,7 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
         };
         auto read = [&](float (&x)[kT], uint32_t at) {
             uint32_t v[kT];
-            tmem_load<kT>(v, mine + at);
+            tmem_load(v, mine + at);
             tmem_ready();
 #pragma unroll
             for (int j = 0; j < kT; ++j) x[j] = __uint_as_float(v[j]);
@@ -436,8 +436,8 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
             uint32_t hi[kT / 2], lo[kT / 2];
 #pragma unroll
             for (int j = 0; j < kT / 2; ++j) split2(x[2 * j], x[2 * j + 1], hi[j], lo[j]);
-            tmem_store<kT / 2>(mine + at + quarter * (kT / 2), hi);
-            tmem_store<kT / 2>(mine + at + 32 + quarter * (kT / 2), lo);
+            tmem_store(mine + at + quarter * (kT / 2), hi);
+            tmem_store(mine + at + 32 + quarter * (kT / 2), lo);
         };
         auto meet = [] { asm volatile("bar.sync 1, %0;" ::"n"(kChainThreads) : "memory"); };
         // the same, and whether no wait of any of the threads was in vain
@@ -495,10 +495,10 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
         auto load_rows = [&](int step) {
             const int c = chunk_of(step), row = row0 + c * kChunk;
             const int n = rows_in(c);
-            load_tile<T, false, kChunk, KD, kChainThreads>(tid, sm + Space::k, Space::kKeys, 0, p.k, batch, row, kh, n, keys, p.wide);
-            load_tile<T, false, kChunk, KD, kChainThreads>(tid, sm + Space::q, Space::kKeys, 0, p.q, batch, row, kh, n, keys, p.wide);
+            load_tile<T, kChunk, KD, kChainThreads>(tid, sm + Space::k, Space::kKeys, 0, p.k, batch, row, kh, n, keys, p.wide);
+            load_tile<T, kChunk, KD, kChainThreads>(tid, sm + Space::q, Space::kKeys, 0, p.q, batch, row, kh, n, keys, p.wide);
             if constexpr (kBack) {
-                load_tile<T, false, kChunk, kMostValues, kChainThreads>(tid, sm + Space::v, Space::kValues, 0, bp.grad_out, batch,
+                load_tile<T, kChunk, kMostValues, kChainThreads>(tid, sm + Space::v, Space::kValues, 0, bp.grad_out, batch,
                                                                         row, head, n, p.values, p.wide);
             } else {
                 const T *src = delta_at<T>(p.v, batch, row, head);
@@ -527,8 +527,8 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
                 uint32_t hi[8], lo[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) split2(S[k + 2 * j], S[k + 2 * j + 1], hi[j], lo[j]);
-                tmem_store<8>(mine + kS + (k0 + k) / 2, hi);
-                tmem_store<8>(mine + kS + KD / 2 + (k0 + k) / 2, lo);
+                tmem_store(mine + kS + (k0 + k) / 2, hi);
+                tmem_store(mine + kS + KD / 2 + (k0 + k) / 2, lo);
                 if (kept)
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
@@ -626,8 +626,8 @@ __global__ void __launch_bounds__(kChainThreads + kHelpThreads, 1)
                 put_rows(kR, x);
             } else {
                 if constexpr (kBack) {
-                    tmem_store<kT / 2>(mine + kU + quarter * (kT / 2), side_hi);
-                    tmem_store<kT / 2>(mine + kU + 32 + quarter * (kT / 2), side_lo);
+                    tmem_store(mine + kU + quarter * (kT / 2), side_hi);
+                    tmem_store(mine + kU + 32 + quarter * (kT / 2), side_lo);
                 }
                 wait_done(0, step);
                 read(x, kD0 + t0);

@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     bool ok = true;  // no wait was in vain: of this thread, and, where they meet, of any
     auto read = [&](float (&x)[kCols], uint32_t at) {
         uint32_t v[kCols];
-        tmem_load<kCols>(v, mine + at);
+        tmem_load(v, mine + at);
         tmem_ready();
 #pragma unroll
         for (int j = 0; j < kCols; ++j) x[j] = __uint_as_float(v[j]);
@@ -227,10 +227,10 @@ __global__ void __launch_bounds__(kGradThreads, 1)
         }
         if constexpr (!kMaps) {
             if (h == 0) {
-                load_tile<T, false, kChunk, kMost, kGradThreads>(tid, sm + Space::k, kRows, 0, p.k, c.batch, c.row, kh, n, keys, p.wide);
-                load_tile<T, false, kChunk, kMost, kGradThreads>(tid, sm + Space::q, kRows, 0, p.q, c.batch, c.row, kh, n, keys, p.wide);
+                load_tile<T, kChunk, kMost, kGradThreads>(tid, sm + Space::k, kRows, 0, p.k, c.batch, c.row, kh, n, keys, p.wide);
+                load_tile<T, kChunk, kMost, kGradThreads>(tid, sm + Space::q, kRows, 0, p.q, c.batch, c.row, kh, n, keys, p.wide);
             }
-            load_tile<T, false, 2 * kChunk, kMost, kGradThreads>(tid, sm + Space::stack, 2 * kRows, 0, bp.grad_out, c.batch, c.row,
+            load_tile<T, 2 * kChunk, kMost, kGradThreads>(tid, sm + Space::stack, 2 * kRows, 0, bp.grad_out, c.batch, c.row,
                                                                  head, n, values, p.wide);
         }
         // this thread's values of V: two pieces of eight

@@ -87,8 +87,8 @@ __global__ void __launch_bounds__(kTeam * kTeams, 4 / kTeams)
     };
     load_rows(team);
     if constexpr (!kMaps) {
-        load_tile<T, false, 2 * kChunk, KD, kTeam * kTeams>(threadIdx.x, tile, kLo, 0, p.k, c.batch, c.row, kh, c.rows, p.keys, p.wide);
-        load_tile<T, false, 2 * kChunk, KD, kTeam * kTeams>(threadIdx.x, tile, kLo, kChunk, p.q, c.batch, c.row, kh, c.rows, p.keys,
+        load_tile<T, 2 * kChunk, KD, kTeam * kTeams>(threadIdx.x, tile, kLo, 0, p.k, c.batch, c.row, kh, c.rows, p.keys, p.wide);
+        load_tile<T, 2 * kChunk, KD, kTeam * kTeams>(threadIdx.x, tile, kLo, kChunk, p.q, c.batch, c.row, kh, c.rows, p.keys,
                                                             p.wide);
         copies_done();
         fence_proxy_async_smem();
@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(kTeam * kTeams, 4 / kTeams)
             float f[16] = {};
             if (j0 < row / 32 * 32 + 32) {  // the whole warp's
                 uint32_t v[16];
-                tmem_load<16>(v, d + (uint32_t(in_team) << 21) + j0);
+                tmem_load(v, d + (uint32_t(in_team) << 21) + j0);
                 tmem_ready();
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {

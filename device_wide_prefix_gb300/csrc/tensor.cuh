@@ -164,42 +164,19 @@ __device__ __forceinline__ void tmem_free(uint32_t at, uint32_t columns) {
 #define DWP_R8(v, o) "=r"(v[o]), "=r"(v[o + 1]), "=r"(v[o + 2]), "=r"(v[o + 3]), "=r"(v[o + 4]), "=r"(v[o + 5]), "=r"(v[o + 6]), "=r"(v[o + 7])
 #define DWP_W8(v, o) "r"(v[o]), "r"(v[o + 1]), "r"(v[o + 2]), "r"(v[o + 3]), "r"(v[o + 4]), "r"(v[o + 5]), "r"(v[o + 6]), "r"(v[o + 7])
 
-// Columns at .. + N of the warp's lanes, one lane a thread.  tmem_ready() before use.
-template <int N>
-__device__ __forceinline__ void tmem_load(uint32_t (&v)[N], uint32_t at) {
-    static_assert(N == 16 || N == 32, "16 or 32 columns");
-    if constexpr (N == 16) {
-        asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-                     "%15}, [%16];"
-                     : DWP_R8(v, 0), DWP_R8(v, 8)
-                     : "r"(at));
-    } else {
-        asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-                     "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-                     : DWP_R8(v, 0), DWP_R8(v, 8), DWP_R8(v, 16), DWP_R8(v, 24)
-                     : "r"(at));
-    }
+// Sixteen columns from `at` on of the warp's lanes, one lane a thread.  tmem_ready() before use.
+__device__ __forceinline__ void tmem_load(uint32_t (&v)[16], uint32_t at) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+                 "%15}, [%16];"
+                 : DWP_R8(v, 0), DWP_R8(v, 8)
+                 : "r"(at));
 }
 __device__ __forceinline__ void tmem_ready() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
-template <int N>
-__device__ __forceinline__ void tmem_store(uint32_t at, const uint32_t (&v)[N]) {
-    static_assert(N == 8 || N == 16 || N == 32, "8, 16 or 32 columns");
-    if constexpr (N == 8) {
-        asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::DWP_W8(v, 0), "r"(at)
-                     : "memory");
-    } else if constexpr (N == 16) {
-        asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, "
-                     "%13, %14, %15};" ::DWP_W8(v, 0),
-                     DWP_W8(v, 8), "r"(at)
-                     : "memory");
-    } else {
-        asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, "
-                     "%13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::DWP_W8(
-                         v, 0),
-                     DWP_W8(v, 8), DWP_W8(v, 16), DWP_W8(v, 24), "r"(at)
-                     : "memory");
-    }
+// Eight columns.
+__device__ __forceinline__ void tmem_store(uint32_t at, const uint32_t (&v)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::DWP_W8(v, 0), "r"(at)
+                 : "memory");
 }
 __device__ __forceinline__ void tmem_stored() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -209,11 +186,6 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t 
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(y), "f"(x));
     const float xh = __uint_as_float(hi << 16), yh = __uint_as_float(hi & 0xffff0000u);
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(lo) : "f"(y - yh), "f"(x - xh));
-}
-__device__ __forceinline__ uint32_t round2(float x, float y) {
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(y), "f"(x));
-    return r;
 }
 
 }  // namespace dwp
