@@ -13,7 +13,7 @@ bool delta_sizes_ok(int64_t dtype, int64_t beta_dtype, int64_t keys, int64_t val
                     double scale) {
     return dtype_ok(dtype) && (beta_dtype == dtype || beta_dtype == DWP_F32) && keys >= 1 && keys <= kMaxHeadSize &&
            values >= 1 && values <= kMaxHeadSize && key_heads >= 1 && heads >= key_heads && heads <= kMaxGroups &&
-           heads % key_heads == 0 && scale - scale == 0.0;
+           heads % key_heads == 0 && float(scale) - float(scale) == 0.0f;  // finite as the kernels take it
 }
 
 DeltaRows delta_rows(const dwp_heads &x) {
