@@ -31,10 +31,10 @@
 // most; 6,900 with 128 blocks), of which the products that wait for one another
 // are 1,500; carrying numbers between tensor memory, registers and pieces is the
 // rest.  4 x 2048 rows x 32 heads take 117 us; x 16 heads, with what the gradient
-// needs kept, 190, and back 168.  Keys up to 64 take half the state (KD 64): 171
-// us a call of 4 x 2048 x 32 in place of 195.  bf16 rows of whole 16-byte pieces
-// come by tensor maps, a chunk ahead (195); others are read and split by the
-// sixteen warps between chunks (off 16 bytes 497, f16 419, f32 443).
+// needs kept, 188, and back 170.  Keys up to 64 take half the state (KD 64): 170
+// us a call of 4 x 2048 x 32 in place of 191.  bf16 rows of whole 16-byte pieces
+// come by tensor maps, a chunk ahead (191); others are read and split by the
+// sixteen warps between chunks (off 16 bytes 468, f16 414, f32 438).
 //
 // Few sequences and heads leave most of the GPU idle while each walks its
 // chunks.  A state goes through a part of a sequence linearly, S -> M S + E, so

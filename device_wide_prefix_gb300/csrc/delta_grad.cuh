@@ -22,8 +22,8 @@
 // 4 x 2048 rows x 16 heads of 128 x 128 take 264 us (239 with two pieces of dA
 // and E and without the smallest products), of which moving the data is 93 (543
 // MB read, 88 written): 2,048 blocks of one chunk each wait for their states and
-// rows (long scoreboard 3.3 cycles an instruction, barriers 2.0; one block fits
-// an SM), tensor cores are 12% busy.  Tried before that and slower than 239:
+// rows (long scoreboard 3.7 cycles an instruction, barriers 2.4; one block fits
+// an SM), tensor cores are 14% busy.  Tried before that and slower than 239:
 // asking for the next block's rows ahead of it (275), loads earlier in the block
 // (273), blocks of one chunk's heads together (287), S1 through shared memory (246).
 #pragma once

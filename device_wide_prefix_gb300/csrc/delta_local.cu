@@ -11,10 +11,10 @@
 // The loops are short on purpose: unrolled, three of ten cycles of a warp went
 // to fetching instructions.
 //
-// 4 x 2048 rows, 16 key heads and 32 heads of 128 keys take 77 us, of which moving
-// the data would be 20; 16 heads 46.  The
-// substitutions' steps bound it: barriers are the longest wait (2.6 cycles an
-// instruction), the scheduler issues 0.43 a cycle, tensor cores are 2% busy.
+// 4 x 2048 rows, 16 key heads and 32 heads of 128 keys take 78 us, of which moving
+// the data (201 MB) would be 30; 16 heads 45.  The substitutions' steps bound it:
+// barriers are the longest wait (2.5 cycles an instruction), the scheduler issues
+// 0.43 a cycle, tensor cores are 2% busy.
 #include "delta.cuh"
 
 namespace dwp {

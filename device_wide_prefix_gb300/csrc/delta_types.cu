@@ -133,8 +133,8 @@ DeltaMaps delta_maps(dwp_dtype t, const DeltaParams &p, const DeltaRows *grad_ou
 // Parts that a walk along a sequence is cut into: as many as fill the GPU's
 // blocks in pass 1, eight chunks each at least, and three or none (of two parts
 // the second would wait for the first as before).  Cut against uncut, bf16 heads
-// of 128 x 128: 1 sequence x 8192 rows x 32 heads 468 us against 502, 32768 rows
-// 1668 against 1961, the training step of 8192 rows x 16 heads 1053 against 1720.
+// of 128 x 128: 1 sequence x 8192 rows x 32 heads 466 us against 502, 32768 rows
+// 1655 against 1961, the training step of 8192 rows x 16 heads 1044 against 1720.
 // With more than 50 walks the two passes would be longer than the one; with
 // offsets the parts would depend on what the host has not read.
 int64_t delta_parts(int64_t walks, int64_t chunks) {

@@ -11,8 +11,11 @@
 //   M2 = sum M2_w + n_w (mean_w - mean)^2,
 // so a mean far from zero costs nothing, and a block meets once a row.
 //
-// Memory bounds the forward: 8192 x 4096 bf16 onto an f32 residual (403 MB) takes
-// 76 us, 0.78 of the copy rate; 8 rows 2 us, the rest of a call is the host's.
+// With a residual memory bounds the forward: 8192 x 4096 bf16 onto an f32 one (403
+// MB) takes 77 us, 0.77 of the copy rate; 8 rows 2 us, the rest of a call is the
+// host's.  Without one a block's load, its warps' meeting and its store are too
+// little to hide one another: 53 us where the bytes take 20, 8192 wide 149 of 40,
+// 16384 wide 237 of 79.
 // The gradient of the same (537 MB) 124 us, 0.64: it holds a row's values, its
 // gradients and the columns' sums, and waits for each row's moments.  4099 x 32
 // groups of 128 in f16 36 us, 0.41: few warps a row's loads are spread over.

@@ -492,6 +492,7 @@ dwp_status dwp_selective_scan_step(const dwp_selective_scan_step_args *args, dwp
  *                  decay.  Below -110 (-infinity too) it counts as -110, whose
  *                  exponential is 0 in f32 all the same
  *   beta           rows of [heads], beta_dtype: dtype or DWP_F32
+ *   scale          finite as an f32
  *   initial_state  f32 [sequences, heads, keys, values], or NULL for zeros
  *   final_state    NULL, or the same after each sequence's last row (may not
  *                  overlap initial_state)
@@ -506,11 +507,14 @@ dwp_status dwp_selective_scan_step(const dwp_selective_scan_step_args *args, dwp
  *                  bf16 batch entries (24 chunks and more) have few heads (under
  *                  51 in all) and are cut in parts
  * A sequence is taken in chunks of DWP_DELTA_CHUNK rows from its first.  A
- * value that is not finite reaches its own sequence and head only, there also
- * the rows before it in its chunk.  Products of two f32 numbers (states,
- * corrections, weights q.k, f32 rows) take each in two pieces of bf16, 16 bits
- * together (f32 outputs are 3e-6 to 8e-6 off in the 2-norm, dg of a few rows up
- * to 1.2e-5; a bf16 output by its own rounding, 1.7e-3).
+ * value that is not finite reaches its own sequence and heads only, but there
+ * the rows before it in its chunk too: a batch entry that is padded at its end
+ * is padded with numbers (zeros, say), never with memory that was not written,
+ * or its length is given by offsets, whose rows outside are not read.
+ * Products of two f32 numbers (states, corrections, weights q.k, f32 rows) take
+ * each in two pieces of bf16, 17 bits together (f32 outputs are 3e-6 to 8e-6
+ * off in the 2-norm, dg of a few rows up to 1.2e-5; a bf16 output by its own
+ * rounding, 1.7e-3); beyond 3.38e38, bf16's largest, one is not finite.
  */
 #define DWP_DELTA_CHUNK 64
 typedef struct dwp_heads {
