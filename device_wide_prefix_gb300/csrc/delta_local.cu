@@ -277,7 +277,7 @@ cudaError_t local_n(const DeltaParams &p, const DeltaMaps &maps, cudaStream_t s)
 // Two teams share a block's keys where heads do, unless there are blocks enough
 // without, of rows that maps bring (others take more threads to load and split).
 // A call with one team against two, 128 x 128, bf16: 4 x 2048 rows x 16 key heads
-// 192 us against 201, 4 key heads 196 against 202, 1 key head (128 blocks) of 16
+// 193 us against 201, 4 key heads 196 against 202, 1 key head (128 blocks) of 16
 // heads 192 against 168, 512 rows x 2 key heads of 16 heads 74 against 61; off 16
 // bytes, 4 x 2048 rows x 16 key heads, 549 against 459, in f32 490 against 429.
 template <class T, int KD, bool kMaps>

@@ -513,8 +513,10 @@ dwp_status dwp_selective_scan_step(const dwp_selective_scan_step_args *args, dwp
  * or its length is given by offsets, whose rows outside are not read.
  * Products of two f32 numbers (states, corrections, weights q.k, f32 rows) take
  * each in two pieces of bf16, 17 bits together (f32 outputs are 3e-6 to 8e-6
- * off in the 2-norm, dg of a few rows up to 1.2e-5; a bf16 output by its own
- * rounding, 1.7e-3); beyond 3.38e38, bf16's largest, one is not finite.
+ * off in the 2-norm; the gradients of g and beta, sums that cancel, up to 1.3e-5
+ * where they have few rows or keys, of one row and head up to 4e-5; a bf16
+ * output by its own rounding, 1.7e-3); beyond 3.38e38, bf16's largest, an f32 is
+ * not finite.
  */
 #define DWP_DELTA_CHUNK 64
 typedef struct dwp_heads {
